@@ -26,7 +26,8 @@ A forward and backward on torch tensors (v, b, c [B, T, H, d] bf16; g, beta
 ``h0``, ``hT``, ``dhT``, ``dh0`` may be None; ``make_shape(..., gate_logits=True,
 norm_bc=True)`` moves the gates' sigmoid and the L2 normalisation of b and c
 into the kernels, and ``gdn_plan(s, backward)`` tells which kernels a call
-will use.
+will use.  The latent-attention operators beside the recurrence (``gdn_mla_*``) are in :mod:`.mla` and exported here
+under their C names.
 """
 from __future__ import annotations
 
@@ -120,6 +121,8 @@ def load(path: str | None = None):
             lib.gdn_last_device_status.restype = ctypes.c_int
             lib.gdn_status_string.argtypes = [ctypes.c_int]
             lib.gdn_status_string.restype = ctypes.c_char_p
+            from . import mla
+            mla.declare(lib)
             _lib = lib
     return _lib
 
@@ -226,3 +229,9 @@ def gdn_status_string(status: int) -> str:
 def check(status: int, what: str = "") -> None:
     if status != GDN_OK:
         raise GdnError(status, what)
+
+
+# latent attention; mla takes the helpers above from this module, so it comes last
+from .mla import (gdn_mla_attn_t, gdn_mla_bwd, gdn_mla_cache_t, gdn_mla_decode, gdn_mla_decode_workspace_bytes,  # noqa: E402
+                  gdn_mla_fwd, gdn_mla_prep, gdn_mla_prep_bwd, gdn_mla_prep_t, gdn_mla_prep_workspace_bytes,
+                  gdn_mla_view_t, gdn_mla_workspace_bytes, make_mla_attn, make_mla_cache, make_mla_prep)

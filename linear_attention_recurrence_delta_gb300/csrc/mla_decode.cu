@@ -1,0 +1,259 @@
+// mla_decode.cu -- attention of a few new tokens over the paged latent cache: the workers' plan, the join of their
+// pieces, and the CUDA-core worker.
+#include "mla_decode_common.cuh"
+
+namespace gdn {
+namespace mla {
+
+DecodePlan decode_plan(const gdn_mla_cache_t& s)
+{
+    DecodePlan p;
+    const int all = s.T * s.H;
+    const int most = 8;
+    p.groups = (all + most - 1) / most;
+    p.rows = (all + p.groups - 1) / p.groups;
+    p.ctas = 152 / p.groups > 0 ? 152 / p.groups : 1;
+    p.slots = p.ctas + s.B;
+    const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    p.err_off = 256;
+    p.l_off = up(p.err_off + (size_t)p.groups * p.ctas * 4);
+    p.o_off = up(p.l_off + (size_t)p.groups * p.slots * p.rows * 4);
+    p.total = up(p.o_off + (size_t)p.groups * p.slots * p.rows * s.dc * 4);
+    return p;
+}
+
+namespace {
+
+constexpr int kThreads = 256, kMaxRows = 8, kStep = 32;   // cache rows in shared memory at a time
+
+// 8 query rows a worker; a warp's lanes take a row's scores for 32 cache rows, a thread two latent columns of the
+// output of all 8 rows.  FMAs bound it.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs a)
+{
+    extern __shared__ float smem[];
+    __shared__ float P[kMaxRows][kStep], keep[kMaxRows], top[kMaxRows], sum[kMaxRows];
+    __shared__ int place[2];
+    __shared__ long long span;
+    const gdn_mla_cache_t& s = a.s;
+    const int W = s.dc + s.dr, pitch = (W + 31) / 32 * 32 + 4;
+    float *Q = smem, *K = smem + kMaxRows * pitch;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cta = blockIdx.x, group = blockIdx.y;
+    const Deal deal{a.len, s.B, s.maxpages * s.page};
+    if (warp == 0) {
+        const long long share = deal_share(deal, a.ctas);
+        int b, tile;
+        deal_find(deal, share * cta, b, tile);
+        if (lane == 0) {
+            place[0] = b;
+            place[1] = tile;
+            span = share;
+            a.cta_err[group * a.ctas + cta] = 0;
+        }
+    }
+    __syncthreads();
+    int b = place[0], tile = place[1];
+    long long left = span;
+    const int row0 = group * a.rows, rows = min(a.rows, s.T * s.H - row0);
+    while (left > 0 && b < s.B) {
+        const int n = deal.rows(b), tiles = deal.tiles(b);
+        if (tiles == 0) {
+            b++;
+            continue;
+        }
+        const int to = (int)min((long long)tiles, tile + left);
+        __syncthreads();
+        for (int i = tid; i < kMaxRows * (pitch - 4) / 8; i += kThreads) {
+            const int r = i / ((pitch - 4) / 8), c = (i - r * ((pitch - 4) / 8)) * 8;
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (r < rows && c < W) {
+                const int t = (row0 + r) / s.H, h = (row0 + r) - t * s.H;
+                const long long tok = (long long)b * s.T + t;
+                if (c < s.dc)
+                    load8((const T*)a.qc.p + tok * a.qc.tok + h * a.qc.head + c, x);
+                else
+                    load8((const T*)a.qr.p + tok * a.qr.tok + h * a.qr.head + (c - s.dc), x);
+            }
+            store8(Q + r * pitch + c, x);
+        }
+        if (tid < kMaxRows) {
+            top[tid] = -INFINITY;
+            sum[tid] = 0.f;
+        }
+        float o[kMaxRows][2] = {};
+        const int last = min(n, to * kDecodeTile);
+        for (int j0 = tile * kDecodeTile; j0 < last; j0 += kStep) {
+            __syncthreads();
+            for (int i = tid; i < kStep * (pitch - 4) / 8; i += kThreads) {
+                const int r = i / ((pitch - 4) / 8), c = (i - r * ((pitch - 4) / 8)) * 8, j = j0 + r;
+                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (j < n && c < W) {
+                    const int page = a.table[(long long)b * s.maxpages + j / s.page];
+                    if (page >= 0 && page < s.npages)
+                        load8((const T*)a.cache + ((long long)page * s.page + j % s.page) * W + c, x);
+                }
+                store8(K + r * pitch + c, x);
+            }
+            __syncthreads();
+            {   // scores of row `warp` with cache row j0 + lane
+                float x = 0.f;
+                for (int c = 0; c < W; c += 4) {
+                    const float4 q = *reinterpret_cast<const float4*>(Q + warp * pitch + c);
+                    const float4 k = *reinterpret_cast<const float4*>(K + lane * pitch + c);
+                    x += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+                }
+                const int t = (row0 + warp) / s.H;
+                x = j0 + lane < n - (s.T - 1 - t) ? x * s.scale * 1.4426950408889634f : -INFINITY;
+                float m = x;
+#pragma unroll
+                for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+                const float was = top[warp];
+                m = fmaxf(m, was);
+                const float base = m == -INFINITY ? 0.f : m;
+                const float p = exp2f(x - base), f = exp2f(was - base);
+                float l = p;
+#pragma unroll
+                for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+                P[warp][lane] = p;
+                __syncwarp();
+                if (lane == 0) {
+                    keep[warp] = f;
+                    top[warp] = m;
+                    sum[warp] = sum[warp] * f + l;
+                }
+            }
+            __syncthreads();
+            if (2 * tid < s.dc) {
+#pragma unroll
+                for (int r = 0; r < kMaxRows; r++) {
+                    o[r][0] *= keep[r];
+                    o[r][1] *= keep[r];
+                }
+#pragma unroll 4
+                for (int k = 0; k < kStep; k++) {
+                    const float2 v = *reinterpret_cast<const float2*>(K + k * pitch + 2 * tid);
+#pragma unroll
+                    for (int r = 0; r < kMaxRows; r++) {
+                        o[r][0] += P[r][k] * v.x;
+                        o[r][1] += P[r][k] * v.y;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = tile == 0 && to == tiles;
+        const long long slot = ((long long)group * a.slots + cta + b) * a.rows;
+        for (int r = 0; r < rows; r++) {
+            const float inv = sum[r] > 0.f ? 1.f / sum[r] : 0.f;
+            const long long out = (long long)b * s.T * s.H + row0 + r;
+            if (2 * tid < s.dc) {
+                if (whole) {
+                    T* p = (T*)a.o + out * s.dc + 2 * tid;
+                    p[0] = (T)(o[r][0] * inv);
+                    p[1] = (T)(o[r][1] * inv);
+                } else {
+                    *reinterpret_cast<float2*>(a.part_o + (slot + r) * s.dc + 2 * tid) =
+                        make_float2(o[r][0] * inv, o[r][1] * inv);
+                }
+            }
+            if (tid == 0) {
+                const float l2 = sum[r] > 0.f ? top[r] + log2f(sum[r]) : -INFINITY;
+                if (!whole)
+                    a.part_l[slot + r] = l2;
+                else if (a.lse)
+                    a.lse[out] = l2 * 0.6931471805599453f;
+            }
+        }
+        left -= to - tile;
+        tile = 0;
+        b++;
+    }
+}
+
+// o = sum_i 2^(l_i - l) o_i over a sequence's pieces, in their order; a block a query row.  Sequences that one worker
+// covered are written already; empty ones become zeros here.  Block (0, 0) also gathers the workers' error words.
+constexpr int kJoinThreads = 128;
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeArgs a)
+{
+    __shared__ long long where[2];
+    const gdn_mla_cache_t& s = a.s;
+    const int row = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const Deal deal{a.len, s.B, s.maxpages * s.page};
+    if (row == 0 && b == 0) {
+        uint32_t err = 0;
+        for (int i = tid; i < a.groups * a.ctas; i += kJoinThreads) err |= a.cta_err[i];
+        err = __syncthreads_or(err != 0);
+        if (tid == 0) {
+            a.status[0] = err ? kDevTimeout : kDevOk;
+            a.status[1] = 0;
+        }
+    }
+    if (tid < 32) {
+        const long long share = deal_share(deal, a.ctas), before = deal_before(deal, b);
+        if (tid == 0) {
+            where[0] = share;
+            where[1] = before;
+        }
+    }
+    __syncthreads();
+    const int tiles = deal.tiles(b);
+    const long long out = (long long)b * s.T * s.H + row;
+    T* o = (T*)a.o + out * s.dc;
+    if (tiles == 0) {
+        for (int c = tid; c < s.dc; c += kJoinThreads) o[c] = (T)0.f;
+        if (tid == 0 && a.lse) a.lse[out] = -INFINITY;
+        return;
+    }
+    const int c0 = (int)(where[1] / where[0]), c1 = (int)((where[1] + tiles - 1) / where[0]);
+    if (c0 == c1) return;
+    const int group = row / a.rows, r = row - group * a.rows;
+    const float* L = a.part_l + ((long long)group * a.slots + b) * a.rows + r;
+    const float* O = a.part_o + (((long long)group * a.slots + b) * a.rows + r) * s.dc;
+    float m = -INFINITY;
+    for (int c = c0; c <= c1; c++) m = fmaxf(m, L[(long long)c * a.rows]);
+    float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+    const int col = 4 * tid;
+    if (m != -INFINITY)
+        for (int c = c0; c <= c1; c++) {
+            const float w = exp2f(L[(long long)c * a.rows] - m);
+            sum += w;
+            if (col < s.dc) {
+                const float4 v = *reinterpret_cast<const float4*>(O + (long long)c * a.rows * s.dc + col);
+                x[0] += w * v.x;
+                x[1] += w * v.y;
+                x[2] += w * v.z;
+                x[3] += w * v.w;
+            }
+        }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (col < s.dc) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) o[col + i] = (T)(x[i] * inv);
+    }
+    if (tid == 0 && a.lse) a.lse[out] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <typename T>
+cudaError_t run(const DecodeArgs& a, cudaStream_t st)
+{
+    const int pitch = (a.s.dc + a.s.dr + 31) / 32 * 32 + 4;
+    const size_t bytes = (size_t)(kMaxRows + kStep) * pitch * sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(decode_rows_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    decode_rows_kernel<T><<<dim3(a.ctas, a.groups), kThreads, bytes, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    decode_join_kernel<T><<<dim3(a.s.T * a.s.H, a.s.B), kJoinThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decode_rows(const DecodeArgs& a, cudaStream_t st)
+{
+    return a.s.io == GDN_BF16 ? run<__nv_bfloat16>(a, st) : run<float>(a, st);
+}
+
+}  // namespace mla
+}  // namespace gdn
