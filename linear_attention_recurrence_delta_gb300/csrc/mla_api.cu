@@ -279,5 +279,5 @@ extern "C" gdn_status_t gdn_mla_decode(const gdn_mla_cache_t* s, const gdn_mla_v
     a.part_l = (float*)(w + p.l_off);
     a.part_o = (float*)(w + p.o_off);
     a.rows = p.rows; a.groups = p.groups; a.ctas = p.ctas; a.slots = p.slots;
-    return launch_decode_rows(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return launch_decode(a, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

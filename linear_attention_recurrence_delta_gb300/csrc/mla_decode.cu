@@ -1,5 +1,5 @@
 // mla_decode.cu -- attention of a few new tokens over the paged latent cache: the workers' plan, the join of their
-// pieces, and the CUDA-core worker.
+// pieces, and the worker for f32 on the CUDA cores.
 #include "mla_decode_common.cuh"
 
 namespace gdn {
@@ -9,7 +9,7 @@ DecodePlan decode_plan(const gdn_mla_cache_t& s)
 {
     DecodePlan p;
     const int all = s.T * s.H;
-    const int most = 8;
+    const int most = s.io == GDN_BF16 ? 64 : 8;   // query rows of a worker on the tensor, the CUDA cores
     p.groups = (all + most - 1) / most;
     p.rows = (all + p.groups - 1) / p.groups;
     p.ctas = 152 / p.groups > 0 ? 152 / p.groups : 1;
@@ -26,9 +26,8 @@ namespace {
 
 constexpr int kThreads = 256, kMaxRows = 8, kStep = 32;   // cache rows in shared memory at a time
 
-// 8 query rows a worker; a warp's lanes take a row's scores for 32 cache rows, a thread two latent columns of the
+// f32: 8 query rows a worker; a warp's lanes take a row's scores for 32 cache rows, a thread two latent columns of the
 // output of all 8 rows.  FMAs bound it.
-template <typename T>
 __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs a)
 {
     extern __shared__ float smem[];
@@ -71,9 +70,9 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs 
                 const int t = (row0 + r) / s.H, h = (row0 + r) - t * s.H;
                 const long long tok = (long long)b * s.T + t;
                 if (c < s.dc)
-                    load8((const T*)a.qc.p + tok * a.qc.tok + h * a.qc.head + c, x);
+                    load8((const float*)a.qc.p + tok * a.qc.tok + h * a.qc.head + c, x);
                 else
-                    load8((const T*)a.qr.p + tok * a.qr.tok + h * a.qr.head + (c - s.dc), x);
+                    load8((const float*)a.qr.p + tok * a.qr.tok + h * a.qr.head + (c - s.dc), x);
             }
             store8(Q + r * pitch + c, x);
         }
@@ -91,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs 
                 if (j < n && c < W) {
                     const int page = a.table[(long long)b * s.maxpages + j / s.page];
                     if (page >= 0 && page < s.npages)
-                        load8((const T*)a.cache + ((long long)page * s.page + j % s.page) * W + c, x);
+                        load8((const float*)a.cache + ((long long)page * s.page + j % s.page) * W + c, x);
                 }
                 store8(K + r * pitch + c, x);
             }
@@ -149,9 +148,9 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs 
             const long long out = (long long)b * s.T * s.H + row0 + r;
             if (2 * tid < s.dc) {
                 if (whole) {
-                    T* p = (T*)a.o + out * s.dc + 2 * tid;
-                    p[0] = (T)(o[r][0] * inv);
-                    p[1] = (T)(o[r][1] * inv);
+                    float* p = (float*)a.o + out * s.dc + 2 * tid;
+                    p[0] = o[r][0] * inv;
+                    p[1] = o[r][1] * inv;
                 } else {
                     *reinterpret_cast<float2*>(a.part_o + (slot + r) * s.dc + 2 * tid) =
                         make_float2(o[r][0] * inv, o[r][1] * inv);
@@ -235,24 +234,31 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeA
     if (tid == 0 && a.lse) a.lse[out] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <typename T>
-cudaError_t run(const DecodeArgs& a, cudaStream_t st)
+cudaError_t run_rows(const DecodeArgs& a, cudaStream_t st)
 {
     const int pitch = (a.s.dc + a.s.dr + 31) / 32 * 32 + 4;
     const size_t bytes = (size_t)(kMaxRows + kStep) * pitch * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(decode_rows_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const cudaError_t e = cudaFuncSetAttribute(decode_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    decode_rows_kernel<T><<<dim3(a.ctas, a.groups), kThreads, bytes, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    decode_rows_kernel<<<dim3(a.ctas, a.groups), kThreads, bytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t run_join(const DecodeArgs& a, cudaStream_t st)
+{
     decode_join_kernel<T><<<dim3(a.s.T * a.s.H, a.s.B), kJoinThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_decode_rows(const DecodeArgs& a, cudaStream_t st)
+cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st)
 {
-    return a.s.io == GDN_BF16 ? run<__nv_bfloat16>(a, st) : run<float>(a, st);
+    const bool bf16 = a.s.io == GDN_BF16;
+    const cudaError_t e = bf16 ? launch_decode_tc(a, st) : run_rows(a, st);
+    if (e != cudaSuccess) return e;
+    return bf16 ? run_join<__nv_bfloat16>(a, st) : run_join<float>(a, st);
 }
 
 }  // namespace mla

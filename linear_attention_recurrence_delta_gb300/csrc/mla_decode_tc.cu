@@ -1,0 +1,558 @@
+// mla_decode_tc.cu -- the decode worker on the tensor cores (bf16).
+//
+// Scores and outputs are formed transposed, S^T = K Q^T and O^T = V^T P^T, so that the cache's rows are the tall side
+// of every product (M = 64 rows, M = 128 latent columns) and the few query rows its narrow one (N = 16..64): with 16
+// heads nothing is padded.  The same shared-memory tile serves both products, as a K-major operand of the first and,
+// its columns read as rows, as an MN-major operand of the second: each cache byte crosses HBM once.
+//
+// Roles of a CTA (one per SM, 10 warps): warp 0 streams the cache by TMA through a ring of 64 rows x 128 columns
+// pieces (page by page: a page's rows are one box); warp 1 issues the products, the next tile's scores ahead of this
+// tile's outputs; warps 4-7 do the softmax; warps 2, 3, 8, 9 lay the queries out.  The softmax keeps a running
+// maximum of each query row but lowers scores by an old one until a score exceeds it by 2^16: exp2 and fp32 hold that
+// range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (at a sequence's first tile
+// and rarely after).  HBM bounds it (figures at the launch below).
+#include "mla_decode_common.cuh"
+#include "mla_tc.cuh"
+
+namespace gdn {
+namespace mla {
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kMaxPairs = 16, kMaxRope = 4;
+constexpr uint32_t kPairBytes = 16384, kBlockBytes = 8192;
+constexpr float kSlack = 16.f;          // log2 by which a score may exceed the maximum it is lowered by
+constexpr float kLowest = -1e30f;       // the maximum before any score
+
+struct Params {
+    DecodeArgs a;
+    CUtensorMap map;
+    int nb, np;                  // 64-column blocks of the latent, pairs of them
+    int npair, nrope;            // ring sizes
+    int box;                     // rows of a TMA box: divides the page and the tile
+    int total_rows;              // rows of the cache; a box that starts there reads as zeros
+    uint32_t rope_off, q_off, p_off;   // shared memory, from the pair ring's start
+};
+
+struct Shared {
+    uint64_t pair_full[kMaxPairs], pair_empty[kMaxPairs], rope_full[kMaxRope], rope_empty[kMaxRope];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], p_empty[2], o_full, drain;
+    float top[64], keep[64], red[4][64], back[64];
+    uint32_t tmem, gave_up;
+    int b, tile;
+    long long share, total;
+};
+
+// the worker's run of tiles: sequence b's tiles [tile, to), then the next sequence's
+struct Run {
+    const Deal& d;
+    int b, tile, to, n, tiles;
+    long long left;
+
+    __device__ __forceinline__ Run(const Deal& deal, int b0, int tile0, long long count) : d(deal), b(b0), tile(tile0), left(count)
+    {
+        load();
+    }
+    __device__ __forceinline__ void load()
+    {
+        n = tiles = to = 0;
+        while (left > 0 && b < d.B) {
+            n = d.rows(b);
+            tiles = (n + kDecodeTile - 1) / kDecodeTile;
+            if (tiles > tile) break;
+            b++;
+            tile = 0;
+        }
+        to = (int)min((long long)tiles, tile + left);
+    }
+    // to the next tile; true if that begins another piece
+    __device__ __forceinline__ bool step()
+    {
+        left--;
+        if (++tile < to) return false;
+        b++;
+        tile = 0;
+        load();
+        return true;
+    }
+};
+
+__device__ __forceinline__ uint32_t lane_base(uint32_t tmem, int quad) { return tmem + ((uint32_t)quad << 21); }
+
+template <int NC>
+__device__ __forceinline__ void load_cols(uint32_t addr, float (&v)[NC])
+{
+#pragma unroll
+    for (int c = 0; c < NC; c += 16) tmem_ld16(addr + c, *reinterpret_cast<float(*)[16]>(&v[c]));
+    tmem_wait_ld();
+}
+
+template <int NC>
+__global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_constant__ Params p)
+{
+    extern __shared__ unsigned char raw[];
+    __shared__ Shared S;
+    unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    const DecodeArgs& a = p.a;
+    const gdn_mla_cache_t& s = a.s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = blockIdx.x, group = blockIdx.y;
+    const int row0 = group * a.rows, rows = min(a.rows, s.T * s.H - row0);
+    const Deal deal{a.len, s.B, s.maxpages * s.page};
+    const bool rope = s.dr > 0;
+    constexpr uint32_t kCols = NC <= 16 ? 128 : NC <= 32 ? 256 : 512;   // 2 score buffers + 4 output blocks
+
+    if (warp == 0) {
+        const long long share = deal_share(deal, a.ctas), start = share * cta;
+        int b, tile;
+        deal_find(deal, start, b, tile);
+        long long t = 0;      // tiles from here to the end, at most the share
+        if (b < s.B) {
+            for (int i = b + lane; i < s.B; i += 32) t += deal.tiles(i);
+#pragma unroll
+            for (int m = 16; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+            t = min(share, t - tile);
+        }
+        if (lane == 0) {
+            S.b = b;
+            S.tile = tile;
+            S.total = t;
+        }
+    } else if (warp == 1) {
+        tmem_alloc(&S.tmem, kCols);
+    } else if (tid == 64) {
+        for (int i = 0; i < kMaxPairs; i++) {
+            mbar_init(&S.pair_full[i], 1);
+            mbar_init(&S.pair_empty[i], 1);
+        }
+        for (int i = 0; i < kMaxRope; i++) {
+            mbar_init(&S.rope_full[i], 1);
+            mbar_init(&S.rope_empty[i], 1);
+        }
+        mbar_init(&S.q_full, 128);
+        mbar_init(&S.q_empty, 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_full[i], 4);
+            mbar_init(&S.p_empty[i], 1);
+        }
+        mbar_init(&S.o_full, 1);
+        mbar_init(&S.drain, 1);
+        fence_mbar_init();
+        S.gave_up = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    const uint32_t pairs = smem_u32(sm), ropes = pairs + p.rope_off, qs = pairs + p.q_off, ps = pairs + p.p_off;
+    const long long total = S.total;
+    volatile uint32_t* gave_up = &S.gave_up;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ the cache, tile by tile
+        Run r(deal, S.b, S.tile, total);
+        const int subs = kDecodeTile / p.box;
+        uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0;
+        long long issued = 0, rissued = 0;
+        if (lane == 0) tma_prefetch_desc(&p.map);
+        for (long long i = 0; i < total; i++) {
+            int at = p.total_rows;
+            const int j = r.tile * kDecodeTile + lane * p.box;
+            if (lane < subs && j < r.n) {
+                const int in = j / s.page, page = a.table[(long long)r.b * s.maxpages + in];
+                if (page >= 0 && page < s.npages) at = page * s.page + (j - in * s.page);
+            }
+            for (int k = 0; k < p.np; k++) {
+                const bool ok = wait_for(&S.pair_empty[slot], phase ^ 1, gave_up) && !*gave_up;
+                const int blocks = min(2, p.nb - 2 * k);
+                if (__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0) mbar_arrive_expect_tx(&S.pair_full[slot], blocks * kBlockBytes);
+                    __syncwarp();
+                    if (lane < subs)
+                        for (int c = 0; c < blocks; c++)
+                            tma_load_2d(pairs + slot * kPairBytes + c * kBlockBytes + lane * p.box * 128, &p.map,
+                                        &S.pair_full[slot], (2 * k + c) * 64, at);
+                    issued++;
+                }
+                if (++slot == (uint32_t)p.npair) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            if (rope) {
+                const bool ok = wait_for(&S.rope_empty[rslot], rphase ^ 1, gave_up) && !*gave_up;
+                if (__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0) mbar_arrive_expect_tx(&S.rope_full[rslot], kBlockBytes);
+                    __syncwarp();
+                    if (lane < subs)
+                        tma_load_2d(ropes + rslot * kBlockBytes + lane * p.box * 128, &p.map, &S.rope_full[rslot], s.dc, at);
+                    rissued++;
+                }
+                if (++rslot == (uint32_t)p.nrope) {
+                    rslot = 0;
+                    rphase ^= 1;
+                }
+            }
+            r.step();
+        }
+        if (*gave_up) {   // a wait expired: the copies in flight land before the CTA ends
+            for (int i = 0; i < p.npair; i++) {
+                const long long n = (issued - i + p.npair - 1) / p.npair;
+                if (n > 0) mbar_wait(&S.pair_full[i], (uint32_t)(n - 1) & 1, nullptr, kWaitNs);
+            }
+            for (int i = 0; i < p.nrope; i++) {
+                const long long n = (rissued - i + p.nrope - 1) / p.nrope;
+                if (n > 0) mbar_wait(&S.rope_full[i], (uint32_t)(n - 1) & 1, nullptr, kWaitNs);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ the products
+        if (lane == 0) {
+            const uint32_t id_s = idesc_bf16(64, NC, false, false), id_o = idesc_bf16(128, NC, true, false);
+            constexpr uint32_t kQBlock = NC * 128;
+            Run rq(deal, S.b, S.tile, total), rp(deal, S.b, S.tile, total);
+            long long iq = 0, ip = 0;            // tiles whose scores, outputs have been issued
+            int k = 0;                           // next pair of the score tile (np: the position block)
+            uint32_t qslot = 0, qphase = 0, rslot = 0, rphase = 0, pslot = 0, piece = 0;
+            bool need_q = true, first = true;
+            uint64_t since = global_ns();
+            uint32_t idle = 0;
+            while (ip < total) {
+                bool did = false;
+                if (ip < iq && mbar_try_wait(&S.p_full[ip & 1], (uint32_t)(ip >> 1) & 1)) {
+                    tc_fence_after();
+                    for (int m = 0; m < p.np; m++) {
+                        const uint32_t v = pairs + pslot * kPairBytes;
+#pragma unroll
+                        for (int ks = 0; ks < 4; ks++)
+                            mma_bf16(tmem + (2 + m) * NC, sdesc(v + ks * 2048u, kBlockBytes, 1024u),
+                                     sdesc(ps + (uint32_t)(ip & 1) * kQBlock + ks * 32u, 16u, 1024u), id_o,
+                                     (first && ks == 0) ? 0u : 1u);
+                        mma_commit(&S.pair_empty[pslot]);
+                        if (++pslot == (uint32_t)p.npair) pslot = 0;
+                    }
+                    mma_commit(&S.p_empty[ip & 1]);
+                    first = rp.step();
+                    if (first) mma_commit(&S.o_full);
+                    ip++;
+                    did = true;
+                } else if (iq < total && iq < ip + 2) {
+                    if (need_q) {
+                        if (mbar_try_wait(&S.q_full, piece & 1)) {
+                            need_q = false;
+                            piece++;
+                            did = true;
+                        }
+                    } else {
+                        const uint32_t d = tmem + (uint32_t)(iq & 1) * NC;
+                        bool done = false;
+                        if (k < p.np) {
+                            if (mbar_try_wait(&S.pair_full[qslot], qphase)) {
+                                tc_fence_after();
+                                const int blocks = min(2, p.nb - 2 * k);
+                                for (int c = 0; c < blocks; c++) {
+                                    const uint32_t kt = pairs + qslot * kPairBytes + c * kBlockBytes;
+                                    const uint32_t qt = qs + (2 * k + c) * kQBlock;
+#pragma unroll
+                                    for (int ks = 0; ks < 4; ks++)
+                                        mma_bf16(d, sdesc(kt + ks * 32u, 16u, 1024u), sdesc(qt + ks * 32u, 16u, 1024u), id_s,
+                                                 (k | c | ks) ? 1u : 0u);
+                                }
+                                if (++qslot == (uint32_t)p.npair) {
+                                    qslot = 0;
+                                    qphase ^= 1;
+                                }
+                                k++;
+                                did = true;
+                                done = k == p.np && !rope;
+                            }
+                        } else if (mbar_try_wait(&S.rope_full[rslot], rphase)) {
+                            tc_fence_after();
+                            const uint32_t kt = ropes + rslot * kBlockBytes, qt = qs + p.nb * kQBlock;
+#pragma unroll
+                            for (int ks = 0; ks < 4; ks++)
+                                mma_bf16(d, sdesc(kt + ks * 32u, 16u, 1024u), sdesc(qt + ks * 32u, 16u, 1024u), id_s, 1u);
+                            mma_commit(&S.rope_empty[rslot]);
+                            if (++rslot == (uint32_t)p.nrope) {
+                                rslot = 0;
+                                rphase ^= 1;
+                            }
+                            did = done = true;
+                        }
+                        if (done) {
+                            mma_commit(&S.s_full[iq & 1]);
+                            if (rq.step()) {
+                                mma_commit(&S.q_empty);
+                                need_q = true;
+                            }
+                            k = 0;
+                            iq++;
+                        }
+                    }
+                }
+                if (did) {
+                    idle = 0;
+                } else if (*gave_up) {
+                    break;
+                } else if ((++idle & 63) == 0) {
+                    const uint64_t t = global_ns();
+                    if (idle == 64) since = t;
+                    if (t - since > kWaitNs || idle > (1u << 30)) {
+                        *gave_up = 1;
+                        break;
+                    }
+                }
+            }
+            if (*gave_up) {   // the products in flight end before TMEM is freed
+                mma_commit(&S.drain);
+                mbar_wait(&S.drain, 0, nullptr, kWaitNs);
+            }
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ------------------------------------------------------------ softmax, outputs
+        const int quad = warp & 3, t = tid - 128, key = quad * 16 + lane;
+        const bool mine = lane < 16;             // an M = 64 product fills the first 16 lanes of each warp's 32
+        const float c = s.scale * kLog2e;
+        float l[NC];
+        Run r(deal, S.b, S.tile, total);
+        uint32_t piece = 0, pslot = 0;
+        if (t < NC) S.back[t] = (float)(s.T - 1 - (row0 + min(t, rows - 1)) / s.H);
+        int from = r.tile;
+        bool first = true;
+        for (long long i = 0; i < total; i++) {
+            const uint32_t buf = (uint32_t)i & 1, phase = (uint32_t)(i >> 1) & 1;
+            if (first) {
+                from = r.tile;
+                if (t < NC) S.top[t] = kLowest;
+#pragma unroll
+                for (int n = 0; n < NC; n++) l[n] = 0.f;
+                named_bar_sync(1, 128);
+            }
+            wait_for(&S.s_full[buf], phase, gave_up);
+            __syncwarp();
+            tc_fence_after();
+            float x[NC];
+            load_cols<NC>(lane_base(tmem, quad) + buf * NC, x);
+            const int j = r.tile * kDecodeTile + key, end = (r.tile + 1) * kDecodeTile;
+            bool over = false;
+            if (end > r.n - (s.T - 1) || !mine) {
+#pragma unroll
+                for (int n = 0; n < NC; n++) x[n] = mine && j < r.n - (int)S.back[n] ? x[n] * c : -INFINITY;
+            } else {
+#pragma unroll
+                for (int n = 0; n < NC; n++) x[n] *= c;
+            }
+#pragma unroll
+            for (int n = 0; n < NC; n += 4) {
+                const float4 m = *reinterpret_cast<const float4*>(&S.top[n]);
+                over |= x[n] > m.x + kSlack || x[n + 1] > m.y + kSlack || x[n + 2] > m.z + kSlack || x[n + 3] > m.w + kSlack;
+            }
+            if (end > r.n) {   // rows past the length hold anything: weights of zero would still meet a NaN
+                const int valid = r.n - r.tile * kDecodeTile, bad = kDecodeTile - valid;
+                for (int k = 0; k < p.nb; k++) {
+                    uint32_t slot = pslot + (k >> 1);
+                    if (slot >= (uint32_t)p.npair) slot -= p.npair;
+                    unsigned char* v = sm + slot * kPairBytes + (k & 1) * kBlockBytes + valid * 128;
+                    for (int e = t; e < bad * 8; e += 128) *reinterpret_cast<uint4*>(v + e * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            if (bar_any(1, 128, over)) {
+#pragma unroll
+                for (int n = 0; n < NC; n++) {
+                    float m = x[n];
+#pragma unroll
+                    for (int k = 8; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+                    if (lane == 0) S.red[quad][n] = m;
+                }
+                named_bar_sync(1, 128);
+                if (t < NC) {
+                    const float was = S.top[t];
+                    const float m = fmaxf(fmaxf(fmaxf(S.red[0][t], S.red[1][t]), fmaxf(S.red[2][t], S.red[3][t])), was);
+                    S.top[t] = m;
+                    S.keep[t] = fast_exp2(was - m);
+                }
+                named_bar_sync(1, 128);
+#pragma unroll
+                for (int n = 0; n < NC; n++) l[n] *= S.keep[n];
+                if (!first) {   // the outputs so far, by the same factors
+                    wait_for(&S.p_empty[buf ^ 1], (uint32_t)((i - 1) >> 1) & 1, gave_up);
+                    __syncwarp();
+                    tc_fence_after();
+                    for (int m = 0; m < p.np; m++) {
+                        const uint32_t addr = lane_base(tmem, quad) + (2 + m) * NC;
+#pragma unroll
+                        for (int n0 = 0; n0 < NC; n0 += 16) {
+                            float o[16];
+                            tmem_ld16(addr + n0, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int n = 0; n < 16; n++) o[n] *= S.keep[n0 + n];
+                            tmem_st16(addr + n0, o);
+                        }
+                    }
+                    tmem_wait_st();
+                }
+            }
+            if (i >= 2) wait_for(&S.p_empty[buf], (uint32_t)((i - 2) >> 1) & 1, gave_up);
+            unsigned char* P = sm + p.p_off + buf * (NC * 128);
+#pragma unroll
+            for (int n = 0; n < NC; n += 4) {
+                const float4 m = *reinterpret_cast<const float4*>(&S.top[n]);
+                const float y[4] = {fast_exp2(x[n] - m.x), fast_exp2(x[n + 1] - m.y), fast_exp2(x[n + 2] - m.z),
+                                    fast_exp2(x[n + 3] - m.w)};
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    l[n + e] += y[e];
+                    if (mine) *reinterpret_cast<__nv_bfloat16*>(P + sw128(n + e, key)) = __float2bfloat16_rn(y[e]);
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_full[buf]);
+            pslot += p.np;
+            while (pslot >= (uint32_t)p.npair) pslot -= p.npair;
+            const int b = r.b, to = r.to, tiles = r.tiles;
+            first = r.step();
+            if (!first) continue;
+            // ---- the piece's end: sums of the 64 rows' threads, outputs out of TMEM
+#pragma unroll
+            for (int n = 0; n < NC; n++) {
+                float m = mine ? l[n] : 0.f;
+#pragma unroll
+                for (int k = 8; k; k >>= 1) m += __shfl_xor_sync(0xffffffffu, m, k);
+                if (lane == 0) S.red[quad][n] = m;
+            }
+            named_bar_sync(1, 128);
+            const bool whole = from == 0 && to == tiles;
+            const long long slot = ((long long)group * a.slots + cta + b) * a.rows;
+            const long long out = (long long)b * s.T * s.H + row0;
+            if (t < NC) {
+                const float sum = S.red[0][t] + S.red[1][t] + S.red[2][t] + S.red[3][t];
+                S.keep[t] = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // a NaN stays one
+                const float l2 = sum == 0.f ? -INFINITY : S.top[t] + log2f(sum);
+                if (t < rows) {
+                    if (!whole)
+                        a.part_l[slot + t] = l2;
+                    else if (a.lse)
+                        a.lse[out + t] = l2 * kLn2;
+                }
+            }
+            named_bar_sync(1, 128);
+            wait_for(&S.o_full, piece & 1, gave_up);
+            __syncwarp();
+            piece++;
+            tc_fence_after();
+            for (int m = 0; m < p.np; m++) {
+                const int d = 128 * m + 32 * quad + lane;
+#pragma unroll
+                for (int n0 = 0; n0 < NC; n0 += 16) {
+                    float o[16];
+                    tmem_ld16(lane_base(tmem, quad) + (2 + m) * NC + n0, o);
+                    tmem_wait_ld();
+                    if (d < s.dc) {
+#pragma unroll
+                        for (int n = 0; n < 16; n++)
+                            if (n0 + n < rows) {
+                                const float y = o[n] * S.keep[n0 + n];
+                                if (whole)
+                                    ((__nv_bfloat16*)a.o)[(out + n0 + n) * s.dc + d] = __float2bfloat16_rn(y);
+                                else
+                                    a.part_o[(slot + n0 + n) * s.dc + d] = y;
+                            }
+                    }
+                }
+            }
+            tc_fence_before();
+            named_bar_sync(1, 128);   // the sums' words are free for the next piece
+        }
+    } else {
+        // ------------------------------------------------------------ queries: [query rows][64 columns] blocks
+        const int t = warp < 4 ? tid - 64 : tid - 192, blocks = p.nb + (rope ? 1 : 0);
+        Run r(deal, S.b, S.tile, total);
+        uint32_t piece = 0;
+        const long long last = total;
+        for (long long i = 0; i < last;) {
+            if (piece > 0) wait_for(&S.q_empty, (piece - 1) & 1, gave_up);
+            for (int e = t; e < NC * blocks * 8; e += 128) {
+                const int blk = e / (NC * 8), n = (e >> 3) % NC, q = e & 7, col = q * 8;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (n < rows) {
+                    const int tt = (row0 + n) / s.H, h = row0 + n - tt * s.H;
+                    const long long tok = (long long)r.b * s.T + tt;
+                    if (blk < p.nb) {
+                        if (blk * 64 + col < s.dc)
+                            v = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.qc.p + tok * a.qc.tok + h * a.qc.head +
+                                                                blk * 64 + col);
+                    } else if (col < s.dr) {
+                        v = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.qr.p + tok * a.qr.tok + h * a.qr.head + col);
+                    }
+                }
+                *reinterpret_cast<uint4*>(sm + p.q_off + blk * (NC * 128) + sw128(n, col)) = v;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&S.q_full);
+            piece++;
+            do i++;
+            while (!r.step() && i < last);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+    if (tid == 0) a.cta_err[group * a.ctas + cta] = S.gave_up;
+}
+
+template <int NC>
+cudaError_t run(Params& p, cudaStream_t st)
+{
+    const int blocks = p.nb + (p.a.s.dr > 0 ? 1 : 0);
+    const uint32_t q = blocks * NC * 128, pp = 2 * NC * 128;
+    const uint32_t room = 232448 - 1024 - (uint32_t)sizeof(Shared) - 256;
+    p.nrope = p.a.s.dr == 0 ? 0 : p.np >= 3 ? 2 : 4;
+    const uint32_t fixed = q + pp + p.nrope * kBlockBytes;
+    p.npair = (int)((room - fixed) / kPairBytes);
+    if (p.npair > kMaxPairs) p.npair = kMaxPairs;
+    if (p.npair < p.np) return cudaErrorInvalidValue;
+    p.rope_off = p.npair * kPairBytes;
+    p.q_off = p.rope_off + p.nrope * kBlockBytes;
+    p.p_off = p.q_off + q;
+    const size_t bytes = 1024 + p.p_off + pp;
+    const cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    decode_tc_kernel<NC><<<dim3(p.a.ctas, p.a.groups), kThreads, bytes, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Workers on the tensor cores: bf16 query rows in groups of at most 64.
+cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st)
+{
+    const gdn_mla_cache_t& s = a.s;
+    Params p;
+    p.a = a;
+    p.nb = (s.dc + 63) / 64;
+    p.np = (p.nb + 1) / 2;
+    p.box = 8;
+    while (p.box < kDecodeTile && s.page % (2 * p.box) == 0) p.box *= 2;
+    p.total_rows = s.npages * s.page;
+    const fwdtc::EncodeTiledFn enc = fwdtc::get_encode();
+    if (!enc) return cudaErrorNotSupported;
+    const int W = s.dc + s.dr;
+    const cuuint64_t dims[2] = {(cuuint64_t)W, (cuuint64_t)p.total_rows}, strides[1] = {(cuuint64_t)W * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)p.box}, one[2] = {1, 1};
+    if (enc(&p.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.cache), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    return a.rows <= 16 ? run<16>(p, st) : a.rows <= 32 ? run<32>(p, st) : a.rows <= 48 ? run<48>(p, st) : run<64>(p, st);
+}
+
+}  // namespace mla
+}  // namespace gdn

@@ -73,7 +73,8 @@ cudaError_t launch_prep(const PrepArgs& a, cudaStream_t st);
 cudaError_t launch_prep_bwd(const PrepArgs& a, cudaStream_t st);
 cudaError_t launch_attn_f32(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_attn_bwd_f32(const AttnArgs& a, cudaStream_t st);
-cudaError_t launch_decode_rows(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st);   // bf16 workers, without the join
 
 #ifdef __CUDACC__
 // the rows of sequence b: cu's, cut to T rows and held inside [0, N], or the b-th T rows
