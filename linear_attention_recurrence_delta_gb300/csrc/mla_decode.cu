@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs 
         }
     }
     __syncthreads();
+    cudaTriggerProgrammaticLaunchCompletion();   // the join's blocks may take their places
     int b = place[0], tile = place[1];
     long long left = span;
     const int row0 = group * a.rows, rows = min(a.rows, s.T * s.H - row0);
@@ -170,26 +171,18 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs 
     }
 }
 
-// o = sum_i 2^(l_i - l) o_i over a sequence's pieces, in their order; a block a query row.  Sequences that one worker
-// covered are written already; empty ones become zeros here.  Block (0, 0) also gathers the workers' error words.
-constexpr int kJoinThreads = 128;
+// o = sum_i 2^(l_i - l) o_i over a sequence's pieces, in their order; a warp a query row, a thread 4 columns of it at a
+// time.  Sequences that one worker covered are written already; empty ones become zeros here.  Block (0, 0) also
+// gathers the workers' error words.
+constexpr int kJoinWarps = 4, kJoinAhead = 8;
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeArgs a)
+__global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const DecodeArgs a)
 {
     __shared__ long long where[2];
     const gdn_mla_cache_t& s = a.s;
-    const int row = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     const Deal deal{a.len, s.B, s.maxpages * s.page};
-    if (row == 0 && b == 0) {
-        uint32_t err = 0;
-        for (int i = tid; i < a.groups * a.ctas; i += kJoinThreads) err |= a.cta_err[i];
-        err = __syncthreads_or(err != 0);
-        if (tid == 0) {
-            a.status[0] = err ? kDevTimeout : kDevOk;
-            a.status[1] = 0;
-        }
-    }
-    if (tid < 32) {
+    if (tid < 32) {      // the lengths are the caller's: read them before the workers are done
         const long long share = deal_share(deal, a.ctas), before = deal_before(deal, b);
         if (tid == 0) {
             where[0] = share;
@@ -197,41 +190,71 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeA
         }
     }
     __syncthreads();
+    cudaGridDependencySynchronize();
+    if (blockIdx.x == 0 && b == 0) {
+        uint32_t err = 0;
+        for (int i = tid; i < a.groups * a.ctas; i += kJoinWarps * 32) err |= a.cta_err[i];
+        err = __syncthreads_or(err != 0);
+        if (tid == 0) {
+            a.status[0] = err ? kDevTimeout : kDevOk;
+            a.status[1] = 0;
+        }
+    }
+    const int row = blockIdx.x * kJoinWarps + (tid >> 5);
+    if (row >= s.T * s.H) return;
     const int tiles = deal.tiles(b);
     const long long out = (long long)b * s.T * s.H + row;
     T* o = (T*)a.o + out * s.dc;
     if (tiles == 0) {
-        for (int c = tid; c < s.dc; c += kJoinThreads) o[c] = (T)0.f;
-        if (tid == 0 && a.lse) a.lse[out] = -INFINITY;
+        const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int c = 8 * lane; c < s.dc; c += 256) store8(o + c, z);
+        if (lane == 0 && a.lse) a.lse[out] = -INFINITY;
         return;
     }
-    const int c0 = (int)(where[1] / where[0]), c1 = (int)((where[1] + tiles - 1) / where[0]);
-    if (c0 == c1) return;
+    const int c0 = (int)(where[1] / where[0]), n = (int)((where[1] + tiles - 1) / where[0]) - c0 + 1;
+    if (n == 1) return;
     const int group = row / a.rows, r = row - group * a.rows;
-    const float* L = a.part_l + ((long long)group * a.slots + b) * a.rows + r;
-    const float* O = a.part_o + (((long long)group * a.slots + b) * a.rows + r) * s.dc;
+    const long long slot = (long long)group * a.slots + b + c0;
+    const float* L = a.part_l + slot * a.rows + r;
+    const float* O = a.part_o + (slot * a.rows + r) * s.dc;
+    const long long next = (long long)a.rows * s.dc;
     float m = -INFINITY;
-    for (int c = c0; c <= c1; c++) m = fmaxf(m, L[(long long)c * a.rows]);
-    float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-    const int col = 4 * tid;
-    if (m != -INFINITY)
-        for (int c = c0; c <= c1; c++) {
-            const float w = exp2f(L[(long long)c * a.rows] - m);
-            sum += w;
-            if (col < s.dc) {
-                const float4 v = *reinterpret_cast<const float4*>(O + (long long)c * a.rows * s.dc + col);
-                x[0] += w * v.x;
-                x[1] += w * v.y;
-                x[2] += w * v.z;
-                x[3] += w * v.w;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, L[(long long)i * a.rows]);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    const float base = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
+    for (int c = 8 * lane; c < 8 * 32 * ((s.dc + 255) / 256); c += 256) {   // every lane passes every shuffle
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        sum = 0.f;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const float w = i0 + lane < n ? exp2f(L[(long long)(i0 + lane) * a.rows] - base) : 0.f;
+            const int upto = min(32, n - i0);
+            for (int i = 0; i < upto; i += kJoinAhead) {
+                float v[kJoinAhead][8];
+#pragma unroll
+                for (int e = 0; e < kJoinAhead; e++)
+                    if (c < s.dc && i + e < upto) load8(O + (i0 + i + e) * next + c, v[e]);
+#pragma unroll
+                for (int e = 0; e < kJoinAhead; e++)
+                    if (i + e < upto) {
+                        const float f = __shfl_sync(0xffffffffu, w, i + e);
+                        sum += f;
+                        if (c < s.dc) {
+#pragma unroll
+                            for (int k = 0; k < 8; k++) x[k] += f * v[e][k];
+                        }
+                    }
             }
         }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    if (col < s.dc) {
+        const float inv = sum > 0.f ? 1.f / sum : sum;    // zero stays zero, a NaN a NaN
+        if (c < s.dc) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) o[col + i] = (T)(x[i] * inv);
+            for (int k = 0; k < 8; k++) x[k] *= inv;
+            store8(o + c, x);
+        }
     }
-    if (tid == 0 && a.lse) a.lse[out] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    if (lane == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
 }
 
 cudaError_t run_rows(const DecodeArgs& a, cudaStream_t st)
@@ -244,11 +267,20 @@ cudaError_t run_rows(const DecodeArgs& a, cudaStream_t st)
     return cudaGetLastError();
 }
 
+// launched as a dependent of the workers' kernel: its blocks find their place while the last workers finish
 template <typename T>
 cudaError_t run_join(const DecodeArgs& a, cudaStream_t st)
 {
-    decode_join_kernel<T><<<dim3(a.s.T * a.s.H, a.s.B), kJoinThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.s.T * a.s.H + kJoinWarps - 1) / kJoinWarps, a.s.B);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<T>, a);
 }
 
 }  // namespace

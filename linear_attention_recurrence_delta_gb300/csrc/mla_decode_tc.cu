@@ -5,9 +5,9 @@
 // heads nothing is padded.  The same shared-memory tile serves both products, as a K-major operand of the first and,
 // its columns read as rows, as an MN-major operand of the second: each cache byte crosses HBM once.
 //
-// Roles of a CTA (one per SM, 10 warps): warp 0 streams the cache by TMA through a ring of 64 rows x 128 columns
+// Roles of a CTA (one per SM, 8 warps): warp 0 streams the cache by TMA through a ring of 64 rows x 128 columns
 // pieces (page by page: a page's rows are one box); warp 1 issues the products, the next tile's scores ahead of this
-// tile's outputs; warps 4-7 do the softmax; warps 2, 3, 8, 9 lay the queries out.  The softmax keeps a running
+// tile's outputs; warps 4-7 do the softmax; warps 2 and 3 lay the queries out.  The softmax keeps a running
 // maximum of each query row but lowers scores by an old one until a score exceeds it by 2^16: exp2 and fp32 hold that
 // range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (at a sequence's first tile
 // and rarely after).  HBM bounds it (figures at the launch below).
@@ -19,11 +19,10 @@ namespace mla {
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 256;
 constexpr int kMaxPairs = 16, kMaxRope = 4;
 constexpr uint32_t kPairBytes = 16384, kBlockBytes = 8192;
 constexpr float kSlack = 16.f;          // log2 by which a score may exceed the maximum it is lowered by
-constexpr float kLowest = -1e30f;       // the maximum before any score
 
 struct Params {
     DecodeArgs a;
@@ -38,7 +37,7 @@ struct Params {
 struct Shared {
     uint64_t pair_full[kMaxPairs], pair_empty[kMaxPairs], rope_full[kMaxRope], rope_empty[kMaxRope];
     uint64_t q_full, q_empty, s_full[2], p_full[2], p_empty[2], o_full, drain;
-    float top[64], keep[64], red[4][64], back[64];
+    float top[64], keep[64], up[64], red[4][64], back[64];
     uint32_t tmem, gave_up;
     int b, tile;
     long long share, total;
@@ -130,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             mbar_init(&S.rope_full[i], 1);
             mbar_init(&S.rope_empty[i], 1);
         }
-        mbar_init(&S.q_full, 128);
+        mbar_init(&S.q_full, 64);
         mbar_init(&S.q_empty, 1);
         for (int i = 0; i < 2; i++) {
             mbar_init(&S.s_full[i], 1);
@@ -145,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    cudaTriggerProgrammaticLaunchCompletion();   // the join's blocks may take their places
     const uint32_t tmem = S.tmem;
     const uint32_t pairs = smem_u32(sm), ropes = pairs + p.rope_off, qs = pairs + p.q_off, ps = pairs + p.p_off;
     const long long total = S.total;
@@ -153,27 +153,28 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     if (warp == 0) {
         // ------------------------------------------------------------ the cache, tile by tile
         Run r(deal, S.b, S.tile, total);
-        const int subs = kDecodeTile / p.box;
+        const int subs = kDecodeTile / p.box, sub = lane & (subs - 1), blk = lane / subs;   // subs: 1, 2, 4 or 8
         uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0;
         long long issued = 0, rissued = 0;
         if (lane == 0) tma_prefetch_desc(&p.map);
         for (long long i = 0; i < total; i++) {
             int at = p.total_rows;
-            const int j = r.tile * kDecodeTile + lane * p.box;
-            if (lane < subs && j < r.n) {
+            const int j = r.tile * kDecodeTile + sub * p.box;
+            if (blk < 2 && j < r.n) {
                 const int in = j / s.page, page = a.table[(long long)r.b * s.maxpages + in];
                 if (page >= 0 && page < s.npages) at = page * s.page + (j - in * s.page);
             }
             for (int k = 0; k < p.np; k++) {
-                const bool ok = wait_for(&S.pair_empty[slot], phase ^ 1, gave_up) && !*gave_up;
-                const int blocks = min(2, p.nb - 2 * k);
-                if (__all_sync(0xffffffffu, ok)) {
-                    if (lane == 0) mbar_arrive_expect_tx(&S.pair_full[slot], blocks * kBlockBytes);
+                wait_for(&S.pair_empty[slot], phase ^ 1, gave_up);
+                __syncwarp();
+                if (!__any_sync(0xffffffffu, *gave_up != 0)) {
+                    const int blocks = min(2, p.nb - 2 * k);
+                    uint64_t* bar = &S.pair_full[slot];
+                    if (elect_one()) mbar_arrive_expect_tx(bar, blocks * kBlockBytes);
                     __syncwarp();
-                    if (lane < subs)
-                        for (int c = 0; c < blocks; c++)
-                            tma_load_2d(pairs + slot * kPairBytes + c * kBlockBytes + lane * p.box * 128, &p.map,
-                                        &S.pair_full[slot], (2 * k + c) * 64, at);
+                    if (lane < blocks * subs)   // a lane a box
+                        tma_load_2d(pairs + slot * kPairBytes + blk * kBlockBytes + sub * p.box * 128, &p.map, bar,
+                                    128 * k + 64 * blk, at);
                     issued++;
                 }
                 if (++slot == (uint32_t)p.npair) {
@@ -182,12 +183,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 }
             }
             if (rope) {
-                const bool ok = wait_for(&S.rope_empty[rslot], rphase ^ 1, gave_up) && !*gave_up;
-                if (__all_sync(0xffffffffu, ok)) {
-                    if (lane == 0) mbar_arrive_expect_tx(&S.rope_full[rslot], kBlockBytes);
+                wait_for(&S.rope_empty[rslot], rphase ^ 1, gave_up);
+                __syncwarp();
+                if (!__any_sync(0xffffffffu, *gave_up != 0)) {
+                    uint64_t* bar = &S.rope_full[rslot];
+                    if (elect_one()) mbar_arrive_expect_tx(bar, kBlockBytes);
                     __syncwarp();
-                    if (lane < subs)
-                        tma_load_2d(ropes + rslot * kBlockBytes + lane * p.box * 128, &p.map, &S.rope_full[rslot], s.dc, at);
+                    if (lane < subs) tma_load_2d(ropes + rslot * kBlockBytes + sub * p.box * 128, &p.map, bar, s.dc, at);
                     rissued++;
                 }
                 if (++rslot == (uint32_t)p.nrope) {
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ the products
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t id_s = idesc_bf16(64, NC, false, false), id_o = idesc_bf16(128, NC, true, false);
             constexpr uint32_t kQBlock = NC * 128;
             Run rq(deal, S.b, S.tile, total), rp(deal, S.b, S.tile, total);
@@ -310,12 +312,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 mbar_wait(&S.drain, 0, nullptr, kWaitNs);
             }
         }
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax, outputs
-        const int quad = warp & 3, t = tid - 128, key = quad * 16 + lane;
-        const bool mine = lane < 16;             // an M = 64 product fills the first 16 lanes of each warp's 32
+        // An M = 64 product fills the first 16 lanes of each warp's 32 in TMEM: lanes 16..31 take over the second half
+        // of these rows' columns.
+        constexpr int HC = NC / 2;
+        const int quad = warp & 3, t = tid - 128, key = quad * 16 + (lane & 15), col0 = lane < 16 ? 0 : HC;
         const float c = s.scale * kLog2e;
-        float l[NC];
+        float l[HC];
         Run r(deal, S.b, S.tile, total);
         uint32_t piece = 0, pslot = 0;
         if (t < NC) S.back[t] = (float)(s.T - 1 - (row0 + min(t, rows - 1)) / s.H);
@@ -325,29 +329,42 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             const uint32_t buf = (uint32_t)i & 1, phase = (uint32_t)(i >> 1) & 1;
             if (first) {
                 from = r.tile;
-                if (t < NC) S.top[t] = kLowest;
+                if (t < NC) S.top[t] = 0.f;
 #pragma unroll
-                for (int n = 0; n < NC; n++) l[n] = 0.f;
+                for (int n = 0; n < HC; n++) l[n] = 0.f;
                 named_bar_sync(1, 128);
             }
             wait_for(&S.s_full[buf], phase, gave_up);
             __syncwarp();
             tc_fence_after();
-            float x[NC];
-            load_cols<NC>(lane_base(tmem, quad) + buf * NC, x);
-            const int j = r.tile * kDecodeTile + key, end = (r.tile + 1) * kDecodeTile;
-            bool over = false;
-            if (end > r.n - (s.T - 1) || !mine) {
+            float x[HC];
+            {
+                float y[NC];
+                load_cols<NC>(lane_base(tmem, quad) + buf * NC, y);
 #pragma unroll
-                for (int n = 0; n < NC; n++) x[n] = mine && j < r.n - (int)S.back[n] ? x[n] * c : -INFINITY;
+                for (int n = 0; n < HC; n++) {
+                    const float other = __shfl_sync(0xffffffffu, y[n + HC], lane & 15);
+                    x[n] = lane < 16 ? y[n] : other;
+                }
+            }
+            const int j = r.tile * kDecodeTile + key, end = (r.tile + 1) * kDecodeTile;
+            if (end > r.n - (s.T - 1)) {
+#pragma unroll
+                for (int n = 0; n < HC; n++) x[n] = j < r.n - (int)S.back[col0 + n] ? x[n] * c : -INFINITY;
             } else {
 #pragma unroll
-                for (int n = 0; n < NC; n++) x[n] *= c;
+                for (int n = 0; n < HC; n++) x[n] *= c;
             }
+            // the first tile of a piece sets the maximum; a query that sees none of it sees none of the later ones either
+            bool over = first;
 #pragma unroll
-            for (int n = 0; n < NC; n += 4) {
-                const float4 m = *reinterpret_cast<const float4*>(&S.top[n]);
-                over |= x[n] > m.x + kSlack || x[n + 1] > m.y + kSlack || x[n + 2] > m.z + kSlack || x[n + 3] > m.w + kSlack;
+            for (int n = 0; n < HC; n += 4) {
+                const float4 m = *reinterpret_cast<const float4*>(&S.top[col0 + n]);
+                x[n] -= m.x;       // lowered by the maximum so far
+                x[n + 1] -= m.y;
+                x[n + 2] -= m.z;
+                x[n + 3] -= m.w;
+                over |= fmaxf(fmaxf(x[n], x[n + 1]), fmaxf(x[n + 2], x[n + 3])) > kSlack;
             }
             if (end > r.n) {   // rows past the length hold anything: weights of zero would still meet a NaN
                 const int valid = r.n - r.tile * kDecodeTile, bad = kDecodeTile - valid;
@@ -360,22 +377,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             }
             if (bar_any(1, 128, over)) {
 #pragma unroll
-                for (int n = 0; n < NC; n++) {
+                for (int n = 0; n < HC; n++) {
                     float m = x[n];
 #pragma unroll
                     for (int k = 8; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-                    if (lane == 0) S.red[quad][n] = m;
+                    if ((lane & 15) == 0) S.red[quad][col0 + n] = m;
                 }
                 named_bar_sync(1, 128);
                 if (t < NC) {
-                    const float was = S.top[t];
-                    const float m = fmaxf(fmaxf(fmaxf(S.red[0][t], S.red[1][t]), fmaxf(S.red[2][t], S.red[3][t])), was);
-                    S.top[t] = m;
-                    S.keep[t] = fast_exp2(was - m);
+                    const float m = fmaxf(fmaxf(S.red[0][t], S.red[1][t]), fmaxf(S.red[2][t], S.red[3][t]));
+                    const float up = first ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);   // what the maximum rises by
+                    S.up[t] = up;
+                    S.top[t] += up;
+                    S.keep[t] = first ? 1.f : fast_exp2(-up);
                 }
                 named_bar_sync(1, 128);
 #pragma unroll
-                for (int n = 0; n < NC; n++) l[n] *= S.keep[n];
+                for (int n = 0; n < HC; n++) {
+                    l[n] *= S.keep[col0 + n];
+                    x[n] -= S.up[col0 + n];
+                }
                 if (!first) {   // the outputs so far, by the same factors
                     wait_for(&S.p_empty[buf ^ 1], (uint32_t)((i - 1) >> 1) & 1, gave_up);
                     __syncwarp();
@@ -398,15 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             if (i >= 2) wait_for(&S.p_empty[buf], (uint32_t)((i - 2) >> 1) & 1, gave_up);
             unsigned char* P = sm + p.p_off + buf * (NC * 128);
 #pragma unroll
-            for (int n = 0; n < NC; n += 4) {
-                const float4 m = *reinterpret_cast<const float4*>(&S.top[n]);
-                const float y[4] = {fast_exp2(x[n] - m.x), fast_exp2(x[n + 1] - m.y), fast_exp2(x[n + 2] - m.z),
-                                    fast_exp2(x[n + 3] - m.w)};
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    l[n + e] += y[e];
-                    if (mine) *reinterpret_cast<__nv_bfloat16*>(P + sw128(n + e, key)) = __float2bfloat16_rn(y[e]);
-                }
+            for (int n = 0; n < HC; n++) {
+                const float y = fast_exp2(x[n]);
+                l[n] += y;
+                *reinterpret_cast<__nv_bfloat16*>(P + sw128(col0 + n, key)) = __float2bfloat16_rn(y);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -419,11 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             if (!first) continue;
             // ---- the piece's end: sums of the 64 rows' threads, outputs out of TMEM
 #pragma unroll
-            for (int n = 0; n < NC; n++) {
-                float m = mine ? l[n] : 0.f;
+            for (int n = 0; n < HC; n++) {
+                float m = l[n];
 #pragma unroll
                 for (int k = 8; k; k >>= 1) m += __shfl_xor_sync(0xffffffffu, m, k);
-                if (lane == 0) S.red[quad][n] = m;
+                if ((lane & 15) == 0) S.red[quad][col0 + n] = m;
             }
             named_bar_sync(1, 128);
             const bool whole = from == 0 && to == tiles;
@@ -470,28 +486,33 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
     } else {
         // ------------------------------------------------------------ queries: [query rows][64 columns] blocks
-        const int t = warp < 4 ? tid - 64 : tid - 192, blocks = p.nb + (rope ? 1 : 0);
+        const int t = tid - 64, blocks = p.nb + (rope ? 1 : 0);
         Run r(deal, S.b, S.tile, total);
         uint32_t piece = 0;
         const long long last = total;
         for (long long i = 0; i < last;) {
             if (piece > 0) wait_for(&S.q_empty, (piece - 1) & 1, gave_up);
-            for (int e = t; e < NC * blocks * 8; e += 128) {
-                const int blk = e / (NC * 8), n = (e >> 3) % NC, q = e & 7, col = q * 8;
-                uint4 v = make_uint4(0, 0, 0, 0);
+for (int e = t; e < NC * blocks * 8; e += 64) {
+                const int blk = e / (NC * 8), n = (e >> 3) % NC, col = (e & 7) * 8;
+                const __nv_bfloat16* from = (const __nv_bfloat16*)a.qc.p;
+                uint32_t bytes = 0;              // past the rows or the width: zeros
                 if (n < rows) {
                     const int tt = (row0 + n) / s.H, h = row0 + n - tt * s.H;
                     const long long tok = (long long)r.b * s.T + tt;
                     if (blk < p.nb) {
-                        if (blk * 64 + col < s.dc)
-                            v = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.qc.p + tok * a.qc.tok + h * a.qc.head +
-                                                                blk * 64 + col);
-                    } else if (col < s.dr) {
-                        v = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.qr.p + tok * a.qr.tok + h * a.qr.head + col);
+                        from = (const __nv_bfloat16*)a.qc.p + tok * a.qc.tok + h * a.qc.head + blk * 64 + col;
+                        bytes = blk * 64 + col < s.dc ? 16 : 0;
+                    } else {
+                        from = (const __nv_bfloat16*)a.qr.p + tok * a.qr.tok + h * a.qr.head + col;
+                        bytes = col < s.dr ? 16 : 0;
                     }
                 }
-                *reinterpret_cast<uint4*>(sm + p.q_off + blk * (NC * 128) + sw128(n, col)) = v;
+                if (bytes == 0) from = (const __nv_bfloat16*)a.qc.p;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(qs + blk * (NC * 128) + sw128(n, col)),
+                             "l"(from), "r"(bytes)
+                             : "memory");
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             mbar_arrive(&S.q_full);
             piece++;
