@@ -6,8 +6,9 @@
 // its columns read as rows, as an MN-major operand of the second: each cache byte crosses HBM once.
 //
 // Roles of a CTA (one per SM, 8 warps): warp 0 streams the cache by TMA through a ring of 64 rows x 128 columns
-// pieces (page by page: a page's rows are one box); warp 1 issues the products, the next tile's scores ahead of this
-// tile's outputs; warps 4-7 do the softmax; warps 2 and 3 lay the queries out.  The softmax keeps a running
+// pieces (page by page: a page's rows are one box); warp 1 issues the scores' products and warp 2 the outputs', each
+// waiting for its own operands only, so that the next tiles' scores run ahead of this tile's outputs; warp 3 lays the
+// queries out; warps 4-7 do the softmax.  The softmax keeps a running
 // maximum of each query row but lowers scores by an old one until a score exceeds it by 2^16: exp2 and fp32 hold that
 // range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (at a sequence's first tile
 // and rarely after).  HBM bounds it (figures at the launch below).
@@ -36,8 +37,9 @@ struct Params {
 
 struct Shared {
     uint64_t pair_full[kMaxPairs], pair_empty[kMaxPairs], rope_full[kMaxRope], rope_empty[kMaxRope];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], p_empty[2], o_full, drain;
-    float top[64], keep[64], up[64], red[4][64], back[64];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], p_empty[2], o_full, drain[2];
+    alignas(16) float top[64];   // read four at a time
+    float keep[64], up[64], red[4][64], back[64];
     uint32_t tmem, gave_up;
     int b, tile;
     long long share, total;
@@ -87,6 +89,13 @@ __device__ __forceinline__ void load_cols(uint32_t addr, float (&v)[NC])
     tmem_wait_ld();
 }
 
+// 16 bytes to shared memory, zeros if `in` is false
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in)
+{
+    const uint32_t bytes = in ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 template <int NC>
 __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_constant__ Params p)
 {
@@ -129,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             mbar_init(&S.rope_full[i], 1);
             mbar_init(&S.rope_empty[i], 1);
         }
-        mbar_init(&S.q_full, 64);
+        mbar_init(&S.q_full, 32);
         mbar_init(&S.q_empty, 1);
         for (int i = 0; i < 2; i++) {
             mbar_init(&S.s_full[i], 1);
@@ -137,7 +146,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             mbar_init(&S.p_empty[i], 1);
         }
         mbar_init(&S.o_full, 1);
-        mbar_init(&S.drain, 1);
+        mbar_init(&S.drain[0], 1);
+        mbar_init(&S.drain[1], 1);
         fence_mbar_init();
         S.gave_up = 0;
     }
@@ -210,106 +220,91 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             }
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ the products
+        // ------------------------------------------------------------ the scores' products
         if (elect_one()) {
-            const uint32_t id_s = idesc_bf16(64, NC, false, false), id_o = idesc_bf16(128, NC, true, false);
+            const uint32_t id = idesc_bf16(64, NC, false, false);
             constexpr uint32_t kQBlock = NC * 128;
-            Run rq(deal, S.b, S.tile, total), rp(deal, S.b, S.tile, total);
-            long long iq = 0, ip = 0;            // tiles whose scores, outputs have been issued
-            int k = 0;                           // next pair of the score tile (np: the position block)
-            uint32_t qslot = 0, qphase = 0, rslot = 0, rphase = 0, pslot = 0, piece = 0;
-            bool need_q = true, first = true;
-            uint64_t since = global_ns();
-            uint32_t idle = 0;
-            while (ip < total) {
-                bool did = false;
-                if (ip < iq && mbar_try_wait(&S.p_full[ip & 1], (uint32_t)(ip >> 1) & 1)) {
+            const uint64_t base = sdesc(0, 16u, 1024u);
+            Run r(deal, S.b, S.tile, total);
+            uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0, piece = 0;
+            bool first = true;
+            for (long long i = 0; i < total; i++) {
+                const uint32_t d = tmem + (uint32_t)(i & 1) * NC;
+                if (first) wait_for(&S.q_full, piece++ & 1, gave_up);
+                if (i >= 2) wait_for(&S.p_full[i & 1], (uint32_t)((i - 2) >> 1) & 1, gave_up);   // the buffer's last scores are read
+                uint64_t q = base + (qs >> 4);
+                for (int k = 0; k < p.np; k++) {
+                    wait_for(&S.pair_full[slot], phase, gave_up);
                     tc_fence_after();
-                    for (int m = 0; m < p.np; m++) {
-                        const uint32_t v = pairs + pslot * kPairBytes;
+                    if (!*gave_up) {
+                        const uint64_t kt = base + ((pairs + slot * kPairBytes) >> 4);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ks++)
-                            mma_bf16(tmem + (2 + m) * NC, sdesc(v + ks * 2048u, kBlockBytes, 1024u),
-                                     sdesc(ps + (uint32_t)(ip & 1) * kQBlock + ks * 32u, 16u, 1024u), id_o,
-                                     (first && ks == 0) ? 0u : 1u);
-                        mma_commit(&S.pair_empty[pslot]);
-                        if (++pslot == (uint32_t)p.npair) pslot = 0;
-                    }
-                    mma_commit(&S.p_empty[ip & 1]);
-                    first = rp.step();
-                    if (first) mma_commit(&S.o_full);
-                    ip++;
-                    did = true;
-                } else if (iq < total && iq < ip + 2) {
-                    if (need_q) {
-                        if (mbar_try_wait(&S.q_full, piece & 1)) {
-                            need_q = false;
-                            piece++;
-                            did = true;
-                        }
-                    } else {
-                        const uint32_t d = tmem + (uint32_t)(iq & 1) * NC;
-                        bool done = false;
-                        if (k < p.np) {
-                            if (mbar_try_wait(&S.pair_full[qslot], qphase)) {
-                                tc_fence_after();
-                                const int blocks = min(2, p.nb - 2 * k);
-                                for (int c = 0; c < blocks; c++) {
-                                    const uint32_t kt = pairs + qslot * kPairBytes + c * kBlockBytes;
-                                    const uint32_t qt = qs + (2 * k + c) * kQBlock;
-#pragma unroll
-                                    for (int ks = 0; ks < 4; ks++)
-                                        mma_bf16(d, sdesc(kt + ks * 32u, 16u, 1024u), sdesc(qt + ks * 32u, 16u, 1024u), id_s,
-                                                 (k | c | ks) ? 1u : 0u);
-                                }
-                                if (++qslot == (uint32_t)p.npair) {
-                                    qslot = 0;
-                                    qphase ^= 1;
-                                }
-                                k++;
-                                did = true;
-                                done = k == p.np && !rope;
-                            }
-                        } else if (mbar_try_wait(&S.rope_full[rslot], rphase)) {
-                            tc_fence_after();
-                            const uint32_t kt = ropes + rslot * kBlockBytes, qt = qs + p.nb * kQBlock;
+                        for (int ks = 0; ks < 4; ks++) mma_bf16(d, kt + 2 * ks, q + 2 * ks, id, (k | ks) ? 1u : 0u);
+                        if (2 * k + 1 < p.nb) {
 #pragma unroll
                             for (int ks = 0; ks < 4; ks++)
-                                mma_bf16(d, sdesc(kt + ks * 32u, 16u, 1024u), sdesc(qt + ks * 32u, 16u, 1024u), id_s, 1u);
-                            mma_commit(&S.rope_empty[rslot]);
-                            if (++rslot == (uint32_t)p.nrope) {
-                                rslot = 0;
-                                rphase ^= 1;
-                            }
-                            did = done = true;
-                        }
-                        if (done) {
-                            mma_commit(&S.s_full[iq & 1]);
-                            if (rq.step()) {
-                                mma_commit(&S.q_empty);
-                                need_q = true;
-                            }
-                            k = 0;
-                            iq++;
+                                mma_bf16(d, kt + (kBlockBytes >> 4) + 2 * ks, q + (kQBlock >> 4) + 2 * ks, id, 1u);
                         }
                     }
-                }
-                if (did) {
-                    idle = 0;
-                } else if (*gave_up) {
-                    break;
-                } else if ((++idle & 63) == 0) {
-                    const uint64_t t = global_ns();
-                    if (idle == 64) since = t;
-                    if (t - since > kWaitNs || idle > (1u << 30)) {
-                        *gave_up = 1;
-                        break;
+                    q += 2 * (kQBlock >> 4);
+                    if (++slot == (uint32_t)p.npair) {
+                        slot = 0;
+                        phase ^= 1;
                     }
                 }
+                if (rope) {
+                    wait_for(&S.rope_full[rslot], rphase, gave_up);
+                    tc_fence_after();
+                    if (!*gave_up) {
+                        const uint64_t kt = base + ((ropes + rslot * kBlockBytes) >> 4), qt = base + ((qs + p.nb * kQBlock) >> 4);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ks++) mma_bf16(d, kt + 2 * ks, qt + 2 * ks, id, 1u);
+                    }
+                    mma_commit(&S.rope_empty[rslot]);
+                    if (++rslot == (uint32_t)p.nrope) {
+                        rslot = 0;
+                        rphase ^= 1;
+                    }
+                }
+                mma_commit(&S.s_full[i & 1]);
+                first = r.step();
+                if (first) mma_commit(&S.q_empty);
             }
             if (*gave_up) {   // the products in flight end before TMEM is freed
-                mma_commit(&S.drain);
-                mbar_wait(&S.drain, 0, nullptr, kWaitNs);
+                mma_commit(&S.drain[0]);
+                mbar_wait(&S.drain[0], 0, nullptr, kWaitNs);
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ the outputs' products
+        if (elect_one()) {
+            const uint32_t id = idesc_bf16(128, NC, true, false);
+            const uint64_t vbase = sdesc(0, kBlockBytes, 1024u), pbase = sdesc(0, 16u, 1024u);
+            Run r(deal, S.b, S.tile, total);
+            uint32_t slot = 0;
+            bool first = true;
+            for (long long i = 0; i < total; i++) {
+                wait_for(&S.p_full[i & 1], (uint32_t)(i >> 1) & 1, gave_up);
+                tc_fence_after();
+                const bool go = !*gave_up;
+                const uint64_t pt = pbase + ((ps + (uint32_t)(i & 1) * (NC * 128)) >> 4);
+                for (int m = 0; m < p.np; m++) {
+                    const uint64_t v = vbase + ((pairs + slot * kPairBytes) >> 4);
+                    if (go) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ks++)
+                            mma_bf16(tmem + (2 + m) * NC, v + 128 * ks, pt + 2 * ks, id, (first && ks == 0) ? 0u : 1u);
+                    }
+                    mma_commit(&S.pair_empty[slot]);
+                    if (++slot == (uint32_t)p.npair) slot = 0;
+                }
+                mma_commit(&S.p_empty[i & 1]);
+                first = r.step();
+                if (first) mma_commit(&S.o_full);
+            }
+            if (*gave_up) {
+                mma_commit(&S.drain[1]);
+                mbar_wait(&S.drain[1], 0, nullptr, kWaitNs);
             }
         }
     } else if (warp >= 4) {
@@ -486,38 +481,33 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
     } else {
         // ------------------------------------------------------------ queries: [query rows][64 columns] blocks
-        const int t = tid - 64, blocks = p.nb + (rope ? 1 : 0);
+        const int col = (lane & 7) * 8;
         Run r(deal, S.b, S.tile, total);
         uint32_t piece = 0;
-        const long long last = total;
-        for (long long i = 0; i < last;) {
+        for (long long i = 0; i < total;) {
             if (piece > 0) wait_for(&S.q_empty, (piece - 1) & 1, gave_up);
-for (int e = t; e < NC * blocks * 8; e += 64) {
-                const int blk = e / (NC * 8), n = (e >> 3) % NC, col = (e & 7) * 8;
-                const __nv_bfloat16* from = (const __nv_bfloat16*)a.qc.p;
-                uint32_t bytes = 0;              // past the rows or the width: zeros
-                if (n < rows) {
-                    const int tt = (row0 + n) / s.H, h = row0 + n - tt * s.H;
-                    const long long tok = (long long)r.b * s.T + tt;
-                    if (blk < p.nb) {
-                        from = (const __nv_bfloat16*)a.qc.p + tok * a.qc.tok + h * a.qc.head + blk * 64 + col;
-                        bytes = blk * 64 + col < s.dc ? 16 : 0;
-                    } else {
-                        from = (const __nv_bfloat16*)a.qr.p + tok * a.qr.tok + h * a.qr.head + col;
-                        bytes = col < s.dr ? 16 : 0;
-                    }
+            for (int n = lane >> 3; n < NC; n += 4) {    // past the rows or the width: zeros
+                const bool row = n < rows;
+                const int tt = row ? (row0 + n) / s.H : 0, h = row ? row0 + n - tt * s.H : 0;
+                const long long tok = (long long)r.b * s.T + tt;
+                const __nv_bfloat16* c = (const __nv_bfloat16*)a.qc.p + tok * a.qc.tok + h * a.qc.head;
+                uint32_t dst = qs + sw128(n, col);
+                for (int k = 0; k < p.nb; k++, dst += NC * 128) {
+                    const bool in = row && 64 * k + col < s.dc;
+                    copy16(dst, c + (in ? 64 * k + col : 0), in);
                 }
-                if (bytes == 0) from = (const __nv_bfloat16*)a.qc.p;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(qs + blk * (NC * 128) + sw128(n, col)),
-                             "l"(from), "r"(bytes)
-                             : "memory");
+                if (rope) {
+                    const __nv_bfloat16* x = (const __nv_bfloat16*)a.qr.p + tok * a.qr.tok + h * a.qr.head;
+                    const bool in = row && col < s.dr;
+                    copy16(dst, x + (in ? col : 0), in);
+                }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             mbar_arrive(&S.q_full);
             piece++;
             do i++;
-            while (!r.step() && i < last);
+            while (!r.step() && i < total);
         }
     }
     tc_fence_before();
