@@ -116,6 +116,8 @@ bool cache_ok(const gdn_mla_cache_t& s)
     if (s.dc < 8 || s.dc > 512 || s.dc % 8 || s.dr < 0 || s.dr > 64 || s.dr % 8) return false;
     if (s.page < 8 || s.page % 8 || s.npages < 1 || s.maxpages < 1) return false;
     if ((double)s.npages * s.page >= 2147483648.0 || (double)s.maxpages * s.page >= 2147483648.0) return false;
+    // the tiles that the lengths can name are counted in 32 bits
+    if ((double)s.B * (((double)s.maxpages * s.page + kDecodeTile - 1) / kDecodeTile + 1) >= 2147483648.0) return false;
     return s.scale == s.scale;
 }
 

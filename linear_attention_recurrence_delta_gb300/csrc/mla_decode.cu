@@ -32,8 +32,7 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs 
 {
     extern __shared__ float smem[];
     __shared__ float P[kMaxRows][kStep], keep[kMaxRows], top[kMaxRows], sum[kMaxRows];
-    __shared__ int place[2];
-    __shared__ long long span;
+    __shared__ int place[3];
     const gdn_mla_cache_t& s = a.s;
     const int W = s.dc + s.dr, pitch = (W + 31) / 32 * 32 + 4;
     float *Q = smem, *K = smem + kMaxRows * pitch;
@@ -41,20 +40,21 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs 
     const int cta = blockIdx.x, group = blockIdx.y;
     const Deal deal{a.len, s.B, s.maxpages * s.page};
     if (warp == 0) {
-        const long long share = deal_share(deal, a.ctas);
+        const int all = deal_tiles(deal), share = deal_share(all, a.ctas);
+        const int start = min((long long)share * cta, (long long)all);
         int b, tile;
-        deal_find(deal, share * cta, b, tile);
+        deal_find(deal, start, b, tile);
         if (lane == 0) {
             place[0] = b;
             place[1] = tile;
-            span = share;
+            place[2] = min(share, all - start);
             a.cta_err[group * a.ctas + cta] = 0;
         }
     }
     __syncthreads();
     cudaTriggerProgrammaticLaunchCompletion();   // the join's blocks may take their places
     int b = place[0], tile = place[1];
-    long long left = span;
+    int left = place[2];
     const int row0 = group * a.rows, rows = min(a.rows, s.T * s.H - row0);
     while (left > 0 && b < s.B) {
         const int n = deal.rows(b), tiles = deal.tiles(b);
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs 
             b++;
             continue;
         }
-        const int to = (int)min((long long)tiles, tile + left);
+        const int to = min(tiles, tile + left);
         __syncthreads();
         for (int i = tid; i < kMaxRows * (pitch - 4) / 8; i += kThreads) {
             const int r = i / ((pitch - 4) / 8), c = (i - r * ((pitch - 4) / 8)) * 8;
@@ -178,12 +178,12 @@ constexpr int kJoinWarps = 4, kJoinAhead = 8;
 template <typename T>
 __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const DecodeArgs a)
 {
-    __shared__ long long where[2];
+    __shared__ int where[2];
     const gdn_mla_cache_t& s = a.s;
     const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     const Deal deal{a.len, s.B, s.maxpages * s.page};
     if (tid < 32) {      // the lengths are the caller's: read them before the workers are done
-        const long long share = deal_share(deal, a.ctas), before = deal_before(deal, b);
+        const int share = deal_share(deal_tiles(deal), a.ctas), before = deal_before(deal, b);
         if (tid == 0) {
             where[0] = share;
             where[1] = before;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
         if (lane == 0 && a.lse) a.lse[out] = -INFINITY;
         return;
     }
-    const int c0 = (int)(where[1] / where[0]), n = (int)((where[1] + tiles - 1) / where[0]) - c0 + 1;
+    const int c0 = where[1] / where[0], n = (where[1] + tiles - 1) / where[0] - c0 + 1;
     if (n == 1) return;
     const int group = row / a.rows, r = row - group * a.rows;
     const long long slot = (long long)group * a.slots + b + c0;

@@ -20,28 +20,29 @@ struct Deal {
     __device__ __forceinline__ int tiles(int b) const { return (rows(b) + kDecodeTile - 1) / kDecodeTile; }
 };
 
-// by all lanes of one warp: tiles of all sequences, divided evenly
-__device__ __forceinline__ long long deal_share(const Deal& d, int ctas)
+// by all lanes of one warp: tiles of all sequences (the entry point bounds their number by 2^31)
+__device__ __forceinline__ int deal_tiles(const Deal& d)
 {
-    long long t = 0;
+    int t = 0;
     for (int b = threadIdx.x & 31; b < d.B; b += 32) t += d.tiles(b);
-#pragma unroll
-    for (int m = 16; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
-    return (t + ctas - 1) / ctas;
+    return __reduce_add_sync(0xffffffffu, t);
 }
+
+// a worker's share of them
+__device__ __forceinline__ int deal_share(int tiles, int ctas) { return tiles / ctas + (tiles % ctas != 0); }
 
 // by all lanes of one warp: the sequence that holds the tile `at` of the whole row, and the tile's place in it
 // (b = B: past the end)
-__device__ __forceinline__ void deal_find(const Deal& d, long long at, int& b, int& tile)
+__device__ __forceinline__ void deal_find(const Deal& d, int at, int& b, int& tile)
 {
     const int lane = threadIdx.x & 31;
-    long long base = 0;
+    int base = 0;
     for (int b0 = 0; b0 < d.B; b0 += 32) {
         const int n = b0 + lane < d.B ? d.tiles(b0 + lane) : 0;
-        long long to = n;
+        int to = n;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, to, m);
+            const int x = __shfl_up_sync(0xffffffffu, to, m);
             if (lane >= m) to += x;
         }
         const uint32_t past = __ballot_sync(0xffffffffu, base + to > at);
@@ -58,13 +59,11 @@ __device__ __forceinline__ void deal_find(const Deal& d, long long at, int& b, i
 }
 
 // by all lanes of one warp: tiles before sequence b
-__device__ __forceinline__ long long deal_before(const Deal& d, int b)
+__device__ __forceinline__ int deal_before(const Deal& d, int b)
 {
-    long long t = 0;
+    int t = 0;
     for (int i = threadIdx.x & 31; i < b; i += 32) t += d.tiles(i);
-#pragma unroll
-    for (int m = 16; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
-    return t;
+    return __reduce_add_sync(0xffffffffu, t);
 }
 
 }  // namespace mla

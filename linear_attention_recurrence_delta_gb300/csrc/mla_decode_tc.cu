@@ -41,17 +41,15 @@ struct Shared {
     alignas(16) float top[64];   // read four at a time
     float keep[64], up[64], red[4][64], back[64];
     uint32_t tmem, gave_up;
-    int b, tile;
-    long long share, total;
+    int b, tile, total;
 };
 
 // the worker's run of tiles: sequence b's tiles [tile, to), then the next sequence's
 struct Run {
     const Deal& d;
-    int b, tile, to, n, tiles;
-    long long left;
+    int b, tile, to, n, tiles, left;
 
-    __device__ __forceinline__ Run(const Deal& deal, int b0, int tile0, long long count) : d(deal), b(b0), tile(tile0), left(count)
+    __device__ __forceinline__ Run(const Deal& deal, int b0, int tile0, int count) : d(deal), b(b0), tile(tile0), left(count)
     {
         load();
     }
@@ -65,7 +63,7 @@ struct Run {
             b++;
             tile = 0;
         }
-        to = (int)min((long long)tiles, tile + left);
+        to = min(tiles, tile + left);
     }
     // to the next tile; true if that begins another piece
     __device__ __forceinline__ bool step()
@@ -112,20 +110,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     constexpr uint32_t kCols = NC <= 16 ? 128 : NC <= 32 ? 256 : 512;   // 2 score buffers + 4 output blocks
 
     if (warp == 0) {
-        const long long share = deal_share(deal, a.ctas), start = share * cta;
+        const int all = deal_tiles(deal), share = deal_share(all, a.ctas);
+        const int start = min((long long)share * cta, (long long)all);
         int b, tile;
         deal_find(deal, start, b, tile);
-        long long t = 0;      // tiles from here to the end, at most the share
-        if (b < s.B) {
-            for (int i = b + lane; i < s.B; i += 32) t += deal.tiles(i);
-#pragma unroll
-            for (int m = 16; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
-            t = min(share, t - tile);
-        }
         if (lane == 0) {
             S.b = b;
             S.tile = tile;
-            S.total = t;
+            S.total = min(share, all - start);
         }
     } else if (warp == 1) {
         tmem_alloc(&S.tmem, kCols);
@@ -157,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     cudaTriggerProgrammaticLaunchCompletion();   // the join's blocks may take their places
     const uint32_t tmem = S.tmem;
     const uint32_t pairs = smem_u32(sm), ropes = pairs + p.rope_off, qs = pairs + p.q_off, ps = pairs + p.p_off;
-    const long long total = S.total;
+    const int total = S.total;
     volatile uint32_t* gave_up = &S.gave_up;
 
     if (warp == 0) {
@@ -165,9 +157,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         Run r(deal, S.b, S.tile, total);
         const int subs = kDecodeTile / p.box, sub = lane & (subs - 1), blk = lane / subs;   // subs: 1, 2, 4 or 8
         uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0;
-        long long issued = 0, rissued = 0;
+        int issued = 0, rissued = 0;
         if (lane == 0) tma_prefetch_desc(&p.map);
-        for (long long i = 0; i < total; i++) {
+        for (int i = 0; i < total; i++) {
             int at = p.total_rows;
             const int j = r.tile * kDecodeTile + sub * p.box;
             if (blk < 2 && j < r.n) {
@@ -211,11 +203,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
         if (*gave_up) {   // a wait expired: the copies in flight land before the CTA ends
             for (int i = 0; i < p.npair; i++) {
-                const long long n = (issued - i + p.npair - 1) / p.npair;
+                const int n = (issued - i + p.npair - 1) / p.npair;
                 if (n > 0) mbar_wait(&S.pair_full[i], (uint32_t)(n - 1) & 1, nullptr, kWaitNs);
             }
             for (int i = 0; i < p.nrope; i++) {
-                const long long n = (rissued - i + p.nrope - 1) / p.nrope;
+                const int n = (rissued - i + p.nrope - 1) / p.nrope;
                 if (n > 0) mbar_wait(&S.rope_full[i], (uint32_t)(n - 1) & 1, nullptr, kWaitNs);
             }
         }
@@ -228,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             Run r(deal, S.b, S.tile, total);
             uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0, piece = 0;
             bool first = true;
-            for (long long i = 0; i < total; i++) {
+            for (int i = 0; i < total; i++) {
                 const uint32_t d = tmem + (uint32_t)(i & 1) * NC;
                 if (first) wait_for(&S.q_full, piece++ & 1, gave_up);
                 if (i >= 2) wait_for(&S.p_full[i & 1], (uint32_t)((i - 2) >> 1) & 1, gave_up);   // the buffer's last scores are read
@@ -283,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             Run r(deal, S.b, S.tile, total);
             uint32_t slot = 0;
             bool first = true;
-            for (long long i = 0; i < total; i++) {
+            for (int i = 0; i < total; i++) {
                 wait_for(&S.p_full[i & 1], (uint32_t)(i >> 1) & 1, gave_up);
                 tc_fence_after();
                 const bool go = !*gave_up;
@@ -320,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         if (t < NC) S.back[t] = (float)(s.T - 1 - (row0 + min(t, rows - 1)) / s.H);
         int from = r.tile;
         bool first = true;
-        for (long long i = 0; i < total; i++) {
+        for (int i = 0; i < total; i++) {
             const uint32_t buf = (uint32_t)i & 1, phase = (uint32_t)(i >> 1) & 1;
             if (first) {
                 from = r.tile;
@@ -396,16 +388,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     wait_for(&S.p_empty[buf ^ 1], (uint32_t)((i - 1) >> 1) & 1, gave_up);
                     __syncwarp();
                     tc_fence_after();
-                    for (int m = 0; m < p.np; m++) {
-                        const uint32_t addr = lane_base(tmem, quad) + (2 + m) * NC;
+#pragma unroll 1
+                    for (int n0 = 0; n0 < NC; n0 += 16) {
+                        float f[16];
 #pragma unroll
-                        for (int n0 = 0; n0 < NC; n0 += 16) {
+                        for (int n = 0; n < 16; n++) f[n] = S.keep[n0 + n];
+#pragma unroll 1
+                        for (int m = 0; m < p.np; m++) {
+                            const uint32_t addr = lane_base(tmem, quad) + (2 + m) * NC + n0;
                             float o[16];
-                            tmem_ld16(addr + n0, o);
+                            tmem_ld16(addr, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int n = 0; n < 16; n++) o[n] *= S.keep[n0 + n];
-                            tmem_st16(addr + n0, o);
+                            for (int n = 0; n < 16; n++) o[n] *= f[n];
+                            tmem_st16(addr, o);
                         }
                     }
                     tmem_wait_st();
@@ -456,23 +452,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             __syncwarp();
             piece++;
             tc_fence_after();
-            for (int m = 0; m < p.np; m++) {
-                const int d = 128 * m + 32 * quad + lane;
+#pragma unroll 1
+            for (int n0 = 0; n0 < rows; n0 += 16) {
+                float f[16];
 #pragma unroll
-                for (int n0 = 0; n0 < NC; n0 += 16) {
+                for (int n = 0; n < 16; n++) f[n] = S.keep[n0 + n];
+                const int here = rows - n0;
+#pragma unroll 1
+                for (int m = 0; m < p.np; m++) {
+                    const int d = 128 * m + 32 * quad + lane;
                     float o[16];
                     tmem_ld16(lane_base(tmem, quad) + (2 + m) * NC + n0, o);
                     tmem_wait_ld();
-                    if (d < s.dc) {
+                    if (d >= s.dc) continue;
+                    if (whole) {
+                        __nv_bfloat16* y = (__nv_bfloat16*)a.o + (out + n0) * s.dc + d;
 #pragma unroll
-                        for (int n = 0; n < 16; n++)
-                            if (n0 + n < rows) {
-                                const float y = o[n] * S.keep[n0 + n];
-                                if (whole)
-                                    ((__nv_bfloat16*)a.o)[(out + n0 + n) * s.dc + d] = __float2bfloat16_rn(y);
-                                else
-                                    a.part_o[(slot + n0 + n) * s.dc + d] = y;
-                            }
+                        for (int n = 0; n < 16; n++, y += s.dc)
+                            if (n < here) *y = __float2bfloat16_rn(o[n] * f[n]);
+                    } else {
+                        float* y = a.part_o + (slot + n0) * s.dc + d;
+#pragma unroll
+                        for (int n = 0; n < 16; n++, y += s.dc)
+                            if (n < here) *y = o[n] * f[n];
                     }
                 }
             }
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         const int col = (lane & 7) * 8;
         Run r(deal, S.b, S.tile, total);
         uint32_t piece = 0;
-        for (long long i = 0; i < total;) {
+        for (int i = 0; i < total;) {
             if (piece > 0) wait_for(&S.q_empty, (piece - 1) & 1, gave_up);
             for (int n = lane >> 3; n < NC; n += 4) {    // past the rows or the width: zeros
                 const bool row = n < rows;
@@ -524,7 +526,7 @@ cudaError_t run(Params& p, cudaStream_t st)
 {
     const int blocks = p.nb + (p.a.s.dr > 0 ? 1 : 0);
     const uint32_t q = blocks * NC * 128, pp = 2 * NC * 128;
-    const uint32_t room = 232448 - 1024 - (uint32_t)sizeof(Shared) - 256;
+    const uint32_t room = 232448 - 1024 - (uint32_t)sizeof(Shared) - 4096;   // 4 KB: a join block beside the worker
     p.nrope = p.a.s.dr == 0 ? 0 : p.np >= 3 ? 2 : 4;
     const uint32_t fixed = q + pp + p.nrope * kBlockBytes;
     p.npair = (int)((room - fixed) / kPairBytes);
