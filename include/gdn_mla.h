@@ -88,7 +88,7 @@ gdn_status_t gdn_mla_prep_bwd(const gdn_mla_prep_t* shape, const void* kv, long 
  * outside [0, Nq] or [0, Nk] are taken as the nearer bound).  Rows of no sequence are neither read into a result nor
  * written.  Values in one sequence never reach another, NaN and Inf included; within a sequence a NaN or Inf in a
  * key's v, kn or kr reaches the queries of its 128-key tile that precede it as well.
- * Limits: H a multiple of Hkv; dn, dv in 8..128, dr in 0..64; B, H <= 65535; Nq, Nk < 2^31. */
+ * Limits: H a multiple of Hkv; dn, dv in 8..128, dr in 0..64; B, H <= 65535; Nq, Nk < 2^31; scale >= 0. */
 typedef struct {
     int B, H, Hkv;
     int Tq, Tk;                       /* most rows of one sequence                      */
@@ -127,7 +127,8 @@ gdn_status_t gdn_mla_bwd(const gdn_mla_attn_t* shape, const gdn_mla_view_t* qn, 
  * lse[b, t, h] = log sum_j exp(s) (fp32, NULL: not written).  A query that sees no row gets o = 0 and lse = -inf.
  * len[b] is taken between 0 and maxpages * page; a page number outside [0, npages) reads as rows of zeros; nothing
  * past len[b] reaches a result.  Limits: 1 <= T <= 8, T * H <= 1024, dc in 8..512, dr in 0..64, page a multiple of 8,
- * B <= 65535, npages * page < 2^31, B * (maxpages * page / 64 + 2) < 2^31. */
+ * B <= 65535, npages * page < 2^31, B * (maxpages * page / 64 + 2) < 2^31,
+ * scale >= 0. */
 typedef struct {
     int B, T, H;
     int dc, dr;

@@ -68,7 +68,7 @@ bool attn_ok(const gdn_mla_attn_t& s)
     if (s.dn < 8 || s.dn > 128 || s.dn % 8 || s.dr < 0 || s.dr > 64 || s.dr % 8 || s.dv < 8 || s.dv > 128 || s.dv % 8)
         return false;
     // query rows with their heads are numbered by 64 bits, launched by 32
-    return (double)s.Nq * s.H < 8.0 * 2147483647.0 && s.scale == s.scale;
+    return (double)s.Nq * s.H < 8.0 * 2147483647.0 && s.scale >= 0.f && s.scale < 1e30f;
 }
 
 struct AttnWs {
@@ -93,6 +93,8 @@ gdn_status_t attn_common(const gdn_mla_attn_t* s, const gdn_mla_view_t* qn, cons
     if (!attn_ok(*s)) return GDN_ERR_SHAPE;
     memset(a, 0, sizeof(*a));
     a->s = *s;
+    a->s.Tq = s->Tq < s->Nq ? s->Tq : s->Nq;
+    a->s.Tk = s->Tk < s->Nk ? s->Tk : s->Nk;
     const bool q = s->Nq > 0, k = s->Nk > 0;
     GDN_TAKE(qn, q, s->H, s->io, &a->qn);
     GDN_TAKE(qr, q && s->dr > 0, s->H, s->io, &a->qr);
@@ -118,7 +120,7 @@ bool cache_ok(const gdn_mla_cache_t& s)
     if ((double)s.npages * s.page >= 2147483648.0 || (double)s.maxpages * s.page >= 2147483648.0) return false;
     // the tiles that the lengths can name are counted in 32 bits
     if ((double)s.B * (((double)s.maxpages * s.page + kDecodeTile - 1) / kDecodeTile + 1) >= 2147483648.0) return false;
-    return s.scale == s.scale;
+    return s.scale >= 0.f && s.scale < 1e30f;
 }
 
 }  // namespace
@@ -215,7 +217,8 @@ extern "C" gdn_status_t gdn_mla_fwd(const gdn_mla_attn_t* s, const gdn_mla_view_
     if (s->Nq == 0 || s->Tq == 0) return GDN_OK;
     a.o = o;
     a.lse = lse;
-    return launch_attn_f32(a, st) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    const cudaError_t e = s->io == GDN_BF16 ? launch_attn_tc(a, st) : launch_attn_f32(a, st);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 extern "C" gdn_status_t gdn_mla_bwd(const gdn_mla_attn_t* s, const gdn_mla_view_t* qn, const gdn_mla_view_t* qr,

@@ -125,7 +125,7 @@ def test_attention_refusals(backward):
     refused(attn(None, backward), NULL)
     for bad in (dict(B=0), dict(B=65536), dict(H=0), dict(Hkv=0), dict(Hkv=3), dict(dn=0), dict(dn=12), dict(dn=136), dict(dr=4),
                 dict(dr=72), dict(dv=0), dict(dv=136), dict(Tq=-1, Nq=0), dict(Tk=-1, Nk=0), dict(Nq=-1), dict(Nk=-1),
-                dict(scale=float("nan"))):
+                dict(scale=float("nan")), dict(scale=-0.1)):
         refused(attn(attn_shape(**bad), backward), SHAPE)
         assert gdn.gdn_mla_workspace_bytes(attn_shape(**bad), backward) == 0
     refused(attn(attn_shape(io=5), backward), MODE)
@@ -171,7 +171,8 @@ def test_decode_refusals():
     refused(decode(None), NULL)
     for bad in (dict(B=0), dict(T=0), dict(T=9), dict(H=0), dict(T=8, H=129), dict(dc=0), dict(dc=20), dict(dc=520), dict(dr=4),
                 dict(dr=72), dict(page=0), dict(page=12), dict(npages=0), dict(maxpages=0), dict(npages=1 << 26),
-                dict(maxpages=1 << 26), dict(scale=float("nan"))):
+                dict(maxpages=1 << 26), dict(scale=float("nan")), dict(scale=-1.0),
+                dict(B=65535, maxpages=1 << 20)):
         refused(decode(gdn.make_mla_cache(**{**CACHE, **bad})), SHAPE)
         assert gdn.gdn_mla_decode_workspace_bytes(gdn.make_mla_cache(**{**CACHE, **bad})) == 0
     refused(decode(gdn.make_mla_cache(**CACHE, io=3)), MODE)
