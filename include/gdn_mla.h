@@ -88,7 +88,7 @@ gdn_status_t gdn_mla_prep_bwd(const gdn_mla_prep_t* shape, const void* kv, long 
  * outside [0, Nq] or [0, Nk] are taken as the nearer bound).  Rows of no sequence are neither read into a result nor
  * written.  Values in one sequence never reach another, NaN and Inf included; within a sequence a NaN or Inf in a
  * key's v, kn or kr reaches the queries of its 128-key tile that precede it as well.
- * Limits: H a multiple of Hkv; dn, dv in 8..128, dr in 0..64; B, H <= 65535; Nq, Nk < 2^31; scale >= 0. */
+ * Limits: H a multiple of Hkv; dn, dv in 8..128, dr in 0..64; B, H <= 65535; Nq, Nk < 2^31, Nq * H and Nk * Hkv < 2^34; scale >= 0. */
 typedef struct {
     int B, H, Hkv;
     int Tq, Tk;                       /* most rows of one sequence                      */

@@ -67,8 +67,8 @@ bool attn_ok(const gdn_mla_attn_t& s)
     if (s.Tq < 0 || s.Tk < 0 || s.Nq < 0 || s.Nk < 0) return false;
     if (s.dn < 8 || s.dn > 128 || s.dn % 8 || s.dr < 0 || s.dr > 64 || s.dr % 8 || s.dv < 8 || s.dv > 128 || s.dv % 8)
         return false;
-    // query rows with their heads are numbered by 64 bits, launched by 32
-    return (double)s.Nq * s.H < 8.0 * 2147483647.0 && s.scale >= 0.f && s.scale < 1e30f;
+    // rows with their heads are numbered by 64 bits, launched by 32
+    return (double)s.Nq * s.H < 8.0 * 2147483647.0 && (double)s.Nk * s.Hkv < 8.0 * 2147483647.0 && s.scale >= 0.f && s.scale < 1e30f;
 }
 
 struct AttnWs {
@@ -248,7 +248,8 @@ extern "C" gdn_status_t gdn_mla_bwd(const gdn_mla_attn_t* s, const gdn_mla_view_
     a.dO = dO;
     a.delta = (float*)((unsigned char*)ws + w.delta);
     a.dkr_part = (float*)((unsigned char*)ws + w.dkr);
-    return launch_attn_bwd_f32(a, st) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    const cudaError_t e = s->io == GDN_BF16 ? launch_attn_bwd_tc(a, st) : launch_attn_bwd_f32(a, st);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 extern "C" size_t gdn_mla_decode_workspace_bytes(const gdn_mla_cache_t* s)

@@ -17,8 +17,7 @@ __host__ __device__ inline int pitch_of(int d) { return (d + 63) / 64 * 64 + 4; 
 
 // rows [r0, r0 + 64) of a tensor given as a main part of width d1 and a shared part of width d2 behind it; rows past
 // n and columns past d1 + d2 as zeros
-template <typename T>
-__device__ __forceinline__ void load_tile(float* s, int pitch, const T* a, long long tok_a, int d1, const T* b,
+__device__ __forceinline__ void load_tile(float* s, int pitch, const float* a, long long tok_a, int d1, const float* b,
                                           long long tok_b, int d2, int r0, int n)
 {
     const int per = (pitch - 4) >> 3;
@@ -86,19 +85,9 @@ __device__ __forceinline__ void accumulate(float (&acc)[4][4 * NJ], const float*
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store4(T* p, float a, float b, float c, float d);
-template <>
 __device__ __forceinline__ void store4(float* p, float a, float b, float c, float d)
 {
     *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
-}
-template <>
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d)
-{
-    const __nv_bfloat162 u = __floats2bfloat162_rn(a, b), v = __floats2bfloat162_rn(c, d);
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
 }
 
 // reduction over the 16 threads that share four rows
@@ -116,13 +105,11 @@ __device__ __forceinline__ float row_sum(float x)
 }
 
 // one head's slice of a view, from row `first`
-template <typename T>
-__device__ __forceinline__ T* head_of(const gdn_mla_view_t& v, int first, int h)
+__device__ __forceinline__ float* head_of(const gdn_mla_view_t& v, int first, int h)
 {
-    return (T*)v.p + (long long)first * v.tok + (long long)h * v.head;
+    return (float*)v.p + (long long)first * v.tok + (long long)h * v.head;
 }
 
-template <typename T>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a)
 {
     extern __shared__ float smem[];
@@ -135,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a)
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int off = rk.n - rq.n;
     const int end = s.causal ? min(rk.n, min(q0 + kTile, rq.n) + off) : rk.n;
-    load_tile<T>(Q, pq, head_of<T>(a.qn, rq.first, h), a.qn.tok, s.dn, head_of<T>(a.qr, rq.first, h), a.qr.tok, s.dr, q0,
+    load_tile(Q, pq, head_of(a.qn, rq.first, h), a.qn.tok, s.dn, head_of(a.qr, rq.first, h), a.qr.tok, s.dr, q0,
                  rq.n);
     float m[4], l[4], o[4][8];
 #pragma unroll
@@ -147,9 +134,9 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a)
     }
     for (int k0 = 0; k0 < end; k0 += kTile) {
         __syncthreads();
-        load_tile<T>(K, pq, head_of<T>(a.kn, rk.first, g), a.kn.tok, s.dn, head_of<T>(a.kr, rk.first, 0), a.kr.tok, s.dr, k0,
+        load_tile(K, pq, head_of(a.kn, rk.first, g), a.kn.tok, s.dn, head_of(a.kr, rk.first, 0), a.kr.tok, s.dr, k0,
                      rk.n);
-        load_tile<T>(V, pv, head_of<T>(a.v, rk.first, g), a.v.tok, s.dv, (const T*)nullptr, 0, 0, k0, rk.n);
+        load_tile(V, pv, head_of(a.v, rk.first, g), a.v.tok, s.dv, (const float*)nullptr, 0, 0, k0, rk.n);
         __syncthreads();
         float x[4][4];
         dots(x, Q, K, pq, d, ty, tx);
@@ -179,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a)
         __syncthreads();
         accumulate<false, 2>(o, P, V, pv, nj, ty, tx);
     }
-    T* out = (T*)a.o + ((long long)rq.first * s.H + h) * s.dv;
+    float* out = (float*)a.o + ((long long)rq.first * s.H + h) * s.dv;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int r = q0 + 4 * ty + i;
@@ -194,27 +181,6 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a)
                        o[i][4 * j + 3] * inv);
         }
     }
-}
-
-// delta[h, i] = dO[i, h] . o[i, h], a warp a row of one head
-template <typename T>
-__global__ void __launch_bounds__(kThreads) delta_kernel(const AttnArgs a)
-{
-    const gdn_mla_attn_t& s = a.s;
-    const long long u = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (u >= (long long)s.Nq * s.H) return;
-    const int lane = threadIdx.x & 31;
-    float t = 0.f;
-    if (lane * 8 < s.dv) {
-        float x[8], y[8];
-        load8((const T*)a.o + u * s.dv + 8 * lane, x);
-        load8((const T*)a.dO + u * s.dv + 8 * lane, y);
-#pragma unroll
-        for (int i = 0; i < 8; i++) t += x[i] * y[i];
-    }
-#pragma unroll
-    for (int m = 8; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
-    if (lane == 0) a.delta[(u % s.H) * s.Nq + u / s.H] = t;
 }
 
 // p and ds = p (dO . v - delta) scale of one thread's 4 x 4 block of a tile; zero where the query does not see the key
@@ -239,7 +205,6 @@ __device__ __forceinline__ void grads(float (&x)[4][4], float (&y)[4][4], const 
     }
 }
 
-template <typename T>
 __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a)
 {
     extern __shared__ float smem[];
@@ -251,16 +216,16 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a)
     float *Q = smem, *K = Q + kTile * pq, *V = K + kTile * pq, *D = V + kTile * pv, *S = D + kTile * pv;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int end = s.causal ? min(rk.n, min(q0 + kTile, rq.n) + rk.n - rq.n) : rk.n;
-    load_tile<T>(Q, pq, head_of<T>(a.qn, rq.first, h), a.qn.tok, s.dn, head_of<T>(a.qr, rq.first, h), a.qr.tok, s.dr, q0,
+    load_tile(Q, pq, head_of(a.qn, rq.first, h), a.qn.tok, s.dn, head_of(a.qr, rq.first, h), a.qr.tok, s.dr, q0,
                  rq.n);
-    load_tile<T>(D, pv, (const T*)a.dO + ((long long)rq.first * s.H + h) * s.dv, (long long)s.H * s.dv, s.dv,
-                 (const T*)nullptr, 0, 0, q0, rq.n);
+    load_tile(D, pv, (const float*)a.dO + ((long long)rq.first * s.H + h) * s.dv, (long long)s.H * s.dv, s.dv,
+                 (const float*)nullptr, 0, 0, q0, rq.n);
     float dq[4][12] = {};
     for (int k0 = 0; k0 < end; k0 += kTile) {
         __syncthreads();
-        load_tile<T>(K, pq, head_of<T>(a.kn, rk.first, g), a.kn.tok, s.dn, head_of<T>(a.kr, rk.first, 0), a.kr.tok, s.dr, k0,
+        load_tile(K, pq, head_of(a.kn, rk.first, g), a.kn.tok, s.dn, head_of(a.kr, rk.first, 0), a.kr.tok, s.dr, k0,
                      rk.n);
-        load_tile<T>(V, pv, head_of<T>(a.v, rk.first, g), a.v.tok, s.dv, (const T*)nullptr, 0, 0, k0, rk.n);
+        load_tile(V, pv, head_of(a.v, rk.first, g), a.v.tok, s.dv, (const float*)nullptr, 0, 0, k0, rk.n);
         __syncthreads();
         float x[4][4], y[4][4];
         dots(x, Q, K, pq, d, ty, tx);
@@ -273,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a)
         __syncthreads();
         accumulate<false, 3>(dq, S, K, pq, nj, ty, tx);
     }
-    T *on = head_of<T>(a.dqn, rq.first, h), *orr = head_of<T>(a.dqr, rq.first, h);
+    float *on = head_of(a.dqn, rq.first, h), *orr = head_of(a.dqr, rq.first, h);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int r = q0 + 4 * ty + i;
@@ -290,7 +255,6 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a)
     }
 }
 
-template <typename T>
 __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a)
 {
     extern __shared__ float smem[];
@@ -304,16 +268,16 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a)
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     // the first query that sees key k0
     const int first = s.causal ? max(0, k0 - (rk.n - rq.n)) / kTile * kTile : 0;
-    load_tile<T>(K, pq, head_of<T>(a.kn, rk.first, g), a.kn.tok, s.dn, head_of<T>(a.kr, rk.first, 0), a.kr.tok, s.dr, k0, rk.n);
-    load_tile<T>(V, pv, head_of<T>(a.v, rk.first, g), a.v.tok, s.dv, (const T*)nullptr, 0, 0, k0, rk.n);
+    load_tile(K, pq, head_of(a.kn, rk.first, g), a.kn.tok, s.dn, head_of(a.kr, rk.first, 0), a.kr.tok, s.dr, k0, rk.n);
+    load_tile(V, pv, head_of(a.v, rk.first, g), a.v.tok, s.dv, (const float*)nullptr, 0, 0, k0, rk.n);
     float dk[4][12] = {}, dv[4][8] = {};
     for (int h = g * G; h < (g + 1) * G; h++)
         for (int q0 = first; q0 < rq.n; q0 += kTile) {
             __syncthreads();
-            load_tile<T>(Q, pq, head_of<T>(a.qn, rq.first, h), a.qn.tok, s.dn, head_of<T>(a.qr, rq.first, h), a.qr.tok,
+            load_tile(Q, pq, head_of(a.qn, rq.first, h), a.qn.tok, s.dn, head_of(a.qr, rq.first, h), a.qr.tok,
                          s.dr, q0, rq.n);
-            load_tile<T>(D, pv, (const T*)a.dO + ((long long)rq.first * s.H + h) * s.dv, (long long)s.H * s.dv, s.dv,
-                         (const T*)nullptr, 0, 0, q0, rq.n);
+            load_tile(D, pv, (const float*)a.dO + ((long long)rq.first * s.H + h) * s.dv, (long long)s.H * s.dv, s.dv,
+                         (const float*)nullptr, 0, 0, q0, rq.n);
             __syncthreads();
             float x[4][4], y[4][4];
             dots(x, Q, K, pq, d, ty, tx);
@@ -330,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a)
             accumulate<true, 2>(dv, P, D, pv, njv, ty, tx);
             accumulate<true, 3>(dk, S, Q, pq, njk, ty, tx);
         }
-    T *on = head_of<T>(a.dkn, rk.first, g), *ov = head_of<T>(a.dv, rk.first, g);
+    float *on = head_of(a.dkn, rk.first, g), *ov = head_of(a.dv, rk.first, g);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int r = k0 + 4 * ty + i;
@@ -353,79 +317,44 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a)
     }
 }
 
-// dkr = the key heads' shares, added in the heads' order
-template <typename T>
-__global__ void __launch_bounds__(kThreads) dkr_kernel(const AttnArgs a)
-{
-    const gdn_mla_attn_t& s = a.s;
-    const Rows rk = rows_of(a.cu_k, blockIdx.y, s.Tk, s.Nk);
-    const int per = s.dr >> 3;
-    const long long u = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int r = (int)(u / per), c = (int)(u - (long long)r * per) << 3;
-    if (r >= rk.n) return;
-    float t[8] = {};
-    for (int g = 0; g < s.Hkv; g++) {
-        float x[8];
-        load8(a.dkr_part + ((long long)g * s.Nk + rk.first + r) * s.dr + c, x);
-#pragma unroll
-        for (int i = 0; i < 8; i++) t[i] += x[i];
-    }
-    store8((T*)a.dkr.p + (long long)(rk.first + r) * a.dkr.tok + c, t);
-}
-
 template <typename F>
 cudaError_t with_smem(F f, size_t bytes)
 {
     return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T>
-cudaError_t run_fwd(const AttnArgs& a, cudaStream_t st)
+}  // namespace
+
+cudaError_t launch_attn_f32(const AttnArgs& a, cudaStream_t st)
 {
     const gdn_mla_attn_t& s = a.s;
-    if (s.Tq == 0) return cudaSuccess;
     const int pq = pitch_of(s.dn + s.dr), pv = pitch_of(s.dv);
     const size_t bytes = (size_t)kTile * (2 * pq + pv + kSP) * sizeof(float);
-    const cudaError_t e = with_smem(fwd_kernel<T>, bytes);
+    const cudaError_t e = with_smem(fwd_kernel, bytes);
     if (e != cudaSuccess) return e;
-    fwd_kernel<T><<<dim3((s.Tq + kTile - 1) / kTile, s.H, s.B), kThreads, bytes, st>>>(a);
+    fwd_kernel<<<dim3((s.Tq + kTile - 1) / kTile, s.H, s.B), kThreads, bytes, st>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t run_bwd(const AttnArgs& a, cudaStream_t st)
+cudaError_t launch_attn_bwd_f32(const AttnArgs& a, cudaStream_t st)
 {
     const gdn_mla_attn_t& s = a.s;
     const int pq = pitch_of(s.dn + s.dr), pv = pitch_of(s.dv);
     const size_t bytes = (size_t)kTile * (2 * pq + 2 * pv + 2 * kSP) * sizeof(float);
     cudaError_t e;
     if (s.Tq > 0) {
-        const long long units = (long long)s.Nq * s.H;
-        if (units > 0) delta_kernel<T><<<(unsigned)((units + 7) / 8), kThreads, 0, st>>>(a);
-        if ((e = with_smem(dq_kernel<T>, bytes)) != cudaSuccess) return e;
-        dq_kernel<T><<<dim3((s.Tq + kTile - 1) / kTile, s.H, s.B), kThreads, bytes, st>>>(a);
+        if ((e = launch_delta(a, st)) != cudaSuccess) return e;
+        if ((e = with_smem(dq_kernel, bytes)) != cudaSuccess) return e;
+        dq_kernel<<<dim3((s.Tq + kTile - 1) / kTile, s.H, s.B), kThreads, bytes, st>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (s.Tk > 0) {
-        if ((e = with_smem(dkv_kernel<T>, bytes)) != cudaSuccess) return e;
-        dkv_kernel<T><<<dim3((s.Tk + kTile - 1) / kTile, s.Hkv, s.B), kThreads, bytes, st>>>(a);
-        if (s.dr > 0) {
-            const long long units = (long long)s.Tk * (s.dr >> 3);
-            dkr_kernel<T><<<dim3((unsigned)((units + kThreads - 1) / kThreads), s.B), kThreads, 0, st>>>(a);
-        }
+        if ((e = with_smem(dkv_kernel, bytes)) != cudaSuccess) return e;
+        dkv_kernel<<<dim3((s.Tk + kTile - 1) / kTile, s.Hkv, s.B), kThreads, bytes, st>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (s.dr > 0) return launch_dkr(a, st);
     }
-    return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_attn_f32(const AttnArgs& a, cudaStream_t st)
-{
-    return a.s.io == GDN_BF16 ? run_fwd<__nv_bfloat16>(a, st) : run_fwd<float>(a, st);
-}
-
-cudaError_t launch_attn_bwd_f32(const AttnArgs& a, cudaStream_t st)
-{
-    return a.s.io == GDN_BF16 ? run_bwd<__nv_bfloat16>(a, st) : run_bwd<float>(a, st);
+    return cudaSuccess;
 }
 
 }  // namespace mla

@@ -1,0 +1,688 @@
+// mla_bwd_tc.cu -- gradients of the expanded attention on the tensor cores (bf16).
+//
+//   P = exp(scale S - lse),  dP = dO V^T,  dS = P (dP - delta),  delta = rowsum(dO O)
+//   dQ = scale dS K,   dK = scale dS^T Q,   dV = P^T dO
+//
+// Two kernels, so that every sum has one owner and a fixed order: one holds a tile of queries and walks the keys (dQ),
+// one holds a tile of keys and walks its head group's queries (dK, dV, with the scores transposed so that a thread is
+// a key).  Both recompute S and dP: 7 products a tile pair instead of the 5 of a kernel that adds dQ up atomically.
+// S, dP and the sums live in TMEM.  P and dS go back over S and dP as bf16 pairs and are the A operand of the next
+// products from there.  One product's tensor-core time covers the other's elementwise work: while the threads turn
+// S(i+1) into P, dK(i) and dP(i+1) run; while they turn dP into dS, dV and the next S run.
+//
+// Roles (12 warps): warp 0 loads tiles by TMA, warp 1 issues products, warps 2-3 bring lse and delta and blank the
+// rows past a ragged end, warps 4-11 do the elementwise work, half of a tile's columns each.
+#include "mla_tc.cuh"
+
+namespace gdn {
+namespace mla {
+
+namespace {
+
+constexpr int kThreads = 384, kTile = 128;
+constexpr uint32_t kBlock = 16384;      // 128 rows x 64 columns of bf16
+
+struct Params {
+    AttnArgs a;
+    CUtensorMap qn, qr, dO, kn, kr, v;   // boxes: the held side 128 rows, the walked side as many as a step takes
+    int nb, vb;                          // 64-column blocks of dn, dv
+    int tiles;                           // tiles of the held side in the longest sequence
+};
+
+// 16-value steps of block c of a query or key
+__device__ __forceinline__ int block_steps(const Params& p, int c)
+{
+    return c < p.nb ? (min(64, p.a.s.dn - 64 * c) + 15) >> 4 : (p.a.s.dr + 15) >> 4;
+}
+// columns of a product over a query's or key's whole width
+__device__ __forceinline__ int width16(const Params& p)
+{
+    return p.a.s.dr > 0 ? 64 * p.nb + ((p.a.s.dr + 15) & ~15) : (p.a.s.dn + 15) & ~15;
+}
+
+// 8 scaled columns of a row of sums as bf16
+__device__ __forceinline__ uint4 pack8(const float* x, float f)
+{
+    return make_uint4(pack_bf16(x[0] * f, x[1] * f), pack_bf16(x[2] * f, x[3] * f), pack_bf16(x[4] * f, x[5] * f),
+                      pack_bf16(x[6] * f, x[7] * f));
+}
+
+// ================================================================ dQ: a tile of queries walks the keys
+
+struct SharedQ {
+    uint64_t q_full, do_full, k_full[2], k_empty[2], v_full[2], v_empty[2], k_last, k_fixed, s_full, s_read, dp_full, ds_full,
+        dq_full, drain;
+    uint32_t tmem, gave_up;
+};
+
+// KB: 64-column blocks of a query or key (the position block among them); VS: stages of V
+template <int KB, int VS>
+__global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constant__ Params p)
+{
+    extern __shared__ unsigned char raw[];
+    __shared__ SharedQ S;
+    const AttnArgs& a = p.a;
+    const gdn_mla_attn_t& s = a.s;
+    const int h = blockIdx.x % s.H, b = blockIdx.y, g = h / (s.H / s.Hkv);
+    const int q0 = (p.tiles - 1 - (int)(blockIdx.x / s.H)) * kTile;     // the longest walks first
+    const Rows rq = rows_of(a.cu_q, b, s.Tq, s.Nq), rk = rows_of(a.cu_k, b, s.Tk, s.Nk);
+    if (q0 >= rq.n) return;
+    const int off = rk.n - rq.n;
+    const int end = s.causal ? min(rk.n, min(q0 + kTile, rq.n) + off) : rk.n;
+    const int n = end > 0 ? (end + kTile - 1) / kTile : 0;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t qs = smem_u32(sm), dos = qs + KB * kBlock, ks = dos + p.vb * kBlock, vs = ks + 2 * KB * kBlock;
+
+    if (warp == 0) {
+        if (elect_one()) {
+            for (uint64_t* x : {&S.q_full, &S.do_full, &S.k_last, &S.s_full, &S.dp_full, &S.dq_full, &S.drain}) mbar_init(x, 1);
+            for (int i = 0; i < 2; i++)
+                for (uint64_t* x : {&S.k_full[i], &S.k_empty[i], &S.v_full[i], &S.v_empty[i]}) mbar_init(x, 1);
+            mbar_init(&S.k_fixed, 64);
+            mbar_init(&S.s_read, 8);
+            mbar_init(&S.ds_full, 8);
+            fence_mbar_init();
+            S.gave_up = 0;
+        }
+    } else if (warp == 1) {
+        tmem_alloc(&S.tmem, 512);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    volatile uint32_t* gave_up = &S.gave_up;
+    const bool ragged = rk.n % kTile != 0 && n == (rk.n + kTile - 1) / kTile;   // the last key tile has rows to blank
+    constexpr uint32_t TS = 0, TP = 128, TQ = 256;     // TMEM columns of S, dP (dS over it), dQ
+
+    if (warp == 0) {
+        if (elect_one() && n > 0) {
+            const bool rope = s.dr > 0;
+            mbar_arrive_expect_tx(&S.q_full, KB * kBlock);
+            for (int c = 0; c < p.nb; c++) tma_load_3d(qs + c * kBlock, &p.qn, &S.q_full, 64 * c, h, rq.first + q0);
+            if (rope) tma_load_3d(qs + p.nb * kBlock, &p.qr, &S.q_full, 0, h, rq.first + q0);
+            int kdone = 0, vdone = 0;
+            for (int j = 0; j < n; j++) {
+                const int ks_ = j & 1, vs_ = j % VS;
+                if (!wait_for(&S.k_empty[ks_], ((j >> 1) & 1) ^ 1, gave_up) || *gave_up) break;
+                uint64_t* bar = ragged && j == n - 1 ? &S.k_last : &S.k_full[ks_];   // to the warps that blank rows
+                mbar_arrive_expect_tx(bar, KB * kBlock);
+                const uint32_t d = ks + ks_ * KB * kBlock;
+                for (int c = 0; c < p.nb; c++) tma_load_3d(d + c * kBlock, &p.kn, bar, 64 * c, g, rk.first + j * kTile);
+                if (rope) tma_load_3d(d + p.nb * kBlock, &p.kr, bar, 0, 0, rk.first + j * kTile);
+                kdone = j + 1;
+                if (j == 0) {
+                    mbar_arrive_expect_tx(&S.do_full, p.vb * kBlock);
+                    for (int c = 0; c < p.vb; c++) tma_load_3d(dos + c * kBlock, &p.dO, &S.do_full, 64 * c, h, rq.first + q0);
+                }
+                if (!wait_for(&S.v_empty[vs_], ((j / VS) & 1) ^ 1, gave_up) || *gave_up) break;
+                mbar_arrive_expect_tx(&S.v_full[vs_], p.vb * kBlock);
+                for (int c = 0; c < p.vb; c++)
+                    tma_load_3d(vs + (vs_ * p.vb + c) * kBlock, &p.v, &S.v_full[vs_], 64 * c, g, rk.first + j * kTile);
+                vdone = j + 1;
+            }
+            if (*gave_up) {   // a wait expired: the loads in flight land before the CTA ends
+                mbar_wait(&S.q_full, 0, nullptr, kWaitNs);
+                if (kdone > 0) mbar_wait(&S.do_full, 0, nullptr, kWaitNs);
+                for (int j = max(0, kdone - 2); j < kdone; j++) {
+                    if (ragged && j == n - 1)
+                        mbar_wait(&S.k_last, 0, nullptr, kWaitNs);
+                    else
+                        mbar_wait(&S.k_full[j & 1], (j >> 1) & 1, nullptr, kWaitNs);
+                }
+                for (int j = max(0, vdone - VS); j < vdone; j++) mbar_wait(&S.v_full[j % VS], (j / VS) & 1, nullptr, kWaitNs);
+            }
+        }
+    } else if (warp == 1) {
+        if (elect_one() && n > 0) {
+            const uint32_t id_s = idesc_bf16(128, 128, false, false), id_q = idesc_bf16(128, width16(p), false, true);
+            const uint64_t kmajor = sdesc(0, 16u, 1024u), nmajor = sdesc(0, kBlock, 1024u);
+            int steps[KB];
+#pragma unroll
+            for (int c = 0; c < KB; c++) steps[c] = block_steps(p, c);
+            const int vsteps = (s.dv + 15) >> 4;
+            auto scores = [&](int j) {
+                if (ragged && j == n - 1)
+                    wait_for(&S.k_fixed, 0, gave_up);
+                else
+                    wait_for(&S.k_full[j & 1], (j >> 1) & 1, gave_up);
+                tc_fence_after();
+                if (!*gave_up) {
+                    const uint64_t q = kmajor + (qs >> 4), k = kmajor + ((ks + (j & 1) * KB * kBlock) >> 4);
+#pragma unroll
+                    for (int c = 0; c < KB; c++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            if (e < steps[c])
+                                mma_bf16(tmem + TS, q + c * (kBlock >> 4) + 2 * e, k + c * (kBlock >> 4) + 2 * e, id_s,
+                                         (c | e) ? 1u : 0u);
+                }
+                mma_commit(&S.s_full);
+            };
+            auto dprobs = [&](int j) {
+                wait_for(&S.v_full[j % VS], (j / VS) & 1, gave_up);
+                tc_fence_after();
+                if (!*gave_up) {
+                    const uint64_t d = kmajor + (dos >> 4), v = kmajor + ((vs + (j % VS) * p.vb * kBlock) >> 4);
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        if (e < vsteps)
+                            mma_bf16(tmem + TP, d + (e >> 2) * (kBlock >> 4) + 2 * (e & 3), v + (e >> 2) * (kBlock >> 4) + 2 * (e & 3),
+                                     id_s, e ? 1u : 0u);
+                }
+                mma_commit(&S.dp_full);
+                mma_commit(&S.v_empty[j % VS]);
+            };
+            wait_for(&S.q_full, 0, gave_up);
+            scores(0);
+            wait_for(&S.do_full, 0, gave_up);
+            dprobs(0);
+            for (int j = 0; j < n; j++) {
+                wait_for(&S.s_read, j & 1, gave_up);
+                if (j + 1 < n) scores(j + 1);
+                wait_for(&S.ds_full, j & 1, gave_up);
+                tc_fence_after();
+                if (!*gave_up) {
+                    const uint64_t k = nmajor + ((ks + (j & 1) * KB * kBlock) >> 4);
+#pragma unroll
+                    for (int e = 0; e < 8; e++)     // dS: columns 0..31 of each half of dP's
+                        mma_bf16_ts(tmem + TQ, tmem + TP + (e >> 2) * 64 + 8 * (e & 3), k + 128 * e, id_q, (j | e) ? 1u : 0u);
+                }
+                mma_commit(&S.k_empty[j & 1]);
+                if (j + 1 < n) dprobs(j + 1);
+            }
+            mma_commit(&S.dq_full);
+            if (*gave_up) {   // the products in flight end before TMEM is freed
+                mma_commit(&S.drain);
+                mbar_wait(&S.drain, 0, nullptr, kWaitNs);
+            }
+        }
+    } else if (warp < 4) {
+        if (ragged) {
+            wait_for(&S.k_last, 0, gave_up);
+            const int valid = rk.n - (n - 1) * kTile, bad = kTile - valid;
+            for (int c = 0; c < KB; c++) {
+                unsigned char* k = sm + (ks - qs) + (((n - 1) & 1) * KB + c) * kBlock + valid * 128;
+                for (int e = tid - 64; e < bad * 8; e += 64) *reinterpret_cast<uint4*>(k + e * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&S.k_fixed);
+        }
+    } else {
+        const int half = (warp - 4) >> 2, quad = warp & 3, row = q0 + quad * 32 + lane;
+        const uint32_t base = tmem + ((uint32_t)quad << 21);
+        const bool mine = row < rq.n;
+        const long long at = (long long)h * s.Nq + rq.first + (mine ? row : 0);
+        const float c = s.scale * kLog2e;
+        const float lse = mine ? a.lse[at] : -INFINITY, delta = mine ? a.delta[at] : 0.f;
+        const float lower = lse == -INFINITY ? -INFINITY : -lse * kLog2e;       // a row without keys: weights of zero
+        // a query that sees one key has a constant weight: no gradient, not the difference of two roundings
+        int last = !mine ? -1 : s.causal ? min(rk.n - 1, row + off) : rk.n - 1;
+        if (last == 0) last = -1;
+        const int calm = min(rk.n - 1, s.causal ? q0 + quad * 32 + off : rk.n - 1);
+        const uint64_t c2 = pack2(c, c), l2 = pack2(lower, lower), d2 = pack2(-delta, -delta);
+        for (int j = 0; j < n; j++) {
+            uint32_t x[64];
+            wait_for(&S.s_full, j & 1, gave_up);
+            __syncwarp();
+            tc_fence_after();
+            tmem_ld32(base + TS + 64 * half, x);
+            tmem_ld32(base + TS + 64 * half + 32, x + 32);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.s_read);
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+                float u, w;
+                unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, l2), u, w);
+                x[i] = __float_as_uint(fast_exp2(u));
+                x[i + 1] = __float_as_uint(fast_exp2(w));
+            }
+            const int j0 = j * kTile + 64 * half;
+            const bool masked = j0 + 63 > calm || calm <= 0;
+            wait_for(&S.dp_full, j & 1, gave_up);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int i0 = 0; i0 < 64; i0 += 32) {
+                uint32_t y[32], z[16];
+                tmem_ld32(base + TP + 64 * half + i0, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const uint64_t t = mul2(pack2(__uint_as_float(x[i0 + i]), __uint_as_float(x[i0 + i + 1])),
+                                            add2(pack2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), d2));
+                    float u, w;
+                    unpack2(t, u, w);
+                    if (masked) {
+                        u = j0 + i0 + i <= last ? u : 0.f;
+                        w = j0 + i0 + i + 1 <= last ? w : 0.f;
+                    }
+                    z[i >> 1] = pack_bf16(u, w);
+                }
+                tmem_st16u(base + TP + 64 * half + (i0 >> 1), z);   // over columns of this half that have been read
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.ds_full);
+        }
+        if (n > 0) {
+            wait_for(&S.dq_full, 0, gave_up);
+            __syncwarp();
+            tc_fence_after();
+        }
+        __nv_bfloat16* on = (__nv_bfloat16*)a.dqn.p + (long long)(rq.first + row) * a.dqn.tok + (long long)h * a.dqn.head;
+        __nv_bfloat16* op = (__nv_bfloat16*)a.dqr.p + (long long)(rq.first + row) * a.dqr.tok + (long long)h * a.dqr.head;
+#pragma unroll 1
+        for (int i = 16 * half; i < 64 * KB; i += 32) {     // the two halves take 16 columns in turn
+            float o[16];
+            if (n > 0) {
+                tmem_ld16(base + TQ + i, o);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; e++) o[e] = 0.f;
+            }
+            if (!mine) continue;
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+                const int col = i + e, rcol = col - 64 * p.nb;
+                if (rcol < 0) {
+                    if (col < s.dn) *reinterpret_cast<uint4*>(on + col) = pack8(o + e, s.scale);
+                } else if (rcol < s.dr) {
+                    *reinterpret_cast<uint4*>(op + rcol) = pack8(o + e, s.scale);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0 && *gave_up) atomicExch(a.status, kDevTimeout);
+}
+
+// ================================================================ dK, dV: a tile of keys walks the queries
+
+template <int NQ>
+struct SharedK {
+    uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], st_full[2], st_empty[2], s_full, p_full, dp_full, ds_full,
+        acc_full, drain[2];
+    alignas(16) float lower[2][NQ];     // -lse log2(e), minus infinity for a row that adds nothing
+    alignas(16) float delta[2][NQ];     // -delta
+    uint32_t tmem, gave_up;
+};
+
+// NQ: queries a step; TMEM holds two NQ columns of scores, dV and dK
+template <int KB, int NQ>
+__global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_constant__ Params p)
+{
+    extern __shared__ unsigned char raw[];
+    __shared__ SharedK<NQ> S;
+    const AttnArgs& a = p.a;
+    const gdn_mla_attn_t& s = a.s;
+    const int g = blockIdx.x % s.Hkv, b = blockIdx.y, G = s.H / s.Hkv;
+    const int k0 = (int)(blockIdx.x / s.Hkv) * kTile;       // under the causal mask the first keys have most queries
+    const Rows rq = rows_of(a.cu_q, b, s.Tq, s.Nq), rk = rows_of(a.cu_k, b, s.Tk, s.Nk);
+    if (k0 >= rk.n) return;
+    const int off = rk.n - rq.n;
+    const int first = s.causal ? max(0, k0 - off) / NQ : 0;                // the first step whose queries see key k0
+    const int per = max(0, (rq.n + NQ - 1) / NQ - first), n = per * G;     // steps a head, in all
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    constexpr uint32_t kStep = NQ * 128;                                   // bytes of a 64-column block of a step
+    const uint32_t ks = smem_u32(sm), vs = ks + KB * kBlock, qs = vs + p.vb * kBlock, dos = qs + 2 * KB * kStep;
+
+    if (warp == 0) {
+        if (elect_one()) {
+            for (uint64_t* x : {&S.kv_full, &S.s_full, &S.dp_full, &S.acc_full, &S.drain[0]}) mbar_init(x, 1);
+            for (int i = 0; i < 2; i++) {
+                for (uint64_t* x : {&S.q_full[i], &S.q_empty[i], &S.do_full[i], &S.do_empty[i]}) mbar_init(x, 1);
+                mbar_init(&S.st_full[i], 64);
+                mbar_init(&S.st_empty[i], 8);
+            }
+            mbar_init(&S.p_full, 8);
+            mbar_init(&S.ds_full, 8);
+            fence_mbar_init();
+            S.gave_up = 0;
+        }
+    } else if (warp == 1) {
+        tmem_alloc(&S.tmem, 512);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    volatile uint32_t* gave_up = &S.gave_up;
+    constexpr uint32_t TS = 0, TP = NQ, TV = 2 * NQ, TK = 2 * NQ + 128;    // TMEM columns of S, dP, dV, dK
+    constexpr int HC = NQ / 2, KS = NQ / 16;                               // columns a half, 16-query steps
+
+    if (warp == 0) {
+        if (elect_one() && n > 0) {
+            const bool rope = s.dr > 0;
+            mbar_arrive_expect_tx(&S.kv_full, (KB + p.vb) * kBlock);
+            for (int c = 0; c < p.nb; c++) tma_load_3d(ks + c * kBlock, &p.kn, &S.kv_full, 64 * c, g, rk.first + k0);
+            if (rope) tma_load_3d(ks + p.nb * kBlock, &p.kr, &S.kv_full, 0, 0, rk.first + k0);
+            for (int c = 0; c < p.vb; c++) tma_load_3d(vs + c * kBlock, &p.v, &S.kv_full, 64 * c, g, rk.first + k0);
+            int qdone = 0, ddone = 0;
+            for (int i = 0, h = g * G, t = first; i < n; i++) {
+                const int st = i & 1;
+                const uint32_t ph = ((i >> 1) & 1) ^ 1;
+                const int row = rq.first + t * NQ;
+                if (!wait_for(&S.q_empty[st], ph, gave_up) || *gave_up) break;
+                mbar_arrive_expect_tx(&S.q_full[st], KB * kStep);
+                const uint32_t q = qs + st * KB * kStep, d = dos + st * p.vb * kStep;
+                for (int c = 0; c < p.nb; c++) tma_load_3d(q + c * kStep, &p.qn, &S.q_full[st], 64 * c, h, row);
+                if (rope) tma_load_3d(q + p.nb * kStep, &p.qr, &S.q_full[st], 0, h, row);
+                qdone = i + 1;
+                if (!wait_for(&S.do_empty[st], ph, gave_up) || *gave_up) break;
+                mbar_arrive_expect_tx(&S.do_full[st], p.vb * kStep);
+                for (int c = 0; c < p.vb; c++) tma_load_3d(d + c * kStep, &p.dO, &S.do_full[st], 64 * c, h, row);
+                ddone = i + 1;
+                if (++t == first + per) {
+                    t = first;
+                    h++;
+                }
+            }
+            if (*gave_up) {   // a wait expired: the loads in flight land before the CTA ends
+                mbar_wait(&S.kv_full, 0, nullptr, kWaitNs);
+                for (int i = max(0, qdone - 2); i < qdone; i++) mbar_wait(&S.q_full[i & 1], (i >> 1) & 1, nullptr, kWaitNs);
+                for (int i = max(0, ddone - 2); i < ddone; i++) mbar_wait(&S.do_full[i & 1], (i >> 1) & 1, nullptr, kWaitNs);
+            }
+        }
+    } else if (warp == 1) {
+        if (elect_one() && n > 0) {
+            const uint32_t id_s = idesc_bf16(128, NQ, false, false);
+            const uint32_t id_v = idesc_bf16(128, (s.dv + 15) & ~15, false, true), id_k = idesc_bf16(128, width16(p), false, true);
+            const uint64_t kmajor = sdesc(0, 16u, 1024u), nmajor = sdesc(0, kStep, 1024u);
+            int steps[KB];
+#pragma unroll
+            for (int c = 0; c < KB; c++) steps[c] = block_steps(p, c);
+            const int vsteps = (s.dv + 15) >> 4;
+            const bool ragged = rq.n % NQ != 0;
+            auto scores = [&](int i) {
+                wait_for(&S.q_full[i & 1], (i >> 1) & 1, gave_up);
+                if (ragged && i % per == per - 1) wait_for(&S.st_full[i & 1], (i >> 1) & 1, gave_up);   // rows past the end blanked
+                tc_fence_after();
+                if (!*gave_up) {
+                    const uint64_t k = kmajor + (ks >> 4), q = kmajor + ((qs + (i & 1) * KB * kStep) >> 4);
+#pragma unroll
+                    for (int c = 0; c < KB; c++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            if (e < steps[c])
+                                mma_bf16(tmem + TS, k + c * (kBlock >> 4) + 2 * e, q + c * (kStep >> 4) + 2 * e, id_s,
+                                         (c | e) ? 1u : 0u);
+                }
+                mma_commit(&S.s_full);
+            };
+            auto dprobs = [&](int i) {
+                wait_for(&S.do_full[i & 1], (i >> 1) & 1, gave_up);
+                tc_fence_after();
+                if (!*gave_up) {
+                    const uint64_t v = kmajor + (vs >> 4), d = kmajor + ((dos + (i & 1) * p.vb * kStep) >> 4);
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        if (e < vsteps)
+                            mma_bf16(tmem + TP, v + (e >> 2) * (kBlock >> 4) + 2 * (e & 3), d + (e >> 2) * (kStep >> 4) + 2 * (e & 3),
+                                     id_s, e ? 1u : 0u);
+                }
+                mma_commit(&S.dp_full);
+            };
+            wait_for(&S.kv_full, 0, gave_up);
+            scores(0);
+            dprobs(0);
+            for (int i = 0; i < n; i++) {
+                wait_for(&S.p_full, i & 1, gave_up);
+                tc_fence_after();
+                if (!*gave_up) {
+                    const uint64_t d = nmajor + ((dos + (i & 1) * p.vb * kStep) >> 4);
+#pragma unroll
+                    for (int e = 0; e < KS; e++)     // P: the first quarter of S's columns and the third
+                        mma_bf16_ts(tmem + TV, tmem + TS + (e >= KS / 2 ? HC + 8 * (e - KS / 2) : 8 * e), d + 128 * e, id_v,
+                                    (i | e) ? 1u : 0u);
+                }
+                mma_commit(&S.do_empty[i & 1]);
+                if (i + 1 < n) scores(i + 1);
+                wait_for(&S.ds_full, i & 1, gave_up);
+                tc_fence_after();
+                if (!*gave_up) {
+                    const uint64_t q = nmajor + ((qs + (i & 1) * KB * kStep) >> 4);
+#pragma unroll
+                    for (int e = 0; e < KS; e++)
+                        mma_bf16_ts(tmem + TK, tmem + TP + (e >= KS / 2 ? HC + 8 * (e - KS / 2) : 8 * e), q + 128 * e, id_k,
+                                    (i | e) ? 1u : 0u);
+                }
+                mma_commit(&S.q_empty[i & 1]);
+                if (i + 1 < n) dprobs(i + 1);
+            }
+            mma_commit(&S.acc_full);
+            if (*gave_up) {   // the products in flight end before TMEM is freed
+                mma_commit(&S.drain[0]);
+                mbar_wait(&S.drain[0], 0, nullptr, kWaitNs);
+            }
+        }
+    } else if (warp < 4) {
+        const int t0 = tid - 64;
+        for (int i = 0, h = g * G, t = first; i < n; i++) {
+            const int st = i & 1;
+            wait_for(&S.st_empty[st], ((i >> 1) & 1) ^ 1, gave_up);
+            const long long at = (long long)h * s.Nq + rq.first;
+            for (int e = t0; e < NQ; e += 64) {
+                const int row = t * NQ + e;
+                const float lse = row < rq.n ? a.lse[at + row] : -INFINITY;
+                S.lower[st][e] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+                S.delta[st][e] = row < rq.n ? -a.delta[at + row] : 0.f;
+            }
+            const int valid = rq.n - t * NQ;
+            if (valid < NQ) {      // rows past the end hold anything: weights of zero would still meet a NaN
+                wait_for(&S.q_full[st], (i >> 1) & 1, gave_up);
+                wait_for(&S.do_full[st], (i >> 1) & 1, gave_up);
+                for (int c = 0; c < KB + p.vb; c++) {
+                    const uint32_t from = c < KB ? qs - ks + (st * KB + c) * kStep : dos - ks + (st * p.vb + c - KB) * kStep;
+                    unsigned char* x = sm + from + valid * 128;
+                    for (int e = t0; e < (NQ - valid) * 8; e += 64) *reinterpret_cast<uint4*>(x + e * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            mbar_arrive(&S.st_full[st]);
+            if (++t == first + per) {
+                t = first;
+                h++;
+            }
+        }
+    } else {
+        const int half = (warp - 4) >> 2, quad = warp & 3, key = k0 + quad * 32 + lane;
+        const uint32_t base = tmem + ((uint32_t)quad << 21);
+        const float c = s.scale * kLog2e;
+        const uint64_t c2 = pack2(c, c);
+        for (int i = 0, t = first; i < n; i++) {
+            const int st = i & 1, q0 = t * NQ + HC * half;
+            // column e is seen from q0 + e on; a query that sees one key has a constant weight, and no gradient of it
+            const bool masked = s.causal ? q0 + off < k0 + kTile - 1 || q0 + off <= 0 : rk.n == 1;
+            const int from = s.causal ? key - off - q0 : 0;
+            const int from_s = rk.n == 1 ? NQ : s.causal ? max(from, 1 - off - q0) : 0;
+            float x[HC];
+            wait_for(&S.st_full[st], (i >> 1) & 1, gave_up);
+            wait_for(&S.s_full, i & 1, gave_up);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int e = 0; e < HC; e += 16) tmem_ld16(base + TS + HC * half + e, *reinterpret_cast<float(*)[16]>(&x[e]));
+            tmem_wait_ld();
+#pragma unroll
+            for (int e0 = 0; e0 < HC; e0 += 16) {
+                uint32_t y[8];
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(&S.lower[st][HC * half + e0 + e]);
+                    float* v = &x[e0 + e];
+                    unpack2(fma2(pack2(v[0], v[1]), c2, l.x), v[0], v[1]);
+                    unpack2(fma2(pack2(v[2], v[3]), c2, l.y), v[2], v[3]);
+#pragma unroll
+                    for (int f = 0; f < 4; f++) {
+                        v[f] = fast_exp2(v[f]);
+                        if (masked) v[f] = e0 + e + f >= from ? v[f] : 0.f;
+                    }
+                    y[e >> 1] = pack_bf16(v[0], v[1]);
+                    y[(e >> 1) + 1] = pack_bf16(v[2], v[3]);
+                }
+                asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(base + TS + HC * half +
+                                                                                                         (e0 >> 1)),
+                             "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                             : "memory");
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_full);
+            wait_for(&S.dp_full, i & 1, gave_up);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int e0 = 0; e0 < HC; e0 += 16) {
+                float d[16];
+                uint32_t y[8];
+                tmem_ld16(base + TP + HC * half + e0, d);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(&S.delta[st][HC * half + e0 + e]);
+                    float v[4];
+                    unpack2(mul2(pack2(x[e0 + e], x[e0 + e + 1]), add2(pack2(d[e], d[e + 1]), l.x)), v[0], v[1]);
+                    unpack2(mul2(pack2(x[e0 + e + 2], x[e0 + e + 3]), add2(pack2(d[e + 2], d[e + 3]), l.y)), v[2], v[3]);
+                    if (masked) {
+#pragma unroll
+                        for (int f = 0; f < 4; f++) v[f] = e0 + e + f >= from_s ? v[f] : 0.f;
+                    }
+                    y[e >> 1] = pack_bf16(v[0], v[1]);
+                    y[(e >> 1) + 1] = pack_bf16(v[2], v[3]);
+                }
+                asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(base + TP + HC * half +
+                                                                                                         (e0 >> 1)),
+                             "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                             : "memory");
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&S.ds_full);
+                mbar_arrive(&S.st_empty[st]);
+            }
+            if (++t == first + per) t = first;
+        }
+        if (n > 0) {
+            wait_for(&S.acc_full, 0, gave_up);
+            __syncwarp();
+            tc_fence_after();
+        }
+        const bool mine = key < rk.n;
+        __nv_bfloat16* ov = (__nv_bfloat16*)a.dv.p + (long long)(rk.first + key) * a.dv.tok + (long long)g * a.dv.head;
+        __nv_bfloat16* on = (__nv_bfloat16*)a.dkn.p + (long long)(rk.first + key) * a.dkn.tok + (long long)g * a.dkn.head;
+        float* op = a.dkr_part + ((long long)g * s.Nk + rk.first + key) * s.dr;
+#pragma unroll 1
+        for (int i = 16 * half; i < 128 + 64 * KB; i += 32) {     // the two halves take 16 columns in turn
+            float o[16];
+            if (n > 0) {
+                tmem_ld16(base + TV + i, o);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; e++) o[e] = 0.f;
+            }
+            if (!mine) continue;
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+                const int vcol = i + e, col = vcol - 128, rcol = col - 64 * p.nb;
+                if (col < 0) {
+                    if (vcol < s.dv) *reinterpret_cast<uint4*>(ov + vcol) = pack8(o + e, 1.f);
+                } else if (rcol < 0) {
+                    if (col < s.dn) *reinterpret_cast<uint4*>(on + col) = pack8(o + e, s.scale);
+                } else if (rcol < s.dr) {
+                    *reinterpret_cast<float4*>(op + rcol) =
+                        make_float4(o[e] * s.scale, o[e + 1] * s.scale, o[e + 2] * s.scale, o[e + 3] * s.scale);
+                    *reinterpret_cast<float4*>(op + rcol + 4) =
+                        make_float4(o[e + 4] * s.scale, o[e + 5] * s.scale, o[e + 6] * s.scale, o[e + 7] * s.scale);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0 && *gave_up) atomicExch(a.status, kDevTimeout);
+}
+
+bool maps(Params& p, int q_rows, int k_rows)
+{
+    const AttnArgs& a = p.a;
+    const gdn_mla_attn_t& s = a.s;
+    const gdn_mla_view_t dO = {const_cast<void*>(a.dO), (long long)s.H * s.dv, s.dv};
+    // a side without rows is never loaded
+    if (s.Nq > 0 && (!view_map(&p.qn, a.qn, s.Nq, s.H, s.dn, q_rows) || !view_map(&p.dO, dO, s.Nq, s.H, s.dv, q_rows) ||
+                     (s.dr > 0 && !view_map(&p.qr, a.qr, s.Nq, s.H, s.dr, q_rows))))
+        return false;
+    return s.Nk == 0 || (view_map(&p.kn, a.kn, s.Nk, s.Hkv, s.dn, k_rows) && view_map(&p.v, a.v, s.Nk, s.Hkv, s.dv, k_rows) &&
+                         (s.dr == 0 || view_map(&p.kr, a.kr, s.Nk, 1, s.dr, k_rows)));
+}
+
+template <int KB, int VS>
+cudaError_t run_dq(Params& p, cudaStream_t st)
+{
+    if (!maps(p, kTile, kTile)) return cudaErrorInvalidValue;
+    p.tiles = (p.a.s.Tq + kTile - 1) / kTile;
+    const size_t bytes = 1024 + (size_t)(KB + p.vb + 2 * KB + VS * p.vb) * kBlock;
+    const cudaError_t e = cudaFuncSetAttribute(dq_tc_kernel<KB, VS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    dq_tc_kernel<KB, VS><<<dim3((unsigned)p.a.s.H * p.tiles, p.a.s.B), kThreads, bytes, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int KB, int NQ>
+cudaError_t run_dkv(Params& p, cudaStream_t st)
+{
+    if (!maps(p, NQ, kTile)) return cudaErrorInvalidValue;
+    p.tiles = (p.a.s.Tk + kTile - 1) / kTile;
+    const size_t bytes = 1024 + (size_t)(KB + p.vb) * kBlock + (size_t)2 * (KB + p.vb) * NQ * 128;
+    const cudaError_t e = cudaFuncSetAttribute(dkv_tc_kernel<KB, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    dkv_tc_kernel<KB, NQ><<<dim3((unsigned)p.a.s.Hkv * p.tiles, p.a.s.B), kThreads, bytes, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_bwd_tc(const AttnArgs& a, cudaStream_t st)
+{
+    const gdn_mla_attn_t& s = a.s;
+    Params p;
+    memset(&p, 0, sizeof(p));
+    p.a = a;
+    p.nb = (s.dn + 63) / 64;
+    p.vb = (s.dv + 63) / 64;
+    const int kb = p.nb + (s.dr > 0 ? 1 : 0);
+    cudaError_t e = cudaSuccess;
+    if (s.Tq > 0) {
+        e = launch_delta(a, st);
+        // three blocks of Q and two K stages leave room for one V stage only
+        if (e == cudaSuccess) e = kb == 1 ? run_dq<1, 2>(p, st) : kb == 2 ? run_dq<2, 2>(p, st) : run_dq<3, 1>(p, st);
+    }
+    if (e == cudaSuccess && s.Tk > 0) {
+        // dV and 192 columns of dK leave 192 for S and dP
+        e = kb == 1 ? run_dkv<1, 128>(p, st) : kb == 2 ? run_dkv<2, 128>(p, st) : run_dkv<3, 96>(p, st);
+        if (e == cudaSuccess && s.dr > 0) e = launch_dkr(a, st);
+    }
+    return e;
+}
+
+}  // namespace mla
+}  // namespace gdn

@@ -72,6 +72,9 @@ int prep_bwd_blocks(int N);
 cudaError_t launch_prep(const PrepArgs& a, cudaStream_t st);
 cudaError_t launch_prep_bwd(const PrepArgs& a, cudaStream_t st);
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st);        // bf16
+cudaError_t launch_attn_bwd_tc(const AttnArgs& a, cudaStream_t st);    // bf16
+cudaError_t launch_delta(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_dkr(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_attn_f32(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_attn_bwd_f32(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st);
