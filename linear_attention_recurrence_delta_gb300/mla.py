@@ -86,6 +86,9 @@ def declare(lib):
         f.argtypes, f.restype = args, res
 
 
+_ref = ctypes.byref
+
+
 def _view(t, heads=True):
     """A tensor as (address, row stride, head stride); None and a ready view pass through."""
     if t is None or isinstance(t, gdn_mla_view_t):
@@ -106,6 +109,30 @@ def _view(t, heads=True):
     return gdn_mla_view_t(t.data_ptr(), tok, stride[lead] if heads else tok)
 
 
+# A decoding step waits for these calls' host time, so the common layouts take a short way (half a microsecond a view).
+
+def _heads(t):
+    """[rows, heads, d] or [B, T, heads, d] by reference."""
+    if t is None:
+        return None
+    if type(t) is not gdn_mla_view_t:
+        s = t.stride()
+        if len(s) == 3 and s[2] == 1 and s[0] % 8 == 0 and s[0] > 0:
+            return _ref(gdn_mla_view_t(t.data_ptr(), s[0], s[1]))
+        if len(s) == 4 and t.is_contiguous():
+            n = t.shape
+            return _ref(gdn_mla_view_t(t.data_ptr(), n[2] * n[3], n[3]))
+        t = _view(t)
+    return _ref(t)
+
+
+def _flat(t):
+    """[rows, d] by reference."""
+    if t is None:
+        return None
+    return _ref(_view(t, heads=False))
+
+
 def _size(ws, ws_bytes):
     return _nbytes(ws) if ws_bytes is None and ws is not None else (ws_bytes or 0)
 
@@ -114,69 +141,63 @@ def _rows(t):
     """A tensor of contiguous rows as (address, row stride)."""
     if t is None or isinstance(t, int):
         return t, 0
+    s = t.stride()
+    if len(s) == 2 and s[1] == 1 and s[0] % 8 == 0 and s[0] > 0:
+        return t.data_ptr(), s[0]
     v = _view(t, heads=False)
     return v.p, v.tok
 
 
-_ref = ctypes.byref
-
-
-def _by(v):
-    return None if v is None else _ref(v)
-
-
-def _dense(*ts):
-    for t in ts:
-        if t is not None and not isinstance(t, int) and not t.is_contiguous():
-            raise ValueError("o, dO, lse, cache, table, lengths, offsets, positions and workspaces are contiguous")
-    return [_ptr(t) for t in ts]
+def _dense(t):
+    """The address of a contiguous tensor."""
+    if t is None or type(t) is int:
+        return t
+    if not t.is_contiguous():
+        raise ValueError("o, dO, lse, cache, table, lengths, offsets, positions and workspaces are contiguous")
+    return t.data_ptr()
 
 
 def gdn_mla_prep(shape, kv, w, rot, pos, seq, table, qr, lat, kr, qr_out, stream=None) -> int:
     """Norm, rotate and write: into the paged cache `lat` (shape.page > 0; kr None), or to dense rows lat, kr."""
-    lat_v = gdn_mla_view_t(_ptr(lat), 0, 0) if shape.page > 0 else _view(lat, heads=False)
-    if shape.page > 0:
-        _dense(lat)
-    return int(load().gdn_mla_prep(_ref(shape), *_rows(kv), *_dense(w, rot, pos, seq, table), _by(_view(qr)), _by(lat_v),
-                                   _by(_view(kr, heads=False)), _by(_view(qr_out)), _stream(stream)))
+    rows = _ref(gdn_mla_view_t(_dense(lat), 0, 0)) if shape.page > 0 else _flat(lat)
+    return load().gdn_mla_prep(_ref(shape), *_rows(kv), _dense(w), _dense(rot), _dense(pos), _dense(seq), _dense(table),
+                               _heads(qr), rows, _flat(kr), _heads(qr_out), _stream(stream))
 
 
 def gdn_mla_prep_workspace_bytes(shape) -> int:
-    return int(load().gdn_mla_prep_workspace_bytes(_ref(shape)))
+    return load().gdn_mla_prep_workspace_bytes(_ref(shape))
 
 
 def gdn_mla_prep_bwd(shape, kv, w, rot, pos, dlat, dkr, dqr, dkv, dw, dqr_out, ws, ws_bytes=None, stream=None) -> int:
     """Gradients of the dense form: dkv [N, dc + dr], dw [dc] fp32 and dqr_out."""
-    return int(load().gdn_mla_prep_bwd(_ref(shape), *_rows(kv), *_dense(w, rot, pos), _by(_view(dlat, heads=False)),
-                                       _by(_view(dkr, heads=False)), _by(_view(dqr)), *_rows(dkv), *_dense(dw),
-                                       _by(_view(dqr_out)), _ptr(ws), _size(ws, ws_bytes), _stream(stream)))
+    return load().gdn_mla_prep_bwd(_ref(shape), *_rows(kv), _dense(w), _dense(rot), _dense(pos), _flat(dlat), _flat(dkr),
+                                   _heads(dqr), *_rows(dkv), _dense(dw), _heads(dqr_out), _ptr(ws), _size(ws, ws_bytes),
+                                   _stream(stream))
 
 
 def gdn_mla_workspace_bytes(shape, backward) -> int:
-    return int(load().gdn_mla_workspace_bytes(_ref(shape), int(backward)))
+    return load().gdn_mla_workspace_bytes(_ref(shape), int(backward))
 
 
 def gdn_mla_fwd(shape, qn, qr, kn, kr, v, cu_q, cu_k, o, lse, ws, ws_bytes=None, stream=None) -> int:
     """o and, if given, lse [H, Nq] fp32."""
-    return int(load().gdn_mla_fwd(_ref(shape), _by(_view(qn)), _by(_view(qr)), _by(_view(kn)), _by(_view(kr, heads=False)),
-                                  _by(_view(v)), *_dense(cu_q, cu_k, o, lse), _ptr(ws), _size(ws, ws_bytes),
-                                  _stream(stream)))
+    return load().gdn_mla_fwd(_ref(shape), _heads(qn), _heads(qr), _heads(kn), _flat(kr), _heads(v), _dense(cu_q),
+                              _dense(cu_k), _dense(o), _dense(lse), _ptr(ws), _size(ws, ws_bytes), _stream(stream))
 
 
 def gdn_mla_bwd(shape, qn, qr, kn, kr, v, cu_q, cu_k, o, lse, dO, dqn, dqr, dkn, dkr, dv, ws, ws_bytes=None,
                 stream=None) -> int:
     """The gradients of qn, qr, kn, kr and v from dO and the forward's o and lse."""
-    return int(load().gdn_mla_bwd(_ref(shape), _by(_view(qn)), _by(_view(qr)), _by(_view(kn)), _by(_view(kr, heads=False)),
-                                  _by(_view(v)), *_dense(cu_q, cu_k, o, lse, dO), _by(_view(dqn)), _by(_view(dqr)),
-                                  _by(_view(dkn)), _by(_view(dkr, heads=False)), _by(_view(dv)), _ptr(ws),
-                                  _size(ws, ws_bytes), _stream(stream)))
+    return load().gdn_mla_bwd(_ref(shape), _heads(qn), _heads(qr), _heads(kn), _flat(kr), _heads(v), _dense(cu_q),
+                              _dense(cu_k), _dense(o), _dense(lse), _dense(dO), _heads(dqn), _heads(dqr), _heads(dkn),
+                              _flat(dkr), _heads(dv), _ptr(ws), _size(ws, ws_bytes), _stream(stream))
 
 
 def gdn_mla_decode_workspace_bytes(shape) -> int:
-    return int(load().gdn_mla_decode_workspace_bytes(_ref(shape)))
+    return load().gdn_mla_decode_workspace_bytes(_ref(shape))
 
 
 def gdn_mla_decode(shape, qc, qr, cache, table, lens, o, lse, ws, ws_bytes=None, stream=None) -> int:
     """o [B, T, H, dc] and, if given, lse [B, T, H] fp32 of new tokens over the paged latent cache."""
-    return int(load().gdn_mla_decode(_ref(shape), _by(_view(qc)), _by(_view(qr)), *_dense(cache, table, lens, o, lse),
-                                     _ptr(ws), _size(ws, ws_bytes), _stream(stream)))
+    return load().gdn_mla_decode(_ref(shape), _heads(qc), _heads(qr), _dense(cache), _dense(table), _dense(lens), _dense(o),
+                                 _dense(lse), _ptr(ws), _size(ws, ws_bytes), _stream(stream))
