@@ -32,7 +32,7 @@ struct Params {
 
 struct Shared {
     uint64_t q_full[2], k_full[kMaxStage], k_empty[kMaxStage], v_full[kMaxStage], v_empty[kMaxStage], v_last, v_fixed, s_full[2],
-        p_full[2], o_full[2], drain;
+        p_full[2][2], o_full[2], drain;
     uint32_t tmem, gave_up;
 };
 
@@ -62,12 +62,32 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     const uint32_t qs = smem_u32(sm), ks = qs + 2 * KB * kBlock, vs = qs + p.v_off;
 
+    const bool rope = s.dr > 0;
+    const bool ragged = rk.n % kTile != 0 && n == (rk.n + kTile - 1) / kTile;   // the last value tile has rows to blank
+    const auto load_q = [&](int t) {
+        mbar_arrive_expect_tx(&S.q_full[t], KB * kBlock);
+        for (int c = 0; c < p.nb; c++)
+            tma_load_3d(qs + (t * KB + c) * kBlock, &p.qn, &S.q_full[t], 64 * c, h, rq.first + q0 + t * kTile);
+        if (rope) tma_load_3d(qs + (t * KB + p.nb) * kBlock, &p.qr, &S.q_full[t], 0, h, rq.first + q0 + t * kTile);
+    };
+    const auto load_k = [&](int j, int st) {
+        mbar_arrive_expect_tx(&S.k_full[st], KB * kBlock);
+        const uint32_t d = ks + st * KB * kBlock;
+        for (int c = 0; c < p.nb; c++) tma_load_3d(d + c * kBlock, &p.kn, &S.k_full[st], 64 * c, g, rk.first + j * kTile);
+        if (rope) tma_load_3d(d + p.nb * kBlock, &p.kr, &S.k_full[st], 0, 0, rk.first + j * kTile);
+    };
+    const auto load_v = [&](int j, int st) {
+        uint64_t* bar = ragged && j == n - 1 ? &S.v_last : &S.v_full[st];   // to the warps that blank rows
+        mbar_arrive_expect_tx(bar, p.vb * kBlock);
+        for (int c = 0; c < p.vb; c++) tma_load_3d(vs + (st * p.vb + c) * kBlock, &p.v, bar, 64 * c, g, rk.first + j * kTile);
+    };
     if (warp == 0) {
         if (elect_one()) {
             for (int i = 0; i < 2; i++) {
                 mbar_init(&S.q_full[i], 1);
                 mbar_init(&S.s_full[i], 1);
-                mbar_init(&S.p_full[i], 4);
+                mbar_init(&S.p_full[i][0], 4);
+                mbar_init(&S.p_full[i][1], 4);
                 mbar_init(&S.o_full[i], 1);
             }
             for (int i = 0; i < kMaxStage; i++) {
@@ -81,6 +101,12 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
             mbar_init(&S.drain, 1);
             fence_mbar_init();
             S.gave_up = 0;
+            if (n > 0) {      // the first tiles come while the other warps set up
+                if (nt[0]) load_q(0);
+                load_k(0, 0);
+                if (nt[1]) load_q(1);
+                load_v(0, 0);
+            }
         }
     } else if (warp == 1) {
         tmem_alloc(&S.tmem, 512);
@@ -90,55 +116,23 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tmem = S.tmem;
     volatile uint32_t* gave_up = &S.gave_up;
-    const bool ragged = rk.n % kTile != 0 && n == (rk.n + kTile - 1) / kTile;   // the last value tile has rows to blank
-
     if (warp < 4) {
         regs_down<80>();
         if (warp == 0) {
-            if (elect_one()) {
-                const bool rope = s.dr > 0;
-                int klast = -1, vlast = -1;
-                auto load_q = [&](int t) {
-                    mbar_arrive_expect_tx(&S.q_full[t], KB * kBlock);
-                    for (int c = 0; c < p.nb; c++)
-                        tma_load_3d(qs + (t * KB + c) * kBlock, &p.qn, &S.q_full[t], 64 * c, h, rq.first + q0 + t * kTile);
-                    if (rope) tma_load_3d(qs + (t * KB + p.nb) * kBlock, &p.qr, &S.q_full[t], 0, h, rq.first + q0 + t * kTile);
-                };
-                auto load_k = [&](int j, int st, uint32_t phase) {
-                    if (!wait_for(&S.k_empty[st], phase ^ 1, gave_up) || *gave_up) return;
-                    klast = j;
-                    mbar_arrive_expect_tx(&S.k_full[st], KB * kBlock);
-                    const uint32_t d = ks + st * KB * kBlock;
-                    for (int c = 0; c < p.nb; c++) tma_load_3d(d + c * kBlock, &p.kn, &S.k_full[st], 64 * c, g, rk.first + j * kTile);
-                    if (rope) tma_load_3d(d + p.nb * kBlock, &p.kr, &S.k_full[st], 0, 0, rk.first + j * kTile);
-                };
-                auto load_v = [&](int j, int st, uint32_t phase) {
-                    if (!wait_for(&S.v_empty[st], phase ^ 1, gave_up) || *gave_up) return;
-                    uint64_t* bar = ragged && j == n - 1 ? &S.v_last : &S.v_full[st];   // to the warps that blank rows
-                    vlast = j;
-                    mbar_arrive_expect_tx(bar, p.vb * kBlock);
-                    for (int c = 0; c < p.vb; c++)
-                        tma_load_3d(vs + (st * p.vb + c) * kBlock, &p.v, bar, 64 * c, g, rk.first + j * kTile);
-                };
-                int kst = 0, vst = 0;
-                uint32_t kph = 0, vph = 0;
-                if (n > 0) {
-                    if (nt[0]) load_q(0);
-                    load_k(0, 0, 0);
-                    if (nt[1]) load_q(1);
-                    if (++kst == p.kstages) kst = 0, kph = 1;
-                }
-                for (int j = 0; j < n; j++) {
-                    if (j + 1 < n) {
-                        load_k(j + 1, kst, kph);
-                        if (++kst == p.kstages) kst = 0, kph ^= 1;
-                    }
-                    load_v(j, vst, vph);
+            if (elect_one() && n > 0) {
+                int klast = 0, vlast = 0, kst = 1 % p.kstages, vst = 1 % p.vstages;
+                uint32_t kph = p.kstages == 1, vph = p.vstages == 1;
+                for (int j = 1; j < n; j++) {
+                    if (!wait_for(&S.k_empty[kst], kph ^ 1, gave_up) || *gave_up) break;
+                    load_k(klast = j, kst);
+                    if (++kst == p.kstages) kst = 0, kph ^= 1;
+                    if (!wait_for(&S.v_empty[vst], vph ^ 1, gave_up) || *gave_up) break;
+                    load_v(vlast = j, vst);
                     if (++vst == p.vstages) vst = 0, vph ^= 1;
                 }
                 if (*gave_up) {   // a wait expired: the loads in flight land before the CTA ends
                     for (int t = 0; t < 2; t++)
-                        if (n > 0 && nt[t]) mbar_wait(&S.q_full[t], 0, nullptr, kWaitNs);
+                        if (nt[t]) mbar_wait(&S.q_full[t], 0, nullptr, kWaitNs);
                     for (int j = max(0, klast - p.kstages + 1); j <= klast; j++)
                         mbar_wait(&S.k_full[j % p.kstages], (j / p.kstages) & 1, nullptr, kWaitNs);
                     for (int j = max(0, vlast - p.vstages + 1); j <= vlast; j++) {
@@ -192,13 +186,17 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
 #pragma unroll
                     for (int t = 0; t < 2; t++)
                         if (j < nt[t]) {
-                            wait_for(&S.p_full[t], j & 1, gave_up);
-                            tc_fence_after();
                             const uint64_t v = vmajor + ((vs + vst * p.vb * kBlock) >> 4);
-                            if (!*gave_up) {
 #pragma unroll
-                                for (int e = 0; e < 8; e++)
-                                    mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * e, v + 128 * e, id_o, (j | e) ? 1u : 0u);
+                            for (int half = 0; half < 2; half++) {
+                                wait_for(&S.p_full[t][half], j & 1, gave_up);
+                                tc_fence_after();
+                                if (!*gave_up) {
+#pragma unroll
+                                    for (int e = 4 * half; e < 4 * half + 4; e++)
+                                        mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * e, v + 128 * e, id_o,
+                                                    (j | e) ? 1u : 0u);
+                                }
                             }
                             if (j + 1 < nt[t]) {
                                 if (!k_ready) wait_for(&S.k_full[kst], kph, gave_up);
@@ -248,20 +246,28 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
             __syncwarp();
             tc_fence_after();
             uint32_t x[128];
-#pragma unroll
-            for (int i = 0; i < 128; i += 32) tmem_ld32(sa + i, x + i);
-            tmem_wait_ld();
-            if (j * kTile + kTile - 1 > calm) {
-                const int lim = last - j * kTile;
-#pragma unroll
-                for (int i = 0; i < 128; i++) x[i] = i <= lim ? x[i] : 0xff800000u;
-            }
             float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            const bool masked = j * kTile + kTile - 1 > calm;
+            const int lim = last - j * kTile;
+            tmem_ld32(sa, x);
+            tmem_ld32(sa + 32, x + 32);
 #pragma unroll
-            for (int i = 0; i < 128; i += 8)
+            for (int i0 = 0; i0 < 128; i0 += 64) {
+                tmem_wait_ld();
+                if (i0 == 0) {       // the second half comes while the first one's maximum is taken
+                    tmem_ld32(sa + 64, x + 64);
+                    tmem_ld32(sa + 96, x + 96);
+                }
+                if (masked) {
 #pragma unroll
-                for (int e = 0; e < 4; e++)
-                    m[e] = fmaxf(m[e], fmaxf(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])));
+                    for (int i = i0; i < i0 + 64; i++) x[i] = i <= lim ? x[i] : 0xff800000u;
+                }
+#pragma unroll
+                for (int i = i0; i < i0 + 64; i += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        m[e] = fmaxf(m[e], fmaxf(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])));
+            }
             const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
             const bool raise = most > top + slack || top == -INFINITY;
             if (__any_sync(0xffffffffu, raise)) {
@@ -298,11 +304,13 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                     y[e] = pack_bf16(u, w);
                 }
                 tmem_st16u(sa + (i >> 1), y);
+                if (i == 32 || i == 96) {     // 64 keys' weights at a time: their products need not wait for the rest
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.p_full[t][i >> 6]);
+                }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.p_full[t]);
         }
         float l = 0.f;
         {
@@ -318,21 +326,33 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
             __syncwarp();
             tc_fence_after();
         }
-        __nv_bfloat16* out = (__nv_bfloat16*)a.o + ((long long)(rq.first + row) * s.H + h) * s.dv;
+        // rows to global memory by way of this tile's Q, which no product reads any more: a thread holds a row, but a
+        // store of the warp is to cover whole lines
+        unsigned char* stage = sm + t * KB * kBlock + quad * 32 * 128;
+        __nv_bfloat16* out = (__nv_bfloat16*)a.o + ((long long)(rq.first + q0 + t * kTile + quad * 32) * s.H + h) * s.dv;
 #pragma unroll 1
-        for (int i = 0; i < s.dv; i += 16) {
-            float o[16];
-            if (steps > 0) {
-                tmem_ld16(oa + i, o);
-                tmem_wait_ld();
-            }
-            if (mine) {
+        for (int i = 0; i < s.dv; i += 64) {
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 64; e += 16) {
+                float o[16];
+                if (steps > 0) {
+                    tmem_ld16(oa + i + e, o);
+                    tmem_wait_ld();
+                }
                 uint32_t y[8];
 #pragma unroll
-                for (int e = 0; e < 8; e++) y[e] = steps > 0 ? pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
-                *reinterpret_cast<uint4*>(out + i) = make_uint4(y[0], y[1], y[2], y[3]);
-                if (i + 8 < s.dv) *reinterpret_cast<uint4*>(out + i + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                for (int f = 0; f < 8; f++) y[f] = steps > 0 ? pack_bf16(o[2 * f] * inv, o[2 * f + 1] * inv) : 0u;
+                *reinterpret_cast<uint4*>(stage + sw128(lane, e)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(stage + sw128(lane, e + 8)) = make_uint4(y[4], y[5], y[6], y[7]);
             }
+            __syncwarp();
+            const int col = (lane & 7) * 8, rows = rq.n - (q0 + t * kTile + quad * 32);
+#pragma unroll
+            for (int r = lane >> 3; r < 32; r += 4)
+                if (r < rows && i + col < s.dv)
+                    *reinterpret_cast<uint4*>(out + (long long)r * s.H * s.dv + i + col) =
+                        *reinterpret_cast<const uint4*>(stage + sw128(r, col));
         }
     }
     tc_fence_before();
