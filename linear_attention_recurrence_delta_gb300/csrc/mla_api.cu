@@ -43,8 +43,7 @@ bool prep_ok(const gdn_mla_prep_t& s)
         if (s.B < 1 || s.npages < 1 || s.maxpages < 1) return false;
         if ((double)s.npages * s.page >= 2147483648.0) return false;
     }
-    // threads of the queries' share stay within a grid's 2^31 blocks
-    return (double)s.N * (s.H + 1) < (double)(1LL << 36);
+    return (double)s.N * (s.H + 1) < (double)(1LL << 36);   // blocks of a launch stay below 2^31
 }
 
 gdn_status_t prep_common(const gdn_mla_prep_t* s, const void* kv, long long kv_tok, const float* w, const float* rot,

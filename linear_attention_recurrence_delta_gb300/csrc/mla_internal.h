@@ -109,6 +109,38 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8])
         x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
+// the same eight values as they lie in memory, to be held while others are worked on
+template <typename T>
+struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* p)
+{
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; i++) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+    return r;
+}
+__device__ __forceinline__ void values(const Raw8<float>& r, float (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        x[4 * i] = __uint_as_float(r.v[i].x);
+        x[4 * i + 1] = __uint_as_float(r.v[i].y);
+        x[4 * i + 2] = __uint_as_float(r.v[i].z);
+        x[4 * i + 3] = __uint_as_float(r.v[i].w);
+    }
+}
+__device__ __forceinline__ void values(const Raw8<__nv_bfloat16>& r, float (&x)[8])
+{
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
 __device__ __forceinline__ void store8(float* p, const float (&x)[8])
 {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);

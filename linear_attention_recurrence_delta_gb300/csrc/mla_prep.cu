@@ -2,8 +2,8 @@
 //
 // Elementwise but for one sum a token, so HBM bounds it: each input is read once and each output written once, in
 // 16-byte pieces.  A warp holds a token's whole latent in registers (its sum of squares is one warp reduction); a
-// thread rotates 8 pairs of a query head.  Both kinds of block run in one launch, because a decoding step is bound
-// by launches, not bytes.
+// thread rotates 8 pairs of two query heads by angles that it reads once.  Forwards both kinds of block run in one launch, because a decoding step is
+// bound by launches, not bytes.
 #include "mla_internal.h"
 
 namespace gdn {
@@ -12,7 +12,6 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxVec = 4;     // 8-value vectors of a latent a lane holds: dc <= 1024
 
 __device__ __forceinline__ float warp_sum(float x)
 {
@@ -21,120 +20,157 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-// Rotates pairs 8u .. 8u+7 of a row of width dr by the angles of `rot`'s row (backwards if BACK).
-template <typename T, bool BACK>
-__device__ __forceinline__ void rotate8(const T* x, T* y, const float* rot, int u, int dr, bool interleaved)
+// eight pairs as loaded: the two 8-value pieces of a row that hold them
+struct Pairs {
+    float a[8], b[8];
+};
+
+// pairs 8u .. 8u+7 of a row of width dr: where its pieces lie
+template <bool IL>
+__device__ __forceinline__ void piece(int u, int dr, int& ia, int& ib)
 {
-    const int half = dr >> 1;
-    const int ia = interleaved ? 16 * u : 8 * u, ib = interleaved ? ia + 8 : half + 8 * u;
-    float a[8], b[8], c[8], s[8];
-    load8(x + ia, a);
-    load8(x + ib, b);
+    ia = IL ? 16 * u : 8 * u;
+    ib = IL ? ia + 8 : (dr >> 1) + 8 * u;
+}
+
+// turns them by the angles c, s.  IL: a pair is two neighbours, else equal places of the two pieces
+template <bool IL>
+__device__ __forceinline__ void turn(Pairs& x, const float (&c)[8], const float (&s)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        float& p = IL ? (i < 4 ? x.a[2 * i] : x.b[2 * i - 8]) : x.a[i];
+        float& q = IL ? (i < 4 ? x.a[2 * i + 1] : x.b[2 * i - 7]) : x.b[i];
+        const float v = p * c[i] - q * s[i];
+        q = p * s[i] + q * c[i];
+        p = v;
+    }
+}
+
+// the angles of pairs 8u .. 8u+7 at a position, the other way round if BACK
+template <bool BACK>
+__device__ __forceinline__ void angles(const float* rot, int u, int dr, float (&c)[8], float (&s)[8])
+{
     load8(rot + 8 * u, c);
-    load8(rot + half + 8 * u, s);
-    float p[8], q[8];
+    load8(rot + (dr >> 1) + 8 * u, s);
+    if (BACK) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        if (BACK) s[i] = -s[i];
-        p[i] = a[i];
-        q[i] = b[i];
-    }
-    if (interleaved) {   // a pair is two neighbours: gather the firsts into p and the seconds into q
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            p[i] = a[2 * i];
-            q[i] = a[2 * i + 1];
-            p[i + 4] = b[2 * i];
-            q[i + 4] = b[2 * i + 1];
-        }
-    }
-    float v[8], w[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        v[i] = p[i] * c[i] - q[i] * s[i];
-        w[i] = p[i] * s[i] + q[i] * c[i];
-    }
-    if (interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            a[2 * i] = v[i];
-            a[2 * i + 1] = w[i];
-            b[2 * i] = v[i + 4];
-            b[2 * i + 1] = w[i + 4];
-        }
-        store8(y + ia, a);
-        store8(y + ib, b);
-    } else {
-        store8(y + ia, v);
-        store8(y + ib, w);
+        for (int i = 0; i < 8; i++) s[i] = -s[i];
     }
 }
 
-// one thread of the queries' share: 8 pairs of one head
-template <typename T, bool BACK>
-__device__ __forceinline__ void rotate_query(const PrepArgs& a, const gdn_mla_view_t& in, const gdn_mla_view_t& out,
-                                             long long unit)
+// What is rotated: a thread turns 8 pairs of kHeads query heads of one token by the same angles, or 8 pairs of its key.
+constexpr int kHeads = 2;
+__host__ __device__ inline int threads_a_token(const gdn_mla_prep_t& s)
 {
-    const int per = a.s.dr >> 4;
-    const long long nh = unit / per;
-    const int u = (int)(unit - nh * per);
-    const long long n = nh / a.s.H;
-    const int h = (int)(nh - n * a.s.H);
-    if (n >= a.s.N) return;
-    const int pos = a.pos[n];
-    T* y = (T*)out.p + n * out.tok + h * out.head;
-    if (pos < 0 || pos >= a.s.npos) {
-        if (BACK) {
-            const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            store8(y + 16 * u, z);
-            store8(y + 16 * u + 8, z);
-        }
-        return;
-    }
-    rotate8<T, BACK>((const T*)in.p + n * in.tok + h * in.head, y, a.rot + (long long)pos * a.s.dr, u, a.s.dr,
-                     a.s.interleaved != 0);
+    return ((s.H + kHeads - 1) / kHeads + 1) * (s.dr >> 4);
+}
+__host__ __device__ inline int tokens_a_block(const gdn_mla_prep_t& s)
+{
+    const int p = threads_a_token(s);
+    return p == 0 || p > kThreads ? 1 : kThreads / p;
 }
 
-// blocks [0, lat_blocks): a warp a token; the rest: a thread 8 pairs of a query head
+// where token n's row of the cache begins, or null
 template <typename T>
-__global__ void __launch_bounds__(kThreads) prep_kernel(const PrepArgs a, int lat_blocks)
+__device__ __forceinline__ T* cache_row(const PrepArgs& a, long long n, int pos)
 {
-    if ((int)blockIdx.x >= lat_blocks) {
-        rotate_query<T, false>(a, a.qr, a.qr_out, (long long)(blockIdx.x - lat_blocks) * kThreads + threadIdx.x);
+    const int b = a.seq[n], at = pos / a.s.page;
+    if (b < 0 || b >= a.s.B || at >= a.s.maxpages) return nullptr;
+    const int page = a.table[(long long)b * a.s.maxpages + at];
+    if (page < 0 || page >= a.s.npages) return nullptr;
+    return (T*)a.lat.p + ((long long)page * a.s.page + (pos - at * a.s.page)) * (a.s.dc + a.s.dr);
+}
+
+// Block `block` of them.  BACK: the gradients' way (dqr to dqr_out, dkr to dkv), which zeroes a skipped token's.
+template <typename T, bool BACK, bool IL>
+__device__ __forceinline__ void rotate_rows(const PrepArgs& a, int block)
+{
+    const int p = threads_a_token(a.s), each = tokens_a_block(a.s), per = a.s.dr >> 4;
+    const long long n = (long long)block * each + (each > 1 ? threadIdx.x / p : 0);
+    if (n >= a.s.N || (each > 1 && (int)threadIdx.x >= each * p)) return;
+    const int pos = a.pos[n];
+    const bool bad = pos < 0 || pos >= a.s.npos;
+    if (bad && !BACK) return;
+    for (int r = each > 1 ? threadIdx.x % p : threadIdx.x; r < p; r += kThreads) {
+        const int u = r % per, h = r / per * kHeads;
+        const bool key = h >= a.s.H;
+        const gdn_mla_view_t& in = BACK ? a.dqr : a.qr;
+        const gdn_mla_view_t& out = BACK ? a.dqr_out : a.qr_out;
+        const T* x = key ? (BACK ? (const T*)a.dkr.p + n * a.dkr.tok : (const T*)a.kv + n * a.kv_tok + a.s.dc)
+                         : (const T*)in.p + n * in.tok + h * in.head;
+        const int heads = key ? 1 : min(kHeads, a.s.H - h);
+        int ia, ib;
+        piece<IL>(u, a.s.dr, ia, ib);
+        Raw8<T> va[kHeads], vb[kHeads];      // as loaded: converted, twice the registers would hold fewer threads
+#pragma unroll
+        for (int k = 0; k < kHeads; k++)
+            if (k < heads) {
+                va[k] = raw8(x + k * in.head + ia);
+                vb[k] = raw8(x + k * in.head + ib);
+            }
+        float c[8] = {}, s[8] = {};
+        if (!bad) angles<BACK>(a.rot + (long long)pos * a.s.dr, u, a.s.dr, c, s);
+        T* y = (T*)out.p + n * out.tok + h * out.head;
+        if (key) {
+            if (BACK) {
+                y = (T*)a.dkv + n * a.dkv_tok + a.s.dc;
+            } else if (a.s.page > 0) {
+                y = cache_row<T>(a, n, pos);
+                if (!y) continue;
+                y += a.s.dc;
+            } else {
+                y = (T*)a.kr.p + n * a.kr.tok;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kHeads; k++)
+            if (k < heads) {
+                Pairs v;
+                values(va[k], v.a);
+                values(vb[k], v.b);
+                turn<IL>(v, c, s);
+                if (bad) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) v.a[i] = v.b[i] = 0.f;
+                }
+                store8(y + k * out.head + ia, v.a);
+                store8(y + k * out.head + ib, v.b);
+            }
+    }
+}
+
+// blocks [0, rows_blocks): what is rotated; the rest: a warp a token's norm, NV 8-value vectors of its latent a lane
+template <typename T, bool IL, int NV>
+__global__ void __launch_bounds__(kThreads, NV == 4 ? 2 : sizeof(T) == 4 ? 3 : 4) prep_kernel(const PrepArgs a, int rows_blocks)
+{
+    if ((int)blockIdx.x < rows_blocks) {
+        rotate_rows<T, false, IL>(a, blockIdx.x);
         return;
     }
     const int lane = threadIdx.x & 31;
-    const long long n = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const long long n = (long long)(blockIdx.x - rows_blocks) * kWarps + (threadIdx.x >> 5);
     if (n >= a.s.N) return;
-    const int dc = a.s.dc, dr = a.s.dr, nv = dc >> 3;
+    const int dc = a.s.dc, nv = dc >> 3;
     const int pos = a.pos[n];
-    const bool paged = a.s.page > 0;
     const T* x = (const T*)a.kv + n * a.kv_tok;
-    float v[kMaxVec][8];
+    float v[NV][8];
     float ss = 0.f;
 #pragma unroll
-    for (int k = 0; k < kMaxVec; k++)
+    for (int k = 0; k < NV; k++)
+        if (lane + 32 * k < nv) load8(x + 8 * (lane + 32 * k), v[k]);
+    if (pos < 0 || pos >= a.s.npos) return;
+    T* lat = a.s.page > 0 ? cache_row<T>(a, n, pos) : (T*)a.lat.p + n * a.lat.tok;
+    if (!lat) return;
+#pragma unroll
+    for (int k = 0; k < NV; k++)
         if (lane + 32 * k < nv) {
-            load8(x + 8 * (lane + 32 * k), v[k]);
 #pragma unroll
             for (int i = 0; i < 8; i++) ss += v[k][i] * v[k][i];
         }
-    if (pos < 0 || pos >= a.s.npos) return;
-    T *lat, *kr;
-    if (paged) {
-        const int b = a.seq[n], at = pos / a.s.page;
-        if (b < 0 || b >= a.s.B || at >= a.s.maxpages) return;
-        const int page = a.table[(long long)b * a.s.maxpages + at];
-        if (page < 0 || page >= a.s.npages) return;
-        lat = (T*)a.lat.p + ((long long)page * a.s.page + (pos - at * a.s.page)) * (dc + dr);
-        kr = lat + dc;
-    } else {
-        lat = (T*)a.lat.p + n * a.lat.tok;
-        kr = (T*)a.kr.p + n * a.kr.tok;
-    }
     const float r = rsqrtf(warp_sum(ss) / (float)dc + a.s.eps);
 #pragma unroll
-    for (int k = 0; k < kMaxVec; k++)
+    for (int k = 0; k < NV; k++)
         if (lane + 32 * k < nv) {
             float w[8];
             const float* wp = a.w + 8 * (lane + 32 * k);
@@ -142,78 +178,81 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const PrepArgs a, int la
             for (int i = 0; i < 8; i++) w[i] = v[k][i] * r * wp[i];
             store8(lat + 8 * (lane + 32 * k), w);
         }
-    if (lane < (dr >> 4))
-        rotate8<T, false>(x + dc, kr, a.rot + (long long)pos * dr, lane, dr, a.s.interleaved != 0);
 }
 
 // Gradients: with r = rsqrt(mean x^2 + eps) and g = dy w,  dx = r (g - x r^2 mean(g x)),  dw = sum_n dy x r.
 // A block's warps walk tokens a fixed way apart and keep their share of dw in registers; the shares are added in a
 // fixed order here and in sum_dw_kernel.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) prep_bwd_kernel(const PrepArgs a, int lat_blocks)
+template <typename T, bool IL>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) rows_bwd_kernel(const PrepArgs a)
 {
-    if ((int)blockIdx.x >= lat_blocks) {
-        rotate_query<T, true>(a, a.dqr, a.dqr_out, (long long)(blockIdx.x - lat_blocks) * kThreads + threadIdx.x);
-        return;
-    }
-    __shared__ float red[kWarps][kMaxVec * 256 / 4];   // a quarter of a latent's widest share at a time
+    rotate_rows<T, true, IL>(a, blockIdx.x);
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kThreads, NV == 1 ? 4 : NV == 2 ? 2 : 1) latents_bwd_kernel(const PrepArgs a)
+{
+    __shared__ float red[kWarps][256];   // a quarter of the widest latent's shares at a time
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int dc = a.s.dc, dr = a.s.dr, nv = dc >> 3;
-    float dw[kMaxVec][8] = {};
-    for (long long n = (long long)blockIdx.x * kWarps + warp; n < a.s.N; n += (long long)lat_blocks * kWarps) {
-        const int pos = a.pos[n];
-        T* dx = (T*)a.dkv + n * a.dkv_tok;
-        if (pos < 0 || pos >= a.s.npos) {
-            const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            for (int i = lane; i < (dc + dr) >> 3; i += 32) store8(dx + 8 * i, z);
-            continue;
+    const int dc = a.s.dc, nv = dc >> 3;
+    float dw[NV][8] = {}, w[NV][8];
+#pragma unroll
+    for (int k = 0; k < NV; k++)
+        if (lane + 32 * k < nv && a.s.N > 0) {     // without tokens there need be no weight
+#pragma unroll
+            for (int i = 0; i < 8; i++) w[k][i] = a.w[8 * (lane + 32 * k) + i];
         }
+    const long long step = (long long)gridDim.x * kWarps;
+    for (long long n = (long long)blockIdx.x * kWarps + warp; n < a.s.N; n += step) {
+        const int pos = a.pos[n];
+        const bool bad = pos < 0 || pos >= a.s.npos;
         const T* x = (const T*)a.kv + n * a.kv_tok;
         const T* dy = (const T*)a.dlat.p + n * a.dlat.tok;
-        float v[kMaxVec][8], g[kMaxVec][8];
+        T* dx = (T*)a.dkv + n * a.dkv_tok;
+        float v[NV][8], g[NV][8];
         float ss = 0.f, gx = 0.f;
 #pragma unroll
-        for (int k = 0; k < kMaxVec; k++)
+        for (int k = 0; k < NV; k++)
             if (lane + 32 * k < nv) {
                 load8(x + 8 * (lane + 32 * k), v[k]);
                 load8(dy + 8 * (lane + 32 * k), g[k]);
-                const float* wp = a.w + 8 * (lane + 32 * k);
+            }
+#pragma unroll
+        for (int k = 0; k < NV; k++)
+            if (lane + 32 * k < nv) {
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
+                    if (bad) g[k][i] = v[k][i] = 0.f;      // whatever a skipped token holds, it adds nothing
                     ss += v[k][i] * v[k][i];
-                    gx += g[k][i] * wp[i] * v[k][i];
+                    gx += g[k][i] * w[k][i] * v[k][i];
                 }
             }
         const float r = rsqrtf(warp_sum(ss) / (float)dc + a.s.eps);
         const float m = warp_sum(gx) / (float)dc * r * r;
 #pragma unroll
-        for (int k = 0; k < kMaxVec; k++)
+        for (int k = 0; k < NV; k++)
             if (lane + 32 * k < nv) {
-                const float* wp = a.w + 8 * (lane + 32 * k);
                 float d[8];
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    d[i] = r * (g[k][i] * wp[i] - v[k][i] * m);
-                    dw[k][i] += g[k][i] * (v[k][i] * r);
+                    d[i] = bad ? 0.f : r * (g[k][i] * w[k][i] - v[k][i] * m);
+                    dw[k][i] += bad ? 0.f : g[k][i] * (v[k][i] * r);
                 }
                 store8(dx + 8 * (lane + 32 * k), d);
             }
-        if (lane < (dr >> 4))
-            rotate8<T, true>((const T*)a.dkr.p + n * a.dkr.tok, dx + dc, a.rot + (long long)pos * dr, lane, dr,
-                             a.s.interleaved != 0);
     }
 #pragma unroll
-    for (int k = 0; k < kMaxVec; k++) {
+    for (int k = 0; k < NV; k++) {
         if (256 * k >= dc) break;
 #pragma unroll
         for (int i = 0; i < 8; i++) red[warp][8 * lane + i] = dw[k][i];
         __syncthreads();
-        const int c = 256 * k + threadIdx.x;
-        if (c < dc) {
-            float s = 0.f;
+        const int col = 256 * k + threadIdx.x;
+        if (col < dc) {
+            float sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; w++) s += red[w][threadIdx.x];
-            a.partial[(long long)blockIdx.x * dc + c] = s;
+            for (int i = 0; i < kWarps; i++) sum += red[i][threadIdx.x];
+            a.partial[(long long)blockIdx.x * dc + col] = sum;
         }
         __syncthreads();
     }
@@ -236,43 +275,62 @@ __global__ void __launch_bounds__(1024) sum_dw_kernel(const float* part, float* 
     }
 }
 
-long long query_blocks(const gdn_mla_prep_t& s)
+long long rows_blocks(const gdn_mla_prep_t& s)
 {
-    return ((long long)s.N * s.H * (s.dr >> 4) + kThreads - 1) / kThreads;
+    if (threads_a_token(s) == 0) return 0;
+    const int each = tokens_a_block(s);
+    return ((long long)s.N + each - 1) / each;
+}
+
+template <typename T, bool IL, int NV>
+void start(const PrepArgs& a, bool backward, cudaStream_t st)
+{
+    const long long rows = rows_blocks(a.s);
+    if (backward) {
+        if (rows > 0) rows_bwd_kernel<T, IL><<<(unsigned)rows, kThreads, 0, st>>>(a);
+        latents_bwd_kernel<T, NV><<<prep_bwd_blocks(a.s.N), kThreads, 0, st>>>(a);
+    } else {
+        prep_kernel<T, IL, NV><<<(unsigned)(rows + (a.s.N + kWarps - 1) / kWarps), kThreads, 0, st>>>(a, (int)rows);
+    }
+}
+
+template <typename T, bool IL>
+void start(const PrepArgs& a, bool backward, cudaStream_t st)
+{
+    if (a.s.dc <= 256)
+        start<T, IL, 1>(a, backward, st);
+    else if (a.s.dc <= 512)
+        start<T, IL, 2>(a, backward, st);
+    else
+        start<T, IL, 4>(a, backward, st);
+}
+
+cudaError_t launch(const PrepArgs& a, bool backward, cudaStream_t st)
+{
+    const bool il = a.s.interleaved != 0;
+    if (a.s.io == GDN_BF16)
+        il ? start<__nv_bfloat16, true>(a, backward, st) : start<__nv_bfloat16, false>(a, backward, st);
+    else
+        il ? start<float, true>(a, backward, st) : start<float, false>(a, backward, st);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-// blocks that walk the tokens of the backward pass: two resident on each SM, or one a token's warp
+// blocks that walk the tokens of the backward pass: four on each SM, or a warp a token
 int prep_bwd_blocks(int N)
 {
     const int need = (N + kWarps - 1) / kWarps;
-    return need < 1 ? 1 : (need < 2 * 152 ? need : 2 * 152);
+    return need < 1 ? 1 : (need < 4 * 152 ? need : 4 * 152);
 }
 
-cudaError_t launch_prep(const PrepArgs& a, cudaStream_t st)
-{
-    const int lat = (a.s.N + kWarps - 1) / kWarps;
-    const long long grid = lat + query_blocks(a.s);
-    if (grid == 0) return cudaSuccess;
-    if (a.s.io == GDN_BF16)
-        prep_kernel<__nv_bfloat16><<<(unsigned)grid, kThreads, 0, st>>>(a, lat);
-    else
-        prep_kernel<float><<<(unsigned)grid, kThreads, 0, st>>>(a, lat);
-    return cudaGetLastError();
-}
+cudaError_t launch_prep(const PrepArgs& a, cudaStream_t st) { return launch(a, false, st); }
 
 cudaError_t launch_prep_bwd(const PrepArgs& a, cudaStream_t st)
 {
-    const int lat = prep_bwd_blocks(a.s.N);
-    const long long grid = lat + query_blocks(a.s);
-    if (a.s.io == GDN_BF16)
-        prep_bwd_kernel<__nv_bfloat16><<<(unsigned)grid, kThreads, 0, st>>>(a, lat);
-    else
-        prep_bwd_kernel<float><<<(unsigned)grid, kThreads, 0, st>>>(a, lat);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch(a, true, st);
     if (e != cudaSuccess) return e;
-    sum_dw_kernel<<<(a.s.dc + 31) / 32, dim3(32, 32), 0, st>>>(a.partial, a.dw, lat, a.s.dc);
+    sum_dw_kernel<<<(a.s.dc + 31) / 32, dim3(32, 32), 0, st>>>(a.partial, a.dw, prep_bwd_blocks(a.s.N), a.s.dc);
     return cudaGetLastError();
 }
 
