@@ -89,9 +89,7 @@ __device__ __forceinline__ void rotate_rows(const PrepArgs& a, int block)
     const int p = threads_a_token(a.s), each = tokens_a_block(a.s), per = a.s.dr >> 4;
     const long long n = (long long)block * each + (each > 1 ? threadIdx.x / p : 0);
     if (n >= a.s.N || (each > 1 && (int)threadIdx.x >= each * p)) return;
-    const int pos = a.pos[n];
-    const bool bad = pos < 0 || pos >= a.s.npos;
-    if (bad && !BACK) return;
+    const int pos = a.pos[n];      // on its way while the rows are asked for
     for (int r = each > 1 ? threadIdx.x % p : threadIdx.x; r < p; r += kThreads) {
         const int u = r % per, h = r / per * kHeads;
         const bool key = h >= a.s.H;
@@ -109,6 +107,8 @@ __device__ __forceinline__ void rotate_rows(const PrepArgs& a, int block)
                 va[k] = raw8(x + k * in.head + ia);
                 vb[k] = raw8(x + k * in.head + ib);
             }
+        const bool bad = pos < 0 || pos >= a.s.npos;
+        if (bad && !BACK) return;
         float c[8] = {}, s[8] = {};
         if (!bad) angles<BACK>(a.rot + (long long)pos * a.s.dr, u, a.s.dr, c, s);
         T* y = (T*)out.p + n * out.tok + h * out.head;
