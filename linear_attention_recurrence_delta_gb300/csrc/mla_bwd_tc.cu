@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                     wait_for(&S.k_full[j & 1], (j >> 1) & 1, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t q = kmajor + (qs >> 4), k = kmajor + ((ks + (j & 1) * KB * kBlock) >> 4);
+                    const uint64_t q = kmajor + at_desc(qs), k = kmajor + at_desc(ks + (j & 1) * KB * kBlock);
 #pragma unroll
                     for (int c = 0; c < KB; c++)
 #pragma unroll
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 wait_for(&S.v_full[j % VS], (j / VS) & 1, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t d = kmajor + (dos >> 4), v = kmajor + ((vs + (j % VS) * p.vb * kBlock) >> 4);
+                    const uint64_t d = kmajor + at_desc(dos), v = kmajor + at_desc(vs + (j % VS) * p.vb * kBlock);
 #pragma unroll
                     for (int e = 0; e < 8; e++)
                         if (e < vsteps)
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 wait_for(&S.ds_full, j & 1, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t k = nmajor + ((ks + (j & 1) * KB * kBlock) >> 4);
+                    const uint64_t k = nmajor + at_desc(ks + (j & 1) * KB * kBlock);
 #pragma unroll
                     for (int e = 0; e < 8; e++)     // dS: columns 0..31 of each half of dP's
                         mma_bf16_ts(tmem + TQ, tmem + TP + (e >> 2) * 64 + 8 * (e & 3), k + 128 * e, id_q, (j | e) ? 1u : 0u);
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
                 if (ragged && i % per == per - 1) wait_for(&S.st_full[i & 1], (i >> 1) & 1, gave_up);   // rows past the end blanked
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t k = kmajor + (ks >> 4), q = kmajor + ((qs + (i & 1) * KB * kStep) >> 4);
+                    const uint64_t k = kmajor + at_desc(ks), q = kmajor + at_desc(qs + (i & 1) * KB * kStep);
 #pragma unroll
                     for (int c = 0; c < KB; c++)
 #pragma unroll
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
                 wait_for(&S.do_full[i & 1], (i >> 1) & 1, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t v = kmajor + (vs >> 4), d = kmajor + ((dos + (i & 1) * p.vb * kStep) >> 4);
+                    const uint64_t v = kmajor + at_desc(vs), d = kmajor + at_desc(dos + (i & 1) * p.vb * kStep);
 #pragma unroll
                     for (int e = 0; e < 8; e++)
                         if (e < vsteps)
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
                 wait_for(&S.p_full, i & 1, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t d = nmajor + ((dos + (i & 1) * p.vb * kStep) >> 4);
+                    const uint64_t d = nmajor + at_desc(dos + (i & 1) * p.vb * kStep);
 #pragma unroll
                     for (int e = 0; e < KS; e++)     // P: the first quarter of S's columns and the third
                         mma_bf16_ts(tmem + TV, tmem + TS + (e >= KS / 2 ? HC + 8 * (e - KS / 2) : 8 * e), d + 128 * e, id_v,
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
                 wait_for(&S.ds_full, i & 1, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t q = nmajor + ((qs + (i & 1) * KB * kStep) >> 4);
+                    const uint64_t q = nmajor + at_desc(qs + (i & 1) * KB * kStep);
 #pragma unroll
                     for (int e = 0; e < KS; e++)
                         mma_bf16_ts(tmem + TK, tmem + TP + (e >= KS / 2 ? HC + 8 * (e - KS / 2) : 8 * e), q + 128 * e, id_k,

@@ -11,6 +11,8 @@ DecodePlan decode_plan(const gdn_mla_cache_t& s)
     const int all = s.T * s.H;
     const int most = s.io == GDN_BF16 ? 64 : 8;   // query rows of a worker on the tensor, the CUDA cores
     p.groups = (all + most - 1) / most;
+    // on the tensor cores two groups share each load of the cache (a cluster of two CTAs)
+    if (s.io == GDN_BF16 && p.groups > 1 && p.groups % 2) p.groups++;
     p.rows = (all + p.groups - 1) / p.groups;
     p.ctas = 152 / p.groups > 0 ? 152 / p.groups : 1;
     p.slots = p.ctas + s.B;

@@ -94,7 +94,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-template <int NC>
+// PAIR: the CTAs of two groups form a cluster.  They walk the same tiles; each loads half of one and the copy goes to both.
+template <int NC, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ unsigned char raw[];
@@ -121,14 +122,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
     } else if (warp == 1) {
         tmem_alloc(&S.tmem, kCols);
+    } else if (warp == 3) {
+        if (elect_one()) tma_prefetch_desc(&p.map);
     } else if (tid == 64) {
         for (int i = 0; i < kMaxPairs; i++) {
             mbar_init(&S.pair_full[i], 1);
-            mbar_init(&S.pair_empty[i], 1);
+            mbar_init(&S.pair_empty[i], PAIR ? 2 : 1);
         }
         for (int i = 0; i < kMaxRope; i++) {
             mbar_init(&S.rope_full[i], 1);
-            mbar_init(&S.rope_empty[i], 1);
+            mbar_init(&S.rope_empty[i], PAIR ? 2 : 1);
         }
         mbar_init(&S.q_full, 32);
         mbar_init(&S.q_empty, 1);
@@ -144,8 +147,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         S.gave_up = 0;
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR)
+        cluster_sync();      // both CTAs' barriers are set before either's copies arrive on them
+    else
+        __syncthreads();
     tc_fence_after();
+    const uint32_t rank = PAIR ? cluster_rank() : 0;
     cudaTriggerProgrammaticLaunchCompletion();   // the join's blocks may take their places
     const uint32_t tmem = S.tmem;
     const uint32_t pairs = smem_u32(sm), ropes = pairs + p.rope_off, qs = pairs + p.q_off, ps = pairs + p.p_off;
@@ -158,8 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         const int subs = kDecodeTile / p.box, sub = lane & (subs - 1), blk = lane / subs;   // subs: 1, 2, 4 or 8
         uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0;
         int issued = 0, rissued = 0;
-        if (lane == 0) tma_prefetch_desc(&p.map);
-        for (int i = 0; i < total; i++) {
+            for (int i = 0; i < total; i++) {
             int at = p.total_rows;
             const int j = r.tile * kDecodeTile + sub * p.box;
             if (blk < 2 && j < r.n) {
@@ -174,9 +180,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     uint64_t* bar = &S.pair_full[slot];
                     if (elect_one()) mbar_arrive_expect_tx(bar, blocks * kBlockBytes);
                     __syncwarp();
-                    if (lane < blocks * subs)   // a lane a box
-                        tma_load_2d(pairs + slot * kPairBytes + blk * kBlockBytes + sub * p.box * 128, &p.map, bar,
-                                    128 * k + 64 * blk, at);
+                    if (PAIR ? lane < subs && (int)rank < blocks : lane < blocks * subs) {   // a lane a box
+                        const int c = PAIR ? rank : blk;
+                        const uint32_t dst = pairs + slot * kPairBytes + c * kBlockBytes + sub * p.box * 128;
+                        if (PAIR)
+                            tma_load_2d_multicast(dst, &p.map, bar, 128 * k + 64 * c, at, 3);
+                        else
+                            tma_load_2d(dst, &p.map, bar, 128 * k + 64 * c, at);
+                    }
                     issued++;
                 }
                 if (++slot == (uint32_t)p.npair) {
@@ -191,7 +202,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     uint64_t* bar = &S.rope_full[rslot];
                     if (elect_one()) mbar_arrive_expect_tx(bar, kBlockBytes);
                     __syncwarp();
-                    if (lane < subs) tma_load_2d(ropes + rslot * kBlockBytes + sub * p.box * 128, &p.map, bar, s.dc, at);
+                    const uint32_t dst = ropes + rslot * kBlockBytes + sub * p.box * 128;
+                    if (PAIR) {
+                        if (lane < subs && (i & 1) == (int)rank) tma_load_2d_multicast(dst, &p.map, bar, s.dc, at, 3);   // in turn
+                    } else if (lane < subs) {
+                        tma_load_2d(dst, &p.map, bar, s.dc, at);
+                    }
                     rissued++;
                 }
                 if (++rslot == (uint32_t)p.nrope) {
@@ -200,6 +216,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 }
             }
             r.step();
+        }
+        if (PAIR) {   // the other CTA's last arrivals on this one's barriers come before either ends
+            for (int i = 0; i < p.npair; i++) {
+                wait_for(&S.pair_empty[slot], phase ^ 1, gave_up);
+                if (++slot == (uint32_t)p.npair) slot = 0, phase ^= 1;
+            }
+            for (int i = 0; i < p.nrope; i++) {
+                wait_for(&S.rope_empty[rslot], rphase ^ 1, gave_up);
+                if (++rslot == (uint32_t)p.nrope) rslot = 0, rphase ^= 1;
+            }
         }
         if (*gave_up) {   // a wait expired: the copies in flight land before the CTA ends
             for (int i = 0; i < p.npair; i++) {
@@ -224,12 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 const uint32_t d = tmem + (uint32_t)(i & 1) * NC;
                 if (first) wait_for(&S.q_full, piece++ & 1, gave_up);
                 if (i >= 2) wait_for(&S.p_full[i & 1], (uint32_t)((i - 2) >> 1) & 1, gave_up);   // the buffer's last scores are read
-                uint64_t q = base + (qs >> 4);
+                uint64_t q = base + at_desc(qs);
                 for (int k = 0; k < p.np; k++) {
                     wait_for(&S.pair_full[slot], phase, gave_up);
                     tc_fence_after();
                     if (!*gave_up) {
-                        const uint64_t kt = base + ((pairs + slot * kPairBytes) >> 4);
+                        const uint64_t kt = base + at_desc(pairs + slot * kPairBytes);
 #pragma unroll
                         for (int ks = 0; ks < 4; ks++) mma_bf16(d, kt + 2 * ks, q + 2 * ks, id, (k | ks) ? 1u : 0u);
                         if (2 * k + 1 < p.nb) {
@@ -248,11 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     wait_for(&S.rope_full[rslot], rphase, gave_up);
                     tc_fence_after();
                     if (!*gave_up) {
-                        const uint64_t kt = base + ((ropes + rslot * kBlockBytes) >> 4), qt = base + ((qs + p.nb * kQBlock) >> 4);
+                        const uint64_t kt = base + at_desc(ropes + rslot * kBlockBytes), qt = base + at_desc(qs + p.nb * kQBlock);
 #pragma unroll
                         for (int ks = 0; ks < 4; ks++) mma_bf16(d, kt + 2 * ks, qt + 2 * ks, id, 1u);
                     }
-                    mma_commit(&S.rope_empty[rslot]);
+                    PAIR ? mma_commit_multicast(&S.rope_empty[rslot], 3) : mma_commit(&S.rope_empty[rslot]);
                     if (++rslot == (uint32_t)p.nrope) {
                         rslot = 0;
                         rphase ^= 1;
@@ -279,15 +305,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 wait_for(&S.p_full[i & 1], (uint32_t)(i >> 1) & 1, gave_up);
                 tc_fence_after();
                 const bool go = !*gave_up;
-                const uint64_t pt = pbase + ((ps + (uint32_t)(i & 1) * (NC * 128)) >> 4);
+                const uint64_t pt = pbase + at_desc(ps + (uint32_t)(i & 1) * (NC * 128));
                 for (int m = 0; m < p.np; m++) {
-                    const uint64_t v = vbase + ((pairs + slot * kPairBytes) >> 4);
+                    const uint64_t v = vbase + at_desc(pairs + slot * kPairBytes);
                     if (go) {
 #pragma unroll
                         for (int ks = 0; ks < 4; ks++)
                             mma_bf16(tmem + (2 + m) * NC, v + 128 * ks, pt + 2 * ks, id, (first && ks == 0) ? 0u : 1u);
                     }
-                    mma_commit(&S.pair_empty[slot]);
+                    PAIR ? mma_commit_multicast(&S.pair_empty[slot], 3) : mma_commit(&S.pair_empty[slot]);
                     if (++slot == (uint32_t)p.npair) slot = 0;
                 }
                 mma_commit(&S.p_empty[i & 1]);
@@ -513,7 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR)
+        cluster_sync();      // neither CTA ends while the other's copies or arrivals may still come
+    else
+        __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kCols);
@@ -521,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     if (tid == 0) a.cta_err[group * a.ctas + cta] = S.gave_up;
 }
 
-template <int NC>
+template <int NC, bool PAIR>
 cudaError_t run(Params& p, cudaStream_t st)
 {
     const int blocks = p.nb + (p.a.s.dr > 0 ? 1 : 0);
@@ -536,10 +565,21 @@ cudaError_t run(Params& p, cudaStream_t st)
     p.q_off = p.rope_off + p.nrope * kBlockBytes;
     p.p_off = p.q_off + q;
     const size_t bytes = 1024 + p.p_off + pp;
-    const cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<NC, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    decode_tc_kernel<NC><<<dim3(p.a.ctas, p.a.groups), kThreads, bytes, st>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.a.ctas, p.a.groups);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1;
+    attr.val.clusterDim.y = 2;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, decode_tc_kernel<NC, PAIR>, p);
 }
 
 }  // namespace
@@ -564,7 +604,13 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st)
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    return a.rows <= 16 ? run<16>(p, st) : a.rows <= 32 ? run<32>(p, st) : a.rows <= 48 ? run<48>(p, st) : run<64>(p, st);
+    if (a.groups == 1)
+        return a.rows <= 16   ? run<16, false>(p, st)
+               : a.rows <= 32 ? run<32, false>(p, st)
+               : a.rows <= 48 ? run<48, false>(p, st)
+                              : run<64, false>(p, st);
+    // two groups and more have more than 64 rows in all: at least 33 each
+    return a.rows <= 48 ? run<48, true>(p, st) : run<64, true>(p, st);
 }
 
 }  // namespace mla

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
 #pragma unroll
                 for (int c = 0; c < KB; c++) steps[c] = c < p.nb ? (min(64, s.dn - 64 * c) + 15) >> 4 : (s.dr + 15) >> 4;
                 auto scores = [&](int t, int st) {
-                    const uint64_t q = kmajor + ((qs + t * KB * kBlock) >> 4), k = kmajor + ((ks + st * KB * kBlock) >> 4);
+                    const uint64_t q = kmajor + at_desc(qs + t * KB * kBlock), k = kmajor + at_desc(ks + st * KB * kBlock);
 #pragma unroll
                     for (int c = 0; c < KB; c++)
 #pragma unroll
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
 #pragma unroll
                     for (int t = 0; t < 2; t++)
                         if (j < nt[t]) {
-                            const uint64_t v = vmajor + ((vs + vst * p.vb * kBlock) >> 4);
+                            const uint64_t v = vmajor + at_desc(vs + vst * p.vb * kBlock);
 #pragma unroll
                             for (int half = 0; half < 2; half++) {
                                 wait_for(&S.p_full[t][half], j & 1, gave_up);
