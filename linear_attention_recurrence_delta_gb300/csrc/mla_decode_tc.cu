@@ -27,7 +27,8 @@ constexpr float kSlack = 16.f;          // log2 by which a score may exceed the 
 
 struct Params {
     DecodeArgs a;
-    CUtensorMap map;
+    CUtensorMap map, qc, qr;     // the cache; the queries as rows (b, t, h), where their strides allow that
+    int q_tma;
     int nb, np;                  // 64-column blocks of the latent, pairs of them
     int npair, nrope;            // ring sizes
     int box;                     // rows of a TMA box: divides the page and the tile
@@ -123,7 +124,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     } else if (warp == 1) {
         tmem_alloc(&S.tmem, kCols);
     } else if (warp == 3) {
-        if (elect_one()) tma_prefetch_desc(&p.map);
+        if (elect_one()) {
+            tma_prefetch_desc(&p.map);
+            if (p.q_tma) {
+                tma_prefetch_desc(&p.qc);
+                if (rope) tma_prefetch_desc(&p.qr);
+            }
+        }
     } else if (tid == 64) {
         for (int i = 0; i < kMaxPairs; i++) {
             mbar_init(&S.pair_full[i], 1);
@@ -133,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             mbar_init(&S.rope_full[i], 1);
             mbar_init(&S.rope_empty[i], PAIR ? 2 : 1);
         }
-        mbar_init(&S.q_full, 32);
+        mbar_init(&S.q_full, p.q_tma ? 1 : 32);
         mbar_init(&S.q_empty, 1);
         for (int i = 0; i < 2; i++) {
             mbar_init(&S.s_full[i], 1);
@@ -511,9 +518,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         // ------------------------------------------------------------ queries: [query rows][64 columns] blocks
         const int col = (lane & 7) * 8;
         Run r(deal, S.b, S.tile, total);
-        uint32_t piece = 0;
+        uint32_t piece = 0, loaded = ~0u;
         for (int i = 0; i < total;) {
             if (piece > 0) wait_for(&S.q_empty, (piece - 1) & 1, gave_up);
+            if (p.q_tma) {
+                // rows past the group's are another's: their scores and outputs are columns that nobody reads
+                __syncwarp();
+                if (elect_one() && !*gave_up) {
+                    const int from = r.b * s.T * s.H + row0;
+                    mbar_arrive_expect_tx(&S.q_full, (p.nb + (rope ? 1 : 0)) * NC * 128);
+                    for (int k = 0; k < p.nb; k++) tma_load_2d(qs + k * NC * 128, &p.qc, &S.q_full, 64 * k, from);
+                    if (rope) tma_load_2d(qs + p.nb * NC * 128, &p.qr, &S.q_full, 0, from);
+                    loaded = piece;
+                }
+                piece++;
+                do i++;
+                while (!r.step() && i < total);
+                continue;
+            }
             for (int n = lane >> 3; n < NC; n += 4) {    // past the rows or the width: zeros
                 const bool row = n < rows;
                 const int tt = row ? (row0 + n) / s.H : 0, h = row ? row0 + n - tt * s.H : 0;
@@ -537,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             do i++;
             while (!r.step() && i < total);
         }
+        if (loaded != ~0u && *gave_up) mbar_wait(&S.q_full, loaded & 1, nullptr, kWaitNs);   // the copy in flight lands
     }
     tc_fence_before();
     if (PAIR)
@@ -595,22 +618,17 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st)
     p.box = 8;
     while (p.box < kDecodeTile && s.page % (2 * p.box) == 0) p.box *= 2;
     p.total_rows = s.npages * s.page;
-    const fwdtc::EncodeTiledFn enc = fwdtc::get_encode();
-    if (!enc) return cudaErrorNotSupported;
     const int W = s.dc + s.dr;
-    const cuuint64_t dims[2] = {(cuuint64_t)W, (cuuint64_t)p.total_rows}, strides[1] = {(cuuint64_t)W * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)p.box}, one[2] = {1, 1};
-    if (enc(&p.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.cache), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    p.q_tma = a.qc.tok == (long long)s.H * a.qc.head && (s.dr == 0 || a.qr.tok == (long long)s.H * a.qr.head) &&
+              (long long)s.B * s.T * s.H < 0x7fffffffLL;
+    const int nc = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 48 ? 48 : 64;
+    if (!row_map(&p.map, a.cache, (long long)W, p.total_rows, W, p.box) ||
+        (p.q_tma && (!row_map(&p.qc, a.qc.p, a.qc.head, (long long)s.B * s.T * s.H, s.dc, nc) ||
+                     (s.dr > 0 && !row_map(&p.qr, a.qr.p, a.qr.head, (long long)s.B * s.T * s.H, s.dr, nc)))))
         return cudaErrorInvalidValue;
-    if (a.groups == 1)
-        return a.rows <= 16   ? run<16, false>(p, st)
-               : a.rows <= 32 ? run<32, false>(p, st)
-               : a.rows <= 48 ? run<48, false>(p, st)
-                              : run<64, false>(p, st);
+    if (a.groups == 1) return nc == 16 ? run<16, false>(p, st) : nc == 32 ? run<32, false>(p, st) : nc == 48 ? run<48, false>(p, st) : run<64, false>(p, st);
     // two groups and more have more than 64 rows in all: at least 33 each
-    return a.rows <= 48 ? run<48, true>(p, st) : run<64, true>(p, st);
+    return nc == 48 ? run<48, true>(p, st) : run<64, true>(p, st);
 }
 
 }  // namespace mla

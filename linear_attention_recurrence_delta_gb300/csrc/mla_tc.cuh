@@ -206,5 +206,17 @@ inline bool view_map(CUtensorMap* m, const gdn_mla_view_t& v, long long n, int h
            CUDA_SUCCESS;
 }
 
+// rows [n, d] with a row stride in elements -> 2-D map, box 64 x box_rows, 128-byte swizzle
+inline bool row_map(CUtensorMap* m, const void* base, long long stride, long long n, int d, int box_rows)
+{
+    const fwdtc::EncodeTiledFn enc = fwdtc::get_encode();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)n}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace mla
 }  // namespace gdn

@@ -134,3 +134,15 @@ def test_long_cache_offsets(past):
     qc, qr = normal(g, (1, 1, H, dc), "bf16", 0.5), normal(g, (1, 1, H, dr), "bf16")
     o, _ = call(n, 1, H, dc, dr, page, "bf16", table, pages, cache, qc, qr, 0.1)
     close(o[0], decode_ref(qc[0], qr[0], data.flatten(0, 1)[:130], 0.1)[0], "bf16", "fwd", "o")
+
+
+@pytest.mark.parametrize("T,H", [(2, 6), (4, 40)])
+def test_some_heads_of_a_wider_query(T, H):
+    """Queries that are the first heads of a tensor with more: rows of one token lie apart from the next one's."""
+    n, dc, dr, page = [500, 77, 130], 128, 64, 32
+    table, pages, cache, rows, qc, qr = setup(8, n, T, H, dc, dr, page, "bf16")
+    a = call(n, T, H, dc, dr, page, "bf16", table, pages, cache, qc, qr, 0.1)
+    wide = torch.full((3, T, H + 3, dc + dr), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:, :, :H, :dc], wide[:, :, :H, dc:] = qc.cuda(), qr.cuda()
+    b = call(n, T, H, dc, dr, page, "bf16", table, pages, cache, wide[:, :, :H, :dc], wide[:, :, :H, dc:], 0.1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
