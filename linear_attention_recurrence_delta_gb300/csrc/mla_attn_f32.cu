@@ -1,8 +1,10 @@
 // mla_attn_f32.cu -- attention over expanded keys and values on the CUDA cores: the form for f32 I/O.
 //
-// A CTA holds 64 queries (or, for the key gradients, 64 keys) and walks the other side in tiles of 64 through shared
-// memory; each of 256 threads owns a 4 x 4 block of a 64 x 64 score tile and 4 rows of the results.  fp32 FMAs bound
-// it: tf32 products would be faster but keep 10 bits.
+// A CTA holds 16 RI queries (or, for the key gradients, keys) and walks the other side in tiles of 64 rows through
+// shared memory, the next tile on its way by cp.async where two fit; each of 256 threads owns an RI x 4 block of a
+// score tile and RI rows of the results.  fp32 FMAs bound it: tf32 products would be faster but keep 10 bits.
+// RI is as large as leaves every SM a CTA: four rows a thread reuse each operand from shared memory four times, but a
+// small batch then fills a fraction of the SMs (times at both ends at pick_rows below).
 #include "mla_internal.h"
 
 namespace gdn {
@@ -12,85 +14,107 @@ namespace {
 
 constexpr int kThreads = 256, kTile = 64, kSP = kTile + 4;   // row pitch = 4 mod 32 words: 16-byte reads of
                                                              // consecutive rows meet no bank twice
+constexpr size_t kRoom = 227 * 1024;
 
 __host__ __device__ inline int pitch_of(int d) { return (d + 63) / 64 * 64 + 4; }
 
-// rows [r0, r0 + 64) of a tensor given as a main part of width d1 and a shared part of width d2 behind it; rows past
-// n and columns past d1 + d2 as zeros
-__device__ __forceinline__ void load_tile(float* s, int pitch, const float* a, long long tok_a, int d1, const float* b,
-                                          long long tok_b, int d2, int r0, int n)
+template <int BYTES>
+__device__ __forceinline__ void copy_async(float* dst, const float* src, bool in)
 {
-    const int per = (pitch - 4) >> 3;
-    for (int i = threadIdx.x; i < kTile * per; i += kThreads) {
-        const int r = i / per, c = (i - r * per) << 3;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (r0 + r < n) {
-            if (c < d1)
-                load8(a + (long long)(r0 + r) * tok_a + c, x);
-            else if (c < d1 + d2)
-                load8(b + (long long)(r0 + r) * tok_b + (c - d1), x);
-        }
-        store8(s + r * pitch + c, x);
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst), n = in ? BYTES : 0;
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// asks for rows [r0, r0 + ROWS) of a tensor given as a main part of width d1 and a shared part of width d2 behind it;
+// rows past n and columns past d1 + d2 become zeros
+template <int ROWS>
+__device__ __forceinline__ void ask_tile(float* s, int pitch, const float* a, long long tok_a, int d1, const float* b,
+                                         long long tok_b, int d2, int r0, int n)
+{
+    const int per = (pitch - 4) >> 2;
+    for (int i = threadIdx.x; i < ROWS * per; i += kThreads) {
+        const int r = i / per, c = (i - r * per) << 2;
+        const bool row = r0 + r < n, first = c < d1, in = row && c < d1 + d2;
+        const float* src = first ? a + (long long)(r0 + r) * tok_a + c : b + (long long)(r0 + r) * tok_b + (c - d1);
+        copy_async<16>(s + r * pitch + c, in ? src : a, in);
     }
 }
 
-// acc[i][j] = A[4 ty + i] . B[tx + 16 j]
-__device__ __forceinline__ void dots(float (&acc)[4][4], const float* A, const float* B, int pitch, int d, int ty, int tx)
+// acc[i][j] = A[RA ty + i] . B[tx + 16 j]
+template <int RA, int RB>
+__device__ __forceinline__ void dots(float (&acc)[RA][RB], const float* A, const float* B, int pitch, int d, int ty, int tx)
 {
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < RA; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) acc[i][j] = 0.f;
+        for (int j = 0; j < RB; j++) acc[i][j] = 0.f;
+#pragma unroll 2
     for (int c = 0; c < d; c += 4) {
-        float4 x[4], y[4];
+        float4 x[RA], y[RB];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            x[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * pitch + c);
-            y[i] = *reinterpret_cast<const float4*>(B + (tx + 16 * i) * pitch + c);
-        }
+        for (int i = 0; i < RA; i++) x[i] = *reinterpret_cast<const float4*>(A + (RA * ty + i) * pitch + c);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int j = 0; j < RB; j++) y[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * pitch + c);
 #pragma unroll
-            for (int j = 0; j < 4; j++)
+        for (int i = 0; i < RA; i++)
+#pragma unroll
+            for (int j = 0; j < RB; j++)
                 acc[i][j] += x[i].x * y[j].x + x[i].y * y[j].y + x[i].z * y[j].z + x[i].w * y[j].w;
     }
 }
 
-// acc[i][4 j + e] += sum_k P[k][4 ty + i] (TRANSPOSED) or P[4 ty + i][k] times B[k][64 j + 4 tx + e]
-template <bool TRANSPOSED, int NJ>
-__device__ __forceinline__ void accumulate(float (&acc)[4][4 * NJ], const float* P, const float* B, int pitch, int nj,
-                                           int ty, int tx)
+// acc[i][4 j + e] += sum_k P(k, RI ty + i) B[k][64 j + 4 tx + e] over 64 rows of B; P is stored a held row after another
+// (pitch kSP), or TRANSPOSED a walked row after another (pitch 16 RI + 4)
+template <bool TRANSPOSED, int RI, int NJ>
+__device__ __forceinline__ void accumulate(float (&acc)[RI][4 * NJ], const float* P, const float* B, int pitch, int nj, int ty,
+                                           int tx)
 {
-    for (int k = 0; k < kTile; k++) {
-        float p[4];
+#pragma unroll 2
+    for (int k = 0; k < kTile; k += 4) {
+        float p[RI][4];
         if (TRANSPOSED) {
-            const float4 v = *reinterpret_cast<const float4*>(P + k * kSP + 4 * ty);
-            p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+#pragma unroll
+                for (int i = 0; i < RI; i++) p[i][e] = P[(k + e) * (16 * RI + 4) + RI * ty + i];
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; i++) p[i] = P[(4 * ty + i) * kSP + k];
+            for (int i = 0; i < RI; i++)
+                *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(P + (RI * ty + i) * kSP + k);
         }
 #pragma unroll
         for (int j = 0; j < NJ; j++)
             if (j < nj) {
-                const float4 b = *reinterpret_cast<const float4*>(B + k * pitch + 64 * j + 4 * tx);
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    acc[i][4 * j] += p[i] * b.x;
-                    acc[i][4 * j + 1] += p[i] * b.y;
-                    acc[i][4 * j + 2] += p[i] * b.z;
-                    acc[i][4 * j + 3] += p[i] * b.w;
+                for (int e = 0; e < 4; e++) {
+                    const float4 b = *reinterpret_cast<const float4*>(B + (k + e) * pitch + 64 * j + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < RI; i++) {
+                        acc[i][4 * j] += p[i][e] * b.x;
+                        acc[i][4 * j + 1] += p[i][e] * b.y;
+                        acc[i][4 * j + 2] += p[i][e] * b.z;
+                        acc[i][4 * j + 3] += p[i][e] * b.w;
+                    }
                 }
             }
     }
 }
 
-__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d)
+__device__ __forceinline__ void store4(float* p, const float* v, float f)
 {
-    *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+    *reinterpret_cast<float4*>(p) = make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
 }
 
-// reduction over the 16 threads that share four rows
+// reduction over the 16 threads that share rows
 __device__ __forceinline__ float row_max(float x)
 {
 #pragma unroll
@@ -110,217 +134,271 @@ __device__ __forceinline__ float* head_of(const gdn_mla_view_t& v, int first, in
     return (float*)v.p + (long long)first * v.tok + (long long)h * v.head;
 }
 
-__global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a)
+// The walk over `n` tiles: ask(i, buffer) requests tile i, work(i, buffer) uses it.  stages: 1 or 2 buffers.
+template <typename Ask, typename Work>
+__device__ __forceinline__ void walk(int n, int stages, Ask ask, Work work)
+{
+    if (n > 0) ask(0, 0);
+    copies_commit();
+    for (int i = 0; i < n; i++) {
+        const int buf = stages == 2 ? i & 1 : 0;
+        if (stages == 2 && i + 1 < n) {
+            ask(i + 1, buf ^ 1);
+            copies_commit();
+            copies_wait<1>();
+        } else {
+            copies_wait<0>();
+        }
+        __syncthreads();
+        work(i, buf);
+        __syncthreads();
+        if (stages == 1 && i + 1 < n) {
+            ask(i + 1, 0);
+            copies_commit();
+        }
+    }
+}
+
+template <int RI>
+__global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a, int stages)
 {
     extern __shared__ float smem[];
+    constexpr int kHeld = 16 * RI;
     const gdn_mla_attn_t& s = a.s;
-    const int h = blockIdx.y, b = blockIdx.z, g = h / (s.H / s.Hkv), q0 = blockIdx.x * kTile;
+    const int h = blockIdx.y, b = blockIdx.z, g = h / (s.H / s.Hkv), q0 = blockIdx.x * kHeld;
     const Rows rq = rows_of(a.cu_q, b, s.Tq, s.Nq), rk = rows_of(a.cu_k, b, s.Tk, s.Nk);
     if (q0 >= rq.n) return;
     const int d = s.dn + s.dr, pq = pitch_of(d), pv = pitch_of(s.dv), nj = (s.dv + 63) >> 6;
-    float *Q = smem, *K = Q + kTile * pq, *V = K + kTile * pq, *P = V + kTile * pv;
+    float *Q = smem, *P = Q + kHeld * pq, *K = P + kHeld * kSP, *V = K + stages * kTile * pq;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int off = rk.n - rq.n;
-    const int end = s.causal ? min(rk.n, min(q0 + kTile, rq.n) + off) : rk.n;
-    load_tile(Q, pq, head_of(a.qn, rq.first, h), a.qn.tok, s.dn, head_of(a.qr, rq.first, h), a.qr.tok, s.dr, q0,
-                 rq.n);
-    float m[4], l[4], o[4][8];
+    const int end = s.causal ? min(rk.n, min(q0 + kHeld, rq.n) + off) : rk.n;
+    ask_tile<kHeld>(Q, pq, head_of(a.qn, rq.first, h), a.qn.tok, s.dn, head_of(a.qr, rq.first, h), a.qr.tok, s.dr, q0, rq.n);
+    float m[RI], l[RI], o[RI][8];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < RI; i++) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; j++) o[i][j] = 0.f;
     }
-    for (int k0 = 0; k0 < end; k0 += kTile) {
-        __syncthreads();
-        load_tile(K, pq, head_of(a.kn, rk.first, g), a.kn.tok, s.dn, head_of(a.kr, rk.first, 0), a.kr.tok, s.dr, k0,
-                     rk.n);
-        load_tile(V, pv, head_of(a.v, rk.first, g), a.v.tok, s.dv, (const float*)nullptr, 0, 0, k0, rk.n);
-        __syncthreads();
-        float x[4][4];
-        dots(x, Q, K, pq, d, ty, tx);
+    const auto ask = [&](int t, int buf) {
+        ask_tile<kTile>(K + buf * kTile * pq, pq, head_of(a.kn, rk.first, g), a.kn.tok, s.dn, head_of(a.kr, rk.first, 0), a.kr.tok,
+                        s.dr, t * kTile, rk.n);
+        ask_tile<kTile>(V + buf * kTile * pv, pv, head_of(a.v, rk.first, g), a.v.tok, s.dv, head_of(a.v, rk.first, g), 0, 0,
+                        t * kTile, rk.n);
+    };
+    const auto work = [&](int t, int buf) {
+        const int k0 = t * kTile;
+        float x[RI][4];
+        dots<RI, 4>(x, Q, K + buf * kTile * pq, pq, d, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int last = s.causal ? min(rk.n - 1, q0 + 4 * ty + i + off) : rk.n - 1;
-            float t = m[i];
+        for (int i = 0; i < RI; i++) {
+            const int last = s.causal ? min(rk.n - 1, q0 + RI * ty + i + off) : rk.n - 1;
+            float top = m[i];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 x[i][j] = k0 + tx + 16 * j <= last ? x[i][j] * s.scale : -INFINITY;
-                t = fmaxf(t, x[i][j]);
+                top = fmaxf(top, x[i][j]);
             }
-            t = row_max(t);
-            const float base = t == -INFINITY ? 0.f : t, keep = expf(m[i] - base);
-            m[i] = t;
+            top = row_max(top);
+            const float base = top == -INFINITY ? 0.f : top, keep = expf(m[i] - base);
+            m[i] = top;
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 x[i][j] = expf(x[i][j] - base);
                 sum += x[i][j];
-                P[(4 * ty + i) * kSP + tx + 16 * j] = x[i][j];
+                P[(RI * ty + i) * kSP + tx + 16 * j] = x[i][j];
             }
             l[i] = l[i] * keep + row_sum(sum);
 #pragma unroll
             for (int j = 0; j < 8; j++) o[i][j] *= keep;
         }
-        __syncthreads();
-        accumulate<false, 2>(o, P, V, pv, nj, ty, tx);
-    }
+        __syncwarp();     // a row's weights come from its own 16 threads
+        accumulate<false, RI, 2>(o, P, V + buf * kTile * pv, pv, nj, ty, tx);
+    };
+    walk((max(end, 0) + kTile - 1) / kTile, stages, ask, work);
     float* out = (float*)a.o + ((long long)rq.first * s.H + h) * s.dv;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = q0 + 4 * ty + i;
+    for (int i = 0; i < RI; i++) {
+        const int r = q0 + RI * ty + i;
         if (r >= rq.n) continue;
-        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-        if (tx == 0 && a.lse) a.lse[(long long)h * s.Nq + rq.first + r] = l[i] > 0.f ? m[i] + logf(l[i]) : -INFINITY;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        if (tx == 0 && a.lse) a.lse[(long long)h * s.Nq + rq.first + r] = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
 #pragma unroll
         for (int j = 0; j < 2; j++) {
             const int c = 64 * j + 4 * tx;
-            if (c < s.dv)
-                store4(out + (long long)r * s.H * s.dv + c, o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
-                       o[i][4 * j + 3] * inv);
+            if (c < s.dv) store4(out + (long long)r * s.H * s.dv + c, &o[i][4 * j], inv);
         }
     }
 }
 
-// p and ds = p (dO . v - delta) scale of one thread's 4 x 4 block of a tile; zero where the query does not see the key
-__device__ __forceinline__ void grads(float (&x)[4][4], float (&y)[4][4], const AttnArgs& a, const Rows& rq, const Rows& rk, int h,
-                                      int q0, int k0, int ty, int tx)
+// p = exp(scale s - lse) and ds = p (dp - delta) for one pair; zero where the query does not see the key
+__device__ __forceinline__ void pair_grads(float& x, float& y, float scale, float lse, float delta, int key, int last)
 {
-    const gdn_mla_attn_t& s = a.s;
-    const int off = rk.n - rq.n;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = q0 + 4 * ty + i;
-        const int last = r >= rq.n ? -1 : s.causal ? min(rk.n - 1, r + off) : rk.n - 1;
-        const long long at = (long long)h * s.Nq + rq.first + min(r, rq.n - 1);
-        const float lse = a.lse[at], delta = a.delta[at];
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const bool seen = k0 + tx + 16 * j <= last;
-            x[i][j] = seen ? expf(x[i][j] * s.scale - lse) : 0.f;
-            // a query that sees one key has a constant weight: zero, not the difference of two roundings
-            y[i][j] = seen && last > 0 ? x[i][j] * (y[i][j] - delta) * s.scale : 0.f;
-        }
-    }
+    const bool seen = key <= last;
+    x = seen ? expf(x * scale - lse) : 0.f;
+    // a query that sees one key has a constant weight: zero, not the difference of two roundings
+    y = seen && last > 0 ? x * (y - delta) : 0.f;
 }
 
-__global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a)
+template <int RI>
+__global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, int stages)
 {
     extern __shared__ float smem[];
+    constexpr int kHeld = 16 * RI;
     const gdn_mla_attn_t& s = a.s;
-    const int h = blockIdx.y, b = blockIdx.z, g = h / (s.H / s.Hkv), q0 = blockIdx.x * kTile;
+    const int h = blockIdx.y, b = blockIdx.z, g = h / (s.H / s.Hkv), q0 = blockIdx.x * kHeld;
     const Rows rq = rows_of(a.cu_q, b, s.Tq, s.Nq), rk = rows_of(a.cu_k, b, s.Tk, s.Nk);
     if (q0 >= rq.n) return;
     const int d = s.dn + s.dr, pq = pitch_of(d), pv = pitch_of(s.dv), nj = (d + 63) >> 6;
-    float *Q = smem, *K = Q + kTile * pq, *V = K + kTile * pq, *D = V + kTile * pv, *S = D + kTile * pv;
+    float *Q = smem, *D = Q + kHeld * pq, *S = D + kHeld * pv, *K = S + kHeld * kSP, *V = K + stages * kTile * pq;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const int end = s.causal ? min(rk.n, min(q0 + kTile, rq.n) + rk.n - rq.n) : rk.n;
-    load_tile(Q, pq, head_of(a.qn, rq.first, h), a.qn.tok, s.dn, head_of(a.qr, rq.first, h), a.qr.tok, s.dr, q0,
-                 rq.n);
-    load_tile(D, pv, (const float*)a.dO + ((long long)rq.first * s.H + h) * s.dv, (long long)s.H * s.dv, s.dv,
-                 (const float*)nullptr, 0, 0, q0, rq.n);
-    float dq[4][12] = {};
-    for (int k0 = 0; k0 < end; k0 += kTile) {
-        __syncthreads();
-        load_tile(K, pq, head_of(a.kn, rk.first, g), a.kn.tok, s.dn, head_of(a.kr, rk.first, 0), a.kr.tok, s.dr, k0,
-                     rk.n);
-        load_tile(V, pv, head_of(a.v, rk.first, g), a.v.tok, s.dv, (const float*)nullptr, 0, 0, k0, rk.n);
-        __syncthreads();
-        float x[4][4], y[4][4];
-        dots(x, Q, K, pq, d, ty, tx);
-        dots(y, D, V, pv, s.dv, ty, tx);
-        grads(x, y, a, rq, rk, h, q0, k0, ty, tx);
+    const int off = rk.n - rq.n, end = s.causal ? min(rk.n, min(q0 + kHeld, rq.n) + off) : rk.n;
+    const float* dO = (const float*)a.dO + ((long long)rq.first * s.H + h) * s.dv;
+    ask_tile<kHeld>(Q, pq, head_of(a.qn, rq.first, h), a.qn.tok, s.dn, head_of(a.qr, rq.first, h), a.qr.tok, s.dr, q0, rq.n);
+    ask_tile<kHeld>(D, pv, dO, (long long)s.H * s.dv, s.dv, dO, 0, 0, q0, rq.n);
+    float lse[RI], delta[RI], dq[RI][12] = {};
+    int last[RI];
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int j = 0; j < 4; j++) S[(4 * ty + i) * kSP + tx + 16 * j] = y[i][j];
-        __syncthreads();
-        accumulate<false, 3>(dq, S, K, pq, nj, ty, tx);
+    for (int i = 0; i < RI; i++) {
+        const int r = q0 + RI * ty + i;
+        const long long at = (long long)h * s.Nq + rq.first + min(r, rq.n - 1);
+        lse[i] = a.lse[at];
+        delta[i] = a.delta[at];
+        last[i] = r >= rq.n ? -1 : s.causal ? min(rk.n - 1, r + off) : rk.n - 1;
     }
-    float *on = head_of(a.dqn, rq.first, h), *orr = head_of(a.dqr, rq.first, h);
+    const auto ask = [&](int t, int buf) {
+        ask_tile<kTile>(K + buf * kTile * pq, pq, head_of(a.kn, rk.first, g), a.kn.tok, s.dn, head_of(a.kr, rk.first, 0), a.kr.tok,
+                        s.dr, t * kTile, rk.n);
+        ask_tile<kTile>(V + buf * kTile * pv, pv, head_of(a.v, rk.first, g), a.v.tok, s.dv, head_of(a.v, rk.first, g), 0, 0,
+                        t * kTile, rk.n);
+    };
+    const auto work = [&](int t, int buf) {
+        float x[RI][4], y[RI][4];
+        dots<RI, 4>(x, Q, K + buf * kTile * pq, pq, d, ty, tx);
+        dots<RI, 4>(y, D, V + buf * kTile * pv, pv, s.dv, ty, tx);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = q0 + 4 * ty + i;
+        for (int i = 0; i < RI; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                pair_grads(x[i][j], y[i][j], s.scale, lse[i], delta[i], t * kTile + tx + 16 * j, last[i]);
+                S[(RI * ty + i) * kSP + tx + 16 * j] = y[i][j];
+            }
+        __syncwarp();
+        accumulate<false, RI, 3>(dq, S, K + buf * kTile * pq, pq, nj, ty, tx);
+    };
+    walk((max(end, 0) + kTile - 1) / kTile, stages, ask, work);
+    float *on = head_of(a.dqn, rq.first, h), *op = head_of(a.dqr, rq.first, h);
+#pragma unroll
+    for (int i = 0; i < RI; i++) {
+        const int r = q0 + RI * ty + i;
         if (r >= rq.n) continue;
 #pragma unroll
         for (int j = 0; j < 3; j++) {
             const int c = 64 * j + 4 * tx;
-            const float* v = &dq[i][4 * j];
             if (c < s.dn)
-                store4(on + (long long)r * a.dqn.tok + c, v[0], v[1], v[2], v[3]);
+                store4(on + (long long)r * a.dqn.tok + c, &dq[i][4 * j], s.scale);
             else if (c < d)
-                store4(orr + (long long)r * a.dqr.tok + (c - s.dn), v[0], v[1], v[2], v[3]);
+                store4(op + (long long)r * a.dqr.tok + (c - s.dn), &dq[i][4 * j], s.scale);
         }
     }
 }
 
-__global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a)
+template <int RI>
+__global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, int stages)
 {
     extern __shared__ float smem[];
+    constexpr int kHeld = 16 * RI, kPP = kHeld + 4;
     const gdn_mla_attn_t& s = a.s;
-    const int g = blockIdx.y, b = blockIdx.z, G = s.H / s.Hkv, k0 = blockIdx.x * kTile;
+    const int g = blockIdx.y, b = blockIdx.z, G = s.H / s.Hkv, k0 = blockIdx.x * kHeld;
     const Rows rq = rows_of(a.cu_q, b, s.Tq, s.Nq), rk = rows_of(a.cu_k, b, s.Tk, s.Nk);
     if (k0 >= rk.n) return;
     const int d = s.dn + s.dr, pq = pitch_of(d), pv = pitch_of(s.dv), njk = (d + 63) >> 6, njv = (s.dv + 63) >> 6;
-    float *Q = smem, *K = Q + kTile * pq, *V = K + kTile * pq, *D = V + kTile * pv, *P = D + kTile * pv,
-          *S = P + kTile * kSP;
+    float *K = smem, *V = K + kHeld * pq, *P = V + kHeld * pv, *S = P + kTile * kPP, *L = S + kTile * kPP,
+          *Q = L + stages * 2 * kTile, *D = Q + stages * kTile * pq;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    // the first query that sees key k0
-    const int first = s.causal ? max(0, k0 - (rk.n - rq.n)) / kTile * kTile : 0;
-    load_tile(K, pq, head_of(a.kn, rk.first, g), a.kn.tok, s.dn, head_of(a.kr, rk.first, 0), a.kr.tok, s.dr, k0, rk.n);
-    load_tile(V, pv, head_of(a.v, rk.first, g), a.v.tok, s.dv, (const float*)nullptr, 0, 0, k0, rk.n);
-    float dk[4][12] = {}, dv[4][8] = {};
-    for (int h = g * G; h < (g + 1) * G; h++)
-        for (int q0 = first; q0 < rq.n; q0 += kTile) {
-            __syncthreads();
-            load_tile(Q, pq, head_of(a.qn, rq.first, h), a.qn.tok, s.dn, head_of(a.qr, rq.first, h), a.qr.tok,
-                         s.dr, q0, rq.n);
-            load_tile(D, pv, (const float*)a.dO + ((long long)rq.first * s.H + h) * s.dv, (long long)s.H * s.dv, s.dv,
-                         (const float*)nullptr, 0, 0, q0, rq.n);
-            __syncthreads();
-            float x[4][4], y[4][4];
-            dots(x, Q, K, pq, d, ty, tx);
-            dots(y, D, V, pv, s.dv, ty, tx);
-            grads(x, y, a, rq, rk, h, q0, k0, ty, tx);
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    P[(4 * ty + i) * kSP + tx + 16 * j] = x[i][j];
-                    S[(4 * ty + i) * kSP + tx + 16 * j] = y[i][j];
-                }
-            __syncthreads();
-            accumulate<true, 2>(dv, P, D, pv, njv, ty, tx);
-            accumulate<true, 3>(dk, S, Q, pq, njk, ty, tx);
+    const int off = rk.n - rq.n;
+    const int first = s.causal ? max(0, k0 - off) / kTile : 0;      // the first tile whose queries see key k0
+    const int per = max(0, (rq.n + kTile - 1) / kTile - first);
+    ask_tile<kHeld>(K, pq, head_of(a.kn, rk.first, g), a.kn.tok, s.dn, head_of(a.kr, rk.first, 0), a.kr.tok, s.dr, k0, rk.n);
+    ask_tile<kHeld>(V, pv, head_of(a.v, rk.first, g), a.v.tok, s.dv, head_of(a.v, rk.first, g), 0, 0, k0, rk.n);
+    float dk[RI][12] = {}, dv[RI][8] = {};
+    const auto ask = [&](int t, int buf) {
+        const int h = g * G + t / per, q0 = (first + t % per) * kTile;
+        const float* dO = (const float*)a.dO + ((long long)rq.first * s.H + h) * s.dv;
+        ask_tile<kTile>(Q + buf * kTile * pq, pq, head_of(a.qn, rq.first, h), a.qn.tok, s.dn, head_of(a.qr, rq.first, h),
+                        a.qr.tok, s.dr, q0, rq.n);
+        ask_tile<kTile>(D + buf * kTile * pv, pv, dO, (long long)s.H * s.dv, s.dv, dO, 0, 0, q0, rq.n);
+        if (tid < 2 * kTile) {     // lse and delta of the tile's queries
+            const int r = q0 + (tid & (kTile - 1));
+            const float* src = (tid < kTile ? a.lse : a.delta) + (long long)h * s.Nq + rq.first;
+            copy_async<4>(L + buf * 2 * kTile + tid, src + min(r, rq.n - 1), r < rq.n);
         }
+    };
+    const auto work = [&](int t, int buf) {
+        const int q0 = (first + t % per) * kTile;
+        const float* lse = L + buf * 2 * kTile;
+        float x[4][RI], y[4][RI];
+        dots<4, RI>(x, Q + buf * kTile * pq, K, pq, d, ty, tx);
+        dots<4, RI>(y, D + buf * kTile * pv, V, pv, s.dv, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int r = q0 + 4 * ty + i;
+            const int last = r >= rq.n ? -1 : s.causal ? min(rk.n - 1, r + off) : rk.n - 1;
+            const float lr = lse[4 * ty + i], dr = lse[kTile + 4 * ty + i];
+#pragma unroll
+            for (int j = 0; j < RI; j++) {
+                pair_grads(x[i][j], y[i][j], s.scale, lr, dr, k0 + tx + 16 * j, last);
+                P[(4 * ty + i) * kPP + tx + 16 * j] = x[i][j];
+                S[(4 * ty + i) * kPP + tx + 16 * j] = y[i][j];
+            }
+        }
+        __syncthreads();
+        accumulate<true, RI, 2>(dv, P, D + buf * kTile * pv, pv, njv, ty, tx);
+        accumulate<true, RI, 3>(dk, S, Q + buf * kTile * pq, pq, njk, ty, tx);
+    };
+    walk(per * G, stages, ask, work);
     float *on = head_of(a.dkn, rk.first, g), *ov = head_of(a.dv, rk.first, g);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = k0 + 4 * ty + i;
+    for (int i = 0; i < RI; i++) {
+        const int r = k0 + RI * ty + i;
         if (r >= rk.n) continue;
 #pragma unroll
         for (int j = 0; j < 2; j++) {
             const int c = 64 * j + 4 * tx;
-            if (c < s.dv)
-                store4(ov + (long long)r * a.dv.tok + c, dv[i][4 * j], dv[i][4 * j + 1], dv[i][4 * j + 2], dv[i][4 * j + 3]);
+            if (c < s.dv) store4(ov + (long long)r * a.dv.tok + c, &dv[i][4 * j], 1.f);
         }
 #pragma unroll
         for (int j = 0; j < 3; j++) {
             const int c = 64 * j + 4 * tx;
-            const float* v = &dk[i][4 * j];
             if (c < s.dn)
-                store4(on + (long long)r * a.dkn.tok + c, v[0], v[1], v[2], v[3]);
+                store4(on + (long long)r * a.dkn.tok + c, &dk[i][4 * j], s.scale);
             else if (c < d)
-                store4(a.dkr_part + ((long long)g * s.Nk + rk.first + r) * s.dr + (c - s.dn), v[0], v[1], v[2], v[3]);
+                store4(a.dkr_part + ((long long)g * s.Nk + rk.first + r) * s.dr + (c - s.dn), &dk[i][4 * j], s.scale);
         }
     }
 }
 
-template <typename F>
-cudaError_t with_smem(F f, size_t bytes)
+// rows a thread for `rows` held rows in each of `units` (head, sequence) pairs
+int pick_rows(int rows, long long units)
 {
-    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    for (int r = 4; r > 1; r >>= 1)
+        if ((long long)((rows + 16 * r - 1) / (16 * r)) * units >= 152) return r;
+    return 1;
+}
+
+// launches kernel(a, stages) with as many buffers of the walked side as fit
+template <typename F>
+cudaError_t start(F kernel, const AttnArgs& a, dim3 grid, size_t held, size_t walked, cudaStream_t st)
+{
+    const int stages = (held + 2 * walked) * sizeof(float) <= kRoom ? 2 : 1;
+    const size_t bytes = (held + stages * walked) * sizeof(float);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, bytes, st>>>(a, stages);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -328,30 +406,31 @@ cudaError_t with_smem(F f, size_t bytes)
 cudaError_t launch_attn_f32(const AttnArgs& a, cudaStream_t st)
 {
     const gdn_mla_attn_t& s = a.s;
-    const int pq = pitch_of(s.dn + s.dr), pv = pitch_of(s.dv);
-    const size_t bytes = (size_t)kTile * (2 * pq + pv + kSP) * sizeof(float);
-    const cudaError_t e = with_smem(fwd_kernel, bytes);
-    if (e != cudaSuccess) return e;
-    fwd_kernel<<<dim3((s.Tq + kTile - 1) / kTile, s.H, s.B), kThreads, bytes, st>>>(a);
-    return cudaGetLastError();
+    const int pq = pitch_of(s.dn + s.dr), pv = pitch_of(s.dv), r = pick_rows(s.Tq, (long long)s.H * s.B), held = 16 * r;
+    const dim3 grid((s.Tq + held - 1) / held, s.H, s.B);
+    const size_t h = (size_t)held * (pq + kSP), w = (size_t)kTile * (pq + pv);
+    return r == 4 ? start(fwd_kernel<4>, a, grid, h, w, st) : r == 2 ? start(fwd_kernel<2>, a, grid, h, w, st) : start(fwd_kernel<1>, a, grid, h, w, st);
 }
 
 cudaError_t launch_attn_bwd_f32(const AttnArgs& a, cudaStream_t st)
 {
     const gdn_mla_attn_t& s = a.s;
     const int pq = pitch_of(s.dn + s.dr), pv = pitch_of(s.dv);
-    const size_t bytes = (size_t)kTile * (2 * pq + 2 * pv + 2 * kSP) * sizeof(float);
     cudaError_t e;
     if (s.Tq > 0) {
         if ((e = launch_delta(a, st)) != cudaSuccess) return e;
-        if ((e = with_smem(dq_kernel, bytes)) != cudaSuccess) return e;
-        dq_kernel<<<dim3((s.Tq + kTile - 1) / kTile, s.H, s.B), kThreads, bytes, st>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        const int r = pick_rows(s.Tq, (long long)s.H * s.B), held = 16 * r;
+        const dim3 grid((s.Tq + held - 1) / held, s.H, s.B);
+        const size_t h = (size_t)held * (pq + pv + kSP), w = (size_t)kTile * (pq + pv);
+        e = r == 4 ? start(dq_kernel<4>, a, grid, h, w, st) : r == 2 ? start(dq_kernel<2>, a, grid, h, w, st) : start(dq_kernel<1>, a, grid, h, w, st);
+        if (e != cudaSuccess) return e;
     }
     if (s.Tk > 0) {
-        if ((e = with_smem(dkv_kernel, bytes)) != cudaSuccess) return e;
-        dkv_kernel<<<dim3((s.Tk + kTile - 1) / kTile, s.Hkv, s.B), kThreads, bytes, st>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        const int r = pick_rows(s.Tk, (long long)s.Hkv * s.B), held = 16 * r;
+        const dim3 grid((s.Tk + held - 1) / held, s.Hkv, s.B);
+        const size_t h = (size_t)held * (pq + pv) + (size_t)2 * kTile * (held + 4), w = (size_t)kTile * (pq + pv + 2);
+        e = r == 4 ? start(dkv_kernel<4>, a, grid, h, w, st) : r == 2 ? start(dkv_kernel<2>, a, grid, h, w, st) : start(dkv_kernel<1>, a, grid, h, w, st);
+        if (e != cudaSuccess) return e;
         if (s.dr > 0) return launch_dkr(a, st);
     }
     return cudaSuccess;
