@@ -8,38 +8,50 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// delta[h, i] = dO[i, h] . o[i, h], a warp a row of one head
+// delta[h, i] = dO[i, h] . o[i, h]: 16 threads a row of one head (dv <= 128), kRows rows each with their loads in flight
+constexpr int kRows = 4;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) delta_kernel(const AttnArgs a)
 {
     const gdn_mla_attn_t& s = a.s;
-    const long long u = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (u >= (long long)s.Nq * s.H) return;
-    const int lane = threadIdx.x & 31;
-    float t = 0.f;
-    if (lane * 8 < s.dv) {
-        float x[8], y[8];
-        load8((const T*)a.o + u * s.dv + 8 * lane, x);
-        load8((const T*)a.dO + u * s.dv + 8 * lane, y);
+    const long long all = (long long)s.Nq * s.H, u0 = ((long long)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4)) * kRows;
+    const int c = 8 * (threadIdx.x & 15);
+    Raw8<T> x[kRows], y[kRows];
 #pragma unroll
-        for (int i = 0; i < 8; i++) t += x[i] * y[i];
+    for (int k = 0; k < kRows; k++)
+        if (u0 + k < all && c < s.dv) {
+            x[k] = raw8((const T*)a.o + (u0 + k) * s.dv + c);
+            y[k] = raw8((const T*)a.dO + (u0 + k) * s.dv + c);
+        }
+#pragma unroll
+    for (int k = 0; k < kRows; k++) {
+        float t = 0.f;
+        if (u0 + k < all && c < s.dv) {
+            float v[8], w[8];
+            values(x[k], v);
+            values(y[k], w);
+#pragma unroll
+            for (int i = 0; i < 8; i++) t += v[i] * w[i];
+        }
+#pragma unroll
+        for (int m = 8; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+        if (c == 0 && u0 + k < all) a.delta[(u0 + k) % s.H * s.Nq + (u0 + k) / s.H] = t;
     }
-#pragma unroll
-    for (int m = 8; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
-    if (lane == 0) a.delta[(u % s.H) * s.Nq + u / s.H] = t;
 }
 
 // dkr = the key heads' shares, added in the heads' order
+constexpr int kDkrThreads = 64;     // few rows: spread them over the SMs
 template <typename T>
-__global__ void __launch_bounds__(kThreads) dkr_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(kDkrThreads) dkr_kernel(const AttnArgs a)
 {
     const gdn_mla_attn_t& s = a.s;
     const Rows rk = rows_of(a.cu_k, blockIdx.y, s.Tk, s.Nk);
     const int per = s.dr >> 3;
-    const long long u = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const long long u = (long long)blockIdx.x * kDkrThreads + threadIdx.x;
     const int r = (int)(u / per), c = (int)(u - (long long)r * per) << 3;
     if (r >= rk.n) return;
     float t[8] = {};
+#pragma unroll 4
     for (int g = 0; g < s.Hkv; g++) {
         float x[8];
         load8(a.dkr_part + ((long long)g * s.Nk + rk.first + r) * s.dr + c, x);
@@ -54,7 +66,8 @@ __global__ void __launch_bounds__(kThreads) dkr_kernel(const AttnArgs a)
 cudaError_t launch_delta(const AttnArgs& a, cudaStream_t st)
 {
     const long long units = (long long)a.s.Nq * a.s.H;
-    const unsigned grid = (unsigned)((units + kThreads / 32 - 1) / (kThreads / 32));
+    const int each = kThreads / 16 * kRows;
+    const unsigned grid = (unsigned)((units + each - 1) / each);
     if (a.s.io == GDN_BF16)
         delta_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a);
     else
@@ -65,11 +78,11 @@ cudaError_t launch_delta(const AttnArgs& a, cudaStream_t st)
 cudaError_t launch_dkr(const AttnArgs& a, cudaStream_t st)
 {
     const long long units = (long long)a.s.Tk * (a.s.dr >> 3);
-    const dim3 grid((unsigned)((units + kThreads - 1) / kThreads), a.s.B);
+    const dim3 grid((unsigned)((units + kDkrThreads - 1) / kDkrThreads), a.s.B);
     if (a.s.io == GDN_BF16)
-        dkr_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a);
+        dkr_kernel<__nv_bfloat16><<<grid, kDkrThreads, 0, st>>>(a);
     else
-        dkr_kernel<float><<<grid, kThreads, 0, st>>>(a);
+        dkr_kernel<float><<<grid, kDkrThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
