@@ -16,16 +16,17 @@ namespace mla {
 
 namespace {
 
-constexpr int kThreads = 384, kTile = 128;
+constexpr int kTile = 128;
 constexpr uint32_t kBlock = 16384;      // 128 rows x 64 columns of bf16
 constexpr float kSlack = 8.f;           // log2 by which a score may exceed the maximum it is lowered by
 constexpr int kMaxStage = 3;
+constexpr int kShort = 1024;            // keys
 
 struct Params {
     AttnArgs a;
     CUtensorMap qn, qr, kn, kr, v;
     int nb, vb;                 // 64-column blocks of dn, dv
-    int tiles;                  // pairs of query tiles of the longest sequence
+    int tiles;                  // CTAs that the longest sequence's queries take
     uint32_t v_off;             // V's stages behind K's in shared memory
     int kstages, vstages;
 };
@@ -36,23 +37,24 @@ struct Shared {
     uint32_t tmem, gave_up;
 };
 
-// KB: 64-column blocks of a query or key (the position block among them)
-template <int KB>
-__global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_constant__ Params p)
+// KB: 64-column blocks of a query or key (the position block among them); NT: query tiles, 2 on an SM of its own or 1 on
+// half of one
+template <int KB, int NT>
+__global__ void __launch_bounds__(128 + 128 * NT, 3 - NT) fwd_tc_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ unsigned char raw[];
     __shared__ Shared S;
     const AttnArgs& a = p.a;
     const gdn_mla_attn_t& s = a.s;
     const int h = blockIdx.x % s.H, b = blockIdx.y, g = h / (s.H / s.Hkv);
-    const int q0 = (p.tiles - 1 - (int)(blockIdx.x / s.H)) * 2 * kTile;     // the longest walks first
+    const int q0 = (p.tiles - 1 - (int)(blockIdx.x / s.H)) * NT * kTile;     // the longest walks first
     const Rows rq = rows_of(a.cu_q, b, s.Tq, s.Nq), rk = rows_of(a.cu_k, b, s.Tk, s.Nk);
     if (q0 >= rq.n) return;
     const int off = rk.n - rq.n;
     // key tiles that each query tile sees
-    int nt[2];
+    int nt[2] = {0, 0};
 #pragma unroll
-    for (int t = 0; t < 2; t++) {
+    for (int t = 0; t < NT; t++) {
         const int first = q0 + t * kTile;
         const int end = s.causal ? min(rk.n, min(first + kTile, rq.n) + off) : rk.n;
         nt[t] = first < rq.n && end > 0 ? (end + kTile - 1) / kTile : 0;
@@ -60,7 +62,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
     const int n = max(nt[0], nt[1]);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    const uint32_t qs = smem_u32(sm), ks = qs + 2 * KB * kBlock, vs = qs + p.v_off;
+    const uint32_t qs = smem_u32(sm), ks = qs + NT * KB * kBlock, vs = qs + p.v_off;
 
     const bool rope = s.dr > 0;
     const bool ragged = rk.n % kTile != 0 && n == (rk.n + kTile - 1) / kTile;   // the last value tile has rows to blank
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
             }
         }
     } else if (warp == 1) {
-        tmem_alloc(&S.tmem, 512);
+        tmem_alloc(&S.tmem, 256 * NT);
     }
     tc_fence_before();
     __syncthreads();
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
     const uint32_t tmem = S.tmem;
     volatile uint32_t* gave_up = &S.gave_up;
     if (warp < 4) {
-        regs_down<80>();
+        regs_down<NT == 2 ? 88 : 64>();      // of 168 a thread in 384, or 128 in 256
         if (warp == 0) {
             if (elect_one() && n > 0) {
                 int klast = 0, vlast = 0, kst = 1 % p.kstages, vst = 1 % p.vstages;
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                 if (n > 0) {
                     wait_for(&S.k_full[0], 0, gave_up);
 #pragma unroll
-                    for (int t = 0; t < 2; t++)
+                    for (int t = 0; t < NT; t++)
                         if (nt[t]) {
                             wait_for(&S.q_full[t], 0, gave_up);
                             tc_fence_after();
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                         wait_for(&S.v_full[vst], vph, gave_up);
                     bool k_ready = false;
 #pragma unroll
-                    for (int t = 0; t < 2; t++)
+                    for (int t = 0; t < NT; t++)
                         if (j < nt[t]) {
                             const uint64_t v = vmajor + at_desc(vs + vst * p.vb * kBlock);
 #pragma unroll
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                                 if (!*gave_up) {
 #pragma unroll
                                     for (int e = 4 * half; e < 4 * half + 4; e++)
-                                        mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * e, v + 128 * e, id_o,
+                                        mma_bf16_ts(tmem + NT * 128 + t * 128, tmem + t * 128 + 8 * e, v + 128 * e, id_o,
                                                     (j | e) ? 1u : 0u);
                                 }
                             }
@@ -231,9 +233,9 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
             mbar_arrive(&S.v_fixed);
         }
     } else {
-        regs_up<208>();
+        regs_up<NT == 2 ? 208 : 192>();
         const int t = (warp - 4) >> 2, quad = warp & 3, row = q0 + t * kTile + quad * 32 + lane;
-        const uint32_t base = tmem + ((uint32_t)quad << 21), sa = base + t * 128, oa = base + 256 + t * 128;
+        const uint32_t base = tmem + ((uint32_t)quad << 21), sa = base + t * 128, oa = base + NT * 128 + t * 128;
         // scores times this are exponents of 2; a scale of zero keeps the masked ones' minus infinity
         const float c = fmaxf(s.scale * kLog2e, 1e-37f), slack = kSlack / c;
         const int last = row < rq.n ? (s.causal ? min(rk.n - 1, row + off) : rk.n - 1) : -1;
@@ -359,16 +361,17 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, 256 * NT);
     }
     if (tid == 0 && *gave_up) atomicExch(a.status, kDevTimeout);
 }
 
-template <int KB>
+template <int KB, int NT>
 cudaError_t run(Params& p, cudaStream_t st)
 {
     const gdn_mla_attn_t& s = p.a.s;
-    const uint32_t room = 232448 - 1024 - (uint32_t)sizeof(Shared) - 64, q = 2 * KB * kBlock;
+    // of the 228 KB an SM has, 1 KB goes with each CTA
+    const uint32_t room = 233472 / (3 - NT) - 1024 - 1024 - (uint32_t)sizeof(Shared) - 64, q = NT * KB * kBlock;
     p.kstages = p.vstages = 1;      // as many stages as fit, keys' first
     const auto total = [&] { return q + (uint32_t)(p.kstages * KB + p.vstages * p.vb) * kBlock; };
     for (int i = 0; i < 2; i++) {
@@ -376,10 +379,11 @@ cudaError_t run(Params& p, cudaStream_t st)
         if (p.vstages < kMaxStage && total() + p.vb * kBlock <= room) p.vstages++;
     }
     p.v_off = q + p.kstages * KB * kBlock;
+    p.tiles = (s.Tq + NT * kTile - 1) / (NT * kTile);
     const size_t bytes = 1024 + total();
-    const cudaError_t e = cudaFuncSetAttribute(fwd_tc_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const cudaError_t e = cudaFuncSetAttribute(fwd_tc_kernel<KB, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    fwd_tc_kernel<KB><<<dim3((unsigned)s.H * p.tiles, s.B), kThreads, bytes, st>>>(p);
+    fwd_tc_kernel<KB, NT><<<dim3((unsigned)s.H * p.tiles, s.B), 128 + 128 * NT, bytes, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -393,7 +397,6 @@ cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st)
     p.a = a;
     p.nb = (s.dn + 63) / 64;
     p.vb = (s.dv + 63) / 64;
-    p.tiles = (s.Tq + 2 * kTile - 1) / (2 * kTile);
     // without keys the maps have nothing to describe and no load is made
     if (!view_map(&p.qn, a.qn, s.Nq, s.H, s.dn, kTile) ||
         (s.dr > 0 && !view_map(&p.qr, a.qr, s.Nq, s.H, s.dr, kTile)) ||
@@ -401,7 +404,12 @@ cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st)
                       (s.dr > 0 && !view_map(&p.kr, a.kr, s.Nk, 1, s.dr, kTile)))))
         return cudaErrorInvalidValue;
     const int kb = p.nb + (s.dr > 0 ? 1 : 0);
-    return kb == 1 ? run<1>(p, st) : kb == 2 ? run<2>(p, st) : run<3>(p, st);
+    // One tile and two CTAs an SM for short walks, where a CTA's start and end weigh most and overlap the other's work;
+    // two tiles share each load of keys and values, which long walks need.
+    const bool single = kb < 3 && s.Tk <= kShort;
+    if (kb == 1) return single ? run<1, 1>(p, st) : run<1, 2>(p, st);
+    if (kb == 2) return single ? run<2, 1>(p, st) : run<2, 2>(p, st);
+    return run<3, 2>(p, st);     // three blocks of Q, K and V's leave no room for a second CTA
 }
 
 }  // namespace mla
