@@ -50,13 +50,14 @@ __device__ __forceinline__ uint4 pack8(const float* x, float f)
 // ================================================================ dQ: a tile of queries walks the keys
 
 struct SharedQ {
-    uint64_t q_full, do_full, k_full[2], k_empty[2], v_full[2], v_empty[2], k_last, k_fixed, s_full, s_read, dp_full, ds_full,
+    uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[2], v_empty[2], k_last, k_fixed, s_full, s_read, dp_full, ds_full,
         dq_full, drain;
     uint32_t tmem, gave_up;
 };
 
-// KB: 64-column blocks of a query or key (the position block among them); VS: stages of V
-template <int KB, int VS>
+// KB: 64-column blocks of a query or key (the position block among them); KS, VS: stages of K and V.  A key tile is held
+// from its scores to its share of dQ, a step later, so K needs three for a load to be ahead
+template <int KB, int KS, int VS>
 __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ unsigned char raw[];
@@ -72,13 +73,15 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     const int n = end > 0 ? (end + kTile - 1) / kTile : 0;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    const uint32_t qs = smem_u32(sm), dos = qs + KB * kBlock, ks = dos + p.vb * kBlock, vs = ks + 2 * KB * kBlock;
+    const uint32_t qs = smem_u32(sm), dos = qs + KB * kBlock, ks = dos + p.vb * kBlock, vs = ks + KS * KB * kBlock;
 
     if (warp == 0) {
         if (elect_one()) {
             for (uint64_t* x : {&S.q_full, &S.do_full, &S.k_last, &S.s_full, &S.dp_full, &S.dq_full, &S.drain}) mbar_init(x, 1);
-            for (int i = 0; i < 2; i++)
-                for (uint64_t* x : {&S.k_full[i], &S.k_empty[i], &S.v_full[i], &S.v_empty[i]}) mbar_init(x, 1);
+            for (int i = 0; i < KS; i++)
+                for (uint64_t* x : {&S.k_full[i], &S.k_empty[i]}) mbar_init(x, 1);
+            for (int i = 0; i < VS; i++)
+                for (uint64_t* x : {&S.v_full[i], &S.v_empty[i]}) mbar_init(x, 1);
             mbar_init(&S.k_fixed, 64);
             mbar_init(&S.s_read, 8);
             mbar_init(&S.ds_full, 8);
@@ -104,8 +107,8 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             if (rope) tma_load_3d(qs + p.nb * kBlock, &p.qr, &S.q_full, 0, h, rq.first + q0);
             int kdone = 0, vdone = 0;
             for (int j = 0; j < n; j++) {
-                const int ks_ = j & 1, vs_ = j % VS;
-                if (!wait_for(&S.k_empty[ks_], ((j >> 1) & 1) ^ 1, gave_up) || *gave_up) break;
+                const int ks_ = j % KS, vs_ = j % VS;
+                if (!wait_for(&S.k_empty[ks_], ((j / KS) & 1) ^ 1, gave_up) || *gave_up) break;
                 uint64_t* bar = ragged && j == n - 1 ? &S.k_last : &S.k_full[ks_];   // to the warps that blank rows
                 mbar_arrive_expect_tx(bar, KB * kBlock);
                 const uint32_t d = ks + ks_ * KB * kBlock;
@@ -125,11 +128,11 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             if (*gave_up) {   // a wait expired: the loads in flight land before the CTA ends
                 mbar_wait(&S.q_full, 0, nullptr, kWaitNs);
                 if (kdone > 0) mbar_wait(&S.do_full, 0, nullptr, kWaitNs);
-                for (int j = max(0, kdone - 2); j < kdone; j++) {
+                for (int j = max(0, kdone - KS); j < kdone; j++) {
                     if (ragged && j == n - 1)
                         mbar_wait(&S.k_last, 0, nullptr, kWaitNs);
                     else
-                        mbar_wait(&S.k_full[j & 1], (j >> 1) & 1, nullptr, kWaitNs);
+                        mbar_wait(&S.k_full[j % KS], (j / KS) & 1, nullptr, kWaitNs);
                 }
                 for (int j = max(0, vdone - VS); j < vdone; j++) mbar_wait(&S.v_full[j % VS], (j / VS) & 1, nullptr, kWaitNs);
             }
@@ -146,10 +149,10 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 if (ragged && j == n - 1)
                     wait_for(&S.k_fixed, 0, gave_up);
                 else
-                    wait_for(&S.k_full[j & 1], (j >> 1) & 1, gave_up);
+                    wait_for(&S.k_full[j % KS], (j / KS) & 1, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t q = kmajor + at_desc(qs), k = kmajor + at_desc(ks + (j & 1) * KB * kBlock);
+                    const uint64_t q = kmajor + at_desc(qs), k = kmajor + at_desc(ks + (j % KS) * KB * kBlock);
 #pragma unroll
                     for (int c = 0; c < KB; c++)
 #pragma unroll
@@ -184,12 +187,12 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 wait_for(&S.ds_full, j & 1, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t k = nmajor + at_desc(ks + (j & 1) * KB * kBlock);
+                    const uint64_t k = nmajor + at_desc(ks + (j % KS) * KB * kBlock);
 #pragma unroll
                     for (int e = 0; e < 8; e++)     // dS: columns 0..31 of each half of dP's
                         mma_bf16_ts(tmem + TQ, tmem + TP + (e >> 2) * 64 + 8 * (e & 3), k + 128 * e, id_q, (j | e) ? 1u : 0u);
                 }
-                mma_commit(&S.k_empty[j & 1]);
+                mma_commit(&S.k_empty[j % KS]);
                 if (j + 1 < n) dprobs(j + 1);
             }
             mma_commit(&S.dq_full);
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             wait_for(&S.k_last, 0, gave_up);
             const int valid = rk.n - (n - 1) * kTile, bad = kTile - valid;
             for (int c = 0; c < KB; c++) {
-                unsigned char* k = sm + (ks - qs) + (((n - 1) & 1) * KB + c) * kBlock + valid * 128;
+                unsigned char* k = sm + (ks - qs) + (((n - 1) % KS) * KB + c) * kBlock + valid * 128;
                 for (int e = tid - 64; e < bad * 8; e += 64) *reinterpret_cast<uint4*>(k + e * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
@@ -311,38 +314,45 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
 
 template <int NQ>
 struct SharedK {
-    uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], st_full[2], st_empty[2], s_full, p_full, dp_full, ds_full,
+    uint64_t kv_full, q_full[3], q_empty[3], do_full[2], do_empty[2], st_full[2], st_empty[2], s_full, p_full, dp_full, ds_full,
         acc_full, drain[2];
     alignas(16) float lower[2][NQ];     // -lse log2(e), minus infinity for a row that adds nothing
     alignas(16) float delta[2][NQ];     // -delta
     uint32_t tmem, gave_up;
 };
 
-// NQ: queries a step; TMEM holds two NQ columns of scores, dV and dK
-template <int KB, int NQ>
+// NQ: queries a step; TMEM holds two NQ columns of scores, dV and dK.  QS: stages of Q, held from the scores to dK; dO and
+// the statistics have two
+template <int KB, int NQ, int QS>
 __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_constant__ Params p)
 {
-    extern __shared__ unsigned char raw[];
-    __shared__ SharedK<NQ> S;
+    extern __shared__ unsigned char raw[];      // tiles (1024-byte aligned), then the shared state
     const AttnArgs& a = p.a;
     const gdn_mla_attn_t& s = a.s;
     const int g = blockIdx.x % s.Hkv, b = blockIdx.y, G = s.H / s.Hkv;
     const int k0 = (int)(blockIdx.x / s.Hkv) * kTile;       // under the causal mask the first keys have most queries
     const Rows rq = rows_of(a.cu_q, b, s.Tq, s.Nq), rk = rows_of(a.cu_k, b, s.Tk, s.Nk);
     if (k0 >= rk.n) return;
+    if (smem_u32(raw) & 1023) {     // never so without static shared memory; the tiles below would not fit otherwise
+        if (threadIdx.x == 0) atomicExch(a.status, kDevTimeout);
+        return;
+    }
     const int off = rk.n - rq.n;
     const int first = s.causal ? max(0, k0 - off) / NQ : 0;                // the first step whose queries see key k0
     const int per = max(0, (rq.n + NQ - 1) / NQ - first), n = per * G;     // steps a head, in all
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    unsigned char* sm = raw;
     constexpr uint32_t kStep = NQ * 128;                                   // bytes of a 64-column block of a step
-    const uint32_t ks = smem_u32(sm), vs = ks + KB * kBlock, qs = vs + p.vb * kBlock, dos = qs + 2 * KB * kStep;
+    SharedK<NQ>& S = *reinterpret_cast<SharedK<NQ>*>(sm + (KB + p.vb) * kBlock + (QS * KB + 2 * p.vb) * kStep);
+    const uint32_t ks = smem_u32(sm), vs = ks + KB * kBlock, qs = vs + p.vb * kBlock, dos = qs + QS * KB * kStep;
 
     if (warp == 0) {
         if (elect_one()) {
             for (uint64_t* x : {&S.kv_full, &S.s_full, &S.dp_full, &S.acc_full, &S.drain[0]}) mbar_init(x, 1);
+            for (int i = 0; i < QS; i++)
+                for (uint64_t* x : {&S.q_full[i], &S.q_empty[i]}) mbar_init(x, 1);
             for (int i = 0; i < 2; i++) {
-                for (uint64_t* x : {&S.q_full[i], &S.q_empty[i], &S.do_full[i], &S.do_empty[i]}) mbar_init(x, 1);
+                for (uint64_t* x : {&S.do_full[i], &S.do_empty[i]}) mbar_init(x, 1);
                 mbar_init(&S.st_full[i], 64);
                 mbar_init(&S.st_empty[i], 8);
             }
@@ -371,16 +381,15 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             for (int c = 0; c < p.vb; c++) tma_load_3d(vs + c * kBlock, &p.v, &S.kv_full, 64 * c, g, rk.first + k0);
             int qdone = 0, ddone = 0;
             for (int i = 0, h = g * G, t = first; i < n; i++) {
-                const int st = i & 1;
-                const uint32_t ph = ((i >> 1) & 1) ^ 1;
+                const int st = i & 1, qst = i % QS;
                 const int row = rq.first + t * NQ;
-                if (!wait_for(&S.q_empty[st], ph, gave_up) || *gave_up) break;
-                mbar_arrive_expect_tx(&S.q_full[st], KB * kStep);
-                const uint32_t q = qs + st * KB * kStep, d = dos + st * p.vb * kStep;
-                for (int c = 0; c < p.nb; c++) tma_load_3d(q + c * kStep, &p.qn, &S.q_full[st], 64 * c, h, row);
-                if (rope) tma_load_3d(q + p.nb * kStep, &p.qr, &S.q_full[st], 0, h, row);
+                if (!wait_for(&S.q_empty[qst], ((i / QS) & 1) ^ 1, gave_up) || *gave_up) break;
+                mbar_arrive_expect_tx(&S.q_full[qst], KB * kStep);
+                const uint32_t q = qs + qst * KB * kStep, d = dos + st * p.vb * kStep;
+                for (int c = 0; c < p.nb; c++) tma_load_3d(q + c * kStep, &p.qn, &S.q_full[qst], 64 * c, h, row);
+                if (rope) tma_load_3d(q + p.nb * kStep, &p.qr, &S.q_full[qst], 0, h, row);
                 qdone = i + 1;
-                if (!wait_for(&S.do_empty[st], ph, gave_up) || *gave_up) break;
+                if (!wait_for(&S.do_empty[st], ((i >> 1) & 1) ^ 1, gave_up) || *gave_up) break;
                 mbar_arrive_expect_tx(&S.do_full[st], p.vb * kStep);
                 for (int c = 0; c < p.vb; c++) tma_load_3d(d + c * kStep, &p.dO, &S.do_full[st], 64 * c, h, row);
                 ddone = i + 1;
@@ -391,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             }
             if (*gave_up) {   // a wait expired: the loads in flight land before the CTA ends
                 mbar_wait(&S.kv_full, 0, nullptr, kWaitNs);
-                for (int i = max(0, qdone - 2); i < qdone; i++) mbar_wait(&S.q_full[i & 1], (i >> 1) & 1, nullptr, kWaitNs);
+                for (int i = max(0, qdone - QS); i < qdone; i++) mbar_wait(&S.q_full[i % QS], (i / QS) & 1, nullptr, kWaitNs);
                 for (int i = max(0, ddone - 2); i < ddone; i++) mbar_wait(&S.do_full[i & 1], (i >> 1) & 1, nullptr, kWaitNs);
             }
         }
@@ -406,11 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             const int vsteps = (s.dv + 15) >> 4;
             const bool ragged = rq.n % NQ != 0;
             auto scores = [&](int i) {
-                wait_for(&S.q_full[i & 1], (i >> 1) & 1, gave_up);
+                wait_for(&S.q_full[i % QS], (i / QS) & 1, gave_up);
                 if (ragged && i % per == per - 1) wait_for(&S.st_full[i & 1], (i >> 1) & 1, gave_up);   // rows past the end blanked
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t k = kmajor + at_desc(ks), q = kmajor + at_desc(qs + (i & 1) * KB * kStep);
+                    const uint64_t k = kmajor + at_desc(ks), q = kmajor + at_desc(qs + (i % QS) * KB * kStep);
 #pragma unroll
                     for (int c = 0; c < KB; c++)
 #pragma unroll
@@ -452,13 +461,13 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
                 wait_for(&S.ds_full, i & 1, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t q = nmajor + at_desc(qs + (i & 1) * KB * kStep);
+                    const uint64_t q = nmajor + at_desc(qs + (i % QS) * KB * kStep);
 #pragma unroll
                     for (int e = 0; e < KS; e++)
                         mma_bf16_ts(tmem + TK, tmem + TP + (e >= KS / 2 ? HC + 8 * (e - KS / 2) : 8 * e), q + 128 * e, id_k,
                                     (i | e) ? 1u : 0u);
                 }
-                mma_commit(&S.q_empty[i & 1]);
+                mma_commit(&S.q_empty[i % QS]);
                 if (i + 1 < n) dprobs(i + 1);
             }
             mma_commit(&S.acc_full);
@@ -481,10 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             }
             const int valid = rq.n - t * NQ;
             if (valid < NQ) {      // rows past the end hold anything: weights of zero would still meet a NaN
-                wait_for(&S.q_full[st], (i >> 1) & 1, gave_up);
+                wait_for(&S.q_full[i % QS], (i / QS) & 1, gave_up);
                 wait_for(&S.do_full[st], (i >> 1) & 1, gave_up);
                 for (int c = 0; c < KB + p.vb; c++) {
-                    const uint32_t from = c < KB ? qs - ks + (st * KB + c) * kStep : dos - ks + (st * p.vb + c - KB) * kStep;
+                    const uint32_t from = c < KB ? qs - ks + ((i % QS) * KB + c) * kStep : dos - ks + (st * p.vb + c - KB) * kStep;
                     unsigned char* x = sm + from + valid * 128;
                     for (int e = t0; e < (NQ - valid) * 8; e += 64) *reinterpret_cast<uint4*>(x + e * 16) = make_uint4(0, 0, 0, 0);
                 }
@@ -635,27 +644,28 @@ bool maps(Params& p, int q_rows, int k_rows)
                          (s.dr == 0 || view_map(&p.kr, a.kr, s.Nk, 1, s.dr, k_rows)));
 }
 
-template <int KB, int VS>
+template <int KB, int KS, int VS>
 cudaError_t run_dq(Params& p, cudaStream_t st)
 {
     if (!maps(p, kTile, kTile)) return cudaErrorInvalidValue;
     p.tiles = (p.a.s.Tq + kTile - 1) / kTile;
-    const size_t bytes = 1024 + (size_t)(KB + p.vb + 2 * KB + VS * p.vb) * kBlock;
-    const cudaError_t e = cudaFuncSetAttribute(dq_tc_kernel<KB, VS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const size_t bytes = 1024 + (size_t)(KB + p.vb + KS * KB + VS * p.vb) * kBlock;
+    const cudaError_t e = cudaFuncSetAttribute(dq_tc_kernel<KB, KS, VS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    dq_tc_kernel<KB, VS><<<dim3((unsigned)p.a.s.H * p.tiles, p.a.s.B), kThreads, bytes, st>>>(p);
+    dq_tc_kernel<KB, KS, VS><<<dim3((unsigned)p.a.s.H * p.tiles, p.a.s.B), kThreads, bytes, st>>>(p);
     return cudaGetLastError();
 }
 
-template <int KB, int NQ>
+template <int KB, int NQ, int QS>
 cudaError_t run_dkv(Params& p, cudaStream_t st)
 {
     if (!maps(p, NQ, kTile)) return cudaErrorInvalidValue;
     p.tiles = (p.a.s.Tk + kTile - 1) / kTile;
-    const size_t bytes = 1024 + (size_t)(KB + p.vb) * kBlock + (size_t)2 * (KB + p.vb) * NQ * 128;
-    const cudaError_t e = cudaFuncSetAttribute(dkv_tc_kernel<KB, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    // (without static shared memory the dynamic part begins 1024-byte aligned)
+    const size_t bytes = (size_t)(KB + p.vb) * kBlock + (size_t)(QS * KB + 2 * p.vb) * NQ * 128 + sizeof(SharedK<NQ>);
+    const cudaError_t e = cudaFuncSetAttribute(dkv_tc_kernel<KB, NQ, QS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    dkv_tc_kernel<KB, NQ><<<dim3((unsigned)p.a.s.Hkv * p.tiles, p.a.s.B), kThreads, bytes, st>>>(p);
+    dkv_tc_kernel<KB, NQ, QS><<<dim3((unsigned)p.a.s.Hkv * p.tiles, p.a.s.B), kThreads, bytes, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -673,12 +683,12 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs& a, cudaStream_t st)
     cudaError_t e = cudaSuccess;
     if (s.Tq > 0) {
         e = launch_delta(a, st);
-        // three blocks of Q and two K stages leave room for one V stage only
-        if (e == cudaSuccess) e = kb == 1 ? run_dq<1, 2>(p, st) : kb == 2 ? run_dq<2, 2>(p, st) : run_dq<3, 1>(p, st);
+        // as many stages as fit beside Q and dO, K's first
+        if (e == cudaSuccess) e = kb == 1 ? run_dq<1, 3, 2>(p, st) : kb == 2 ? run_dq<2, 3, 1>(p, st) : run_dq<3, 2, 1>(p, st);
     }
     if (e == cudaSuccess && s.Tk > 0) {
         // dV and 192 columns of dK leave 192 for S and dP
-        e = kb == 1 ? run_dkv<1, 128>(p, st) : kb == 2 ? run_dkv<2, 128>(p, st) : run_dkv<3, 96>(p, st);
+        e = kb == 1 ? run_dkv<1, 128, 3>(p, st) : kb == 2 ? run_dkv<2, 128, 3>(p, st) : run_dkv<3, 96, 2>(p, st);
         if (e == cudaSuccess && s.dr > 0) e = launch_dkr(a, st);
     }
     return e;
