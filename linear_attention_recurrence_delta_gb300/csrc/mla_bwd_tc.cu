@@ -48,9 +48,13 @@ __device__ __forceinline__ uint4 pack8(const float* x, float f)
 }
 
 // ================================================================ dQ: a tile of queries walks the keys
+//
+// dO is an operand from TMEM for the whole walk (products with both operands in shared memory are bound by its 128 bytes
+// a cycle); it gets there by way of the third K stage.  Where dQ leaves 64 columns, dS has its own (OWN), so that the next
+// tile's dP runs while this one's is turned into dS; else it goes back over dP.
 
 struct SharedQ {
-    uint64_t q_full, do_full, k_full[3], k_empty[3], v_full[2], v_empty[2], k_last, k_fixed, s_full, s_read, dp_full, ds_full,
+    uint64_t q_full, a_full, k_full[3], k_empty[3], v_full[2], v_empty[2], k_last, k_fixed, s_full, s_read, dp_full, dp_read, ds_full, ds_empty,
         dq_full, drain;
     uint32_t tmem, gave_up;
 };
@@ -73,17 +77,22 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     const int n = end > 0 ? (end + kTile - 1) / kTile : 0;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    const uint32_t qs = smem_u32(sm), dos = qs + KB * kBlock, ks = dos + p.vb * kBlock, vs = ks + KS * KB * kBlock;
+    constexpr bool OWN = KB < 3;
+    const uint32_t qs = smem_u32(sm), ks = qs + KB * kBlock, vs = ks + KS * KB * kBlock;
+    static_assert(KS == 3, "");
+    const uint32_t dos = KB == 1 ? vs + VS * p.vb * kBlock : ks + 2 * KB * kBlock;   // one block is too narrow for it
 
     if (warp == 0) {
         if (elect_one()) {
-            for (uint64_t* x : {&S.q_full, &S.do_full, &S.k_last, &S.s_full, &S.dp_full, &S.dq_full, &S.drain}) mbar_init(x, 1);
+            for (uint64_t* x : {&S.q_full, &S.k_last, &S.s_full, &S.dp_full, &S.ds_empty, &S.dq_full, &S.drain}) mbar_init(x, 1);
             for (int i = 0; i < KS; i++)
                 for (uint64_t* x : {&S.k_full[i], &S.k_empty[i]}) mbar_init(x, 1);
             for (int i = 0; i < VS; i++)
                 for (uint64_t* x : {&S.v_full[i], &S.v_empty[i]}) mbar_init(x, 1);
             mbar_init(&S.k_fixed, 64);
+            mbar_init(&S.a_full, 8);
             mbar_init(&S.s_read, 8);
+            mbar_init(&S.dp_read, 8);
             mbar_init(&S.ds_full, 8);
             fence_mbar_init();
             S.gave_up = 0;
@@ -97,17 +106,21 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     const uint32_t tmem = S.tmem;
     volatile uint32_t* gave_up = &S.gave_up;
     const bool ragged = rk.n % kTile != 0 && n == (rk.n + kTile - 1) / kTile;   // the last key tile has rows to blank
-    constexpr uint32_t TS = 0, TP = 128, TQ = 256;     // TMEM columns of S, dP (dS over it), dQ
+    // TMEM columns of S, dP, dQ, dO as bf16 pairs, and dS likewise: a half's 32 columns kDsHalf apart
+    constexpr uint32_t TS = 0, TP = 128, TQ = 256, TD = 256 + 64 * KB, TE = OWN ? TD + 64 : TP, kDsHalf = OWN ? 32 : 64;
+    static_assert(TD + (OWN ? 128 : 64) <= 512, "");
 
     if (warp == 0) {
         if (elect_one() && n > 0) {
             const bool rope = s.dr > 0;
-            mbar_arrive_expect_tx(&S.q_full, KB * kBlock);
+            mbar_arrive_expect_tx(&S.q_full, (KB + p.vb) * kBlock);
             for (int c = 0; c < p.nb; c++) tma_load_3d(qs + c * kBlock, &p.qn, &S.q_full, 64 * c, h, rq.first + q0);
             if (rope) tma_load_3d(qs + p.nb * kBlock, &p.qr, &S.q_full, 0, h, rq.first + q0);
+            for (int c = 0; c < p.vb; c++) tma_load_3d(dos + c * kBlock, &p.dO, &S.q_full, 64 * c, h, rq.first + q0);
             int kdone = 0, vdone = 0;
             for (int j = 0; j < n; j++) {
                 const int ks_ = j % KS, vs_ = j % VS;
+                if (KB > 1 && j == 2) wait_for(&S.a_full, 0, gave_up);      // dO has left the stage
                 if (!wait_for(&S.k_empty[ks_], ((j / KS) & 1) ^ 1, gave_up) || *gave_up) break;
                 uint64_t* bar = ragged && j == n - 1 ? &S.k_last : &S.k_full[ks_];   // to the warps that blank rows
                 mbar_arrive_expect_tx(bar, KB * kBlock);
@@ -115,10 +128,6 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 for (int c = 0; c < p.nb; c++) tma_load_3d(d + c * kBlock, &p.kn, bar, 64 * c, g, rk.first + j * kTile);
                 if (rope) tma_load_3d(d + p.nb * kBlock, &p.kr, bar, 0, 0, rk.first + j * kTile);
                 kdone = j + 1;
-                if (j == 0) {
-                    mbar_arrive_expect_tx(&S.do_full, p.vb * kBlock);
-                    for (int c = 0; c < p.vb; c++) tma_load_3d(dos + c * kBlock, &p.dO, &S.do_full, 64 * c, h, rq.first + q0);
-                }
                 if (!wait_for(&S.v_empty[vs_], ((j / VS) & 1) ^ 1, gave_up) || *gave_up) break;
                 mbar_arrive_expect_tx(&S.v_full[vs_], p.vb * kBlock);
                 for (int c = 0; c < p.vb; c++)
@@ -127,7 +136,6 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             }
             if (*gave_up) {   // a wait expired: the loads in flight land before the CTA ends
                 mbar_wait(&S.q_full, 0, nullptr, kWaitNs);
-                if (kdone > 0) mbar_wait(&S.do_full, 0, nullptr, kWaitNs);
                 for (int j = max(0, kdone - KS); j < kdone; j++) {
                     if (ragged && j == n - 1)
                         mbar_wait(&S.k_last, 0, nullptr, kWaitNs);
@@ -167,33 +175,38 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 wait_for(&S.v_full[j % VS], (j / VS) & 1, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
-                    const uint64_t d = kmajor + at_desc(dos), v = kmajor + at_desc(vs + (j % VS) * p.vb * kBlock);
+                    const uint64_t v = kmajor + at_desc(vs + (j % VS) * p.vb * kBlock);
 #pragma unroll
                     for (int e = 0; e < 8; e++)
                         if (e < vsteps)
-                            mma_bf16(tmem + TP, d + (e >> 2) * (kBlock >> 4) + 2 * (e & 3), v + (e >> 2) * (kBlock >> 4) + 2 * (e & 3),
-                                     id_s, e ? 1u : 0u);
+                            mma_bf16_ts(tmem + TP, tmem + TD + 8 * e, v + (e >> 2) * (kBlock >> 4) + 2 * (e & 3), id_s, e ? 1u : 0u);
                 }
                 mma_commit(&S.dp_full);
                 mma_commit(&S.v_empty[j % VS]);
             };
             wait_for(&S.q_full, 0, gave_up);
+            wait_for(&S.a_full, 0, gave_up);
+            tc_fence_after();
             scores(0);
-            wait_for(&S.do_full, 0, gave_up);
             dprobs(0);
             for (int j = 0; j < n; j++) {
                 wait_for(&S.s_read, j & 1, gave_up);
                 if (j + 1 < n) scores(j + 1);
+                if (OWN) {
+                    wait_for(&S.dp_read, j & 1, gave_up);
+                    if (j + 1 < n) dprobs(j + 1);
+                }
                 wait_for(&S.ds_full, j & 1, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
                     const uint64_t k = nmajor + at_desc(ks + (j % KS) * KB * kBlock);
 #pragma unroll
-                    for (int e = 0; e < 8; e++)     // dS: columns 0..31 of each half of dP's
-                        mma_bf16_ts(tmem + TQ, tmem + TP + (e >> 2) * 64 + 8 * (e & 3), k + 128 * e, id_q, (j | e) ? 1u : 0u);
+                    for (int e = 0; e < 8; e++)
+                        mma_bf16_ts(tmem + TQ, tmem + TE + (e >> 2) * kDsHalf + 8 * (e & 3), k + 128 * e, id_q, (j | e) ? 1u : 0u);
                 }
                 mma_commit(&S.k_empty[j % KS]);
-                if (j + 1 < n) dprobs(j + 1);
+                if (OWN) mma_commit(&S.ds_empty);
+                if (!OWN && j + 1 < n) dprobs(j + 1);
             }
             mma_commit(&S.dq_full);
             if (*gave_up) {   // the products in flight end before TMEM is freed
@@ -218,7 +231,28 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         const bool mine = row < rq.n;
         const long long at = (long long)h * s.Nq + rq.first + (mine ? row : 0);
         const float c = s.scale * kLog2e;
-        const float lse = mine ? a.lse[at] : -INFINITY, delta = mine ? a.delta[at] : 0.f;
+        const float lse = mine ? a.lse[at] : -INFINITY;
+        const float delta = mine ? a.delta[at] : 0.f;
+        if (n > 0) {     // this half's 64 columns of the row of dO into TMEM
+            wait_for(&S.q_full, 0, gave_up);
+            if (half < p.vb) {
+                uint32_t x[32];
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(sm + (dos - qs) + half * kBlock + sw128(quad * 32 + lane, 8 * e));
+                    x[4 * e] = v.x;
+                    x[4 * e + 1] = v.y;
+                    x[4 * e + 2] = v.z;
+                    x[4 * e + 3] = v.w;
+                }
+                __syncwarp();
+                tmem_st32(base + TD + 32 * half, x);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.a_full);
+        }
         const float lower = lse == -INFINITY ? -INFINITY : -lse * kLog2e;       // a row without keys: weights of zero
         // a query that sees one key has a constant weight: no gradient, not the difference of two roundings
         int last = !mine ? -1 : s.causal ? min(rk.n - 1, row + off) : rk.n - 1;
@@ -248,24 +282,36 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             wait_for(&S.dp_full, j & 1, gave_up);
             __syncwarp();
             tc_fence_after();
+            uint32_t y[64];
+            tmem_ld32(base + TP + 64 * half, y);
+            tmem_ld32(base + TP + 64 * half + 32, y + 32);
+            tmem_wait_ld();
+            if (OWN) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.dp_read);
+                if (j > 0) {     // the last tile's dS has been used
+                    wait_for(&S.ds_empty, (j - 1) & 1, gave_up);
+                    __syncwarp();
+                    tc_fence_after();
+                }
+            }
 #pragma unroll
             for (int i0 = 0; i0 < 64; i0 += 32) {
-                uint32_t y[32], z[16];
-                tmem_ld32(base + TP + 64 * half + i0, y);
-                tmem_wait_ld();
+                uint32_t z[16];
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const uint64_t t = mul2(pack2(__uint_as_float(x[i0 + i]), __uint_as_float(x[i0 + i + 1])),
-                                            add2(pack2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), d2));
+                for (int i = i0; i < i0 + 32; i += 2) {
                     float u, w;
-                    unpack2(t, u, w);
+                    unpack2(mul2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                 add2(pack2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), d2)),
+                            u, w);
                     if (masked) {
-                        u = j0 + i0 + i <= last ? u : 0.f;
-                        w = j0 + i0 + i + 1 <= last ? w : 0.f;
+                        u = j0 + i <= last ? u : 0.f;
+                        w = j0 + i + 1 <= last ? w : 0.f;
                     }
-                    z[i >> 1] = pack_bf16(u, w);
+                    z[(i - i0) >> 1] = pack_bf16(u, w);
                 }
-                tmem_st16u(base + TP + 64 * half + (i0 >> 1), z);   // over columns of this half that have been read
+                tmem_st16u(base + TE + kDsHalf * half + (i0 >> 1), z);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -649,7 +695,7 @@ cudaError_t run_dq(Params& p, cudaStream_t st)
 {
     if (!maps(p, kTile, kTile)) return cudaErrorInvalidValue;
     p.tiles = (p.a.s.Tq + kTile - 1) / kTile;
-    const size_t bytes = 1024 + (size_t)(KB + p.vb + KS * KB + VS * p.vb) * kBlock;
+    const size_t bytes = 1024 + (size_t)(KB + KS * KB + VS * p.vb + (KB == 1 ? p.vb : 0)) * kBlock;
     const cudaError_t e = cudaFuncSetAttribute(dq_tc_kernel<KB, KS, VS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
     dq_tc_kernel<KB, KS, VS><<<dim3((unsigned)p.a.s.H * p.tiles, p.a.s.B), kThreads, bytes, st>>>(p);
@@ -683,8 +729,7 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs& a, cudaStream_t st)
     cudaError_t e = cudaSuccess;
     if (s.Tq > 0) {
         e = launch_delta(a, st);
-        // as many stages as fit beside Q and dO, K's first
-        if (e == cudaSuccess) e = kb == 1 ? run_dq<1, 3, 2>(p, st) : kb == 2 ? run_dq<2, 3, 1>(p, st) : run_dq<3, 2, 1>(p, st);
+        if (e == cudaSuccess) e = kb == 1 ? run_dq<1, 3, 2>(p, st) : kb == 2 ? run_dq<2, 3, 2>(p, st) : run_dq<3, 3, 1>(p, st);
     }
     if (e == cudaSuccess && s.Tk > 0) {
         // dV and 192 columns of dK leave 192 for S and dP
