@@ -1,6 +1,6 @@
 // mla_bwd_tc.cu -- gradients of the expanded attention on the tensor cores (bf16).
 //
-//   P = exp(scale S - lse),  dP = dO V^T,  dS = P (dP - delta),  delta = rowsum(dO O)
+//   P = exp(scale S - lse),  dP = dO V^T,  dS = P (dP - delta),  delta = rowsum(dO O) = rowsum(P dP)
 //   dQ = scale dS K,   dK = scale dS^T Q,   dV = P^T dO
 //
 // Two kernels, so that every sum has one owner and a fixed order: one holds a tile of queries and walks the keys (dQ),
@@ -52,10 +52,16 @@ __device__ __forceinline__ uint4 pack8(const float* x, float f)
 // dO is an operand from TMEM for the whole walk (products with both operands in shared memory are bound by its 128 bytes
 // a cycle); it gets there by way of the third K stage.  Where dQ leaves 64 columns, dS has its own (OWN), so that the next
 // tile's dP runs while this one's is turned into dS; else it goes back over dP.
+//
+// delta from the stored o carries o's rounding, which counts where few keys share a weight of one: dP - delta cancels.
+// sum_j P dP is the same number without it.  A tile that walks at most kTwice key tiles takes that sum in a first walk;
+// a longer one corrects delta by its rows' sums of dS (which are zero) for the pass over the keys.
 
+constexpr int kTwice = 2;
 struct SharedQ {
-    uint64_t q_full, a_full, k_full[3], k_empty[3], v_full[2], v_empty[2], k_last, k_fixed, s_full, s_read, dp_full, dp_read, ds_full, ds_empty,
+    uint64_t q_full, a_full, k_full[3], k_empty[3], v_full[2], v_empty[2], k_last[2], k_fixed[2], s_full, s_read, dp_full, dp_read, ds_full, ds_empty,
         dq_full, drain;
+    float part[2][kTile];        // a row's sums from each half of the columns
     uint32_t tmem, gave_up;
 };
 
@@ -84,12 +90,13 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
 
     if (warp == 0) {
         if (elect_one()) {
-            for (uint64_t* x : {&S.q_full, &S.k_last, &S.s_full, &S.dp_full, &S.ds_empty, &S.dq_full, &S.drain}) mbar_init(x, 1);
+            for (uint64_t* x : {&S.q_full, &S.k_last[0], &S.k_last[1], &S.s_full, &S.dp_full, &S.ds_empty, &S.dq_full, &S.drain}) mbar_init(x, 1);
             for (int i = 0; i < KS; i++)
                 for (uint64_t* x : {&S.k_full[i], &S.k_empty[i]}) mbar_init(x, 1);
             for (int i = 0; i < VS; i++)
                 for (uint64_t* x : {&S.v_full[i], &S.v_empty[i]}) mbar_init(x, 1);
-            mbar_init(&S.k_fixed, 64);
+            mbar_init(&S.k_fixed[0], 64);
+            mbar_init(&S.k_fixed[1], 64);
             mbar_init(&S.a_full, 8);
             mbar_init(&S.s_read, 8);
             mbar_init(&S.dp_read, 8);
@@ -106,6 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     const uint32_t tmem = S.tmem;
     volatile uint32_t* gave_up = &S.gave_up;
     const bool ragged = rk.n % kTile != 0 && n == (rk.n + kTile - 1) / kTile;   // the last key tile has rows to blank
+    const int sums = n <= kTwice ? n : 0, steps_all = sums + n;       // steps of the first walk; of both
     // TMEM columns of S, dP, dQ, dO as bf16 pairs, and dS likewise: a half's 32 columns kDsHalf apart
     constexpr uint32_t TS = 0, TP = 128, TQ = 256, TD = 256 + 64 * KB, TE = OWN ? TD + 64 : TP, kDsHalf = OWN ? 32 : 64;
     static_assert(TD + (OWN ? 128 : 64) <= 512, "");
@@ -118,29 +126,28 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             if (rope) tma_load_3d(qs + p.nb * kBlock, &p.qr, &S.q_full, 0, h, rq.first + q0);
             for (int c = 0; c < p.vb; c++) tma_load_3d(dos + c * kBlock, &p.dO, &S.q_full, 64 * c, h, rq.first + q0);
             int kdone = 0, vdone = 0;
-            for (int j = 0; j < n; j++) {
-                const int ks_ = j % KS, vs_ = j % VS;
+            for (int j = 0; j < steps_all; j++) {
+                const int ks_ = j % KS, vs_ = j % VS, walk = j < sums ? 0 : 1, row = rk.first + (walk ? j - sums : j) * kTile;
                 if (KB > 1 && j == 2) wait_for(&S.a_full, 0, gave_up);      // dO has left the stage
                 if (!wait_for(&S.k_empty[ks_], ((j / KS) & 1) ^ 1, gave_up) || *gave_up) break;
-                uint64_t* bar = ragged && j == n - 1 ? &S.k_last : &S.k_full[ks_];   // to the warps that blank rows
+                uint64_t* bar = ragged && (j == sums - 1 || j == steps_all - 1) ? &S.k_last[walk] : &S.k_full[ks_];   // to the warps that blank rows
                 mbar_arrive_expect_tx(bar, KB * kBlock);
                 const uint32_t d = ks + ks_ * KB * kBlock;
-                for (int c = 0; c < p.nb; c++) tma_load_3d(d + c * kBlock, &p.kn, bar, 64 * c, g, rk.first + j * kTile);
-                if (rope) tma_load_3d(d + p.nb * kBlock, &p.kr, bar, 0, 0, rk.first + j * kTile);
+                for (int c = 0; c < p.nb; c++) tma_load_3d(d + c * kBlock, &p.kn, bar, 64 * c, g, row);
+                if (rope) tma_load_3d(d + p.nb * kBlock, &p.kr, bar, 0, 0, row);
+                if (bar != &S.k_full[ks_]) mbar_arrive(&S.k_full[ks_]);     // which keeps count of its stage's uses
                 kdone = j + 1;
                 if (!wait_for(&S.v_empty[vs_], ((j / VS) & 1) ^ 1, gave_up) || *gave_up) break;
                 mbar_arrive_expect_tx(&S.v_full[vs_], p.vb * kBlock);
                 for (int c = 0; c < p.vb; c++)
-                    tma_load_3d(vs + (vs_ * p.vb + c) * kBlock, &p.v, &S.v_full[vs_], 64 * c, g, rk.first + j * kTile);
+                    tma_load_3d(vs + (vs_ * p.vb + c) * kBlock, &p.v, &S.v_full[vs_], 64 * c, g, row);
                 vdone = j + 1;
             }
             if (*gave_up) {   // a wait expired: the loads in flight land before the CTA ends
                 mbar_wait(&S.q_full, 0, nullptr, kWaitNs);
                 for (int j = max(0, kdone - KS); j < kdone; j++) {
-                    if (ragged && j == n - 1)
-                        mbar_wait(&S.k_last, 0, nullptr, kWaitNs);
-                    else
-                        mbar_wait(&S.k_full[j % KS], (j / KS) & 1, nullptr, kWaitNs);
+                    mbar_wait(&S.k_full[j % KS], (j / KS) & 1, nullptr, kWaitNs);
+                    if (ragged && (j == sums - 1 || j == steps_all - 1)) mbar_wait(&S.k_last[j < sums ? 0 : 1], 0, nullptr, kWaitNs);
                 }
                 for (int j = max(0, vdone - VS); j < vdone; j++) mbar_wait(&S.v_full[j % VS], (j / VS) & 1, nullptr, kWaitNs);
             }
@@ -154,10 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             for (int c = 0; c < KB; c++) steps[c] = block_steps(p, c);
             const int vsteps = (s.dv + 15) >> 4;
             auto scores = [&](int j) {
-                if (ragged && j == n - 1)
-                    wait_for(&S.k_fixed, 0, gave_up);
-                else
-                    wait_for(&S.k_full[j % KS], (j / KS) & 1, gave_up);
+                wait_for(&S.k_full[j % KS], (j / KS) & 1, gave_up);
+                if (ragged && (j == sums - 1 || j == steps_all - 1)) wait_for(&S.k_fixed[j < sums ? 0 : 1], 0, gave_up);
                 tc_fence_after();
                 if (!*gave_up) {
                     const uint64_t q = kmajor + at_desc(qs), k = kmajor + at_desc(ks + (j % KS) * KB * kBlock);
@@ -189,24 +194,24 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             tc_fence_after();
             scores(0);
             dprobs(0);
-            for (int j = 0; j < n; j++) {
+            for (int j = 0; j < steps_all; j++) {
                 wait_for(&S.s_read, j & 1, gave_up);
-                if (j + 1 < n) scores(j + 1);
+                if (j + 1 < steps_all) scores(j + 1);
                 if (OWN) {
                     wait_for(&S.dp_read, j & 1, gave_up);
-                    if (j + 1 < n) dprobs(j + 1);
+                    if (j + 1 < steps_all) dprobs(j + 1);
                 }
                 wait_for(&S.ds_full, j & 1, gave_up);
                 tc_fence_after();
-                if (!*gave_up) {
+                if (j >= sums && !*gave_up) {
                     const uint64_t k = nmajor + at_desc(ks + (j % KS) * KB * kBlock);
 #pragma unroll
                     for (int e = 0; e < 8; e++)
-                        mma_bf16_ts(tmem + TQ, tmem + TE + (e >> 2) * kDsHalf + 8 * (e & 3), k + 128 * e, id_q, (j | e) ? 1u : 0u);
+                        mma_bf16_ts(tmem + TQ, tmem + TE + (e >> 2) * kDsHalf + 8 * (e & 3), k + 128 * e, id_q, (j > sums || e) ? 1u : 0u);
                 }
                 mma_commit(&S.k_empty[j % KS]);
                 if (OWN) mma_commit(&S.ds_empty);
-                if (!OWN && j + 1 < n) dprobs(j + 1);
+                if (!OWN && j + 1 < steps_all) dprobs(j + 1);
             }
             mma_commit(&S.dq_full);
             if (*gave_up) {   // the products in flight end before TMEM is freed
@@ -215,16 +220,17 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             }
         }
     } else if (warp < 4) {
-        if (ragged) {
-            wait_for(&S.k_last, 0, gave_up);
-            const int valid = rk.n - (n - 1) * kTile, bad = kTile - valid;
-            for (int c = 0; c < KB; c++) {
-                unsigned char* k = sm + (ks - qs) + (((n - 1) % KS) * KB + c) * kBlock + valid * 128;
-                for (int e = tid - 64; e < bad * 8; e += 64) *reinterpret_cast<uint4*>(k + e * 16) = make_uint4(0, 0, 0, 0);
+        if (ragged)
+            for (int j = sums ? sums - 1 : steps_all - 1; j < steps_all; j += n) {
+                const int walk = j < sums ? 0 : 1, valid = rk.n - (n - 1) * kTile, bad = kTile - valid;
+                wait_for(&S.k_last[walk], 0, gave_up);
+                for (int c = 0; c < KB; c++) {
+                    unsigned char* k = sm + (ks - qs) + ((j % KS) * KB + c) * kBlock + valid * 128;
+                    for (int e = tid - 64; e < bad * 8; e += 64) *reinterpret_cast<uint4*>(k + e * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&S.k_fixed[walk]);
             }
-            fence_proxy_async_smem();
-            mbar_arrive(&S.k_fixed);
-        }
     } else {
         const int half = (warp - 4) >> 2, quad = warp & 3, row = q0 + quad * 32 + lane;
         const uint32_t base = tmem + ((uint32_t)quad << 21);
@@ -232,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         const long long at = (long long)h * s.Nq + rq.first + (mine ? row : 0);
         const float c = s.scale * kLog2e;
         const float lse = mine ? a.lse[at] : -INFINITY;
-        const float delta = mine ? a.delta[at] : 0.f;
+        float delta = mine ? a.delta[at] : 0.f;
         if (n > 0) {     // this half's 64 columns of the row of dO into TMEM
             wait_for(&S.q_full, 0, gave_up);
             if (half < p.vb) {
@@ -258,8 +264,23 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         int last = !mine ? -1 : s.causal ? min(rk.n - 1, row + off) : rk.n - 1;
         if (last == 0) last = -1;
         const int calm = min(rk.n - 1, s.causal ? q0 + quad * 32 + off : rk.n - 1);
-        const uint64_t c2 = pack2(c, c), l2 = pack2(lower, lower), d2 = pack2(-delta, -delta);
-        for (int j = 0; j < n; j++) {
+        const uint64_t c2 = pack2(c, c), l2 = pack2(lower, lower);
+        uint64_t d2 = pack2(sums ? 0.f : -delta, sums ? 0.f : -delta), sum2[2] = {0, 0};
+        // this row's sum over both halves' columns
+        const auto row_total = [&] {
+            float even, odd;
+            unpack2(add2(sum2[0], sum2[1]), even, odd);
+            S.part[half][quad * 32 + lane] = even + odd;
+            named_bar_sync(1, 256);
+            const float t = S.part[0][quad * 32 + lane] + S.part[1][quad * 32 + lane];
+            named_bar_sync(1, 256);
+            return t;
+        };
+        for (int j = 0; j < steps_all; j++) {
+            if (sums > 0 && j == sums) {     // delta is known
+                delta = row_total();
+                d2 = pack2(-delta, -delta);
+            }
             uint32_t x[64];
             wait_for(&S.s_full, j & 1, gave_up);
             __syncwarp();
@@ -277,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 x[i] = __float_as_uint(fast_exp2(u));
                 x[i + 1] = __float_as_uint(fast_exp2(w));
             }
-            const int j0 = j * kTile + 64 * half;
+            const int j0 = (j < sums ? j : j - sums) * kTile + 64 * half;
             const bool masked = j0 + 63 > calm || calm <= 0;
             wait_for(&S.dp_full, j & 1, gave_up);
             __syncwarp();
@@ -301,17 +322,20 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 uint32_t z[16];
 #pragma unroll
                 for (int i = i0; i < i0 + 32; i += 2) {
-                    float u, w;
-                    unpack2(mul2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                                 add2(pack2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), d2)),
-                            u, w);
+                    // P (dP - delta), or P dP in the first walk
+                    uint64_t t = mul2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                      add2(pack2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), d2));
                     if (masked) {
-                        u = j0 + i <= last ? u : 0.f;
-                        w = j0 + i + 1 <= last ? w : 0.f;
+                        float u, w;
+                        unpack2(t, u, w);
+                        t = pack2(j0 + i <= last ? u : 0.f, j0 + i + 1 <= last ? w : 0.f);
                     }
+                    sum2[(i >> 1) & 1] = add2(sum2[(i >> 1) & 1], t);
+                    float u, w;
+                    unpack2(t, u, w);
                     z[(i - i0) >> 1] = pack_bf16(u, w);
                 }
-                tmem_st16u(base + TE + kDsHalf * half + (i0 >> 1), z);
+                if (j >= sums) tmem_st16u(base + TE + kDsHalf * half + (i0 >> 1), z);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -319,6 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             if (lane == 0) mbar_arrive(&S.ds_full);
         }
         if (n > 0) {
+            if (sums == 0) delta += row_total();      // (P's rows add up to one)
+            if (mine && half == 0) a.delta[at] = delta;
             wait_for(&S.dq_full, 0, gave_up);
             __syncwarp();
             tc_fence_after();
