@@ -10,6 +10,10 @@
 // products from there.  One product's tensor-core time covers the other's elementwise work: while the threads turn
 // S(i+1) into P, dK(i) and dP(i+1) run; while they turn dP into dS, dV and the next S run.
 //
+// 8 x 4096 tokens, 16 query and 4 key heads of 128: 0.67 ms for dQ (54 % of the tensor cores' cycles, 2080 a step where
+// the products need 1536, and a start of 6000 a CTA that the loads of its first tiles take) and 0.71 ms for dK and dV
+// (67 %; 2400 a step for 2048).
+//
 // Roles (12 warps): warp 0 loads tiles by TMA, warp 1 issues products, warps 2-3 bring lse and delta and blank the
 // rows past a ragged end, warps 4-11 do the elementwise work, half of a tile's columns each.
 #include "mla_tc.cuh"
@@ -27,6 +31,7 @@ struct Params {
     CUtensorMap qn, qr, dO, kn, kr, v;   // boxes: the held side 128 rows, the walked side as many as a step takes
     int nb, vb;                          // 64-column blocks of dn, dv
     int tiles;                           // tiles of the held side in the longest sequence
+    int starve;                          // failure-path test hook: a step whose K (for dQ) or Q is announced, but never loaded
 };
 
 // 16-value steps of block c of a query or key
@@ -133,8 +138,10 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 uint64_t* bar = ragged && (j == sums - 1 || j == steps_all - 1) ? &S.k_last[walk] : &S.k_full[ks_];   // to the warps that blank rows
                 mbar_arrive_expect_tx(bar, KB * kBlock);
                 const uint32_t d = ks + ks_ * KB * kBlock;
-                for (int c = 0; c < p.nb; c++) tma_load_3d(d + c * kBlock, &p.kn, bar, 64 * c, g, row);
-                if (rope) tma_load_3d(d + p.nb * kBlock, &p.kr, bar, 0, 0, row);
+                if (j != p.starve) {
+                    for (int c = 0; c < p.nb; c++) tma_load_3d(d + c * kBlock, &p.kn, bar, 64 * c, g, row);
+                    if (rope) tma_load_3d(d + p.nb * kBlock, &p.kr, bar, 0, 0, row);
+                }
                 if (bar != &S.k_full[ks_]) mbar_arrive(&S.k_full[ks_]);     // which keeps count of its stage's uses
                 kdone = j + 1;
                 if (!wait_for(&S.v_empty[vs_], ((j / VS) & 1) ^ 1, gave_up) || *gave_up) break;
@@ -144,12 +151,12 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 vdone = j + 1;
             }
             if (*gave_up) {   // a wait expired: the loads in flight land before the CTA ends
-                mbar_wait(&S.q_full, 0, nullptr, kWaitNs);
+                mbar_wait(&S.q_full, 0, nullptr, kDrainNs);
                 for (int j = max(0, kdone - KS); j < kdone; j++) {
-                    mbar_wait(&S.k_full[j % KS], (j / KS) & 1, nullptr, kWaitNs);
-                    if (ragged && (j == sums - 1 || j == steps_all - 1)) mbar_wait(&S.k_last[j < sums ? 0 : 1], 0, nullptr, kWaitNs);
+                    mbar_wait(&S.k_full[j % KS], (j / KS) & 1, nullptr, kDrainNs);
+                    if (ragged && (j == sums - 1 || j == steps_all - 1)) mbar_wait(&S.k_last[j < sums ? 0 : 1], 0, nullptr, kDrainNs);
                 }
-                for (int j = max(0, vdone - VS); j < vdone; j++) mbar_wait(&S.v_full[j % VS], (j / VS) & 1, nullptr, kWaitNs);
+                for (int j = max(0, vdone - VS); j < vdone; j++) mbar_wait(&S.v_full[j % VS], (j / VS) & 1, nullptr, kDrainNs);
             }
         }
     } else if (warp == 1) {
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             mma_commit(&S.dq_full);
             if (*gave_up) {   // the products in flight end before TMEM is freed
                 mma_commit(&S.drain);
-                mbar_wait(&S.drain, 0, nullptr, kWaitNs);
+                mbar_wait(&S.drain, 0, nullptr, kDrainNs);
             }
         }
     } else if (warp < 4) {
@@ -458,8 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
                 if (!wait_for(&S.q_empty[qst], ((i / QS) & 1) ^ 1, gave_up) || *gave_up) break;
                 mbar_arrive_expect_tx(&S.q_full[qst], KB * kStep);
                 const uint32_t q = qs + qst * KB * kStep, d = dos + st * p.vb * kStep;
-                for (int c = 0; c < p.nb; c++) tma_load_3d(q + c * kStep, &p.qn, &S.q_full[qst], 64 * c, h, row);
-                if (rope) tma_load_3d(q + p.nb * kStep, &p.qr, &S.q_full[qst], 0, h, row);
+                if (i != p.starve) {
+                    for (int c = 0; c < p.nb; c++) tma_load_3d(q + c * kStep, &p.qn, &S.q_full[qst], 64 * c, h, row);
+                    if (rope) tma_load_3d(q + p.nb * kStep, &p.qr, &S.q_full[qst], 0, h, row);
+                }
                 qdone = i + 1;
                 if (!wait_for(&S.do_empty[st], ((i >> 1) & 1) ^ 1, gave_up) || *gave_up) break;
                 mbar_arrive_expect_tx(&S.do_full[st], p.vb * kStep);
@@ -471,9 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
                 }
             }
             if (*gave_up) {   // a wait expired: the loads in flight land before the CTA ends
-                mbar_wait(&S.kv_full, 0, nullptr, kWaitNs);
-                for (int i = max(0, qdone - QS); i < qdone; i++) mbar_wait(&S.q_full[i % QS], (i / QS) & 1, nullptr, kWaitNs);
-                for (int i = max(0, ddone - 2); i < ddone; i++) mbar_wait(&S.do_full[i & 1], (i >> 1) & 1, nullptr, kWaitNs);
+                mbar_wait(&S.kv_full, 0, nullptr, kDrainNs);
+                for (int i = max(0, qdone - QS); i < qdone; i++) mbar_wait(&S.q_full[i % QS], (i / QS) & 1, nullptr, kDrainNs);
+                for (int i = max(0, ddone - 2); i < ddone; i++) mbar_wait(&S.do_full[i & 1], (i >> 1) & 1, nullptr, kDrainNs);
             }
         }
     } else if (warp == 1) {
@@ -545,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             mma_commit(&S.acc_full);
             if (*gave_up) {   // the products in flight end before TMEM is freed
                 mma_commit(&S.drain[0]);
-                mbar_wait(&S.drain[0], 0, nullptr, kWaitNs);
+                mbar_wait(&S.drain[0], 0, nullptr, kDrainNs);
             }
         }
     } else if (warp < 4) {
@@ -749,6 +758,7 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs& a, cudaStream_t st)
     Params p;
     memset(&p, 0, sizeof(p));
     p.a = a;
+    p.starve = test_starve_chunk();
     p.nb = (s.dn + 63) / 64;
     p.vb = (s.dv + 63) / 64;
     const int kb = p.nb + (s.dr > 0 ? 1 : 0);

@@ -10,8 +10,11 @@
 // waiting for its own operands only, so that the next tiles' scores run ahead of this tile's outputs; warp 3 lays the
 // queries out; warps 4-7 do the softmax.  The softmax keeps a running
 // maximum of each query row but lowers scores by an old one until a score exceeds it by 2^16: exp2 and fp32 hold that
-// range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (at a sequence's first tile
-// and rarely after).  HBM bounds it (figures at the launch below).
+// range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (rarely after a sequence's first
+// tile).  HBM bounds it while the query rows fit one group: 8 x 32768 rows of 512 + 64 values under 16 heads take 56 us
+// (302 MB, 5.4 TB/s; 3250 cycles a 64-row tile are 22.7 bytes a cycle and SM, the card's rate, the rest start and end).
+// 160 rows in four groups take 104 us where the bytes alone need 20: two tiles fit beside 54 KB of queries, so a tile's
+// load waits for the products of the one before the last.
 #include "mla_decode_common.cuh"
 #include "mla_tc.cuh"
 
@@ -33,6 +36,7 @@ struct Params {
     int npair, nrope;            // ring sizes
     int box;                     // rows of a TMA box: divides the page and the tile
     int total_rows;              // rows of the cache; a box that starts there reads as zeros
+    int starve;                  // failure-path test hook: a worker's tile that is announced, but never loaded (-1: none)
     uint32_t rope_off, q_off, p_off;   // shared memory, from the pair ring's start
 };
 
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     uint64_t* bar = &S.pair_full[slot];
                     if (elect_one()) mbar_arrive_expect_tx(bar, blocks * kBlockBytes);
                     __syncwarp();
-                    if (PAIR ? lane < subs && (int)rank < blocks : lane < blocks * subs) {   // a lane a box
+                    if ((PAIR ? lane < subs && (int)rank < blocks : lane < blocks * subs) && i != p.starve) {   // a lane a box
                         const int c = PAIR ? rank : blk;
                         const uint32_t dst = pairs + slot * kPairBytes + c * kBlockBytes + sub * p.box * 128;
                         if (PAIR)
@@ -237,11 +241,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         if (*gave_up) {   // a wait expired: the copies in flight land before the CTA ends
             for (int i = 0; i < p.npair; i++) {
                 const int n = (issued - i + p.npair - 1) / p.npair;
-                if (n > 0) mbar_wait(&S.pair_full[i], (uint32_t)(n - 1) & 1, nullptr, kWaitNs);
+                if (n > 0) mbar_wait(&S.pair_full[i], (uint32_t)(n - 1) & 1, nullptr, kDrainNs);
             }
             for (int i = 0; i < p.nrope; i++) {
                 const int n = (rissued - i + p.nrope - 1) / p.nrope;
-                if (n > 0) mbar_wait(&S.rope_full[i], (uint32_t)(n - 1) & 1, nullptr, kWaitNs);
+                if (n > 0) mbar_wait(&S.rope_full[i], (uint32_t)(n - 1) & 1, nullptr, kDrainNs);
             }
         }
     } else if (warp == 1) {
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             }
             if (*gave_up) {   // the products in flight end before TMEM is freed
                 mma_commit(&S.drain[0]);
-                mbar_wait(&S.drain[0], 0, nullptr, kWaitNs);
+                mbar_wait(&S.drain[0], 0, nullptr, kDrainNs);
             }
         }
     } else if (warp == 2) {
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             }
             if (*gave_up) {
                 mma_commit(&S.drain[1]);
-                mbar_wait(&S.drain[1], 0, nullptr, kWaitNs);
+                mbar_wait(&S.drain[1], 0, nullptr, kDrainNs);
             }
         }
     } else if (warp >= 4) {
@@ -559,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             do i++;
             while (!r.step() && i < total);
         }
-        if (loaded != ~0u && *gave_up) mbar_wait(&S.q_full, loaded & 1, nullptr, kWaitNs);   // the copy in flight lands
+        if (loaded != ~0u && *gave_up) mbar_wait(&S.q_full, loaded & 1, nullptr, kDrainNs);   // the copy in flight lands
     }
     tc_fence_before();
     if (PAIR)
@@ -618,6 +622,7 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st)
     p.box = 8;
     while (p.box < kDecodeTile && s.page % (2 * p.box) == 0) p.box *= 2;
     p.total_rows = s.npages * s.page;
+    p.starve = test_starve_chunk();
     const int W = s.dc + s.dr;
     p.q_tma = a.qc.tok == (long long)s.H * a.qc.head && (s.dr == 0 || a.qr.tok == (long long)s.H * a.qr.head) &&
               (long long)s.B * s.T * s.H < 0x7fffffffLL;

@@ -7,6 +7,10 @@
 // Q and K (K's is the same for every head).  The maximum that scores are lowered by is raised, and O rescaled, only
 // when a score exceeds it by 2^8: P, the sums and O hold that range with the same relative precision.
 //
+// Shared memory's 128 bytes a cycle and the tensor cores bound a long walk together: a step of two 128 x 128 tiles takes
+// 2640 cycles, 2048 of them products (2 x 2048 queries over 8192 keys, 16 heads of 128: 169 us, 1.42 PFLOP/s; 8 x 4096
+// tokens: 0.39 ms).  With three 64-column blocks a query tile pair leaves V one stage, and its load shows.
+//
 // Roles (12 warps): warp 0 loads tiles by TMA, warp 1 issues products, warps 2-3 blank the value rows past a ragged
 // end (a weight of zero would still meet a NaN there), warps 4-7 and 8-11 are the two tiles' softmax.
 #include "mla_tc.cuh"
@@ -29,6 +33,7 @@ struct Params {
     int tiles;                  // CTAs that the longest sequence's queries take
     uint32_t v_off;             // V's stages behind K's in shared memory
     int kstages, vstages;
+    int starve;                 // failure-path test hook: a key tile that is announced, but never loaded (-1: none)
 };
 
 struct Shared {
@@ -74,6 +79,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 3 - NT) fwd_tc_kernel(const __
     };
     const auto load_k = [&](int j, int st) {
         mbar_arrive_expect_tx(&S.k_full[st], KB * kBlock);
+        if (j == p.starve) return;
         const uint32_t d = ks + st * KB * kBlock;
         for (int c = 0; c < p.nb; c++) tma_load_3d(d + c * kBlock, &p.kn, &S.k_full[st], 64 * c, g, rk.first + j * kTile);
         if (rope) tma_load_3d(d + p.nb * kBlock, &p.kr, &S.k_full[st], 0, 0, rk.first + j * kTile);
@@ -134,14 +140,14 @@ __global__ void __launch_bounds__(128 + 128 * NT, 3 - NT) fwd_tc_kernel(const __
                 }
                 if (*gave_up) {   // a wait expired: the loads in flight land before the CTA ends
                     for (int t = 0; t < 2; t++)
-                        if (nt[t]) mbar_wait(&S.q_full[t], 0, nullptr, kWaitNs);
+                        if (nt[t]) mbar_wait(&S.q_full[t], 0, nullptr, kDrainNs);
                     for (int j = max(0, klast - p.kstages + 1); j <= klast; j++)
-                        mbar_wait(&S.k_full[j % p.kstages], (j / p.kstages) & 1, nullptr, kWaitNs);
+                        mbar_wait(&S.k_full[j % p.kstages], (j / p.kstages) & 1, nullptr, kDrainNs);
                     for (int j = max(0, vlast - p.vstages + 1); j <= vlast; j++) {
                         if (ragged && j == n - 1)
-                            mbar_wait(&S.v_last, 0, nullptr, kWaitNs);
+                            mbar_wait(&S.v_last, 0, nullptr, kDrainNs);
                         else
-                            mbar_wait(&S.v_full[j % p.vstages], (j / p.vstages) & 1, nullptr, kWaitNs);
+                            mbar_wait(&S.v_full[j % p.vstages], (j / p.vstages) & 1, nullptr, kDrainNs);
                     }
                 }
             }
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 3 - NT) fwd_tc_kernel(const __
                 }
                 if (*gave_up) {   // the products in flight end before TMEM is freed
                     mma_commit(&S.drain);
-                    mbar_wait(&S.drain, 0, nullptr, kWaitNs);
+                    mbar_wait(&S.drain, 0, nullptr, kDrainNs);
                 }
             }
         } else if (ragged) {
@@ -395,6 +401,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st)
     Params p;
     memset(&p, 0, sizeof(p));
     p.a = a;
+    p.starve = test_starve_chunk();
     p.nb = (s.dn + 63) / 64;
     p.vb = (s.dv + 63) / 64;
     // without keys the maps have nothing to describe and no load is made
@@ -405,7 +412,8 @@ cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st)
         return cudaErrorInvalidValue;
     const int kb = p.nb + (s.dr > 0 ? 1 : 0);
     // One tile and two CTAs an SM for short walks, where a CTA's start and end weigh most and overlap the other's work;
-    // two tiles share each load of keys and values, which long walks need.
+    // two tiles share each load of keys and values, which long walks need.  Two tiles against one, us: 12 x 256 tokens
+    // 20.0 / 18.0, 12 x 512 32.8 / 30.9, 8 x 1024 51.4 / 51.7, 6 x 1536 65.1 / 69.3, 2 x 4096 105 / 117.
     const bool single = kb < 3 && s.Tk <= kShort;
     if (kb == 1) return single ? run<1, 1>(p, st) : run<1, 2>(p, st);
     if (kb == 2) return single ? run<2, 1>(p, st) : run<2, 2>(p, st);

@@ -17,6 +17,8 @@ using fwdtc::kWaitNs;
 using namespace tc;
 
 constexpr float kLn2 = 0.6931471805599453f;
+// after a wait has expired: the limit for each copy or product still in flight, which lands within microseconds
+constexpr uint64_t kDrainNs = kWaitNs / 8;
 
 // A wait on a phase of `bar`.  After one wait of the CTA has expired, `gave_up` is set and every wait returns at once:
 // the roles then run through their loops without touching data, so that none is left at a barrier.
