@@ -381,7 +381,9 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, int sta
     }
 }
 
-// rows a thread for `rows` held rows in each of `units` (head, sequence) pairs
+// Rows a thread for `rows` held rows in each of `units` (head, sequence) pairs: the most that give every SM a CTA.
+// A training step with 4, 2 and 1 rows, us: 2 x 333 tokens under 4 heads 228 / 174 / 156, 2 x 1024 under 8 672 / 681 / 864,
+// 4 x 2048 under 8 3323 / 3704 / 5464.
 int pick_rows(int rows, long long units)
 {
     for (int r = 4; r > 1; r >>= 1)

@@ -269,7 +269,8 @@ cudaError_t run_rows(const DecodeArgs& a, cudaStream_t st)
     return cudaGetLastError();
 }
 
-// launched as a dependent of the workers' kernel: its blocks find their place while the last workers finish
+// Launched as a dependent of the workers' kernel: its blocks find their place while the last workers finish.  A second
+// launch, not the last worker of a sequence, because the workspace is the caller's and holds no counters between calls.
 template <typename T>
 cudaError_t run_join(const DecodeArgs& a, cudaStream_t st)
 {

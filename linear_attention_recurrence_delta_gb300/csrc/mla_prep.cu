@@ -3,7 +3,9 @@
 // Elementwise but for one sum a token, so HBM bounds it: each input is read once and each output written once, in
 // 16-byte pieces.  A warp holds a token's whole latent in registers (its sum of squares is one warp reduction); a
 // thread rotates 8 pairs of two query heads by angles that it reads once.  Forwards both kinds of block run in one launch, because a decoding step is
-// bound by launches, not bytes.
+// bound by launches, not bytes.  32768 tokens of 256 + 64 values with 16 heads of 64: 41 us forwards (176 MB, 4.3 TB/s),
+// 28 us for the rows and 15 us for the latents of the gradients, 7 us for their sum over 608 blocks; a decoding step of
+// 24 tokens takes 5 us from a cold cache, and the call's host time more.
 #include "mla_internal.h"
 
 namespace gdn {
@@ -60,6 +62,8 @@ __device__ __forceinline__ void angles(const float* rot, int u, int dr, float (&
 }
 
 // What is rotated: a thread turns 8 pairs of kHeads query heads of one token by the same angles, or 8 pairs of its key.
+// (Of 1, 2 and 4 heads two are fastest: 121, 94 and 146 us for the training batch's both passes; more read the angles
+// less often but hold fewer threads on an SM.)
 constexpr int kHeads = 2;
 __host__ __device__ inline int threads_a_token(const gdn_mla_prep_t& s)
 {
