@@ -267,8 +267,10 @@ __global__ void __launch_bounds__(1024) sum_dw_kernel(const float* part, float* 
     __shared__ float red[32][33];
     const int c = blockIdx.x * 32 + threadIdx.x;
     float s = 0.f;
-    if (c < dc)
+    if (c < dc) {
+#pragma unroll 8
         for (int b = threadIdx.y; b < blocks; b += 32) s += part[(long long)b * dc + c];
+    }
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && c < dc) {
