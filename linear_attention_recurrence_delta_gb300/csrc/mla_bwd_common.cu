@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kDkrThreads) dkr_kernel(const AttnArgs a)
     const int r = (int)(u / per), c = (int)(u - (long long)r * per) << 3;
     if (r >= rk.n) return;
     float t[8] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int g = 0; g < s.Hkv; g++) {
         float x[8];
         load8(a.dkr_part + ((long long)g * s.Nk + rk.first + r) * s.dr + c, x);
