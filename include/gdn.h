@@ -42,8 +42,9 @@
  *
  * Test hook: the library's own failure-path tests set the environment
  * variable GDN_TEST_STARVE_CHUNK=k before a process's first call; the
- * tensor-core forward then never loads chunk k, its bounded wait expires and
- * the device status reads GDN_ERR_TIMEOUT.  It is read once per process and
+ * tensor-core forward then never loads chunk k (a latent-attention kernel its
+ * k-th tile), its bounded wait expires and the device status reads
+ * GDN_ERR_TIMEOUT.  It is read once per process and
  * must not be set in production.
  *
  * Limits: B, H >= 1 and B * H <= 2^26; T >= 0 (with T = 0 the per-token pointers may be NULL:

@@ -158,7 +158,7 @@ int decode_max_tokens();
 
 // Failure-path test hook, for the library's own tests only: the value of the environment variable
 // GDN_TEST_STARVE_CHUNK, read once per process (-1 when it is not set).  With it set to k, the tensor-core
-// forward never issues the loads of chunk k, so that chunk's bounded wait expires, the kernel winds down and the
+// forward never issues the loads of chunk k (each latent-attention kernel those of its k-th tile), so that wait expires, the kernel winds down and the
 // status word reads GDN_ERR_TIMEOUT.  Set it before the process's first forward call.
 int test_starve_chunk();
 

@@ -173,14 +173,27 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs 
     }
 }
 
-// o = sum_i 2^(l_i - l) o_i over a sequence's pieces, in their order; a warp a query row, a thread 4 columns of it at a
-// time.  Sequences that one worker covered are written already; empty ones become zeros here.  Block (0, 0) also
-// gathers the workers' error words.
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d)
+{
+    *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d)
+{
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// o = sum_i 2^(l_i - l) o_i over a sequence's pieces, in their order.  Many rows fill the card with a warp a row, a
+// thread 8 columns of it at a time.  Few rows (SPREAD) take a block for 128 columns of a row, a warp a quarter of the
+// pieces and the quarters added in their order: one warp would walk up to 152 pieces in turn.  Sequences that one worker
+// covered are written already; empty ones become zeros here.  Block (0, 0) also gathers the workers' error words.
 constexpr int kJoinWarps = 4, kJoinAhead = 8;
-template <typename T>
+template <typename T, bool SPREAD>
 __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const DecodeArgs a)
 {
     __shared__ int where[2];
+    __shared__ float4 quarter[SPREAD ? kJoinWarps : 1][32];
+    __shared__ float quarter_sum[SPREAD ? kJoinWarps : 1];
     const gdn_mla_cache_t& s = a.s;
     const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     const Deal deal{a.len, s.B, s.maxpages * s.page};
@@ -202,15 +215,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
             a.status[1] = 0;
         }
     }
-    const int row = blockIdx.x * kJoinWarps + (tid >> 5);
+    const int chunks = SPREAD ? (s.dc + 127) >> 7 : 1, warp = tid >> 5;
+    const int row = SPREAD ? blockIdx.x / chunks : blockIdx.x * kJoinWarps + warp;
+    const int part = SPREAD ? blockIdx.x - row * chunks : 0;    // which 128 columns
     if (row >= s.T * s.H) return;
     const int tiles = deal.tiles(b);
     const long long out = (long long)b * s.T * s.H + row;
     T* o = (T*)a.o + out * s.dc;
     if (tiles == 0) {
         const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int c = 8 * lane; c < s.dc; c += 256) store8(o + c, z);
-        if (lane == 0 && a.lse) a.lse[out] = -INFINITY;
+        if (part == 0 && (!SPREAD || warp == 0))
+            for (int c = 8 * lane; c < s.dc; c += 256) store8(o + c, z);
+        if (part == 0 && lane == 0 && (!SPREAD || warp == 0) && a.lse) a.lse[out] = -INFINITY;
         return;
     }
     const int c0 = where[1] / where[0], n = (where[1] + tiles - 1) / where[0] - c0 + 1;
@@ -225,6 +241,41 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
 #pragma unroll
     for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
     const float base = m == -INFINITY ? 0.f : m;
+    if constexpr (SPREAD) {
+        const int c = 128 * part + 4 * lane, from = n * warp / kJoinWarps, to = n * (warp + 1) / kJoinWarps;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        for (int i0 = from; i0 < to; i0 += 32) {
+            const float w = i0 + lane < to ? exp2f(L[(long long)(i0 + lane) * a.rows] - base) : 0.f;
+            const int upto = min(32, to - i0);
+            for (int i = 0; i < upto; i += kJoinAhead) {
+                float4 v[kJoinAhead];
+#pragma unroll
+                for (int e = 0; e < kJoinAhead; e++)
+                    if (c < s.dc && i + e < upto) v[e] = *reinterpret_cast<const float4*>(O + (i0 + i + e) * next + c);
+#pragma unroll
+                for (int e = 0; e < kJoinAhead; e++)
+                    if (i + e < upto) {
+                        const float f = __shfl_sync(0xffffffffu, w, i + e);
+                        sum += f;
+                        if (c < s.dc) x = make_float4(x.x + f * v[e].x, x.y + f * v[e].y, x.z + f * v[e].z, x.w + f * v[e].w);
+                    }
+            }
+        }
+        quarter[warp][lane] = x;
+        if (lane == 0) quarter_sum[warp] = sum;
+        __syncthreads();      // row, tiles and n are the block's: all of its warps come here
+        if (warp) return;
+        for (int k = 1; k < kJoinWarps; k++) {
+            const float4 y = quarter[k][lane];
+            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            sum += quarter_sum[k];
+        }
+        const float inv = sum > 0.f ? 1.f / sum : sum;    // zero stays zero, a NaN a NaN
+        if (c < s.dc) store4(o + c, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+        if (part == 0 && lane == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
+        return;
+    }
     float sum = 0.f;
     for (int c = 8 * lane; c < 8 * 32 * ((s.dc + 255) / 256); c += 256) {   // every lane passes every shuffle
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -271,11 +322,19 @@ cudaError_t run_rows(const DecodeArgs& a, cudaStream_t st)
 
 // Launched as a dependent of the workers' kernel: its blocks find their place while the last workers finish.  A second
 // launch, not the last worker of a sequence, because the workspace is the caller's and holds no counters between calls.
+// The rows' pieces go to a block's warps where rows are few for the pieces that each has, about workers / B.  A warp a row
+// against a block for 128 columns of a row, us of the call (sequences x lengths, rows a sequence, latent width):
+// 1 x 32768, 64, 512: 68.8 / 32.8; 2 x 32768, 16, 512: 40.4 / 26.7; 8 x 32768, 16, 512: 63.6 / 60.4; 16 x 16384, 16, 512:
+// 63.2 / 61.4; 4 x 32768, 160, 512: 108.4 / 109.6; 32 x 8192, 16, 512: 61.8 / 64.1; 16 x 6000, 40, 512: 40.1 / 42.3;
+// 64 x 4096, 16, 256: 43.2 / 47.1.
+constexpr long long kSpread = 4096;
 template <typename T>
 cudaError_t run_join(const DecodeArgs& a, cudaStream_t st)
 {
+    const bool spread = (long long)a.s.B * a.s.B * a.s.T * a.s.H <= kSpread;
+    const int rows = a.s.T * a.s.H, chunks = (a.s.dc + 127) / 128;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.s.T * a.s.H + kJoinWarps - 1) / kJoinWarps, a.s.B);
+    cfg.gridDim = dim3(spread ? rows * chunks : (rows + kJoinWarps - 1) / kJoinWarps, a.s.B);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute attr = {};
@@ -283,7 +342,8 @@ cudaError_t run_join(const DecodeArgs& a, cudaStream_t st)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_join_kernel<T>, a);
+    if (spread) return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, true>, a);
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, false>, a);
 }
 
 }  // namespace

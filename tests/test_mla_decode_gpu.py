@@ -82,6 +82,14 @@ def test_split_and_join(n):
     compare(len(n), n, 1, 16, 64, 32, 64, "bf16")
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n,T,H,dc", [([5000, 0, 3000], 1, 16, 512), ([2500, 1900, 0, 700], 8, 32, 200), ([150], 1, 5, 72),
+                                      ([900, 0] + [700] * 6, 8, 9, 264)])
+def test_both_joins(n, T, H, dc, io):
+    """Rows x sequences on both sides of 4096, where the join of a sequence's pieces changes its form."""
+    compare(T + H, n, T, H, dc, 16, 16, io)
+
+
 def test_sharp_scores():
     """One row takes almost all the weight, and the largest score moves from tile to tile."""
     compare(77, [1000, 333], 1, 16, 256, 64, 64, "bf16", std=8.0)
