@@ -9,7 +9,11 @@ DecodePlan decode_plan(const gdn_mla_cache_t& s)
 {
     DecodePlan p;
     const int all = s.T * s.H;
-    const int most = s.io == GDN_BF16 ? 64 : 8;   // query rows of a worker on the tensor, the CUDA cores
+    // Query rows of a worker on the tensor, the CUDA cores.  Fewer groups send each cache tile through fewer SMs, which
+    // outweighs the shorter ring beside 80 rows.  At most 64 against 80, us: 32 x 4 drafted tokens of 40 heads over 512 + 64,
+    // up to 6000 rows 114.7 / 92.2, over 256 + 64 77.8 / 53.3; 72 rows 65.6 / 60.9; 320 rows 228 / 172; two sequences of 160
+    // rows 22.5 / 24.8.
+    const int most = s.io == GDN_BF16 ? kDecodeRows : 8;
     p.groups = (all + most - 1) / most;
     // on the tensor cores two groups share each load of the cache (a cluster of two CTAs)
     if (s.io == GDN_BF16 && p.groups > 1 && p.groups % 2) p.groups++;

@@ -13,8 +13,8 @@
 // range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (rarely after a sequence's first
 // tile).  HBM bounds it while the query rows fit one group: 8 x 32768 rows of 512 + 64 values under 16 heads take 56 us
 // (302 MB, 5.4 TB/s; 3250 cycles a 64-row tile are 22.7 bytes a cycle and SM, the card's rate, the rest start and end).
-// 160 rows in four groups take 104 us where the bytes alone need 20: two tiles fit beside 54 KB of queries, so a tile's
-// load waits for the products of the one before the last.
+// A call of 160 rows in two groups takes 92 us where the bytes alone need 20: less than two tiles fit beside 92 KB of queries, so a
+// tile's load waits for the products of the one before it.
 #include "mla_decode_common.cuh"
 #include "mla_tc.cuh"
 
@@ -24,8 +24,10 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxPairs = 16, kMaxRope = 4;
+constexpr int kMaxPairs = 16, kMaxRope = 4, kMaxCols = kDecodeRows;
 constexpr uint32_t kPairBytes = 16384, kBlockBytes = 8192;
+// buffers of weights: with 80 query rows a second one would take the room of half a pair of cache blocks
+template <int NC> constexpr int kWeights = NC > 64 ? 1 : 2;
 constexpr float kSlack = 16.f;          // log2 by which a score may exceed the maximum it is lowered by
 
 struct Params {
@@ -43,8 +45,8 @@ struct Params {
 struct Shared {
     uint64_t pair_full[kMaxPairs], pair_empty[kMaxPairs], rope_full[kMaxRope], rope_empty[kMaxRope];
     uint64_t q_full, q_empty, s_full[2], p_full[2], p_empty[2], o_full, drain[2];
-    alignas(16) float top[64];   // read four at a time
-    float keep[64], up[64], red[4][64], back[64];
+    alignas(16) float top[kMaxCols];   // read four at a time
+    float keep[kMaxCols], up[kMaxCols], red[4][kMaxCols], back[kMaxCols];
     uint32_t tmem, gave_up;
     int b, tile, total;
 };
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 wait_for(&S.p_full[i & 1], (uint32_t)(i >> 1) & 1, gave_up);
                 tc_fence_after();
                 const bool go = !*gave_up;
-                const uint64_t pt = pbase + at_desc(ps + (uint32_t)(i & 1) * (NC * 128));
+                const uint64_t pt = pbase + at_desc(ps + (uint32_t)(i & (kWeights<NC> - 1)) * (NC * 128));
                 for (int m = 0; m < p.np; m++) {
                     const uint64_t v = vbase + at_desc(pairs + slot * kPairBytes);
                     if (go) {
@@ -444,8 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     tmem_wait_st();
                 }
             }
-            if (i >= 2) wait_for(&S.p_empty[buf], (uint32_t)((i - 2) >> 1) & 1, gave_up);
-            unsigned char* P = sm + p.p_off + buf * (NC * 128);
+            // the buffer's last weights are read
+            if (i >= kWeights<NC>) wait_for(&S.p_empty[(i - kWeights<NC>) & 1], (uint32_t)((i - kWeights<NC>) >> 1) & 1, gave_up);
+            unsigned char* P = sm + p.p_off + (i & (kWeights<NC> - 1)) * (NC * 128);
 #pragma unroll
             for (int n = 0; n < HC; n++) {
                 const float y = fast_exp2(x[n]);
@@ -581,9 +584,9 @@ template <int NC, bool PAIR>
 cudaError_t run(Params& p, cudaStream_t st)
 {
     const int blocks = p.nb + (p.a.s.dr > 0 ? 1 : 0);
-    const uint32_t q = blocks * NC * 128, pp = 2 * NC * 128;
-    const uint32_t room = 232448 - 1024 - (uint32_t)sizeof(Shared) - 4096;   // 4 KB: a join block beside the worker
-    p.nrope = p.a.s.dr == 0 ? 0 : p.np >= 3 ? 2 : 4;
+    const uint32_t q = blocks * NC * 128, pp = kWeights<NC> * NC * 128;
+    const uint32_t room = 232448 - 1024 - (uint32_t)sizeof(Shared) - (NC > 64 ? 2048 : 4096);   // a join block beside the worker
+    p.nrope = p.a.s.dr == 0 ? 0 : p.np >= 3 ? (NC > 64 ? 1 : 2) : 4;
     const uint32_t fixed = q + pp + p.nrope * kBlockBytes;
     p.npair = (int)((room - fixed) / kPairBytes);
     if (p.npair > kMaxPairs) p.npair = kMaxPairs;
@@ -611,7 +614,7 @@ cudaError_t run(Params& p, cudaStream_t st)
 
 }  // namespace
 
-// Workers on the tensor cores: bf16 query rows in groups of at most 64.
+// Workers on the tensor cores: bf16 query rows in groups of at most 80.
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st)
 {
     const gdn_mla_cache_t& s = a.s;
@@ -626,14 +629,15 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st)
     const int W = s.dc + s.dr;
     p.q_tma = a.qc.tok == (long long)s.H * a.qc.head && (s.dr == 0 || a.qr.tok == (long long)s.H * a.qr.head) &&
               (long long)s.B * s.T * s.H < 0x7fffffffLL;
-    const int nc = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 48 ? 48 : 64;
+    const int nc = a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : a.rows <= 48 ? 48 : a.rows <= 64 ? 64 : 80;
     if (!row_map(&p.map, a.cache, (long long)W, p.total_rows, W, p.box) ||
         (p.q_tma && (!row_map(&p.qc, a.qc.p, a.qc.head, (long long)s.B * s.T * s.H, s.dc, nc) ||
                      (s.dr > 0 && !row_map(&p.qr, a.qr.p, a.qr.head, (long long)s.B * s.T * s.H, s.dr, nc)))))
         return cudaErrorInvalidValue;
-    if (a.groups == 1) return nc == 16 ? run<16, false>(p, st) : nc == 32 ? run<32, false>(p, st) : nc == 48 ? run<48, false>(p, st) : run<64, false>(p, st);
-    // two groups and more have more than 64 rows in all: at least 33 each
-    return nc == 48 ? run<48, true>(p, st) : run<64, true>(p, st);
+    if (a.groups == 1)
+        return nc == 16 ? run<16, false>(p, st) : nc == 32 ? run<32, false>(p, st) : nc == 48 ? run<48, false>(p, st) : nc == 64 ? run<64, false>(p, st) : run<80, false>(p, st);
+    // two groups and more have more than 80 rows in all: at least 41 each
+    return nc == 48 ? run<48, true>(p, st) : nc == 64 ? run<64, true>(p, st) : run<80, true>(p, st);
 }
 
 }  // namespace mla

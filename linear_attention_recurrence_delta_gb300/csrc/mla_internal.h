@@ -66,6 +66,7 @@ struct DecodePlan {
 DecodePlan decode_plan(const gdn_mla_cache_t& s);
 
 constexpr int kDecodeTile = 64;    // cache rows a step of a decode worker covers
+constexpr int kDecodeRows = 80;    // query rows that one takes at most on the tensor cores
 
 int prep_bwd_blocks(int N);
 

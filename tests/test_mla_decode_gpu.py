@@ -57,6 +57,20 @@ def test_rows(io, T, H):
     compare(T * 100 + H, [130, 64, 7, 300], T, H, 128, 32, 16, io)
 
 
+@pytest.mark.parametrize("dc,dr", [(512, 64), (256, 64), (448, 0), (72, 16)])
+@pytest.mark.parametrize("T,H", [(2, 24), (1, 49), (5, 13), (2, 40), (1, 81), (2, 48), (3, 43), (2, 80), (7, 23)])
+def test_group_sizes(T, H, dc, dr):
+    """48 to 161 query rows: every size of a worker's group, alone and in pairs that share the cache's loads."""
+    compare(T * 200 + H + dc, [300, 0, 65, 700], T, H, dc, dr, 16, "bf16")
+
+
+@pytest.mark.parametrize("n", [[20000], [3000, 1, 12000, 0, 500]])
+@pytest.mark.parametrize("T,H", [(2, 40), (4, 40)])
+def test_long_drafts(n, T, H):
+    """Many tiles a worker, so that every ring goes round, with a new piece in between."""
+    compare(len(n) + T, n, T, H, 512, 64, 64, "bf16")
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("dc,dr", [(256, 64), (512, 64), (512, 0), (64, 16), (8, 8), (200, 24), (448, 48), (72, 0)])
 def test_widths(io, dc, dr):
