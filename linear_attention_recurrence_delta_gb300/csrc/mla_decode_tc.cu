@@ -1,19 +1,19 @@
 // mla_decode_tc.cu -- the decode worker on the tensor cores (bf16).
 //
 // Scores and outputs are formed transposed, S^T = K Q^T and O^T = V^T P^T, so that the cache's rows are the tall side
-// of every product (M = 64 rows, M = 128 latent columns) and the few query rows its narrow one (N = 16..64): with 16
+// of every product (M = 64 rows, M = 128 latent columns) and the few query rows its narrow one (N = 16..80): with 16
 // heads nothing is padded.  The same shared-memory tile serves both products, as a K-major operand of the first and,
 // its columns read as rows, as an MN-major operand of the second: each cache byte crosses HBM once.
 //
-// Roles of a CTA (one per SM, 8 warps): warp 0 streams the cache by TMA through a ring of 64 rows x 128 columns
+// Roles of a CTA (one per SM, 12 warps): warp 0 streams the cache by TMA through a ring of 64 rows x 128 columns
 // pieces (page by page: a page's rows are one box); warp 1 issues the scores' products and warp 2 the outputs', each
 // waiting for its own operands only, so that the next tiles' scores run ahead of this tile's outputs; warp 3 lays the
-// queries out; warps 4-7 do the softmax.  The softmax keeps a running
+// queries out; warps 4-11 do the softmax.  The softmax keeps a running
 // maximum of each query row but lowers scores by an old one until a score exceeds it by 2^16: exp2 and fp32 hold that
 // range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (rarely after a sequence's first
 // tile).  HBM bounds it while the query rows fit one group: 8 x 32768 rows of 512 + 64 values under 16 heads take 56 us
 // (302 MB, 5.4 TB/s; 3250 cycles a 64-row tile are 22.7 bytes a cycle and SM, the card's rate, the rest start and end).
-// A call of 160 rows in two groups takes 92 us where the bytes alone need 20: less than two tiles fit beside 92 KB of queries, so a
+// A call of 160 rows in two groups takes 90 us where the bytes alone need 20: less than two tiles fit beside 92 KB of queries, so a
 // tile's load waits for the products of the one before it.
 #include "mla_decode_common.cuh"
 #include "mla_tc.cuh"
@@ -23,7 +23,7 @@ namespace mla {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384, kSoft = 256;   // kSoft of them do the softmax
 constexpr int kMaxPairs = 16, kMaxRope = 4, kMaxCols = kDecodeRows;
 constexpr uint32_t kPairBytes = 16384, kBlockBytes = 8192;
 // buffers of weights: with 80 query rows a second one would take the room of half a pair of cache blocks
@@ -86,11 +86,18 @@ struct Run {
 
 __device__ __forceinline__ uint32_t lane_base(uint32_t tmem, int quad) { return tmem + ((uint32_t)quad << 21); }
 
+__device__ __forceinline__ void tmem_ld4(uint32_t addr, float (&v)[4])
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
 template <int NC>
 __device__ __forceinline__ void load_cols(uint32_t addr, float (&v)[NC])
 {
 #pragma unroll
-    for (int c = 0; c < NC; c += 16) tmem_ld16(addr + c, *reinterpret_cast<float(*)[16]>(&v[c]));
+    for (int c = 0; c + 16 <= NC; c += 16) tmem_ld16(addr + c, *reinterpret_cast<float(*)[16]>(&v[c]));
+#pragma unroll
+    for (int c = NC / 16 * 16; c < NC; c += 4) tmem_ld4(addr + c, *reinterpret_cast<float(*)[4]>(&v[c]));
     tmem_wait_ld();
 }
 
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         mbar_init(&S.q_empty, 1);
         for (int i = 0; i < 2; i++) {
             mbar_init(&S.s_full[i], 1);
-            mbar_init(&S.p_full[i], 4);
+            mbar_init(&S.p_full[i], kSoft / 32);
             mbar_init(&S.p_empty[i], 1);
         }
         mbar_init(&S.o_full, 1);
@@ -340,10 +347,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax, outputs
-        // An M = 64 product fills the first 16 lanes of each warp's 32 in TMEM: lanes 16..31 take over the second half
-        // of these rows' columns.
-        constexpr int HC = NC / 2;
-        const int quad = warp & 3, t = tid - 128, key = quad * 16 + (lane & 15), col0 = lane < 16 ? 0 : HC;
+        // Two warpgroups take half of the query rows' columns each (against one, us: 160 rows 92.3 to 90.1, 128 rows 92.3 to
+        // 88.2, 16 rows unchanged, 160 rows over 256 + 64 53.3 to 55.3).  An M = 64 product fills the first 16 lanes of each
+        // warp's 32 in TMEM: lanes 16..31 take over the second half of these rows' columns.
+        constexpr int HC = NC / 4;
+        const int quad = warp & 3, half = (warp - 4) >> 2, t = tid - 128, key = quad * 16 + (lane & 15);
+        const int col0 = 2 * HC * half + (lane < 16 ? 0 : HC);
         const float c = s.scale * kLog2e;
         float l[HC];
         Run r(deal, S.b, S.tile, total);
@@ -358,15 +367,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 if (t < NC) S.top[t] = 0.f;
 #pragma unroll
                 for (int n = 0; n < HC; n++) l[n] = 0.f;
-                named_bar_sync(1, 128);
+                named_bar_sync(1, kSoft);
             }
             wait_for(&S.s_full[buf], phase, gave_up);
             __syncwarp();
             tc_fence_after();
             float x[HC];
             {
-                float y[NC];
-                load_cols<NC>(lane_base(tmem, quad) + buf * NC, y);
+                float y[2 * HC];
+                load_cols<2 * HC>(lane_base(tmem, quad) + buf * NC + 2 * HC * half, y);
 #pragma unroll
                 for (int n = 0; n < HC; n++) {
                     const float other = __shfl_sync(0xffffffffu, y[n + HC], lane & 15);
@@ -398,10 +407,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     uint32_t slot = pslot + (k >> 1);
                     if (slot >= (uint32_t)p.npair) slot -= p.npair;
                     unsigned char* v = sm + slot * kPairBytes + (k & 1) * kBlockBytes + valid * 128;
-                    for (int e = t; e < bad * 8; e += 128) *reinterpret_cast<uint4*>(v + e * 16) = make_uint4(0, 0, 0, 0);
+                    for (int e = t; e < bad * 8; e += kSoft) *reinterpret_cast<uint4*>(v + e * 16) = make_uint4(0, 0, 0, 0);
                 }
             }
-            if (bar_any(1, 128, over)) {
+            if (bar_any(1, kSoft, over)) {
 #pragma unroll
                 for (int n = 0; n < HC; n++) {
                     float m = x[n];
@@ -409,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     for (int k = 8; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
                     if ((lane & 15) == 0) S.red[quad][col0 + n] = m;
                 }
-                named_bar_sync(1, 128);
+                named_bar_sync(1, kSoft);
                 if (t < NC) {
                     const float m = fmaxf(fmaxf(S.red[0][t], S.red[1][t]), fmaxf(S.red[2][t], S.red[3][t]));
                     const float up = first ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);   // what the maximum rises by
@@ -417,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     S.top[t] += up;
                     S.keep[t] = first ? 1.f : fast_exp2(-up);
                 }
-                named_bar_sync(1, 128);
+                named_bar_sync(1, kSoft);
 #pragma unroll
                 for (int n = 0; n < HC; n++) {
                     l[n] *= S.keep[col0 + n];
@@ -433,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
 #pragma unroll
                         for (int n = 0; n < 16; n++) f[n] = S.keep[n0 + n];
 #pragma unroll 1
-                        for (int m = 0; m < p.np; m++) {
+                        for (int m = half; m < p.np; m += 2) {
                             const uint32_t addr = lane_base(tmem, quad) + (2 + m) * NC + n0;
                             float o[16];
                             tmem_ld16(addr, o);
@@ -472,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 for (int k = 8; k; k >>= 1) m += __shfl_xor_sync(0xffffffffu, m, k);
                 if ((lane & 15) == 0) S.red[quad][col0 + n] = m;
             }
-            named_bar_sync(1, 128);
+            named_bar_sync(1, kSoft);
             const bool whole = from == 0 && to == tiles;
             const long long slot = ((long long)group * a.slots + cta + b) * a.rows;
             const long long out = (long long)b * s.T * s.H + row0;
@@ -487,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                         a.lse[out + t] = l2 * kLn2;
                 }
             }
-            named_bar_sync(1, 128);
+            named_bar_sync(1, kSoft);
             wait_for(&S.o_full, piece & 1, gave_up);
             __syncwarp();
             piece++;
@@ -499,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 for (int n = 0; n < 16; n++) f[n] = S.keep[n0 + n];
                 const int here = rows - n0;
 #pragma unroll 1
-                for (int m = 0; m < p.np; m++) {
+                for (int m = half; m < p.np; m += 2) {
                     const int d = 128 * m + 32 * quad + lane;
                     float o[16];
                     tmem_ld16(lane_base(tmem, quad) + (2 + m) * NC + n0, o);
@@ -519,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 }
             }
             tc_fence_before();
-            named_bar_sync(1, 128);   // the sums' words are free for the next piece
+            named_bar_sync(1, kSoft);   // the sums' words are free for the next piece
         }
     } else {
         // ------------------------------------------------------------ queries: [query rows][64 columns] blocks
