@@ -13,7 +13,7 @@
 // range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (rarely after a sequence's first
 // tile).  HBM bounds it while the query rows fit one group: 8 x 32768 rows of 512 + 64 values under 16 heads take 56 us
 // (302 MB, 5.4 TB/s; 3250 cycles a 64-row tile are 22.7 bytes a cycle and SM, the card's rate, the rest start and end).
-// A call of 160 rows in two groups takes 90 us where the bytes alone need 20: less than two tiles fit beside 92 KB of queries, so a
+// A call of 160 rows in two groups takes 86 us where the bytes alone need 20: less than two tiles fit beside 92 KB of queries, so a
 // tile's load waits for the products of the one before it.
 #include "mla_decode_common.cuh"
 #include "mla_tc.cuh"
@@ -192,6 +192,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 const int in = j / s.page, page = a.table[(long long)r.b * s.maxpages + in];
                 if (page >= 0 && page < s.npages) at = page * s.page + (j - in * s.page);
             }
+            if (rope) {
+                wait_for(&S.rope_empty[rslot], rphase ^ 1, gave_up);
+                __syncwarp();
+                if (!__any_sync(0xffffffffu, *gave_up != 0)) {
+                    uint64_t* bar = &S.rope_full[rslot];
+                    if (elect_one()) mbar_arrive_expect_tx(bar, kBlockBytes);
+                    __syncwarp();
+                    const uint32_t dst = ropes + rslot * kBlockBytes + sub * p.box * 128;
+                    if (PAIR) {
+                        if (lane < subs && (i & 1) == (int)rank) tma_load_2d_multicast(dst, &p.map, bar, s.dc, at, 3);   // in turn
+                    } else if (lane < subs) {
+                        tma_load_2d(dst, &p.map, bar, s.dc, at);
+                    }
+                    rissued++;
+                }
+                if (++rslot == (uint32_t)p.nrope) {
+                    rslot = 0;
+                    rphase ^= 1;
+                }
+            }
             for (int k = 0; k < p.np; k++) {
                 wait_for(&S.pair_empty[slot], phase ^ 1, gave_up);
                 __syncwarp();
@@ -213,26 +233,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 if (++slot == (uint32_t)p.npair) {
                     slot = 0;
                     phase ^= 1;
-                }
-            }
-            if (rope) {
-                wait_for(&S.rope_empty[rslot], rphase ^ 1, gave_up);
-                __syncwarp();
-                if (!__any_sync(0xffffffffu, *gave_up != 0)) {
-                    uint64_t* bar = &S.rope_full[rslot];
-                    if (elect_one()) mbar_arrive_expect_tx(bar, kBlockBytes);
-                    __syncwarp();
-                    const uint32_t dst = ropes + rslot * kBlockBytes + sub * p.box * 128;
-                    if (PAIR) {
-                        if (lane < subs && (i & 1) == (int)rank) tma_load_2d_multicast(dst, &p.map, bar, s.dc, at, 3);   // in turn
-                    } else if (lane < subs) {
-                        tma_load_2d(dst, &p.map, bar, s.dc, at);
-                    }
-                    rissued++;
-                }
-                if (++rslot == (uint32_t)p.nrope) {
-                    rslot = 0;
-                    rphase ^= 1;
                 }
             }
             r.step();
@@ -271,13 +271,27 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 if (first) wait_for(&S.q_full, piece++ & 1, gave_up);
                 if (i >= 2) wait_for(&S.p_full[i & 1], (uint32_t)((i - 2) >> 1) & 1, gave_up);   // the buffer's last scores are read
                 uint64_t q = base + at_desc(qs);
+                if (rope) {      // first: a tile's last latent columns come in late where the ring holds less than two tiles
+                    wait_for(&S.rope_full[rslot], rphase, gave_up);
+                    tc_fence_after();
+                    if (!*gave_up) {
+                        const uint64_t kt = base + at_desc(ropes + rslot * kBlockBytes), qt = base + at_desc(qs + p.nb * kQBlock);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ks++) mma_bf16(d, kt + 2 * ks, qt + 2 * ks, id, ks ? 1u : 0u);
+                    }
+                    PAIR ? mma_commit_multicast(&S.rope_empty[rslot], 3) : mma_commit(&S.rope_empty[rslot]);
+                    if (++rslot == (uint32_t)p.nrope) {
+                        rslot = 0;
+                        rphase ^= 1;
+                    }
+                }
                 for (int k = 0; k < p.np; k++) {
                     wait_for(&S.pair_full[slot], phase, gave_up);
                     tc_fence_after();
                     if (!*gave_up) {
                         const uint64_t kt = base + at_desc(pairs + slot * kPairBytes);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ks++) mma_bf16(d, kt + 2 * ks, q + 2 * ks, id, (k | ks) ? 1u : 0u);
+                        for (int ks = 0; ks < 4; ks++) mma_bf16(d, kt + 2 * ks, q + 2 * ks, id, (rope || (k | ks)) ? 1u : 0u);
                         if (2 * k + 1 < p.nb) {
 #pragma unroll
                             for (int ks = 0; ks < 4; ks++)
@@ -288,20 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     if (++slot == (uint32_t)p.npair) {
                         slot = 0;
                         phase ^= 1;
-                    }
-                }
-                if (rope) {
-                    wait_for(&S.rope_full[rslot], rphase, gave_up);
-                    tc_fence_after();
-                    if (!*gave_up) {
-                        const uint64_t kt = base + at_desc(ropes + rslot * kBlockBytes), qt = base + at_desc(qs + p.nb * kQBlock);
-#pragma unroll
-                        for (int ks = 0; ks < 4; ks++) mma_bf16(d, kt + 2 * ks, qt + 2 * ks, id, 1u);
-                    }
-                    PAIR ? mma_commit_multicast(&S.rope_empty[rslot], 3) : mma_commit(&S.rope_empty[rslot]);
-                    if (++rslot == (uint32_t)p.nrope) {
-                        rslot = 0;
-                        rphase ^= 1;
                     }
                 }
                 mma_commit(&S.s_full[i & 1]);
