@@ -8,20 +8,20 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// delta[h, i] = dO[i, h] . o[i, h]: 16 threads a row of one head (dv <= 128), kRows rows each with their loads in flight
+// f32: delta[h, i] = dO[i, h] . o[i, h]: 16 threads a row of one head (dv <= 128), kRows rows each with their loads in
+// flight.  (With bf16, dQ's kernel holds the rows of dO anyway and takes the sums itself.)
 constexpr int kRows = 4;
-template <typename T>
 __global__ void __launch_bounds__(kThreads) delta_kernel(const AttnArgs a)
 {
     const gdn_mla_attn_t& s = a.s;
     const long long all = (long long)s.Nq * s.H, u0 = ((long long)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4)) * kRows;
     const int c = 8 * (threadIdx.x & 15);
-    Raw8<T> x[kRows], y[kRows];
+    Raw8<float> x[kRows], y[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; k++)
         if (u0 + k < all && c < s.dv) {
-            x[k] = raw8((const T*)a.o + (u0 + k) * s.dv + c);
-            y[k] = raw8((const T*)a.dO + (u0 + k) * s.dv + c);
+            x[k] = raw8((const float*)a.o + (u0 + k) * s.dv + c);
+            y[k] = raw8((const float*)a.dO + (u0 + k) * s.dv + c);
         }
 #pragma unroll
     for (int k = 0; k < kRows; k++) {
@@ -68,10 +68,7 @@ cudaError_t launch_delta(const AttnArgs& a, cudaStream_t st)
     const long long units = (long long)a.s.Nq * a.s.H;
     const int each = kThreads / 16 * kRows;
     const unsigned grid = (unsigned)((units + each - 1) / each);
-    if (a.s.io == GDN_BF16)
-        delta_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a);
-    else
-        delta_kernel<float><<<grid, kThreads, 0, st>>>(a);
+    delta_kernel<<<grid, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -63,6 +63,20 @@ __device__ __forceinline__ uint4 pack8(const float* x, float f)
 // a longer one corrects delta by its rows' sums of dS (which are zero) for the pass over the keys.
 
 constexpr int kTwice = 2;
+
+// the sum of the products of 8 pairs of bf16
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y)
+{
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+    float even = 0.f, odd = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        even += __uint_as_float(u[i] << 16) * __uint_as_float(v[i] << 16);
+        odd += __uint_as_float(u[i] & 0xffff0000u) * __uint_as_float(v[i] & 0xffff0000u);
+    }
+    return even + odd;
+}
+
 struct SharedQ {
     uint64_t q_full, a_full, k_full[3], k_empty[3], v_full[2], v_empty[2], k_last[2], k_fixed[2], s_full, s_read, dp_full, dp_read, ds_full, ds_empty,
         dq_full, drain;
@@ -245,8 +259,17 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         const long long at = (long long)h * s.Nq + rq.first + (mine ? row : 0);
         const float c = s.scale * kLog2e;
         const float lse = mine ? a.lse[at] : -INFINITY;
-        float delta = mine ? a.delta[at] : 0.f;
-        if (n > 0) {     // this half's 64 columns of the row of dO into TMEM
+        float delta = 0.f;
+        if (n > 0) {     // this half's 64 columns of the row of dO into TMEM, and their share of dO . o
+            uint4 o[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) o[e] = make_uint4(0, 0, 0, 0);
+            if (mine && sums == 0) {
+                const __nv_bfloat16* y = (const __nv_bfloat16*)a.o + ((long long)(rq.first + row) * s.H + h) * s.dv + 64 * half;
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    if (64 * half + 8 * e < s.dv) o[e] = __ldg(reinterpret_cast<const uint4*>(y + 8 * e));
+            }
             wait_for(&S.q_full, 0, gave_up);
             if (half < p.vb) {
                 uint32_t x[32];
@@ -257,9 +280,16 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                     x[4 * e + 1] = v.y;
                     x[4 * e + 2] = v.z;
                     x[4 * e + 3] = v.w;
+                    delta += dot8(v, o[e]);
                 }
                 __syncwarp();
                 tmem_st32(base + TD + 32 * half, x);
+            }
+            if (sums == 0) {
+                S.part[half][quad * 32 + lane] = mine ? delta : 0.f;    // another's dO, or none
+                named_bar_sync(1, 256);
+                delta = S.part[0][quad * 32 + lane] + S.part[1][quad * 32 + lane];
+                named_bar_sync(1, 256);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -351,11 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
         }
         if (n > 0) {
             if (sums == 0) delta += row_total();      // (P's rows add up to one)
-            if (mine && half == 0) a.delta[at] = delta;
             wait_for(&S.dq_full, 0, gave_up);
             __syncwarp();
             tc_fence_after();
         }
+        if (mine && half == 0) a.delta[at] = delta;     // for the pass over the keys
         __nv_bfloat16* on = (__nv_bfloat16*)a.dqn.p + (long long)(rq.first + row) * a.dqn.tok + (long long)h * a.dqn.head;
         __nv_bfloat16* op = (__nv_bfloat16*)a.dqr.p + (long long)(rq.first + row) * a.dqr.tok + (long long)h * a.dqr.head;
 #pragma unroll 1
@@ -763,10 +793,7 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs& a, cudaStream_t st)
     p.vb = (s.dv + 63) / 64;
     const int kb = p.nb + (s.dr > 0 ? 1 : 0);
     cudaError_t e = cudaSuccess;
-    if (s.Tq > 0) {
-        e = launch_delta(a, st);
-        if (e == cudaSuccess) e = kb == 1 ? run_dq<1, 3, 2>(p, st) : kb == 2 ? run_dq<2, 3, 2>(p, st) : run_dq<3, 3, 1>(p, st);
-    }
+    if (s.Tq > 0) e = kb == 1 ? run_dq<1, 3, 2>(p, st) : kb == 2 ? run_dq<2, 3, 2>(p, st) : run_dq<3, 3, 1>(p, st);
     if (e == cudaSuccess && s.Tk > 0) {
         // dV and 192 columns of dK leave 192 for S and dP
         e = kb == 1 ? run_dkv<1, 128, 3>(p, st) : kb == 2 ? run_dkv<2, 128, 3>(p, st) : run_dkv<3, 96, 2>(p, st);
