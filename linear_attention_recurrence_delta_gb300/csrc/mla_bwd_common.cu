@@ -44,6 +44,7 @@ constexpr int kDkrThreads = 64;     // few rows: spread them over the SMs
 template <typename T>
 __global__ void __launch_bounds__(kDkrThreads) dkr_kernel(const AttnArgs a)
 {
+    cudaGridDependencySynchronize();     // launched as a dependent of the pass over the keys
     const gdn_mla_attn_t& s = a.s;
     const Rows rk = rows_of(a.cu_k, blockIdx.y, s.Tk, s.Nk);
     const int per = s.dr >> 3;
@@ -76,11 +77,16 @@ cudaError_t launch_dkr(const AttnArgs& a, cudaStream_t st)
 {
     const long long units = (long long)a.s.Tk * (a.s.dr >> 3);
     const dim3 grid((unsigned)((units + kDkrThreads - 1) / kDkrThreads), a.s.B);
-    if (a.s.io == GDN_BF16)
-        dkr_kernel<__nv_bfloat16><<<grid, kDkrThreads, 0, st>>>(a);
-    else
-        dkr_kernel<float><<<grid, kDkrThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kDkrThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return a.s.io == GDN_BF16 ? cudaLaunchKernelEx(&cfg, dkr_kernel<__nv_bfloat16>, a) : cudaLaunchKernelEx(&cfg, dkr_kernel<float>, a);
 }
 
 }  // namespace mla

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     const int h = blockIdx.x % s.H, b = blockIdx.y, g = h / (s.H / s.Hkv);
     const int q0 = (p.tiles - 1 - (int)(blockIdx.x / s.H)) * kTile;     // the longest walks first
     const Rows rq = rows_of(a.cu_q, b, s.Tq, s.Nq), rk = rows_of(a.cu_k, b, s.Tk, s.Nk);
+    cudaTriggerProgrammaticLaunchCompletion();     // the pass over the keys may set up on the SMs that fall free
     if (q0 >= rq.n) return;
     const int off = rk.n - rq.n;
     const int end = s.causal ? min(rk.n, min(q0 + kTile, rq.n) + off) : rk.n;
@@ -441,9 +442,16 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
     const int g = blockIdx.x % s.Hkv, b = blockIdx.y, G = s.H / s.Hkv;
     const int k0 = (int)(blockIdx.x / s.Hkv) * kTile;       // under the causal mask the first keys have most queries
     const Rows rq = rows_of(a.cu_q, b, s.Tq, s.Nq), rk = rows_of(a.cu_k, b, s.Tk, s.Nk);
-    if (k0 >= rk.n) return;
+    cudaTriggerProgrammaticLaunchCompletion();     // the sum over the heads follows likewise
+    // launched as a dependent of dQ's kernel, of which it reads delta alone; a CTA waits for it even if it reads none, so that
+    // its end is the end of both
+    if (k0 >= rk.n) {
+        cudaGridDependencySynchronize();
+        return;
+    }
     if (smem_u32(raw) & 1023) {     // never so without static shared memory; the tiles below would not fit otherwise
         if (threadIdx.x == 0) atomicExch(a.status, kDevTimeout);
+        cudaGridDependencySynchronize();
         return;
     }
     const int off = rk.n - rq.n;
@@ -589,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
         }
     } else if (warp < 4) {
         const int t0 = tid - 64;
+        cudaGridDependencySynchronize();
         for (int i = 0, h = g * G, t = first; i < n; i++) {
             const int st = i & 1;
             wait_for(&S.st_empty[st], ((i >> 1) & 1) ^ 1, gave_up);
@@ -776,8 +785,17 @@ cudaError_t run_dkv(Params& p, cudaStream_t st)
     const size_t bytes = (size_t)(KB + p.vb) * kBlock + (size_t)(QS * KB + 2 * p.vb) * NQ * 128 + sizeof(SharedK<NQ>);
     const cudaError_t e = cudaFuncSetAttribute(dkv_tc_kernel<KB, NQ, QS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    dkv_tc_kernel<KB, NQ, QS><<<dim3((unsigned)p.a.s.Hkv * p.tiles, p.a.s.B), kThreads, bytes, st>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.a.s.Hkv * p.tiles, p.a.s.B);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = p.a.s.Tq > 0 ? 1 : 0;      // after dQ's kernel
+    return cudaLaunchKernelEx(&cfg, dkv_tc_kernel<KB, NQ, QS>, p);
 }
 
 }  // namespace
