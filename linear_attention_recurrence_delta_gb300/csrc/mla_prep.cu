@@ -3,9 +3,8 @@
 // Elementwise but for one sum a token, so HBM bounds it: each input is read once and each output written once, in
 // 16-byte pieces.  A warp holds a token's whole latent in registers (its sum of squares is one warp reduction); a
 // thread rotates 8 pairs of two query heads by angles that it reads once.  Forwards both kinds of block run in one launch, because a decoding step is
-// bound by launches, not bytes.  32768 tokens of 256 + 64 values with 16 heads of 64: 41 us forwards (176 MB, 4.3 TB/s),
-// 28 us for the rows and 15 us for the latents of the gradients, 7 us for their sum over 608 blocks; a decoding step of
-// 24 tokens takes 5 us from a cold cache, and the call's host time more.
+// bound by launches, not bytes.  32768 tokens of 256 + 64 values with 16 heads of 64: 41 us forwards (176 MB, 4.3 TB/s)
+// and 46 us for the gradients; a decoding step of 24 tokens takes 5 us from a cold cache, and the call's host time more.
 #include "mla_internal.h"
 
 namespace gdn {
@@ -187,14 +186,8 @@ __global__ void __launch_bounds__(kThreads, NV == 4 ? 2 : sizeof(T) == 4 ? 3 : 4
 // Gradients: with r = rsqrt(mean x^2 + eps) and g = dy w,  dx = r (g - x r^2 mean(g x)),  dw = sum_n dy x r.
 // A block's warps walk tokens a fixed way apart and keep their share of dw in registers; the shares are added in a
 // fixed order here and in sum_dw_kernel.
-template <typename T, bool IL>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) rows_bwd_kernel(const PrepArgs a)
-{
-    rotate_rows<T, true, IL>(a, blockIdx.x);
-}
-
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads, NV == 1 ? 4 : NV == 2 ? 2 : 1) latents_bwd_kernel(const PrepArgs a)
+__device__ __forceinline__ void latents_bwd(const PrepArgs& a, int block, int blocks)
 {
     __shared__ float red[kWarps][256];   // a quarter of the widest latent's shares at a time
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -206,8 +199,8 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? 4 : NV == 2 ? 2 : 1) laten
 #pragma unroll
             for (int i = 0; i < 8; i++) w[k][i] = a.w[8 * (lane + 32 * k) + i];
         }
-    const long long step = (long long)gridDim.x * kWarps;
-    for (long long n = (long long)blockIdx.x * kWarps + warp; n < a.s.N; n += step) {
+    const long long step = (long long)blocks * kWarps;
+    for (long long n = (long long)block * kWarps + warp; n < a.s.N; n += step) {
         const int pos = a.pos[n];
         const bool bad = pos < 0 || pos >= a.s.npos;
         const T* x = (const T*)a.kv + n * a.kv_tok;
@@ -256,10 +249,29 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? 4 : NV == 2 ? 2 : 1) laten
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < kWarps; i++) sum += red[i][threadIdx.x];
-            a.partial[(long long)blockIdx.x * dc + col] = sum;
+            a.partial[(long long)block * dc + col] = sum;
         }
         __syncthreads();
     }
+}
+
+// Blocks [0, latents): the norm's gradients, which take longest; the rest: what was rotated.  One launch for latents up to
+// 256 wide (32768 tokens, 16 heads of 64: 94.3 to 88.2 us for both passes; f32 144 to 139); wider ones hold twice the
+// registers or more, which would leave the rotation half its threads (512 wide 114.9 against 118.6 us in one launch, 1024
+// wide 95.7 against 100.9), and go in two.
+template <typename T, bool IL, int NV>
+__global__ void __launch_bounds__(kThreads, NV == 4 ? 1 : NV == 2 ? 2 : sizeof(T) == 4 ? 3 : 4) prep_bwd_kernel(const PrepArgs a, int latents)
+{
+    if (NV > 1 || (int)blockIdx.x < latents)
+        latents_bwd<T, NV>(a, blockIdx.x, latents);
+    else
+        rotate_rows<T, true, IL>(a, blockIdx.x - latents);
+}
+
+template <typename T, bool IL>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) rows_bwd_kernel(const PrepArgs a)
+{
+    rotate_rows<T, true, IL>(a, blockIdx.x);
 }
 
 __global__ void __launch_bounds__(1024) sum_dw_kernel(const float* part, float* dw, int blocks, int dc)
@@ -293,8 +305,9 @@ void start(const PrepArgs& a, bool backward, cudaStream_t st)
 {
     const long long rows = rows_blocks(a.s);
     if (backward) {
-        if (rows > 0) rows_bwd_kernel<T, IL><<<(unsigned)rows, kThreads, 0, st>>>(a);
-        latents_bwd_kernel<T, NV><<<prep_bwd_blocks(a.s.N), kThreads, 0, st>>>(a);
+        const int latents = prep_bwd_blocks(a.s.N);
+        if (NV > 1 && rows > 0) rows_bwd_kernel<T, IL><<<(unsigned)rows, kThreads, 0, st>>>(a);
+        prep_bwd_kernel<T, IL, NV><<<(unsigned)(latents + (NV > 1 ? 0 : rows)), kThreads, 0, st>>>(a, latents);
     } else {
         prep_kernel<T, IL, NV><<<(unsigned)(rows + (a.s.N + kWarps - 1) / kWarps), kThreads, 0, st>>>(a, (int)rows);
     }
