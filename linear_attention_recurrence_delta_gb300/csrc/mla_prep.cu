@@ -3,8 +3,8 @@
 // Elementwise but for one sum a token, so HBM bounds it: each input is read once and each output written once, in
 // 16-byte pieces.  A warp holds a token's whole latent in registers (its sum of squares is one warp reduction); a
 // thread rotates 8 pairs of two query heads by angles that it reads once.  Forwards both kinds of block run in one launch, because a decoding step is
-// bound by launches, not bytes.  32768 tokens of 256 + 64 values with 16 heads of 64: 41 us forwards (176 MB, 4.3 TB/s)
-// and 46 us for the gradients; a decoding step of 24 tokens takes 5 us from a cold cache, and the call's host time more.
+// bound by launches, not bytes.  32768 tokens of 256 + 64 values with 16 heads of 64: 41 us forwards (176 MB, 4.3 TB/s),
+// 86 us for both passes; a decoding step of 24 tokens takes 5 us from a cold cache, and the call's host time more.
 #include "mla_internal.h"
 
 namespace gdn {
@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) rows_bwd_ker
 
 __global__ void __launch_bounds__(1024) sum_dw_kernel(const float* part, float* dw, int blocks, int dc)
 {
+    cudaGridDependencySynchronize();     // launched as a dependent of the shares' kernel
     __shared__ float red[32][33];
     const int c = blockIdx.x * 32 + threadIdx.x;
     float s = 0.f;
@@ -349,8 +350,16 @@ cudaError_t launch_prep_bwd(const PrepArgs& a, cudaStream_t st)
 {
     const cudaError_t e = launch(a, true, st);
     if (e != cudaSuccess) return e;
-    sum_dw_kernel<<<(a.s.dc + 31) / 32, dim3(32, 32), 0, st>>>(a.partial, a.dw, prep_bwd_blocks(a.s.N), a.s.dc);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.s.dc + 31) / 32);
+    cfg.blockDim = dim3(32, 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sum_dw_kernel, (const float*)a.partial, a.dw, prep_bwd_blocks(a.s.N), a.s.dc);
 }
 
 }  // namespace mla
