@@ -246,6 +246,7 @@ __device__ __forceinline__ void pair_grads(float& x, float& y, float scale, floa
 template <int RI>
 __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, int stages)
 {
+    cudaGridDependencySynchronize();     // launched as a dependent of the kernel before it
     extern __shared__ float smem[];
     constexpr int kHeld = 16 * RI;
     const gdn_mla_attn_t& s = a.s;
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, int stag
 template <int RI>
 __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, int stages)
 {
+    cudaGridDependencySynchronize();     // launched as a dependent of the kernel before it
     extern __shared__ float smem[];
     constexpr int kHeld = 16 * RI, kPP = kHeld + 4;
     const gdn_mla_attn_t& s = a.s;
@@ -393,14 +395,23 @@ int pick_rows(int rows, long long units)
 
 // launches kernel(a, stages) with as many buffers of the walked side as fit
 template <typename F>
-cudaError_t start(F kernel, const AttnArgs& a, dim3 grid, size_t held, size_t walked, cudaStream_t st)
+cudaError_t start(F kernel, const AttnArgs& a, dim3 grid, size_t held, size_t walked, bool dependent, cudaStream_t st)
 {
     const int stages = (held + 2 * walked) * sizeof(float) <= kRoom ? 2 : 1;
     const size_t bytes = (held + stages * walked) * sizeof(float);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, bytes, st>>>(a, stages);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a, stages);
 }
 
 }  // namespace
@@ -411,7 +422,7 @@ cudaError_t launch_attn_f32(const AttnArgs& a, cudaStream_t st)
     const int pq = pitch_of(s.dn + s.dr), pv = pitch_of(s.dv), r = pick_rows(s.Tq, (long long)s.H * s.B), held = 16 * r;
     const dim3 grid((s.Tq + held - 1) / held, s.H, s.B);
     const size_t h = (size_t)held * (pq + kSP), w = (size_t)kTile * (pq + pv);
-    return r == 4 ? start(fwd_kernel<4>, a, grid, h, w, st) : r == 2 ? start(fwd_kernel<2>, a, grid, h, w, st) : start(fwd_kernel<1>, a, grid, h, w, st);
+    return r == 4 ? start(fwd_kernel<4>, a, grid, h, w, false, st) : r == 2 ? start(fwd_kernel<2>, a, grid, h, w, false, st) : start(fwd_kernel<1>, a, grid, h, w, false, st);
 }
 
 cudaError_t launch_attn_bwd_f32(const AttnArgs& a, cudaStream_t st)
@@ -424,14 +435,14 @@ cudaError_t launch_attn_bwd_f32(const AttnArgs& a, cudaStream_t st)
         const int r = pick_rows(s.Tq, (long long)s.H * s.B), held = 16 * r;
         const dim3 grid((s.Tq + held - 1) / held, s.H, s.B);
         const size_t h = (size_t)held * (pq + pv + kSP), w = (size_t)kTile * (pq + pv);
-        e = r == 4 ? start(dq_kernel<4>, a, grid, h, w, st) : r == 2 ? start(dq_kernel<2>, a, grid, h, w, st) : start(dq_kernel<1>, a, grid, h, w, st);
+        e = r == 4 ? start(dq_kernel<4>, a, grid, h, w, true, st) : r == 2 ? start(dq_kernel<2>, a, grid, h, w, true, st) : start(dq_kernel<1>, a, grid, h, w, true, st);
         if (e != cudaSuccess) return e;
     }
     if (s.Tk > 0) {
         const int r = pick_rows(s.Tk, (long long)s.Hkv * s.B), held = 16 * r;
         const dim3 grid((s.Tk + held - 1) / held, s.Hkv, s.B);
         const size_t h = (size_t)held * (pq + pv) + (size_t)2 * kTile * (held + 4), w = (size_t)kTile * (pq + pv + 2);
-        e = r == 4 ? start(dkv_kernel<4>, a, grid, h, w, st) : r == 2 ? start(dkv_kernel<2>, a, grid, h, w, st) : start(dkv_kernel<1>, a, grid, h, w, st);
+        e = r == 4 ? start(dkv_kernel<4>, a, grid, h, w, s.Tq > 0, st) : r == 2 ? start(dkv_kernel<2>, a, grid, h, w, s.Tq > 0, st) : start(dkv_kernel<1>, a, grid, h, w, s.Tq > 0, st);
         if (e != cudaSuccess) return e;
         if (s.dr > 0) return launch_dkr(a, st);
     }
