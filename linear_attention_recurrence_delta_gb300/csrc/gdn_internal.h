@@ -158,8 +158,8 @@ int decode_max_tokens();
 
 // Failure-path test hook, for the library's own tests only: the value of the environment variable
 // GDN_TEST_STARVE_CHUNK, read once per process (-1 when it is not set).  With it set to k, the tensor-core
-// forward never issues the loads of chunk k (each latent-attention kernel those of its k-th tile), so that wait expires, the kernel winds down and the
-// status word reads GDN_ERR_TIMEOUT.  Set it before the process's first forward call.
+// forward never issues the loads of chunk k (each latent-attention kernel those of its k-th tile), so that wait
+// expires, the kernel winds down and the status word reads GDN_ERR_TIMEOUT.  Set it before the process's first forward call.
 int test_starve_chunk();
 
 // GDN_OK if the current device is an sm_103 GPU, GDN_ERR_DEVICE if not, GDN_ERR_CUDA if it cannot be queried

@@ -58,7 +58,8 @@ __device__ __forceinline__ uint4 pack8(const float* x, float f)
 // a cycle); it gets there by way of the third K stage.  Where dQ leaves 64 columns, dS has its own (OWN), so that the next
 // tile's dP runs while this one's is turned into dS; else it goes back over dP.
 //
-// delta from the stored o carries o's rounding, which counts where few keys share a weight of one: dP - delta cancels.
+// A CTA takes delta = dO . o from the rows of dO that it holds and hands it to the pass over the keys.  That sum carries
+// o's rounding, which counts where few keys share a weight of one: dP - delta cancels.
 // sum_j P dP is the same number without it.  A tile that walks at most kTwice key tiles takes that sum in a first walk;
 // a longer one corrects delta by its rows' sums of dS (which are zero) for the pass over the keys.
 

@@ -8,13 +8,12 @@
 // Roles of a CTA (one per SM, 12 warps): warp 0 streams the cache by TMA through a ring of 64 rows x 128 columns
 // pieces (page by page: a page's rows are one box); warp 1 issues the scores' products and warp 2 the outputs', each
 // waiting for its own operands only, so that the next tiles' scores run ahead of this tile's outputs; warp 3 lays the
-// queries out; warps 4-11 do the softmax.  The softmax keeps a running
-// maximum of each query row but lowers scores by an old one until a score exceeds it by 2^16: exp2 and fp32 hold that
-// range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (rarely after a sequence's first
+// queries out; warps 4-11 do the softmax.  The softmax keeps a running maximum of each query row but lowers scores by an
+// old one until a score exceeds it by 2^16: exp2 and fp32 hold that range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (rarely after a sequence's first
 // tile).  HBM bounds it while the query rows fit one group: 8 x 32768 rows of 512 + 64 values under 16 heads take 56 us
 // (302 MB, 5.4 TB/s; 3250 cycles a 64-row tile are 22.7 bytes a cycle and SM, the card's rate, the rest start and end).
-// A call of 160 rows in two groups takes 86 us where the bytes alone need 20: less than two tiles fit beside 92 KB of queries, so a
-// tile's load waits for the products of the one before it.
+// A call of 160 rows in two groups takes 86 us where the bytes alone need 20: less than two tiles fit beside 92 KB
+// of queries, so a tile's load waits for the products of the one before it.
 #include "mla_decode_common.cuh"
 #include "mla_tc.cuh"
 
@@ -644,7 +643,11 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st)
                      (s.dr > 0 && !row_map(&p.qr, a.qr.p, a.qr.head, (long long)s.B * s.T * s.H, s.dr, nc)))))
         return cudaErrorInvalidValue;
     if (a.groups == 1)
-        return nc == 16 ? run<16, false>(p, st) : nc == 32 ? run<32, false>(p, st) : nc == 48 ? run<48, false>(p, st) : nc == 64 ? run<64, false>(p, st) : run<80, false>(p, st);
+        return nc == 16   ? run<16, false>(p, st)
+               : nc == 32 ? run<32, false>(p, st)
+               : nc == 48 ? run<48, false>(p, st)
+               : nc == 64 ? run<64, false>(p, st)
+                          : run<80, false>(p, st);
     // two groups and more have more than 80 rows in all: at least 41 each
     return nc == 48 ? run<48, true>(p, st) : nc == 64 ? run<64, true>(p, st) : run<80, true>(p, st);
 }

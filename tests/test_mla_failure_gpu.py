@@ -28,6 +28,8 @@ try:
         n, T, H = [3000] * 8, 1, 16
     elif what == "decode pairs":
         n, T, H = [3000] * 8, 2, 40
+    elif what == "decode two groups":
+        n, T, H = [3000] * 8, 4, 40
     if what.startswith("decode"):
         a = (T, H, 64, 32, 64, "bf16")
         table, pages, cache, rows, qc, qr = setup(1, n, *a)
@@ -64,7 +66,7 @@ print(json.dumps({"status": status, "secs": secs}))
 """
 
 
-@pytest.mark.parametrize("what", ["forward 2", "forward 3", "gradients 2", "gradients 3", "decode", "decode pairs"])
+@pytest.mark.parametrize("what", ["forward 2", "forward 3", "gradients 2", "gradients 3", "decode", "decode pairs", "decode two groups"])
 def test_starved_load_times_out_and_context_survives(what):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     env = dict(os.environ, GDN_TEST_STARVE_CHUNK="1", PYTHONPATH=root)
