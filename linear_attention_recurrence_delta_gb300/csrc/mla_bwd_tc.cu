@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                     if (64 * half + 8 * e < s.dv) o[e] = __ldg(reinterpret_cast<const uint4*>(y + 8 * e));
             }
             wait_for(&S.q_full, 0, gave_up);
+            __syncwarp();
             if (half < p.vb) {
                 uint32_t x[32];
 #pragma unroll
@@ -289,9 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             }
             if (sums == 0) {
                 S.part[half][quad * 32 + lane] = mine ? delta : 0.f;    // another's dO, or none
-                named_bar_sync(1, 256);
+                group_sync(1, 256);
                 delta = S.part[0][quad * 32 + lane] + S.part[1][quad * 32 + lane];
-                named_bar_sync(1, 256);
+                group_sync(1, 256);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -310,9 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
             float even, odd;
             unpack2(add2(sum2[0], sum2[1]), even, odd);
             S.part[half][quad * 32 + lane] = even + odd;
-            named_bar_sync(1, 256);
+            group_sync(1, 256);
             const float t = S.part[0][quad * 32 + lane] + S.part[1][quad * 32 + lane];
-            named_bar_sync(1, 256);
+            group_sync(1, 256);
             return t;
         };
         for (int j = 0; j < steps_all; j++) {
@@ -350,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.dp_read);
+                __syncwarp();
                 if (j > 0) {     // the last tile's dS has been used
                     wait_for(&S.ds_empty, (j - 1) & 1, gave_up);
                     __syncwarp();
@@ -393,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
 #pragma unroll 1
         for (int i = 16 * half; i < 64 * KB; i += 32) {     // the two halves take 16 columns in turn
             float o[16];
+            __syncwarp();
             if (n > 0) {
                 tmem_ld16(base + TQ + i, o);
                 tmem_wait_ld();
@@ -415,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -719,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
 #pragma unroll 1
         for (int i = 16 * half; i < 128 + 64 * KB; i += 32) {     // the two halves take 16 columns in turn
             float o[16];
+            __syncwarp();
             if (n > 0) {
                 tmem_ld16(base + TV + i, o);
                 tmem_wait_ld();
@@ -746,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }

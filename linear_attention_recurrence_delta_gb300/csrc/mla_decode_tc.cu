@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 if (t < NC) S.top[t] = 0.f;
 #pragma unroll
                 for (int n = 0; n < HC; n++) l[n] = 0.f;
-                named_bar_sync(1, kSoft);
+                group_sync(1, kSoft);
             }
             wait_for(&S.s_full[buf], phase, gave_up);
             __syncwarp();
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     for (int k = 8; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
                     if ((lane & 15) == 0) S.red[quad][col0 + n] = m;
                 }
-                named_bar_sync(1, kSoft);
+                group_sync(1, kSoft);
                 if (t < NC) {
                     const float m = fmaxf(fmaxf(S.red[0][t], S.red[1][t]), fmaxf(S.red[2][t], S.red[3][t]));
                     const float up = first ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);   // what the maximum rises by
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     S.top[t] += up;
                     S.keep[t] = first ? 1.f : fast_exp2(-up);
                 }
-                named_bar_sync(1, kSoft);
+                group_sync(1, kSoft);
 #pragma unroll
                 for (int n = 0; n < HC; n++) {
                     l[n] *= S.keep[col0 + n];
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 for (int k = 8; k; k >>= 1) m += __shfl_xor_sync(0xffffffffu, m, k);
                 if ((lane & 15) == 0) S.red[quad][col0 + n] = m;
             }
-            named_bar_sync(1, kSoft);
+            group_sync(1, kSoft);
             const bool whole = from == 0 && to == tiles;
             const long long slot = ((long long)group * a.slots + cta + b) * a.rows;
             const long long out = (long long)b * s.T * s.H + row0;
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                         a.lse[out + t] = l2 * kLn2;
                 }
             }
-            named_bar_sync(1, kSoft);
+            group_sync(1, kSoft);
             wait_for(&S.o_full, piece & 1, gave_up);
             __syncwarp();
             piece++;
@@ -510,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 for (int m = half; m < p.np; m += 2) {
                     const int d = 128 * m + 32 * quad + lane;
                     float o[16];
+                    __syncwarp();
                     tmem_ld16(lane_base(tmem, quad) + (2 + m) * NC + n0, o);
                     tmem_wait_ld();
                     if (d >= s.dc) continue;
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 }
             }
             tc_fence_before();
-            named_bar_sync(1, kSoft);   // the sums' words are free for the next piece
+            group_sync(1, kSoft);   // the sums' words are free for the next piece
         }
     } else {
         // ------------------------------------------------------------ queries: [query rows][64 columns] blocks
@@ -582,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     else
         __syncthreads();
     if (warp == 1) {
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, kCols);
     }

@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 3 - NT) fwd_tc_kernel(const __
                 const float now = raise ? fmaxf(most, top) : top;
                 const float keep = now == top ? 1.f : fast_exp2((top - now) * c);     // the first time: 0 of nothing
                 top = now;
+                __syncwarp();
                 const uint64_t k2 = pack2(keep, keep);
                 sum[0] = mul2(sum[0], k2);
                 sum[1] = mul2(sum[1], k2);
@@ -317,6 +318,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 3 - NT) fwd_tc_kernel(const __
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&S.p_full[t][i >> 6]);
+                    __syncwarp();
                 }
             }
         }
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 3 - NT) fwd_tc_kernel(const __
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 256 * NT);
     }

@@ -86,9 +86,10 @@ __device__ __forceinline__ uint32_t cluster_rank()
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-// every thread of the cluster's CTAs
+// every thread of the cluster's CTAs, by whole warps
 __device__ __forceinline__ void cluster_sync()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -99,6 +100,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
             dst),
         "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
         : "memory");
+}
+
+// The named barrier, TMEM's loads, stores and waits, its release and the registers' hand-over are instructions of whole
+// warps: lanes that a condition, a bounded wait or a single lane's work has set apart come together before each of them.
+__device__ __forceinline__ void group_sync(uint32_t id, uint32_t threads)
+{
+    __syncwarp();
+    named_bar_sync(id, threads);
 }
 
 // barrier of `threads` threads that also tells whether any of them said yes
@@ -188,9 +197,17 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 
 // the warpgroup's registers a thread: the other warpgroups' shares have been given up first
 template <int N>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void regs_down()
+{
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 template <int N>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void regs_up()
+{
+    __syncwarp();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // ---------------------------------------------------------------- host side
 

@@ -1,0 +1,31 @@
+"""Latent attention where a warp's lanes part ways: ends of sequences and of widths at every place of a warp."""
+import pytest
+
+import tests.test_mla_attn_gpu as attn
+import tests.test_mla_decode_gpu as decode
+from tests.mla_testlib import attn_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dn,dr,dv", [(64, 0, 64), (64, 64, 128), (128, 64, 128), (128, 0, 24)])
+def test_ends_inside_a_warp(dn, dr, dv, causal):
+    """The last row of a tile in each of its four warps, first, inner and last lane: the lanes past it store nothing while
+    the warp reads on.  One, two and three 64-column blocks a key, and a value that one half of the columns holds."""
+    n = [1, 31, 33, 50, 63, 65, 81, 96, 97, 127, 129, 190, 225]
+    x, dO = attn_inputs(sum((dn, dr, dv)), n, n, 2, 1, dn, dr, dv, "bf16")
+    attn.compare(x, dO, n, n, causal, "bf16")
+
+
+@pytest.mark.parametrize("n", [[64] * 160 + [1], [20000, 70]])
+@pytest.mark.parametrize("dc", [8, 24, 40, 104, 136, 200, 264, 488])
+def test_latents_that_end_inside_a_warp(dc, n):
+    """Widths whose last 32 columns are not all there, of sequences that one worker covers and of ones that many share."""
+    decode.compare(dc + len(n), n, 1, 16, dc, 16, 16, "bf16")
+
+
+@pytest.mark.parametrize("T,H", [(1, 3), (2, 40), (3, 30), (5, 33), (8, 128)])
+def test_query_rows_that_end_inside_a_warp(T, H):
+    """Rows that fill a part of a group's columns, in one group and in several, over enough tiles for a raised maximum."""
+    decode.compare(T * H, [300, 1, 0, 2000, 64], T, H, 200, 32, 16, "bf16", std=4.0)
