@@ -10,13 +10,13 @@ DecodePlan decode_plan(const gdn_mla_cache_t& s)
     DecodePlan p;
     const int all = s.T * s.H;
     // Query rows of a worker on the tensor, the CUDA cores.  Fewer groups send each cache tile through fewer SMs, which
-    // outweighs the shorter ring beside 80 rows.  At most 64 against 80, us: 32 x 4 drafted tokens of 40 heads over 512 + 64,
-    // up to 6000 rows 114.7 / 92.2, over 256 + 64 77.8 / 53.3; 72 rows 65.6 / 60.9; 320 rows 228 / 172; two sequences of 160
-    // rows 22.5 / 24.8.
+    // outweighs the shorter ring beside 80 rows.  At most 64 against 80, us: 32 sequences of 6000 rows of 512 + 64 values
+    // under 72 query rows 88.2 / 73.6, under 160 (up to 6000 rows) 116.8 / 88.5, under 320 237 / 210; 160 over 256 + 64
+    // 94.3 / 72.4; two sequences under 160 28.7 / 30.7.  (A load that filled both of two groups' tiles took 86.6, 172 and
+    // 53.3 for the 160, 320 and 160 rows over 256 + 64.  It is not used: the library also runs on several GPUs at once, where
+    // such loads are not safe.)
     const int most = s.io == GDN_BF16 ? kDecodeRows : 8;
     p.groups = (all + most - 1) / most;
-    // on the tensor cores two groups share each load of the cache (a cluster of two CTAs)
-    if (s.io == GDN_BF16 && p.groups > 1 && p.groups % 2) p.groups++;
     p.rows = (all + p.groups - 1) / p.groups;
     p.ctas = 152 / p.groups > 0 ? 152 / p.groups : 1;
     p.slots = p.ctas + s.B;

@@ -12,7 +12,7 @@
 // old one until a score exceeds it by 2^16: exp2 and fp32 hold that range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (rarely after a sequence's first
 // tile).  HBM bounds it while the query rows fit one group: 8 x 32768 rows of 512 + 64 values under 16 heads take 56 us
 // (302 MB, 5.4 TB/s; 3250 cycles a 64-row tile are 22.7 bytes a cycle and SM, the card's rate, the rest start and end).
-// A call of 160 rows in two groups takes 86 us where the bytes alone need 20: less than two tiles fit beside 92 KB
+// A call of 160 rows in two groups takes 88 us where the bytes alone need 20: less than two tiles fit beside 92 KB
 // of queries, so a tile's load waits for the products of the one before it.
 #include "mla_decode_common.cuh"
 #include "mla_tc.cuh"
@@ -107,8 +107,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// PAIR: the CTAs of two groups form a cluster.  They walk the same tiles; each loads half of one and the copy goes to both.
-template <int NC, bool PAIR>
+template <int NC>
 __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ unsigned char raw[];
@@ -146,11 +145,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     } else if (tid == 64) {
         for (int i = 0; i < kMaxPairs; i++) {
             mbar_init(&S.pair_full[i], 1);
-            mbar_init(&S.pair_empty[i], PAIR ? 2 : 1);
+            mbar_init(&S.pair_empty[i], 1);
         }
         for (int i = 0; i < kMaxRope; i++) {
             mbar_init(&S.rope_full[i], 1);
-            mbar_init(&S.rope_empty[i], PAIR ? 2 : 1);
+            mbar_init(&S.rope_empty[i], 1);
         }
         mbar_init(&S.q_full, p.q_tma ? 1 : 32);
         mbar_init(&S.q_empty, 1);
@@ -166,12 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         S.gave_up = 0;
     }
     tc_fence_before();
-    if (PAIR)
-        cluster_sync();      // both CTAs' barriers are set before either's copies arrive on them
-    else
-        __syncthreads();
+    __syncthreads();
     tc_fence_after();
-    const uint32_t rank = PAIR ? cluster_rank() : 0;
     cudaTriggerProgrammaticLaunchCompletion();   // the join's blocks may take their places
     const uint32_t tmem = S.tmem;
     const uint32_t pairs = smem_u32(sm), ropes = pairs + p.rope_off, qs = pairs + p.q_off, ps = pairs + p.p_off;
@@ -184,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         const int subs = kDecodeTile / p.box, sub = lane & (subs - 1), blk = lane / subs;   // subs: 1, 2, 4 or 8
         uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0;
         int issued = 0, rissued = 0;
-            for (int i = 0; i < total; i++) {
+        for (int i = 0; i < total; i++) {
             int at = p.total_rows;
             const int j = r.tile * kDecodeTile + sub * p.box;
             if (blk < 2 && j < r.n) {
@@ -199,11 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     if (elect_one()) mbar_arrive_expect_tx(bar, kBlockBytes);
                     __syncwarp();
                     const uint32_t dst = ropes + rslot * kBlockBytes + sub * p.box * 128;
-                    if (PAIR) {
-                        if (lane < subs && (i & 1) == (int)rank) tma_load_2d_multicast(dst, &p.map, bar, s.dc, at, 3);   // in turn
-                    } else if (lane < subs) {
-                        tma_load_2d(dst, &p.map, bar, s.dc, at);
-                    }
+                    if (lane < subs) tma_load_2d(dst, &p.map, bar, s.dc, at);
                     rissued++;
                 }
                 if (++rslot == (uint32_t)p.nrope) {
@@ -219,14 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                     uint64_t* bar = &S.pair_full[slot];
                     if (elect_one()) mbar_arrive_expect_tx(bar, blocks * kBlockBytes);
                     __syncwarp();
-                    if ((PAIR ? lane < subs && (int)rank < blocks : lane < blocks * subs) && i != p.starve) {   // a lane a box
-                        const int c = PAIR ? rank : blk;
-                        const uint32_t dst = pairs + slot * kPairBytes + c * kBlockBytes + sub * p.box * 128;
-                        if (PAIR)
-                            tma_load_2d_multicast(dst, &p.map, bar, 128 * k + 64 * c, at, 3);
-                        else
-                            tma_load_2d(dst, &p.map, bar, 128 * k + 64 * c, at);
-                    }
+                    if (lane < blocks * subs && i != p.starve)   // a lane a box
+                        tma_load_2d(pairs + slot * kPairBytes + blk * kBlockBytes + sub * p.box * 128, &p.map, bar, 128 * k + 64 * blk, at);
                     issued++;
                 }
                 if (++slot == (uint32_t)p.npair) {
@@ -235,16 +220,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                 }
             }
             r.step();
-        }
-        if (PAIR) {   // the other CTA's last arrivals on this one's barriers come before either ends
-            for (int i = 0; i < p.npair; i++) {
-                wait_for(&S.pair_empty[slot], phase ^ 1, gave_up);
-                if (++slot == (uint32_t)p.npair) slot = 0, phase ^= 1;
-            }
-            for (int i = 0; i < p.nrope; i++) {
-                wait_for(&S.rope_empty[rslot], rphase ^ 1, gave_up);
-                if (++rslot == (uint32_t)p.nrope) rslot = 0, rphase ^= 1;
-            }
         }
         if (*gave_up) {   // a wait expired: the copies in flight land before the CTA ends
             for (int i = 0; i < p.npair; i++) {
@@ -278,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
 #pragma unroll
                         for (int ks = 0; ks < 4; ks++) mma_bf16(d, kt + 2 * ks, qt + 2 * ks, id, ks ? 1u : 0u);
                     }
-                    PAIR ? mma_commit_multicast(&S.rope_empty[rslot], 3) : mma_commit(&S.rope_empty[rslot]);
+                    mma_commit(&S.rope_empty[rslot]);
                     if (++rslot == (uint32_t)p.nrope) {
                         rslot = 0;
                         rphase ^= 1;
@@ -332,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
                         for (int ks = 0; ks < 4; ks++)
                             mma_bf16(tmem + (2 + m) * NC, v + 128 * ks, pt + 2 * ks, id, (first && ks == 0) ? 0u : 1u);
                     }
-                    PAIR ? mma_commit_multicast(&S.pair_empty[slot], 3) : mma_commit(&S.pair_empty[slot]);
+                    mma_commit(&S.pair_empty[slot]);
                     if (++slot == (uint32_t)p.npair) slot = 0;
                 }
                 mma_commit(&S.p_empty[i & 1]);
@@ -346,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax, outputs
-        // Two warpgroups take half of the query rows' columns each (against one, us: 160 rows 92.3 to 90.1, 128 rows 92.3 to
-        // 88.2, 16 rows unchanged, 160 rows over 256 + 64 53.3 to 55.3).  An M = 64 product fills the first 16 lanes of each
+        // Two warpgroups take half of the query rows' columns each (against one, when a load served two groups, us: 160 rows
+        // 92.3 to 90.1, 128 rows 92.3 to 88.2, 16 rows unchanged, 160 rows over 256 + 64 53.3 to 55.3).  An M = 64 product fills the first 16 lanes of each
         // warp's 32 in TMEM: lanes 16..31 take over the second half of these rows' columns.
         constexpr int HC = NC / 4;
         const int quad = warp & 3, half = (warp - 4) >> 2, t = tid - 128, key = quad * 16 + (lane & 15);
@@ -578,10 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         if (loaded != ~0u && *gave_up) mbar_wait(&S.q_full, loaded & 1, nullptr, kDrainNs);   // the copy in flight lands
     }
     tc_fence_before();
-    if (PAIR)
-        cluster_sync();      // neither CTA ends while the other's copies or arrivals may still come
-    else
-        __syncthreads();
+    __syncthreads();
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
@@ -590,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     if (tid == 0) a.cta_err[group * a.ctas + cta] = S.gave_up;
 }
 
-template <int NC, bool PAIR>
+template <int NC>
 cudaError_t run(Params& p, cudaStream_t st)
 {
     const int blocks = p.nb + (p.a.s.dr > 0 ? 1 : 0);
@@ -605,21 +577,10 @@ cudaError_t run(Params& p, cudaStream_t st)
     p.q_off = p.rope_off + p.nrope * kBlockBytes;
     p.p_off = p.q_off + q;
     const size_t bytes = 1024 + p.p_off + pp;
-    const cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<NC, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.a.ctas, p.a.groups);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = st;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 1;
-    attr.val.clusterDim.y = 2;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = PAIR ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, decode_tc_kernel<NC, PAIR>, p);
+    decode_tc_kernel<NC><<<dim3(p.a.ctas, p.a.groups), kThreads, bytes, st>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -644,14 +605,11 @@ cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st)
         (p.q_tma && (!row_map(&p.qc, a.qc.p, a.qc.head, (long long)s.B * s.T * s.H, s.dc, nc) ||
                      (s.dr > 0 && !row_map(&p.qr, a.qr.p, a.qr.head, (long long)s.B * s.T * s.H, s.dr, nc)))))
         return cudaErrorInvalidValue;
-    if (a.groups == 1)
-        return nc == 16   ? run<16, false>(p, st)
-               : nc == 32 ? run<32, false>(p, st)
-               : nc == 48 ? run<48, false>(p, st)
-               : nc == 64 ? run<64, false>(p, st)
-                          : run<80, false>(p, st);
-    // two groups and more have more than 80 rows in all: at least 41 each
-    return nc == 48 ? run<48, true>(p, st) : nc == 64 ? run<64, true>(p, st) : run<80, true>(p, st);
+    return nc == 16   ? run<16>(p, st)
+           : nc == 32 ? run<32>(p, st)
+           : nc == 48 ? run<48>(p, st)
+           : nc == 64 ? run<64>(p, st)
+                      : run<80>(p, st);
 }
 
 }  // namespace mla

@@ -50,9 +50,8 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-// A matrix descriptor's address field for a shared-memory address, to be added to a descriptor made for address 0.  (In
-// a cluster the address carries the CTA's rank above its 18 bits.)
-__device__ __forceinline__ uint64_t at_desc(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4; }
+// A matrix descriptor's address field for a shared-memory address, to be added to a descriptor made for address 0
+__device__ __forceinline__ uint64_t at_desc(uint32_t saddr) { return saddr >> 4; }
 
 // 2-D and 3-D tiled loads global -> shared, completion counted on `bar`
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint64_t* bar, int c0, int c1)
@@ -62,37 +61,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint
         "l"(tmap), "r"(c0), "r"(c1), "r"(smem_u32(bar))
         : "memory");
 }
-// the same into the CTAs of `mask` in the cluster: at the same place of each one's shared memory, counted on the barrier at
-// the same place of each
-__device__ __forceinline__ void tma_load_2d_multicast(uint32_t dst, const void* tmap, uint64_t* bar, int c0, int c1, uint16_t mask)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(tmap), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "h"(mask)
-        : "memory");
-}
-// mma_commit that arrives on the barrier at this place in each CTA of `mask`
-__device__ __forceinline__ void mma_commit_multicast(uint64_t* bar, uint16_t mask)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                     smem_u32(bar)),
-                 "h"(mask)
-                 : "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// every thread of the cluster's CTAs, by whole warps
-__device__ __forceinline__ void cluster_sync()
-{
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2)
 {
     asm volatile(

@@ -216,3 +216,14 @@ def test_names_are_exported():
     for n in ("gdn_mla_prep", "gdn_mla_prep_bwd", "gdn_mla_prep_workspace_bytes", "gdn_mla_fwd", "gdn_mla_bwd",
               "gdn_mla_workspace_bytes", "gdn_mla_decode", "gdn_mla_decode_workspace_bytes"):
         assert callable(getattr(gdn, n)) and hasattr(gdn.load(), n)
+
+
+# ---------------------------------------------------------------- the sources
+
+def test_each_cta_loads_its_own_tiles():
+    """The library is loaded by every rank of a job on several GPUs: no load or commit of it goes to several CTAs at once."""
+    from linear_attention_recurrence_delta_gb300 import _build
+    for path in _build._inputs():
+        if not path.endswith(".py"):
+            with open(path) as f:
+                assert "multicast" not in f.read().lower(), path
