@@ -75,3 +75,33 @@ def test_starved_load_times_out_and_context_survives(what):
     res = json.loads(r.stdout.strip().splitlines()[-1])
     assert res["status"] == GDN_ERR_TIMEOUT
     assert res["secs"] < 60.0
+
+
+_SECOND_WALK = r"""
+import json
+import torch
+import linear_attention_recurrence_delta_gb300 as gdn
+from tests.mla_testlib import attn_inputs, attn_ref
+# 480 tokens of one head: a tile of queries walks at most four tiles of 128 keys, so step 5 of the queries' gradient belongs
+# to the second walk that sharp scores ask for, and the pass over the keys has five steps of 96 queries, 0 to 4
+N, H, dims = 480, 1, (128, 64, 128)
+x, dO = attn_inputs(1, [N], [N], H, H, *dims, "bf16")
+def grads(scale):
+    s = gdn.make_mla_attn(1, H, H, N, N, *dims, "bf16", scale)
+    dev = {k: t.cuda() for k, t in x.items()}
+    ws = torch.empty(gdn.gdn_mla_workspace_bytes(s, 1), dtype=torch.uint8, device="cuda")
+    ro, rl, _ = attn_ref(x, [N], [N], scale, True)
+    d = [torch.empty_like(t) for t in dev.values()]
+    gdn.check(gdn.gdn_mla_bwd(s, *dev.values(), None, None, ro.cuda().bfloat16(), rl.cuda().float().contiguous(), dO.cuda(), *d, ws))
+    return gdn.gdn_last_device_status(ws)
+sharp, flat = grads(1.0), grads(0.05)
+print(json.dumps({"sharp": sharp, "flat": flat}))
+"""
+
+
+def test_starved_second_walk_times_out_and_context_survives():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, GDN_TEST_STARVE_CHUNK="5", PYTHONPATH=root)
+    r = subprocess.run([sys.executable, "-c", _SECOND_WALK], cwd=root, env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+    assert json.loads(r.stdout.strip().splitlines()[-1]) == {"sharp": GDN_ERR_TIMEOUT, "flat": 0}
