@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs 
         const bool whole = tile == 0 && to == tiles;
         const long long slot = ((long long)group * a.slots + cta + b) * a.rows;
         for (int r = 0; r < rows; r++) {
-            const float inv = sum[r] > 0.f ? 1.f / sum[r] : 0.f;
+            const float inv = sum[r] > 0.f ? 1.f / sum[r] : sum[r];    // zero stays zero, a NaN a NaN
             const long long out = (long long)b * s.T * s.H + row0 + r;
             if (2 * tid < s.dc) {
                 if (whole) {
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) decode_rows_kernel(const DecodeArgs 
                 }
             }
             if (tid == 0) {
-                const float l2 = sum[r] > 0.f ? top[r] + log2f(sum[r]) : -INFINITY;
+                const float l2 = sum[r] == 0.f ? -INFINITY : top[r] + log2f(sum[r]);
                 if (!whole)
                     a.part_l[slot + r] = l2;
                 else if (a.lse)

@@ -1,5 +1,8 @@
 """Latent attention where a warp's lanes part ways: ends of sequences and of widths at every place of a warp."""
+import math
+
 import pytest
+import torch
 
 import tests.test_mla_attn_gpu as attn
 import tests.test_mla_decode_gpu as decode
@@ -29,3 +32,27 @@ def test_latents_that_end_inside_a_warp(dc, n):
 def test_query_rows_that_end_inside_a_warp(T, H):
     """Rows that fill a part of a group's columns, in one group and in several, over enough tiles for a raised maximum."""
     decode.compare(T * H, [300, 1, 0, 2000, 64], T, H, 200, 32, 16, "bf16", std=4.0)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(1, 5), (1, 16), (2, 40), (8, 70)])
+@pytest.mark.parametrize("where", ["latent", "position", "query"])
+def test_nan_that_a_query_sees(where, T, H, io):
+    """A NaN in a row that every query sees, or in the queries, makes o and lse NaN, in a piece of its own or in one of many;
+    the other sequences keep their bits."""
+    n, dc, dr, page = [5000, 40, 300, 700], 128, 32, 16
+    table, pages, cache, rows, qc, qr = decode.setup(T + H, n, T, H, dc, dr, page, io)
+    good = decode.call(n, T, H, dc, dr, page, io, table, pages, cache, qc, qr, 0.1)
+    bad = [0, 1]
+    for b in bad:
+        if where == "query":
+            qc[b, :, :, 3] = math.nan
+        else:
+            cache[table[b, 1], 7, 5 if where == "latent" else dc + 5] = math.nan
+    o, lse = decode.call(n, T, H, dc, dr, page, io, table, pages, cache, qc, qr, 0.1)
+    for b in range(len(n)):
+        if b in bad:
+            assert torch.isnan(lse[b]).all(), b
+            assert torch.isnan(o[b]).all() if where != "latent" else torch.isnan(o[b]).any(-1).all(), b
+        else:
+            assert torch.equal(o[b], good[0][b]) and torch.equal(lse[b], good[1][b]), b
