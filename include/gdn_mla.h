@@ -47,7 +47,8 @@ typedef struct {
  * pos[n] % page, latent first.  page = 0: row n of lat and of kr (views of one head).
  * A token whose pos lies outside [0, npos), or whose seq or page lies outside its table, is skipped: its rows
  * (cache; lat, kr, qr_out when the position is bad) are not written.  No two tokens may name the same place.
- * Limits: N, H >= 0, 8 <= dc <= 1024, dr a multiple of 16 up to 128 (0: no position part). */
+ * Limits: N, H >= 0, npos >= 1 where N > 0 (without a position part too), 8 <= dc <= 1024, dr a multiple of 16 up to 128
+ * (0: no position part). */
 typedef struct {
     int N, H;                         /* tokens; query heads (0: no queries)            */
     int dc, dr;                       /* latent width, width of the position part       */

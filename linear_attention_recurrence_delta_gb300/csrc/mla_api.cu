@@ -36,6 +36,7 @@ gdn_status_t take(const gdn_mla_view_t* v, bool wanted, int heads, int io, gdn_m
 bool prep_ok(const gdn_mla_prep_t& s)
 {
     if (s.N < 0 || s.H < 0 || s.H > 65535 || s.npos < 0) return false;
+    if (s.N > 0 && s.npos == 0) return false;      // no position would be good, no token written
     if (s.dc < 8 || s.dc > 1024 || s.dc % 8 || s.dr < 0 || s.dr > 128 || s.dr % 16) return false;
     if (!(s.eps >= 0.f)) return false;
     if (s.page < 0) return false;

@@ -53,6 +53,7 @@ _IO = {"f32": 0, "bf16": 1}
 
 
 def make_mla_prep(N, H, dc, dr, io="bf16", npos=0, eps=1e-6, interleaved=False, B=0, page=0, npages=0, maxpages=0):
+    """npos: positions lie below it; a shape with tokens and without it is refused by the calls."""
     return gdn_mla_prep_t(int(N), int(H), int(dc), int(dr), _IO.get(io, io), int(npos), int(bool(interleaved)), int(B),
                           int(page), int(npages), int(maxpages), float(eps))
 

@@ -227,3 +227,14 @@ def test_each_cta_loads_its_own_tiles():
         if not path.endswith(".py"):
             with open(path) as f:
                 assert "multicast" not in f.read().lower(), path
+
+
+def test_prep_wants_positions():
+    """With no rows of rot every token's position would be outside the table: a call that writes nothing is refused."""
+    s = gdn.make_mla_prep(8, 4, 256, 64)
+    assert s.npos == 0
+    refused(prep(s), SHAPE)
+    refused(prep_bwd(s), SHAPE)
+    refused(prep(gdn.make_mla_prep(8, 4, 256, 0), rot=None), SHAPE)
+    assert gdn.gdn_mla_prep_workspace_bytes(s) == 0
+    assert prep(gdn.make_mla_prep(0, 4, 256, 64)) == OK
