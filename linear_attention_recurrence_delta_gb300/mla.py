@@ -3,8 +3,9 @@
 Like the recurrence's binding it only marshals arguments.  A tensor given as a view becomes its address and its row
 and head strides, so slices of a projection's output (``q[..., :dn]``, ``kv[..., dn:]``) go in as they are: rows may
 be one leading dimension ``[rows, heads, d]`` or ``[B, T, heads, d]`` whose first two collapse into rows.  A tensor
-whose values are not laid out that way raises ValueError; everything else is checked by the library, which returns
-its status code.
+whose values are not laid out that way or not of the type that the call reads (torch.int32 for positions, offsets,
+lengths and tables, torch.float32 for weights and statistics, the shape's io for the rest) raises ValueError; everything
+else is checked by the library, which returns its status code.
 
 One layer of a hybrid, between its projections (``gdn`` is this package)::
 
@@ -70,8 +71,14 @@ def make_mla_cache(B, T, H, dc, dr, page, npages, maxpages, io="bf16", scale=1.0
                            _IO.get(io, io), float(scale))
 
 
+_F32 = _I32 = _DTYPE = None      # torch's types; by gdn_dtype_t
+
+
 def declare(lib):
     """Signatures of the library's functions (called once, when it is loaded)."""
+    global _F32, _I32, _DTYPE
+    import torch
+    _F32, _I32, _DTYPE = torch.float32, torch.int32, {0: torch.float32, 1: torch.bfloat16}
     vp, ll, sz, vw = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_size_t, ctypes.POINTER(gdn_mla_view_t)
     sp, sa, sc = (ctypes.POINTER(t) for t in (gdn_mla_prep_t, gdn_mla_attn_t, gdn_mla_cache_t))
     for name, args, res in (
@@ -110,13 +117,21 @@ def _view(t, heads=True):
     return gdn_mla_view_t(t.data_ptr(), tok, stride[lead] if heads else tok)
 
 
+def _typed(t, dtype):
+    """For a tensor that is not of the wanted type (None: any will do)."""
+    if dtype is not None:
+        raise ValueError(f"a tensor of {dtype} is wanted here, not of {t.dtype}")
+
+
 # A decoding step waits for these calls' host time, so the common layouts take a short way (half a microsecond a view).
 
-def _heads(t):
+def _heads(t, dtype=None):
     """[rows, heads, d] or [B, T, heads, d] by reference."""
     if t is None:
         return None
     if type(t) is not gdn_mla_view_t:
+        if t.dtype is not dtype:
+            _typed(t, dtype)
         s = t.stride()
         if len(s) == 3 and s[2] == 1 and s[0] % 8 == 0 and s[0] > 0:
             return _ref(gdn_mla_view_t(t.data_ptr(), s[0], s[1]))
@@ -127,10 +142,13 @@ def _heads(t):
     return _ref(t)
 
 
-def _flat(t):
+def _flat(t, dtype=None):
     """[rows, d] by reference."""
     if t is None:
         return None
+    if type(t) is not gdn_mla_view_t:
+        if t.dtype is not dtype:
+            _typed(t, dtype)
     return _ref(_view(t, heads=False))
 
 
@@ -138,10 +156,12 @@ def _size(ws, ws_bytes):
     return _nbytes(ws) if ws_bytes is None and ws is not None else (ws_bytes or 0)
 
 
-def _rows(t):
+def _rows(t, dtype=None):
     """A tensor of contiguous rows as (address, row stride)."""
     if t is None or isinstance(t, int):
         return t, 0
+    if t.dtype is not dtype:
+        _typed(t, dtype)
     s = t.stride()
     if len(s) == 2 and s[1] == 1 and s[0] % 8 == 0 and s[0] > 0:
         return t.data_ptr(), s[0]
@@ -149,10 +169,12 @@ def _rows(t):
     return v.p, v.tok
 
 
-def _dense(t):
+def _dense(t, dtype=None):
     """The address of a contiguous tensor."""
     if t is None or type(t) is int:
         return t
+    if t.dtype is not dtype:
+        _typed(t, dtype)
     if not t.is_contiguous():
         raise ValueError("o, dO, lse, cache, table, lengths, offsets, positions and workspaces are contiguous")
     return t.data_ptr()
@@ -160,9 +182,10 @@ def _dense(t):
 
 def gdn_mla_prep(shape, kv, w, rot, pos, seq, table, qr, lat, kr, qr_out, stream=None) -> int:
     """Norm, rotate and write: into the paged cache `lat` (shape.page > 0; kr None), or to dense rows lat, kr."""
-    rows = _ref(gdn_mla_view_t(_dense(lat), 0, 0)) if shape.page > 0 else _flat(lat)
-    return load().gdn_mla_prep(_ref(shape), *_rows(kv), _dense(w), _dense(rot), _dense(pos), _dense(seq), _dense(table),
-                               _heads(qr), rows, _flat(kr), _heads(qr_out), _stream(stream))
+    f, d = load().gdn_mla_prep, _DTYPE.get(shape.io)
+    rows = _ref(gdn_mla_view_t(_dense(lat, d), 0, 0)) if shape.page > 0 else _flat(lat, d)
+    return f(_ref(shape), *_rows(kv, d), _dense(w, _F32), _dense(rot, _F32), _dense(pos, _I32), _dense(seq, _I32),
+             _dense(table, _I32), _heads(qr, d), rows, _flat(kr, d), _heads(qr_out, d), _stream(stream))
 
 
 def gdn_mla_prep_workspace_bytes(shape) -> int:
@@ -171,9 +194,10 @@ def gdn_mla_prep_workspace_bytes(shape) -> int:
 
 def gdn_mla_prep_bwd(shape, kv, w, rot, pos, dlat, dkr, dqr, dkv, dw, dqr_out, ws, ws_bytes=None, stream=None) -> int:
     """Gradients of the dense form: dkv [N, dc + dr], dw [dc] fp32 and dqr_out."""
-    return load().gdn_mla_prep_bwd(_ref(shape), *_rows(kv), _dense(w), _dense(rot), _dense(pos), _flat(dlat), _flat(dkr),
-                                   _heads(dqr), *_rows(dkv), _dense(dw), _heads(dqr_out), _ptr(ws), _size(ws, ws_bytes),
-                                   _stream(stream))
+    f, d = load().gdn_mla_prep_bwd, _DTYPE.get(shape.io)
+    return f(_ref(shape), *_rows(kv, d), _dense(w, _F32), _dense(rot, _F32), _dense(pos, _I32), _flat(dlat, d), _flat(dkr, d),
+             _heads(dqr, d), *_rows(dkv, d), _dense(dw, _F32), _heads(dqr_out, d), _ptr(ws), _size(ws, ws_bytes),
+             _stream(stream))
 
 
 def gdn_mla_workspace_bytes(shape, backward) -> int:
@@ -182,16 +206,18 @@ def gdn_mla_workspace_bytes(shape, backward) -> int:
 
 def gdn_mla_fwd(shape, qn, qr, kn, kr, v, cu_q, cu_k, o, lse, ws, ws_bytes=None, stream=None) -> int:
     """o and, if given, lse [H, Nq] fp32."""
-    return load().gdn_mla_fwd(_ref(shape), _heads(qn), _heads(qr), _heads(kn), _flat(kr), _heads(v), _dense(cu_q),
-                              _dense(cu_k), _dense(o), _dense(lse), _ptr(ws), _size(ws, ws_bytes), _stream(stream))
+    f, d = load().gdn_mla_fwd, _DTYPE.get(shape.io)
+    return f(_ref(shape), _heads(qn, d), _heads(qr, d), _heads(kn, d), _flat(kr, d), _heads(v, d), _dense(cu_q, _I32),
+             _dense(cu_k, _I32), _dense(o, d), _dense(lse, _F32), _ptr(ws), _size(ws, ws_bytes), _stream(stream))
 
 
 def gdn_mla_bwd(shape, qn, qr, kn, kr, v, cu_q, cu_k, o, lse, dO, dqn, dqr, dkn, dkr, dv, ws, ws_bytes=None,
                 stream=None) -> int:
     """The gradients of qn, qr, kn, kr and v from dO and the forward's o and lse."""
-    return load().gdn_mla_bwd(_ref(shape), _heads(qn), _heads(qr), _heads(kn), _flat(kr), _heads(v), _dense(cu_q),
-                              _dense(cu_k), _dense(o), _dense(lse), _dense(dO), _heads(dqn), _heads(dqr), _heads(dkn),
-                              _flat(dkr), _heads(dv), _ptr(ws), _size(ws, ws_bytes), _stream(stream))
+    f, d = load().gdn_mla_bwd, _DTYPE.get(shape.io)
+    return f(_ref(shape), _heads(qn, d), _heads(qr, d), _heads(kn, d), _flat(kr, d), _heads(v, d), _dense(cu_q, _I32),
+             _dense(cu_k, _I32), _dense(o, d), _dense(lse, _F32), _dense(dO, d), _heads(dqn, d), _heads(dqr, d),
+             _heads(dkn, d), _flat(dkr, d), _heads(dv, d), _ptr(ws), _size(ws, ws_bytes), _stream(stream))
 
 
 def gdn_mla_decode_workspace_bytes(shape) -> int:
@@ -200,5 +226,6 @@ def gdn_mla_decode_workspace_bytes(shape) -> int:
 
 def gdn_mla_decode(shape, qc, qr, cache, table, lens, o, lse, ws, ws_bytes=None, stream=None) -> int:
     """o [B, T, H, dc] and, if given, lse [B, T, H] fp32 of new tokens over the paged latent cache."""
-    return load().gdn_mla_decode(_ref(shape), _heads(qc), _heads(qr), _dense(cache), _dense(table), _dense(lens), _dense(o),
-                                 _dense(lse), _ptr(ws), _size(ws, ws_bytes), _stream(stream))
+    f, d = load().gdn_mla_decode, _DTYPE.get(shape.io)
+    return f(_ref(shape), _heads(qc, d), _heads(qr, d), _dense(cache, d), _dense(table, _I32), _dense(lens, _I32), _dense(o, d),
+             _dense(lse, _F32), _ptr(ws), _size(ws, ws_bytes), _stream(stream))

@@ -238,3 +238,57 @@ def test_prep_wants_positions():
     refused(prep(gdn.make_mla_prep(8, 4, 256, 0), rot=None), SHAPE)
     assert gdn.gdn_mla_prep_workspace_bytes(s) == 0
     assert prep(gdn.make_mla_prep(0, 4, 256, 64)) == OK
+
+
+def _calls():
+    """Each operator as a function of its tensors by name, with tensors of the types that it reads."""
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    z = lambda *shape, dt=bf: torch.zeros(shape, dtype=dt)  # noqa: E731
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    p = gdn.make_mla_prep(8, 4, 64, 32, "bf16", 10)
+    pp = gdn.make_mla_prep(8, 4, 64, 32, "bf16", 10, B=2, page=8, npages=4, maxpages=2)
+    a = gdn.make_mla_attn(1, 4, 2, 8, 8, 64, 32, 64)
+    c = gdn.make_mla_cache(2, 1, 4, 64, 32, 8, 4, 2)
+    rows = dict(kv=z(8, 96), w=z(64, dt=f32), rot=z(10, 32, dt=f32), pos=z(8, dt=i32))
+    qkv = dict(qn=z(8, 4, 64), qr=z(8, 4, 32), kn=z(8, 2, 64), kr=z(8, 32), v=z(8, 2, 64), cu_q=z(2, dt=i32), cu_k=z(2, dt=i32),
+               o=z(8, 4, 64), lse=z(4, 8, dt=f32))
+    return {
+        "prep": (lambda **t: gdn.gdn_mla_prep(p, **t, seq=None, table=None),
+                 dict(rows, qr=z(8, 4, 32), lat=z(8, 64), kr=z(8, 32), qr_out=z(8, 4, 32))),
+        "prep paged": (lambda **t: gdn.gdn_mla_prep(pp, **t, kr=None),
+                       dict(rows, seq=z(8, dt=i32), table=z(2, 2, dt=i32), qr=z(8, 4, 32), lat=z(4, 8, 96), qr_out=z(8, 4, 32))),
+        "prep_bwd": (lambda **t: gdn.gdn_mla_prep_bwd(p, **t, ws=ws),
+                     dict(rows, dlat=z(8, 64), dkr=z(8, 32), dqr=z(8, 4, 32), dkv=z(8, 96), dw=z(64, dt=f32), dqr_out=z(8, 4, 32))),
+        "fwd": (lambda **t: gdn.gdn_mla_fwd(a, **t, ws=ws), qkv),
+        "bwd": (lambda **t: gdn.gdn_mla_bwd(a, **t, ws=ws),
+                dict(qkv, dO=z(8, 4, 64), dqn=z(8, 4, 64), dqr=z(8, 4, 32), dkn=z(8, 2, 64), dkr=z(8, 32), dv=z(8, 2, 64))),
+        "decode": (lambda **t: gdn.gdn_mla_decode(c, **t, ws=ws),
+                   dict(qc=z(2, 1, 4, 64), qr=z(2, 1, 4, 32), cache=z(4, 8, 96), table=z(2, 2, dt=i32), lens=z(2, dt=i32),
+                        o=z(2, 1, 4, 64), lse=z(2, 1, 4, dt=f32))),
+    }
+
+
+@pytest.mark.parametrize("what", list(_calls()))
+def test_tensors_of_other_types(what, monkeypatch):
+    """Positions, offsets, lengths and tables in torch's default int64, norm weights in bf16 and any other tensor of a type
+    that the call would misread raise before the library sees an address."""
+    call, tensors = _calls()[what]
+
+    class Reached(Exception):
+        pass
+
+    class Lib:
+        def __getattr__(self, name):
+            def f(*args):
+                raise Reached
+            return f
+
+    from linear_attention_recurrence_delta_gb300 import mla
+    monkeypatch.setattr(mla, "load", Lib)
+    monkeypatch.setattr(mla, "_stream", lambda s: 0)
+    with pytest.raises(Reached):
+        call(**tensors)
+    for name, t in tensors.items():
+        other = {torch.int32: torch.int64, torch.float32: torch.bfloat16, torch.bfloat16: torch.float32}[t.dtype]
+        with pytest.raises(ValueError):
+            call(**{**tensors, name: t.to(other)})
