@@ -127,7 +127,9 @@ gdn_status_t gdn_mla_bwd(const gdn_mla_attn_t* shape, const gdn_mla_view_t* qn, 
  * over the rows j < len[b] - (T - 1 - t): the new tokens' own rows are in the cache already and token t sees its own.
  * lse[b, t, h] = log sum_j exp(s) (fp32, NULL: not written).  A query that sees no row gets o = 0 and lse = -inf.
  * len[b] is taken between 0 and maxpages * page; a page number outside [0, npages) reads as rows of zeros; nothing
- * past len[b] reaches a result.  Limits: 1 <= T <= 8, T * H <= 1024, dc in 8..512, dr in 0..64, page a multiple of 8,
+ * past len[b] reaches a result, and no sequence another's.  Within a sequence a NaN or Inf in the latent part of one of
+ * its last T - 1 rows may reach o of the new tokens that precede that row as well (a weight of zero meets it); their lse
+ * it never reaches.  A query that sees a NaN gets one for o and lse.  Limits: 1 <= T <= 8, T * H <= 1024, dc in 8..512, dr in 0..64, page a multiple of 8,
  * B <= 65535, npages * page < 2^31, B * (maxpages * page / 64 + 2) < 2^31,
  * scale >= 0. */
 typedef struct {

@@ -56,3 +56,24 @@ def test_nan_that_a_query_sees(where, T, H, io):
             assert torch.isnan(o[b]).all() if where != "latent" else torch.isnan(o[b]).any(-1).all(), b
         else:
             assert torch.equal(o[b], good[0][b]) and torch.equal(lse[b], good[1][b]), b
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("T,H", [(2, 5), (4, 40), (8, 16)])
+def test_reach_of_a_drafted_row(T, H, bad, io):
+    """A NaN or Inf in the last new token's row: the earlier tokens' lse and every other sequence keep their bits, the token
+    itself gets a NaN or an Inf."""
+    n, dc, dr, page = [3000, 70, 64, 300], 128, 32, 16
+    table, pages, cache, rows, qc, qr = decode.setup(3 * T + H, n, T, H, dc, dr, page, io)
+    good = decode.call(n, T, H, dc, dr, page, io, table, pages, cache, qc, qr, 0.1)
+    hit = [0, 1, 2]
+    for b in hit:
+        cache[table[b, (n[b] - 1) // page], (n[b] - 1) % page, :dc] = bad
+    o, lse = decode.call(n, T, H, dc, dr, page, io, table, pages, cache, qc, qr, 0.1)
+    for b in range(len(n)):
+        if b in hit:
+            assert torch.equal(lse[b, :-1], good[1][b, :-1]), b
+            assert (~torch.isfinite(o[b, -1])).all(), b
+        else:
+            assert torch.equal(o[b], good[0][b]) and torch.equal(lse[b], good[1][b]), b
