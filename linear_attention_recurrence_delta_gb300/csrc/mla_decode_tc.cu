@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
             const uint32_t buf = (uint32_t)i & 1, phase = (uint32_t)(i >> 1) & 1;
             if (first) {
                 from = r.tile;
-                if (t < NC) S.top[t] = 0.f;
+                if (t < NC) S.top[t] = t < rows ? 0.f : INFINITY;   // a column of another's queries never asks to raise
 #pragma unroll
                 for (int n = 0; n < HC; n++) l[n] = 0.f;
                 group_sync(1, kSoft);

@@ -77,3 +77,18 @@ def test_reach_of_a_drafted_row(T, H, bad, io):
             assert (~torch.isfinite(o[b, -1])).all(), b
         else:
             assert torch.equal(o[b], good[0][b]) and torch.equal(lse[b], good[1][b]), b
+
+
+@pytest.mark.parametrize("T,H", [(1, 5), (2, 9), (3, 30)])
+def test_another_sequences_queries_change_no_bit(T, H):
+    """The queries of the sequences behind, whose rows fill up a group's columns: large ones, whose scores rise from tile to
+    tile, Inf and NaN leave every bit of the first sequence's results."""
+    n, dc, dr, page = [6000, 500, 300], 128, 32, 16
+    table, pages, cache, rows, qc, qr = decode.setup(T + 7 * H, n, T, H, dc, dr, page, "bf16", 4.0)
+    good = decode.call(n, T, H, dc, dr, page, "bf16", table, pages, cache, qc, qr, 0.1)
+    for factor in (30.0, math.inf, math.nan):
+        c, r = qc.clone(), qr.clone()
+        c[1:] *= factor
+        r[1:] *= factor
+        o, lse = decode.call(n, T, H, dc, dr, page, "bf16", table, pages, cache, c, r, 0.1)
+        assert torch.equal(o[0], good[0][0]) and torch.equal(lse[0], good[1][0]), factor
