@@ -59,7 +59,7 @@ typedef struct {
     float eps;
 } gdn_mla_prep_t;
 
-/* kv [N, dc + dr] with row stride kv_tok; w [dc] fp32; rot [npos, dr] fp32; pos, seq [N] int32;
+/* kv [N, dc + dr] with row stride kv_tok; w [dc] fp32; rot [npos, dr] fp32, 16-byte aligned; pos, seq [N] int32;
  * table [B, maxpages] int32.  qr, qr_out [N, H, dr] views (NULL iff H = 0 or dr = 0); qr_out may be the very
  * same view as qr.  Paged: lat->p is the cache (lat's strides and kr are ignored). */
 gdn_status_t gdn_mla_prep(const gdn_mla_prep_t* shape, const void* kv, long long kv_tok, const float* w,

@@ -292,3 +292,11 @@ def test_tensors_of_other_types(what, monkeypatch):
         other = {torch.int32: torch.int64, torch.float32: torch.bfloat16, torch.bfloat16: torch.float32}[t.dtype]
         with pytest.raises(ValueError):
             call(**{**tensors, name: t.to(other)})
+
+
+def test_alignment_of_rot():
+    """Of the fp32 and int32 arrays rot alone is read 16 bytes at a time."""
+    s = gdn.make_mla_prep(8, 4, 256, 64, "bf16", 100)
+    refused(prep(s, rot=FAKE + 4), ALIGN)
+    refused(prep_bwd(s, rot=FAKE + 8), ALIGN)
+    refused(prep(s, w=FAKE + 2), ALIGN)
