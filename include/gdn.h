@@ -293,7 +293,8 @@ gdn_status_t gdn_bwd_noalloc_status(gdn_stream_t stream);
 
 /* Synchronises `stream` and returns the status the kernels of the last call
  * that used `ws` left in it (GDN_OK, GDN_ERR_TIMEOUT), or GDN_ERR_CUDA if the
- * synchronisation itself failed. */
+ * synchronisation itself failed or a kernel did not get its shared memory as it
+ * was compiled for. */
 gdn_status_t gdn_last_device_status(const void* ws, gdn_stream_t stream);
 
 /* A static, human-readable name for a status code. */

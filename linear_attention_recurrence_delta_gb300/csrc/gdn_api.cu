@@ -551,6 +551,7 @@ extern "C" gdn_status_t gdn_last_device_status(const void* ws, gdn_stream_t stre
     uint32_t word[2] = {0, 0};
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return GDN_ERR_CUDA;
     if (cudaMemcpy(word, ws, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return GDN_ERR_CUDA;
+    if (word[0] == kDevLayout) return GDN_ERR_CUDA;
     if (word[0] != kDevOk) return GDN_ERR_TIMEOUT;
     return word[1] != 0 ? GDN_ERR_NONFINITE : GDN_OK;
 }

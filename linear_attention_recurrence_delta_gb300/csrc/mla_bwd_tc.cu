@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_tc_kernel(const __grid_constan
 template <int NQ>
 struct SharedK {
     uint64_t kv_full, q_full[3], q_empty[3], do_full[2], do_empty[2], st_full[2], st_empty[2], s_full, p_full, dp_full, ds_full,
-        acc_full, drain[2];
+        acc_full, drain;
     alignas(16) float lower[2][NQ];     // -lse log2(e), minus infinity for a row that adds nothing
     alignas(16) float delta[2][NQ];     // -delta
     uint32_t tmem, gave_up;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
         return;
     }
     if (smem_u32(raw) & 1023) {     // never so without static shared memory; the tiles below would not fit otherwise
-        if (threadIdx.x == 0) atomicExch(a.status, kDevTimeout);
+        if (threadIdx.x == 0) atomicExch(a.status, kDevLayout);
         cudaGridDependencySynchronize();
         return;
     }
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
 
     if (warp == 0) {
         if (elect_one()) {
-            for (uint64_t* x : {&S.kv_full, &S.s_full, &S.dp_full, &S.acc_full, &S.drain[0]}) mbar_init(x, 1);
+            for (uint64_t* x : {&S.kv_full, &S.s_full, &S.dp_full, &S.acc_full, &S.drain}) mbar_init(x, 1);
             for (int i = 0; i < QS; i++)
                 for (uint64_t* x : {&S.q_full[i], &S.q_empty[i]}) mbar_init(x, 1);
             for (int i = 0; i < 2; i++) {
@@ -635,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_tc_kernel(const __grid_consta
             }
             mma_commit(&S.acc_full);
             if (*gave_up) {   // the products in flight end before TMEM is freed
-                mma_commit(&S.drain[0]);
-                mbar_wait(&S.drain[0], 0, nullptr, kDrainNs);
+                mma_commit(&S.drain);
+                mbar_wait(&S.drain, 0, nullptr, kDrainNs);
             }
         }
     } else if (warp < 4) {

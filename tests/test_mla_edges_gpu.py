@@ -4,6 +4,7 @@ import math
 import pytest
 import torch
 
+import linear_attention_recurrence_delta_gb300 as gdn
 import tests.test_mla_attn_gpu as attn
 import tests.test_mla_decode_gpu as decode
 from tests.mla_testlib import attn_inputs
@@ -92,3 +93,11 @@ def test_another_sequences_queries_change_no_bit(T, H):
         r[1:] *= factor
         o, lse = decode.call(n, T, H, dc, dr, page, "bf16", table, pages, cache, c, r, 0.1)
         assert torch.equal(o[0], good[0][0]) and torch.equal(lse[0], good[1][0]), factor
+
+
+def test_status_words():
+    """What a kernel may leave in a workspace's first word, as the status reads it."""
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for word, status in ((0, gdn.GDN_OK), (1, 7), (2, 6), (0, gdn.GDN_OK)):     # timeout; shared memory not as compiled for
+        ws[0] = word
+        assert gdn.gdn_last_device_status(ws) == status
