@@ -87,9 +87,11 @@ gdn_status_t gdn_mla_prep_bwd(const gdn_mla_prep_t* shape, const void* kv, long 
  * Sequences: cu_q, cu_k NULL: sequence b holds rows b * Tq .. and b * Tk .. of the tensors; else int32 [B + 1] row
  * offsets on the device, ascending, with sequences of at most Tq and Tk rows (longer ones are cut there, offsets
  * outside [0, Nq] or [0, Nk] are taken as the nearer bound).  Rows of no sequence are neither read into a result nor
- * written.  Values in one sequence never reach another, NaN and Inf included; within a sequence a NaN or Inf in a
- * key's v, kn or kr reaches the queries of its 128-key tile that precede it as well.
- * Limits: H a multiple of Hkv; dn, dv in 8..128, dr in 0..64; B, H <= 65535; Nq, Nk < 2^31, Nq * H and Nk * Hkv < 2^34; scale >= 0. */
+ * written.  Values in one sequence never reach another, NaN and Inf included.  Within a sequence a NaN or Inf in a
+ * key's v, kn or kr may reach o and the gradients of queries that precede it, by up to 254 positions, and one in a
+ * query's qn, qr or dO the gradients of keys that follow it, by up to as many (tiles of 128 meet weights of zero).
+ * Limits: H a multiple of Hkv; dn, dv in 8..128, dr in 0..64; B, H <= 65535; Nq, Nk < 2^31, Nq * H and
+ * Nk * Hkv < 2^34; scale >= 0. */
 typedef struct {
     int B, H, Hkv;
     int Tq, Tk;                       /* most rows of one sequence                      */
@@ -129,9 +131,9 @@ gdn_status_t gdn_mla_bwd(const gdn_mla_attn_t* shape, const gdn_mla_view_t* qn, 
  * len[b] is taken between 0 and maxpages * page; a page number outside [0, npages) reads as rows of zeros; nothing
  * past len[b] reaches a result, and no sequence another's.  Within a sequence a NaN or Inf in the latent part of one of
  * its last T - 1 rows may reach o of the new tokens that precede that row as well (a weight of zero meets it); their lse
- * it never reaches.  A query that sees a NaN gets one for o and lse.  Limits: 1 <= T <= 8, T * H <= 1024, dc in 8..512, dr in 0..64, page a multiple of 8,
- * B <= 65535, npages * page < 2^31, B * (maxpages * page / 64 + 2) < 2^31,
- * scale >= 0. */
+ * it never reaches.  A query that sees a NaN gets one for o and lse.
+ * Limits: 1 <= T <= 8, T * H <= 1024, dc in 8..512, dr in 0..64, page a multiple of 8, B <= 65535,
+ * npages * page < 2^31, B * (maxpages * page / 64 + 2) < 2^31, scale >= 0. */
 typedef struct {
     int B, T, H;
     int dc, dr;

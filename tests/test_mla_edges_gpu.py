@@ -7,7 +7,7 @@ import torch
 import linear_attention_recurrence_delta_gb300 as gdn
 import tests.test_mla_attn_gpu as attn
 import tests.test_mla_decode_gpu as decode
-from tests.mla_testlib import attn_inputs
+from tests.mla_testlib import attn_inputs, attn_run
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +101,37 @@ def test_status_words():
     for word, status in ((0, gdn.GDN_OK), (1, 7), (2, 6), (0, gdn.GDN_OK)):     # timeout; shared memory not as compiled for
         ws[0] = word
         assert gdn.gdn_last_device_status(ws) == status
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("dn,dr,dv", [(64, 32, 64), (128, 64, 128)])
+@pytest.mark.parametrize("nq,nk,at", [(600, 600, 383), (600, 600, 300), (500, 731, 640), (700, 660, 511)])
+def test_reach_of_a_nan_in_a_sequence(nq, nk, at, dn, dr, dv, io):
+    """A NaN in a key: queries 255 positions and more before it keep the bits of their o and gradients.  One in a query's
+    rows: so do the keys 255 positions and more behind it.  Every other head group keeps all."""
+    H, Hkv = 4, 2
+    x, dO = attn_inputs(nq + at, [nq], [nk], H, Hkv, dn, dr, dv, io)
+    good = attn_run(x, [nq], [nk], 0.1, True, io, dO)
+    off = nk - nq
+    y = {k: t.clone() for k, t in x.items()}
+    y["kn"][at, 0] = y["v"][at, 0] = math.nan
+    o, lse, d = attn_run(y, [nq], [nk], 0.1, True, io, dO)
+    far = max(0, at - 254 - off)                     # the queries before this one
+    sees = max(0, at - off)                          # the first that sees the key
+    assert torch.equal(o[:far], good[0][:far]) and torch.equal(lse[:, :sees], good[1][:, :sees])
+    assert torch.equal(o[:, 2:], good[0][:, 2:]) and torch.isnan(o[sees:, :2]).all()
+    for k in ("qn", "qr"):
+        assert torch.equal(d[k][:far], good[2][k][:far]) and torch.equal(d[k][:, 2:], good[2][k][:, 2:]), k
+    for k in ("kn", "v"):
+        assert torch.equal(d[k][:, 1], good[2][k][:, 1]), k
+    row = max(0, at - off - 200)
+    y, dP = {k: t.clone() for k, t in x.items()}, dO.clone()
+    y["qn"][row, 0] = dP[row, 0] = math.nan
+    o, lse, d = attn_run(y, [nq], [nk], 0.1, True, io, dP)
+    keep = torch.arange(nq, device="cuda") != row
+    assert torch.equal(o[keep], good[0][keep]) and torch.equal(lse[:, keep], good[1][:, keep])
+    for k in ("qn", "qr"):
+        assert torch.equal(d[k][keep], good[2][k][keep]), k
+    for k in ("kn", "v"):
+        past = row + off + 255
+        assert torch.equal(d[k][past:], good[2][k][past:]) and torch.equal(d[k][:, 1], good[2][k][:, 1]), k
