@@ -422,7 +422,7 @@ cudaError_t launch_attn_f32(const AttnArgs& a, cudaStream_t st)
     const int pq = pitch_of(s.dn + s.dr), pv = pitch_of(s.dv), r = pick_rows(s.Tq, (long long)s.H * s.B), held = 16 * r;
     const dim3 grid((s.Tq + held - 1) / held, s.H, s.B);
     const size_t h = (size_t)held * (pq + kSP), w = (size_t)kTile * (pq + pv);
-    return r == 4 ? start(fwd_kernel<4>, a, grid, h, w, false, st) : r == 2 ? start(fwd_kernel<2>, a, grid, h, w, false, st) : start(fwd_kernel<1>, a, grid, h, w, false, st);
+    return start(r == 4 ? fwd_kernel<4> : r == 2 ? fwd_kernel<2> : fwd_kernel<1>, a, grid, h, w, false, st);
 }
 
 cudaError_t launch_attn_bwd_f32(const AttnArgs& a, cudaStream_t st)
@@ -435,14 +435,14 @@ cudaError_t launch_attn_bwd_f32(const AttnArgs& a, cudaStream_t st)
         const int r = pick_rows(s.Tq, (long long)s.H * s.B), held = 16 * r;
         const dim3 grid((s.Tq + held - 1) / held, s.H, s.B);
         const size_t h = (size_t)held * (pq + pv + kSP), w = (size_t)kTile * (pq + pv);
-        e = r == 4 ? start(dq_kernel<4>, a, grid, h, w, true, st) : r == 2 ? start(dq_kernel<2>, a, grid, h, w, true, st) : start(dq_kernel<1>, a, grid, h, w, true, st);
+        e = start(r == 4 ? dq_kernel<4> : r == 2 ? dq_kernel<2> : dq_kernel<1>, a, grid, h, w, true, st);
         if (e != cudaSuccess) return e;
     }
     if (s.Tk > 0) {
         const int r = pick_rows(s.Tk, (long long)s.Hkv * s.B), held = 16 * r;
         const dim3 grid((s.Tk + held - 1) / held, s.Hkv, s.B);
         const size_t h = (size_t)held * (pq + pv) + (size_t)2 * kTile * (held + 4), w = (size_t)kTile * (pq + pv + 2);
-        e = r == 4 ? start(dkv_kernel<4>, a, grid, h, w, s.Tq > 0, st) : r == 2 ? start(dkv_kernel<2>, a, grid, h, w, s.Tq > 0, st) : start(dkv_kernel<1>, a, grid, h, w, s.Tq > 0, st);
+        e = start(r == 4 ? dkv_kernel<4> : r == 2 ? dkv_kernel<2> : dkv_kernel<1>, a, grid, h, w, s.Tq > 0, st);
         if (e != cudaSuccess) return e;
         if (s.dr > 0) return launch_dkr(a, st);
     }

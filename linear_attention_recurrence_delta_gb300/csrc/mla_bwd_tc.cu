@@ -10,9 +10,9 @@
 // products from there.  One product's tensor-core time covers the other's elementwise work: while the threads turn
 // S(i+1) into P, dK(i) and dP(i+1) run; while they turn dP into dS, dV and the next S run.
 //
-// 8 x 4096 tokens, 16 query and 4 key heads of 128: 0.67 ms for dQ (54 % of the tensor cores' cycles, 2080 a step where
-// the products need 1536, and a start of 6000 a CTA that the loads of its first tiles take) and 0.71 ms for dK and dV
-// (67 %; 2400 a step for 2048).
+// 8 x 4096 tokens, 16 query and 4 key heads of 128: 0.71 ms for dQ and 0.72 ms for dK and dV (67 % of the tensor cores'
+// cycles; 2400 a step for 2048).  dQ took 0.67 ms (54 %, 2080 a step where the products need 1536, and a start of 6000 a
+// CTA that the loads of its first tiles take) before it formed delta itself, which saves a pass over dO and o.
 //
 // Roles (12 warps): warp 0 loads tiles by TMA, warp 1 issues products, warps 2-3 bring lse and delta and blank the
 // rows past a ragged end, warps 4-11 do the elementwise work, half of a tile's columns each.
@@ -65,8 +65,8 @@ __device__ __forceinline__ uint4 pack8(const float* x, float f)
 // exact delta.  The pass over the keys gets the corrected one.  dQ is off by that much times sum_j P K.  dS's own rounding
 // to bf16 is off by 2^-9 sum_j |dS| at most; where a tile's rows lack more than that (in squares over the rows), few keys
 // take their weight and the tile walks again, by the corrected delta.  The sum of |dS| is twice that over every other key.
-// Training steps of 8 x 4096 tokens (6 documents up to 1900) by the standard deviation of the scores, us: 1.5: 1867 (306), 3: 1905 (308),
-// 4.5: 1991 (319), 6: 2273 (343), 12: 2521 (359); without the sums and the question 7 (1) less.
+// Training steps of 8 x 4096 tokens (6 documents up to 1900) by the standard deviation of the scores, us: 1.5: 1867 (306),
+// 3: 1905 (308), 4.5: 1991 (319), 6: 2273 (343), 12: 2521 (359); without the sums and the question 7 (1) less.
 
 constexpr int kTwice = 2;
 constexpr float kOff = 0.001953125f;     // 2^-9
@@ -85,8 +85,8 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& y)
 }
 
 struct SharedQ {
-    uint64_t q_full, a_full, k_full[3], k_empty[3], v_full[2], v_empty[2], k_last[2], k_fixed[2], s_full, s_read, dp_full, dp_read, ds_full, ds_empty,
-        dq_full, verdict, drain;
+    uint64_t q_full, a_full, k_full[3], k_empty[3], v_full[2], v_empty[2], k_last[2], k_fixed[2], s_full, s_read, dp_full, dp_read,
+        ds_full, ds_empty, dq_full, verdict, drain;
     float part[2][kTile];        // a row's sums from each half of the columns
     uint32_t tmem, gave_up, again;
 };

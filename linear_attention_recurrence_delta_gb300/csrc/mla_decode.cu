@@ -328,9 +328,9 @@ cudaError_t run_rows(const DecodeArgs& a, cudaStream_t st)
 // launch, not the last worker of a sequence, because the workspace is the caller's and holds no counters between calls.
 // The rows' pieces go to a block's warps where rows are few for the pieces that each has, about workers / B.  A warp a row
 // against a block for 128 columns of a row, us of the call (sequences x lengths, rows a sequence, latent width):
-// 1 x 32768, 64, 512: 68.8 / 32.8; 2 x 32768, 16, 512: 40.4 / 26.7; 8 x 32768, 16, 512: 63.6 / 60.4; 16 x 16384, 16, 512:
-// 63.2 / 61.4; 4 x 32768, 160, 512: 108.4 / 109.6; 32 x 8192, 16, 512: 61.8 / 64.1; 16 x 6000, 40, 512: 40.1 / 42.3;
-// 64 x 4096, 16, 256: 43.2 / 47.1.
+// 1 x 32768, 64, 512: 47.3 / 31.0; 2 x 32768, 16, 512: 40.8 / 26.6; 8 x 32768, 16, 512: 63.7 / 61.0; 16 x 16384, 16, 512:
+// 63.5 / 61.5; 4 x 32768, 160, 512: 86.5 / 84.6; 32 x 8192, 16, 512: 62.1 / 64.3; 16 x 6000, 40, 512: 39.0 / 41.1;
+// 64 x 4096, 16, 256: 44.5 / 47.1.
 constexpr long long kSpread = 4096;
 template <typename T>
 cudaError_t run_join(const DecodeArgs& a, cudaStream_t st)

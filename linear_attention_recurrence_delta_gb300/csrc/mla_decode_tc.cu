@@ -9,9 +9,11 @@
 // pieces (page by page: a page's rows are one box); warp 1 issues the scores' products and warp 2 the outputs', each
 // waiting for its own operands only, so that the next tiles' scores run ahead of this tile's outputs; warp 3 lays the
 // queries out; warps 4-11 do the softmax.  The softmax keeps a running maximum of each query row but lowers scores by an
-// old one until a score exceeds it by 2^16: exp2 and fp32 hold that range, P's bf16 rounding is relative, and the outputs in TMEM are rescaled only then (rarely after a sequence's first
-// tile).  HBM bounds it while the query rows fit one group: 8 x 32768 rows of 512 + 64 values under 16 heads take 56 us
-// (302 MB, 5.4 TB/s; 3250 cycles a 64-row tile are 22.7 bytes a cycle and SM, the card's rate, the rest start and end).
+// old one until a score exceeds it by 2^16: exp2 and fp32 hold that range, P's bf16 rounding is relative, and the outputs
+// in TMEM are rescaled only then (rarely after a sequence's first tile).
+//
+// HBM bounds it while the query rows fit one group: 8 x 32768 rows of 512 + 64 values under 16 heads take 57 us
+// (302 MB, 5.3 TB/s; 3250 cycles a 64-row tile are 22.7 bytes a cycle and SM, the card's rate, the rest start and end).
 // A call of 160 rows in two groups takes 88 us where the bytes alone need 20: less than two tiles fit beside 92 KB
 // of queries, so a tile's load waits for the products of the one before it.
 #include "mla_decode_common.cuh"
@@ -322,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax, outputs
         // Two warpgroups take half of the query rows' columns each (against one, when a load served two groups, us: 160 rows
-        // 92.3 to 90.1, 128 rows 92.3 to 88.2, 16 rows unchanged, 160 rows over 256 + 64 53.3 to 55.3).  An M = 64 product fills the first 16 lanes of each
-        // warp's 32 in TMEM: lanes 16..31 take over the second half of these rows' columns.
+        // 92.3 to 90.1, 128 rows 92.3 to 88.2, 16 rows unchanged, 160 rows over 256 + 64 53.3 to 55.3).  An M = 64 product
+        // fills the first 16 lanes of each warp's 32 in TMEM: lanes 16..31 take over the second half of these rows' columns.
         constexpr int HC = NC / 4;
         const int quad = warp & 3, half = (warp - 4) >> 2, t = tid - 128, key = quad * 16 + (lane & 15);
         const int col0 = 2 * HC * half + (lane < 16 ? 0 : HC);

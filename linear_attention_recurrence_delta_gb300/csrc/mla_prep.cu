@@ -3,8 +3,9 @@
 // Elementwise but for one sum a token, so HBM bounds it: each input is read once and each output written once, in
 // 16-byte pieces.  A warp holds a token's whole latent in registers (its sum of squares is one warp reduction); a
 // thread rotates 8 pairs of two query heads by angles that it reads once.  Forwards both kinds of block run in one
-// launch, because a decoding step is bound by launches, not bytes.  32768 tokens of 256 + 64 values with 16 heads of 64: 41 us forwards (176 MB, 4.3 TB/s),
-// 86 us for both passes; a decoding step of 24 tokens takes 5 us from a cold cache, and the call's host time more.
+// launch, because a decoding step is bound by launches, not bytes.  32768 tokens of 256 + 64 values with 16 heads of 64:
+// 41 us forwards (176 MB, 4.3 TB/s), 87 us for both passes; a decoding step of 24 tokens takes 5 us from a cold cache, and
+// the call's host time more.
 #include "mla_internal.h"
 
 namespace gdn {
