@@ -1,4 +1,4 @@
-"""Latent attention where a warp's lanes part ways: ends of sequences and of widths at every place of a warp."""
+"""Latent attention at its edges: ends inside a warp, NaN and Inf and how far they reach, status words."""
 import math
 
 import pytest
