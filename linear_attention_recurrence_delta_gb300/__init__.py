@@ -26,8 +26,9 @@ A forward and backward on torch tensors (v, b, c [B, T, H, d] bf16; g, beta
 ``h0``, ``hT``, ``dhT``, ``dh0`` may be None; ``make_shape(..., gate_logits=True,
 norm_bc=True)`` moves the gates' sigmoid and the L2 normalisation of b and c
 into the kernels, and ``gdn_plan(s, backward)`` tells which kernels a call
-will use.  The latent-attention operators beside the recurrence (``gdn_mla_*``) are in :mod:`.mla` and exported here
-under their C names.
+will use.  The latent-attention operators beside the recurrence (``gdn_mla_*``) are in :mod:`.mla`, those of a
+state-space layer (``gdn_norm_*``, ``gdn_conv_*``, ``gdn_scan_*``) in :mod:`.ssm`; both are exported here under their C
+names.
 """
 from __future__ import annotations
 
@@ -121,8 +122,9 @@ def load(path: str | None = None):
             lib.gdn_last_device_status.restype = ctypes.c_int
             lib.gdn_status_string.argtypes = [ctypes.c_int]
             lib.gdn_status_string.restype = ctypes.c_char_p
-            from . import mla
+            from . import mla, ssm
             mla.declare(lib)
+            ssm.declare(lib)
             _lib = lib
     return _lib
 
@@ -231,7 +233,11 @@ def check(status: int, what: str = "") -> None:
         raise GdnError(status, what)
 
 
-# latent attention; mla takes the helpers above from this module, so it comes last
+# latent attention and the state-space layer; they take the helpers above from this module, so they come last
 from .mla import (gdn_mla_attn_t, gdn_mla_bwd, gdn_mla_cache_t, gdn_mla_decode, gdn_mla_decode_workspace_bytes,  # noqa: E402
                   gdn_mla_fwd, gdn_mla_prep, gdn_mla_prep_bwd, gdn_mla_prep_t, gdn_mla_prep_workspace_bytes,
                   gdn_mla_view_t, gdn_mla_workspace_bytes, make_mla_attn, make_mla_cache, make_mla_prep)
+from .ssm import (GDN_E4M3, gdn_conv_bwd, gdn_conv_fwd, gdn_conv_step, gdn_conv_step_t, gdn_conv_t,  # noqa: E402
+                  gdn_conv_workspace_bytes, gdn_norm_bwd, gdn_norm_fwd, gdn_norm_t, gdn_norm_workspace_bytes, gdn_scan_bwd,
+                  gdn_scan_fwd, gdn_scan_saved_bytes, gdn_scan_step, gdn_scan_step_t, gdn_scan_t, gdn_scan_workspace_bytes,
+                  make_conv, make_conv_step, make_norm, make_scan, make_scan_step)

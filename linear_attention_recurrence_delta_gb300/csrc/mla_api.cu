@@ -8,31 +8,6 @@ using namespace gdn::mla;
 
 namespace {
 
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-bool io_ok(int io) { return io == GDN_F32 || io == GDN_BF16; }
-
-// A view of `heads` heads of width `d`: present iff d > 0 and there are rows, 16-byte aligned, with strides that keep
-// every row and head aligned.  `w` receives it, with a head stride that is valid for one head too.
-gdn_status_t take(const gdn_mla_view_t* v, bool wanted, int heads, int io, gdn_mla_view_t* w)
-{
-    memset(w, 0, sizeof(*w));
-    if (!wanted) return GDN_OK;
-    if (!v || !v->p) return GDN_ERR_NULL;
-    const long long unit = io == GDN_BF16 ? 8 : 4;
-    *w = *v;
-    if (heads == 1) w->head = w->tok;
-    if (w->tok <= 0 || w->head <= 0 || w->tok >= (1LL << 38) || w->head >= (1LL << 38)) return GDN_ERR_SHAPE;
-    if (!aligned(w->p, 16) || w->tok % unit || w->head % unit) return GDN_ERR_ALIGN;
-    return GDN_OK;
-}
-
-#define GDN_TAKE(...)                                  \
-    do {                                               \
-        const gdn_status_t r_ = take(__VA_ARGS__);     \
-        if (r_ != GDN_OK) return r_;                   \
-    } while (0)
-
 bool prep_ok(const gdn_mla_prep_t& s)
 {
     if (s.N < 0 || s.H < 0 || s.H > 65535 || s.npos < 0) return false;

@@ -1,0 +1,100 @@
+// ssm_internal.h -- what the translation units of the state-space operators share (not part of the ABI).
+#pragma once
+
+#include "../../include/gdn_ssm.h"
+#include "mla_internal.h"
+
+namespace gdn {
+namespace ssm {
+
+using mla::Raw8;
+using mla::Rows;
+
+struct NormArgs {
+    gdn_norm_t s;
+    const void *x, *res;      // x is the forward's input; the backward's `sum` arrives in res
+    const float* w;
+    void *y, *sum;
+    float* scale;
+    const void *dy, *dsum;
+    void *dx, *dres;
+    float *dw, *partial;      // partial [norm_bwd_blocks][D]
+    long long x_tok, res_tok, y_tok, sum_tok, dy_tok, dsum_tok, dx_tok, dres_tok;
+};
+
+struct ConvArgs {
+    gdn_conv_t s;
+    gdn_mla_view_t x, y, dy, dx;
+    const float *w, *bias;
+    const int* cu;
+    const void *s0, *dsT;
+    void *sT, *ds0;
+    float *dw, *dbias, *partial;   // partial [conv_bwd_blocks][D (W + 1)]
+};
+
+struct ConvStepArgs {
+    gdn_conv_step_t s;
+    gdn_mla_view_t x, y;
+    const float *w, *bias;
+    void* state;
+    const int *src, *dst;
+};
+
+struct ScanArgs {
+    gdn_scan_t s;
+    gdn_mla_view_t x, dt, z, Bm, Cm, y, dy, dx, ddt, dz, dBm, dCm;
+    const float *A_log, *D_skip, *dt_bias, *h0, *dhT;
+    const int* cu;
+    float *hT, *dh0, *dA_log, *dD_skip, *ddt_bias;
+    float* saved;             // states entering every kSaveEvery tokens: [rows / kSaveEvery + B + 1][D][N]
+    float* wpart;             // backward: [B * segments][D (N + 2)] shares of dA_log, dD_skip, ddt_bias
+    float* bcpart;            // backward: [channel blocks of a group][rows][G][2 N] shares of dBm, dCm
+    float *seg_h, *seg_d;     // split in time: [segments][B][D][N] states from zero, [segments][B][D] sums of delta
+    int segments, seg_len;    // segments a sequence is cut into, tokens of one (a multiple of the tile)
+};
+
+struct ScanStepArgs {
+    gdn_scan_step_t s;
+    gdn_mla_view_t x, dt, z, Bm, Cm, y;
+    const float *A_log, *D_skip, *dt_bias;
+    float* state;
+    const int *src, *dst;
+};
+
+int norm_bwd_blocks(const gdn_norm_t& s);
+int conv_bwd_blocks(const gdn_conv_t& s);
+
+constexpr int kSaveEvery = 16;    // tokens between the states that a training forward keeps
+
+// How a scan's call is laid out: blocks of channels (within a group), segments of time, workspace.
+struct ScanPlan {
+    int channels;                 // channels a CTA takes
+    int blocks;                   // CTAs a group's channels need
+    int segments, seg_len;
+    size_t h_off, d_off, w_off, bc_off, total;
+};
+ScanPlan scan_plan(const gdn_scan_t& s, int backward);
+inline size_t saved_states(const gdn_scan_t& s) { return (size_t)(s.rows / kSaveEvery) + s.B + 1; }
+
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_conv(const ConvArgs& a, cudaStream_t st);
+cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t st);
+cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t st);
+cudaError_t launch_scan(const ScanArgs& a, cudaStream_t st);
+cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t st);
+cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t st);
+
+// Sums over the rows of partial [rows][cols], in a fixed order: the first `a` columns go to out_a, the next `b` to out_b,
+// the rest to out_c (NULL: dropped).
+struct ColumnSums {
+    const float* partial;
+    int rows;
+    long long cols, a, b;
+    float *out_a, *out_b, *out_c;
+    const float* decay;       // A_log: out_a's sums are multiplied by -exp of it (NULL: as they are)
+};
+cudaError_t launch_column_sums(const ColumnSums& c, cudaStream_t st);
+
+}  // namespace ssm
+}  // namespace gdn
