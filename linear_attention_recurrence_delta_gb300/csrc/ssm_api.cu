@@ -104,6 +104,8 @@ gdn_status_t scan_inputs(const gdn_scan_t* s, const gdn_mla_view_t* x, const gdn
 void scan_layout(const ScanPlan& p, void* ws, ScanArgs* a)
 {
     unsigned char* w = (unsigned char*)ws;
+    a->ctas = p.ctas;
+    a->warps = p.warps;
     a->segments = p.segments;
     a->seg_len = p.seg_len;
     a->seg_h = (float*)(w + p.h_off);
@@ -120,21 +122,23 @@ namespace ssm {
 ScanPlan scan_plan(const gdn_scan_t& s, int backward)
 {
     ScanPlan p;
-    p.channels = 128 / (s.N <= 8 ? 2 : s.N <= 16 ? 4 : s.N <= 32 ? 8 : 16);
-    p.blocks = (s.D / s.G + p.channels - 1) / p.channels;
-    const long long ctas = (long long)p.blocks * s.G * s.B, T = s.T < s.rows ? s.T : s.rows;
-    long long seg = 152 * 8 / ctas;
+    const int each = s.D / s.G, cta = backward ? kBackWarps * back_channels(s.N) : 32;
+    p.warps = (each + 31) / 32;
+    p.ctas = (each + cta - 1) / cta;
+    const long long blocks = (long long)p.ctas * s.G * (backward ? kBackWarps : 1), T = s.T < s.rows ? s.T : s.rows;
+    const long long warps = (long long)p.warps * s.G * s.B;
+    long long seg = 152 * 8 / warps;
     if (seg > T / 128) seg = T / 128;
     if (seg > 32) seg = 32;
     if (seg < 3) seg = 1;
     p.seg_len = seg > 1 ? (int)(((T + seg - 1) / seg + 31) / 32 * 32) : (T > 0 ? (int)((T + 31) / 32 * 32) : 32);
     p.segments = T > 0 ? (int)((T + p.seg_len - 1) / p.seg_len) : 1;
-    const size_t states = (size_t)s.B * s.D * s.N, steps = (size_t)s.B * s.D;
+    const size_t places = p.segments > 1 ? (size_t)p.segments * s.B * blocks : 0;
     p.h_off = 256;
-    p.d_off = p.h_off + (p.segments > 1 ? round_up(p.segments * states * 4, 256) : 0);
-    p.w_off = p.d_off + (p.segments > 1 ? round_up(p.segments * steps * 4, 256) : 0);
+    p.d_off = p.h_off + round_up(places * 32 * state_values(s.N) * 4, 256);      // blocks of 32 channels at most
+    p.w_off = p.d_off + round_up(places * 32 * 4, 256);
     p.bc_off = p.w_off + (backward ? round_up((size_t)p.segments * s.B * s.D * (s.N + 2) * 4, 256) : 0);
-    p.total = p.bc_off + (backward ? round_up((size_t)p.blocks * s.rows * s.G * 2 * s.N * 4, 256) : 0);
+    p.total = p.bc_off + (backward ? round_up((size_t)p.ctas * s.rows * s.G * 2 * s.N * 4, 256) : 0);
     return p;
 }
 
@@ -272,7 +276,7 @@ extern "C" size_t gdn_scan_workspace_bytes(const gdn_scan_t* s, int backward)
 
 extern "C" size_t gdn_scan_saved_bytes(const gdn_scan_t* s)
 {
-    return scan_check(s) != GDN_OK ? 0 : round_up(saved_states(*s) * s->D * s->N * 4, 256);
+    return scan_check(s) != GDN_OK ? 0 : saved_bytes_of(*s);
 }
 
 extern "C" gdn_status_t gdn_scan_fwd(const gdn_scan_t* s, const gdn_mla_view_t* x, const gdn_mla_view_t* dt, const gdn_mla_view_t* z,

@@ -44,6 +44,13 @@ __device__ __forceinline__ float softplus(float v, float& slope)
     return fmaf(2.f * s, p, fmaxf(v, 0.f));
 }
 
+// 16 bytes to shared memory, zeros unless ok
+__device__ __forceinline__ void cp_async16_zero(void* to, const void* from, bool ok)
+{
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to), n = ok ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(from), "r"(n) : "memory");
+}
+
 __device__ __forceinline__ float warp_sum(float x)
 {
 #pragma unroll

@@ -13,131 +13,126 @@ namespace ssm {
 
 namespace {
 
-template <typename IO, int LS, bool FIRST>      // FIRST: the first of the two launches
-__global__ void __launch_bounds__(kScanThreads) scan_kernel(const ScanArgs a, int blocks)
+// FIRST: the first of the two launches
+template <typename IO, int LS, bool FIRST>
+__global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a)
 {
-    using L = Lay<LS>;
-    constexpr int K = LS == 2 ? 16 : 32, UNITS = K * L::PP, U = (UNITS + kScanThreads - 1) / kScanThreads;
-    __shared__ float2 sd[K][L::CH];            // delta, delta x
-    __shared__ float sB[K][L::NS], sC[FIRST ? 1 : K][L::NS], sy[FIRST ? 1 : K][L::CH];
-    const Spot p = spot<L>(a, blocks);
-    const int D = a.s.D, N = a.s.N, cl = threadIdx.x / LS, q = threadIdx.x % LS, d = p.d0 + cl;
-    const bool mine = cl < p.channels && 4 * q < N;
+    using L = Lay<LS, LS>;
+    __shared__ __align__(16) float sB[kTile][L::NS], sC[FIRST ? 1 : kTile][L::NS];
+    const int lane = threadIdx.x, ng = lane / L::CL;
+    const Spot p = spot<L, 1>(a);
     if (FIRST && p.t0 >= p.t1) return;
-    const long long at = ((long long)p.b * D + d) * N + 4 * q, all = (long long)a.s.B * D;
-    float A[4], h[4] = {}, sum = 0.f;
-    load_rates(a, d, 4 * q, mine, A);
-    if (!FIRST && mine) {
-        if (a.h0) get4(a.h0 + at, h);
-        for (int s = 0; s < p.seg && (long long)s * a.seg_len < p.r.n; s++) {
-            float e[4];
-            const float w = a.seg_d[s * all + (long long)p.b * D + d];
-            get4(a.seg_h + s * all * N + at, e);
+    float2 A[LS][4], h[LS][4];
+    float sum = 0.f;
+    load_rates<L>(a, p, lane, A);
 #pragma unroll
-            for (int i = 0; i < 4; i++) h[i] = fmaf(ex2_approx(w * A[i]), h[i], e[i]);
-        }
+    for (int r = 0; r < LS; r++) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) h[r][k] = f2(0.f, 0.f);
+        if (!FIRST && a.h0 && p.has(L::channel(lane, r)) && 8 * ng < a.s.N) get8(a.h0 + state_at<L>(a, p, lane, r), h[r]);
     }
-    float bias[U][8], skip[U][8];
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-        const int unit = u * kScanThreads + threadIdx.x, c = 8 * (unit % L::PP);
-#pragma unroll
-        for (int i = 0; i < 8; i++) bias[u][i] = skip[u][i] = 0.f;
-        if (unit < UNITS && c < p.channels) {
-            if (a.dt_bias) load8(a.dt_bias + p.d0 + c, bias[u]);
-            if (!FIRST && a.D_skip) load8(a.D_skip + p.d0 + c, skip[u]);
+    if (!FIRST)
+        for (int s = 0; s < p.seg; s++) {
+            if ((long long)s * a.seg_len >= p.r.n) break;
+            carry<L, 1>(a, p, lane, s, A, h);
         }
-    }
-    for (int t0 = p.t0; t0 < p.t1; t0 += K) {
-        float x[U][8];
-        __syncthreads();      // the last tile's outputs have left
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int unit = u * kScanThreads + threadIdx.x, j = unit / L::PP, c = 8 * (unit % L::PP);
-            if (unit >= UNITS) continue;
-            float v[8];
-            const bool in = t0 + j < p.t1 && c < p.channels;
-#pragma unroll
-            for (int i = 0; i < 8; i++) x[u][i] = v[i] = 0.f;
-            if (in) {
-                const long long row = p.r.first + t0 + j;
-                load8((const IO*)a.x.p + row * a.x.tok + p.d0 + c, x[u]);
-                load8((const IO*)a.dt.p + row * a.dt.tok + p.d0 + c, v);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                float slope, w = v[i] + bias[u][i];
-                if (a.s.softplus) w = softplus(w, slope);
-                if (!in) w = 0.f;          // a step of size zero changes nothing
-                sd[j][c + i] = f2(w, w * x[u][i]);
-            }
+    const bool in = p.has(lane), gated = a.z.p != nullptr;
+    const float bias = in && a.dt_bias ? a.dt_bias[p.d0 + lane] : 0.f;
+    const float skip = !FIRST && in && a.D_skip ? a.D_skip[p.d0 + lane] : 0.f;
+    Column<IO> rx, rdt, rz;
+    Vectors<L, IO> rB, rC;
+    auto ask = [&](int t0) {
+        rx.load(a.x, p, t0, lane);
+        rdt.load(a.dt, p, t0, lane);
+        rB.load(a.Bm, p, a.s.N, t0, lane);
+        if (!FIRST) {
+            rC.load(a.Cm, p, a.s.N, t0, lane);
+            if (gated) rz.load(a.z, p, t0, lane);
         }
-        stage_vectors<L, IO, K>(a, a.Bm, p, t0, p.t1, sB);
-        if (!FIRST) stage_vectors<L, IO, K>(a, a.Cm, p, t0, p.t1, sC);
-        __syncthreads();
-#pragma unroll 4
-        for (int j = 0; j < K; j++) {
-            if (!FIRST && a.saved && j % kSaveEvery == 0 && mine && t0 + j < p.t1)
-                put4(a.saved + (saved_at(p, t0 + j) * D + d) * N + 4 * q, h);
-            const float2 v = sd[j][cl];
-            float B[4], C[4], y = 0.f;
-            get4(&sB[j][4 * q], B);
-            if (!FIRST) get4(&sC[j][4 * q], C);
+    };
+    if (p.t0 < p.t1) ask(p.t0);
+    for (int t0 = p.t0; t0 < p.t1; t0 += kTile) {
+        float x[kTile], w[kTile], z[kTile], y[kTile], slope;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                h[i] = fmaf(ex2_approx(v.x * A[i]), h[i], v.y * B[i]);
-                if (!FIRST) y = fmaf(h[i], C[i], y);
+        for (int j = 0; j < kTile; j++) {
+            x[j] = rec::to_f(rx.v[j]);
+            if (!FIRST) z[j] = rec::to_f(rz.v[j]);
+            w[j] = rec::to_f(rdt.v[j]) + bias;
+        }
+        if (a.s.softplus)
+#pragma unroll
+            for (int j = 0; j < kTile; j++) w[j] = softplus(w[j], slope);
+        if (t0 + kTile > p.t1)
+#pragma unroll
+            for (int j = 0; j < kTile; j++)
+                if (t0 + j >= p.t1) w[j] = 0.f;      // a step of size zero changes nothing
+        __syncwarp();      // the last tile's vectors have been read
+        rB.store(&sB[0][0], lane);
+        if (!FIRST) rC.store(&sC[0][0], lane);
+        __syncwarp();
+        if (t0 + kTile < p.t1) ask(t0 + kTile);
+        if (!FIRST && a.saved) put_state<L>(a.saved, saved_at(a, p, t0) + p.block, lane, h);
+#pragma unroll
+        for (int j = 0; j < kTile; j++) {
+            float2 B[4], C[4];
+            float part[LS];
+            get8(&sB[j][8 * ng], B);
+            if (!FIRST) get8(&sC[j][8 * ng], C);
+            const float ux = w[j] * x[j];
+#pragma unroll
+            for (int r = 0; r < LS; r++) {
+                const float wr = r ? __shfl_xor_sync(0xffffffffu, w[j], L::CL * r) : w[j];
+                const float ur = r ? __shfl_xor_sync(0xffffffffu, ux, L::CL * r) : ux;
+                float2 o = f2(0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    h[r][k] = fma2(ex2x2(mul2(f2(wr, wr), A[r][k])), h[r][k], mul2(f2(ur, ur), B[k]));
+                    if (!FIRST) o = k ? fma2(h[r][k], C[k], o) : mul2(h[r][k], C[k]);
+                }
+                part[r] = o.x + o.y;
             }
             if (FIRST) {
-                sum += v.x;
-            } else {
-                y = lanes_sum<LS>(y);
-                if (q == 0) sy[j][cl] = y;
+                sum += w[j];
+                continue;
             }
+            y[j] = part[0];
+#pragma unroll
+            for (int r = 1; r < LS; r++) y[j] += __shfl_xor_sync(0xffffffffu, part[r], L::CL * r);
         }
         if (FIRST) continue;
-        __syncthreads();
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int unit = u * kScanThreads + threadIdx.x, j = unit / L::PP, c = 8 * (unit % L::PP);
-            if (unit >= UNITS || t0 + j >= p.t1 || c >= p.channels) continue;
-            const long long row = p.r.first + t0 + j;
-            float y[8];
-            load8(&sy[j][c], y);
+        for (int j = 0; j < kTile; j++) y[j] = fmaf(skip, x[j], y[j]);
+        if (gated)
 #pragma unroll
-            for (int i = 0; i < 8; i++) y[i] = fmaf(skip[u][i], x[u][i], y[i]);
-            if (a.z.p) {
-                float z[8];
-                load8((const IO*)a.z.p + row * a.z.tok + p.d0 + c, z);
+            for (int j = 0; j < kTile; j++) y[j] *= z[j] * sigmoid(z[j]);
+        IO* out = (IO*)a.y.p + (long long)(p.r.first + t0) * a.y.tok + p.d0 + lane;
 #pragma unroll
-                for (int i = 0; i < 8; i++) y[i] *= z[i] * sigmoid(z[i]);
-            }
-            store8((IO*)a.y.p + row * a.y.tok + p.d0 + c, y);
-        }
+        for (int j = 0; j < kTile; j++) store_if(in && t0 + j < p.t1, out + j * a.y.tok, y[j]);
     }
     if (FIRST) {
-        if (mine) put4(a.seg_h + p.seg * all * N + at, h);
-        if (mine && q == 0) a.seg_d[p.seg * all + (long long)p.b * D + d] = sum;
-    } else if (mine && a.hT && p.t1 == p.r.n && (p.t0 < p.t1 || p.seg == 0)) {
-        put4(a.hT + at, h);
+        put_state<L>(a.seg_h, segment_at<1>(a, p, p.seg), lane, h);
+        a.seg_d[segment_at<1>(a, p, p.seg) * 32 + lane] = sum;
+    } else if (a.hT && p.t1 == p.r.n && (p.t0 < p.t1 || p.seg == 0)) {
+#pragma unroll
+        for (int r = 0; r < LS; r++)
+            if (p.has(L::channel(lane, r)) && 8 * ng < a.s.N) put8(a.hT + state_at<L>(a, p, lane, r), h[r]);
     }
 }
 
 template <typename IO, int LS>
 cudaError_t launch_lanes(const ScanArgs& a, cudaStream_t st)
 {
-    const ScanPlan plan = scan_plan(a.s, 0);
-    const dim3 grid(a.s.G * plan.blocks, a.s.B, a.segments);
-    if (a.segments > 1) scan_kernel<IO, LS, true><<<grid, kScanThreads, 0, st>>>(a, plan.blocks);
-    scan_kernel<IO, LS, false><<<grid, kScanThreads, 0, st>>>(a, plan.blocks);
+    const dim3 grid(a.s.G * a.ctas, a.s.B, a.segments);
+    if (a.segments > 1) scan_kernel<IO, LS, true><<<grid, 32, 0, st>>>(a);
+    scan_kernel<IO, LS, false><<<grid, 32, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename IO>
 cudaError_t launch_typed(const ScanArgs& a, cudaStream_t st)
 {
-    if (a.s.N <= 8) return launch_lanes<IO, 2>(a, st);
-    if (a.s.N <= 16) return launch_lanes<IO, 4>(a, st);
-    return a.s.N <= 32 ? launch_lanes<IO, 8>(a, st) : launch_lanes<IO, 16>(a, st);
+    if (a.s.N <= 8) return launch_lanes<IO, 1>(a, st);
+    if (a.s.N <= 16) return launch_lanes<IO, 2>(a, st);
+    return a.s.N <= 32 ? launch_lanes<IO, 4>(a, st) : launch_lanes<IO, 8>(a, st);
 }
 
 // New tokens: a lane has 4 states of a channel, and takes the sequences blockIdx.y, blockIdx.y + gridDim.y, ... in turn.
@@ -150,14 +145,14 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepA
     const bool mine = u < D && n < N;
     float A[4] = {}, bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.D_skip ? a.D_skip[d] : 0.f;
     if (mine) {
-        get4(a.A_log + (long long)d * N + n, A);
+        { const float4 v = *reinterpret_cast<const float4*>(a.A_log + (long long)d * N + n); A[0] = v.x; A[1] = v.y; A[2] = v.z; A[3] = v.w; }
 #pragma unroll
         for (int i = 0; i < 4; i++) A[i] = -expf(A[i]) * kLog2e;
     }
     for (int b = blockIdx.y; b < a.s.B; b += gridDim.y) {
         const int src = a.src ? a.src[b] : b, dst = a.dst ? a.dst[b] : src;
         float h[4] = {};
-        if (mine && src >= 0 && src < a.s.slots) get4(a.state + ((long long)src * D + d) * N + n, h);
+        if (mine && src >= 0 && src < a.s.slots) { const float4 v = *reinterpret_cast<const float4*>(a.state + ((long long)src * D + d) * N + n); h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w; }
         for (int t = 0; t < a.s.T; t++) {
             const long long row = (long long)b * a.s.T + t;
             const float x = rec::to_f(((const IO*)a.x.p)[row * a.x.tok + d]);
@@ -172,7 +167,8 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepA
                     y = fmaf(h[i], C, y);
                 }
             }
-            y = lanes_sum<LS>(y);
+            #pragma unroll
+            for (int m = LS / 2; m; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
             if (q == 0 && u < D) {
                 y = fmaf(skip, x, y);
                 if (a.z.p) {
@@ -182,7 +178,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepA
                 ((IO*)a.y.p)[row * a.y.tok + d] = rec::from_f<IO>(y);
             }
         }
-        if (mine && dst >= 0 && dst < a.s.slots) put4(a.state + ((long long)dst * D + d) * N + n, h);
+        if (mine && dst >= 0 && dst < a.s.slots) *reinterpret_cast<float4*>(a.state + ((long long)dst * D + d) * N + n) = make_float4(h[0], h[1], h[2], h[3]);
     }
 }
 
