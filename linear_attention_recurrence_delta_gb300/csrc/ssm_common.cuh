@@ -12,6 +12,7 @@ using mla::raw8;
 using mla::rows_of;
 using mla::store8;
 using mla::values;
+using rec::add2;
 using rec::ex2_approx;
 using rec::f2;
 using rec::fma2;
@@ -51,11 +52,55 @@ __device__ __forceinline__ void cp_async16_zero(void* to, const void* from, bool
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(from), "r"(n) : "memory");
 }
 
-__device__ __forceinline__ float warp_sum(float x)
+// four values as two packed pairs
+struct Four {
+    float2 a, b;
+};
+__device__ __forceinline__ Four four(const float (&x)[4]) { return {f2(x[0], x[1]), f2(x[2], x[3])}; }
+__device__ __forceinline__ Four mul(Four x, Four y) { return {mul2(x.a, y.a), mul2(x.b, y.b)}; }
+__device__ __forceinline__ Four fma(Four x, Four y, Four z) { return {fma2(x.a, y.a, z.a), fma2(x.b, y.b, z.b)}; }
+__device__ __forceinline__ Four add(Four x, Four y) { return {add2(x.a, y.a), add2(x.b, y.b)}; }
+__device__ __forceinline__ Four all(float x) { return {f2(x, x), f2(x, x)}; }
+__device__ __forceinline__ float2 sigmoid2(float2 x)
 {
-#pragma unroll
-    for (int m = 16; m; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-    return x;
+    const float2 e = mul2(x, f2(-kLog2e, -kLog2e)), d = add2(f2(ex2_approx(e.x), ex2_approx(e.y)), f2(1.f, 1.f));
+    return f2(rcp(d.x), rcp(d.y));
+}
+__device__ __forceinline__ Four sigmoid4(Four x) { return {sigmoid2(x.a), sigmoid2(x.b)}; }
+
+__device__ __forceinline__ void store4(float* p, const float (&x)[4])
+{
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4])
+{
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// four values as they lie in memory
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<float> {
+    float4 v;
+    __device__ __forceinline__ Four get() const { return {f2(v.x, v.y), f2(v.z, v.w)}; }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ Four get() const
+    {
+        return {f2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u)), f2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u))};
+    }
+};
+__device__ __forceinline__ Raw4<float> raw4(const float* p) { return {*reinterpret_cast<const float4*>(p)}; }
+__device__ __forceinline__ Raw4<__nv_bfloat16> raw4(const __nv_bfloat16* p) { return {*reinterpret_cast<const uint2*>(p)}; }
+template <typename IO>
+__device__ __forceinline__ void put(IO* p, Four x)
+{
+    const float v[4] = {x.a.x, x.a.y, x.b.x, x.b.y};
+    store4(p, v);
 }
 
 }  // namespace ssm

@@ -1,8 +1,8 @@
 // ssm_conv.cu -- short causal convolution of each channel with SiLU, its gradients, and its form for new tokens.
 //
-// pre[t] = bias + sum_k w[k] x[t - W + 1 + k], y = silu(pre).  A thread walks a strip of time for a few neighbouring
-// channels with the last W - 1 rows in registers, so that a row is read once (and W - 1 rows more a strip, from L2);
-// HBM bounds it.
+// pre[t] = bias + sum_k w[k] x[t - W + 1 + k], y = silu(pre).  A thread walks a strip of time for four neighbouring
+// channels with the last rows in registers, in rings of four whose turning the unrolled loop knows, so that a row is read
+// once (and W - 1 rows more a strip, from L2).  HBM bounds it, once four rows are asked for ahead and the arithmetic is packed.
 #include "ssm_common.cuh"
 
 namespace gdn {
@@ -10,33 +10,9 @@ namespace ssm {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kBackThreads = 128;
 constexpr int kStrip = 32;        // rows a thread walks forwards
-constexpr int kAhead = 4;         // rows asked for together
-constexpr int kBackStrip = 64;    // rows a thread walks for the gradients
-
-__device__ __forceinline__ void load4(const float* p, float (&x)[4])
-{
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4])
-{
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    x[0] = __uint_as_float(v.x << 16);
-    x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16);
-    x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-__device__ __forceinline__ void store4(float* p, const float (&x)[4])
-{
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4])
-{
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
+constexpr int kBackStrip = 128;    // rows a thread walks for the gradients
 
 // the taps of C channels: w[k][c] of [D, W]
 template <int W, int C>
@@ -72,48 +48,82 @@ __device__ __forceinline__ void step8(const float (&taps)[W][8], const float (&b
     }
 }
 
-// Sequence blockIdx.y; threads run over (strip, piece of 8 channels), pieces fastest.
+template <int W>
+__device__ __forceinline__ void load_taps(const float* w, Four (&t)[W])
+{
+    float raw[W][4];
+    load_taps<W, 4>(w, raw);
+#pragma unroll
+    for (int k = 0; k < W; k++) t[k] = four(raw[k]);
+}
+
+// rows t0 - (W - 1) .. t0 - 1 of a sequence into a ring (t0 a multiple of 4): its own, its state's, or zeros
 template <typename IO, int W>
+__device__ __forceinline__ void load_past(const IO* x, long long tok, const void* s0, int b, int D, int c, int t0, Four (&ring)[4])
+{
+    ring[0] = all(0.f);
+#pragma unroll
+    for (int k = 1; k < W; k++) {
+        const int t = t0 - k;
+        ring[4 - k] = all(0.f);
+        if (t >= 0) ring[4 - k] = raw4(x + t * tok).get();
+        else if (s0) ring[4 - k] = raw4((const IO*)s0 + ((long long)b * (W - 1) + t + W - 1) * D + c).get();
+    }
+}
+
+// Sequence blockIdx.y; threads run over (strip, piece of 4 channels), pieces fastest.
+template <typename IO, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a)
 {
-    const int D = a.s.D, pieces = D >> 3, b = blockIdx.y;
+    const int D = a.s.D, pieces = D >> 2, b = blockIdx.y;
     const long long u = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int strip = (int)(u / pieces), c = (int)(u - (long long)strip * pieces) << 3;
+    const int strip = (int)(u / pieces), c = (int)(u - (long long)strip * pieces) << 2;
     const Rows r = rows_of(a.cu, b, a.s.T, a.s.rows);
-    const long long t0 = (long long)strip * kStrip;
-    if (t0 >= r.n && strip > 0) return;
-    const int end = (int)min((long long)r.n, t0 + kStrip);
+    const long long first = (long long)strip * kStrip;
+    if (first >= r.n && strip > 0) return;
+    const int t0 = (int)first, end = min(r.n, t0 + kStrip);
     const IO* x = (const IO*)a.x.p + (long long)r.first * a.x.tok + c;
     IO* y = (IO*)a.y.p + (long long)r.first * a.y.tok + c;
-    float taps[W][8], bias[8] = {}, past[W - 1][8];
-    load_taps<W, 8>(a.w + (long long)c * W, taps);
-    if (a.bias) load8(a.bias + c, bias);
+    Four taps[W], bias = all(0.f), ring[4];
+    load_taps<W>(a.w + (long long)c * W, taps);
+    if (a.bias) bias = raw4(a.bias + c).get();
+    Raw4<IO> next[4];
+    auto ask = [&](int t) {      // without a branch a row where all four are there
+        if (t + 4 <= end)
 #pragma unroll
-    for (int k = 0; k < W - 1; k++) {
-        const long long t = t0 - (W - 1) + k;
-        if (t >= 0) load8(x + t * a.x.tok, past[k]);
-        else if (a.s0) load8((const IO*)a.s0 + ((long long)b * (W - 1) + t + W - 1) * D + c, past[k]);
+            for (int j = 0; j < 4; j++) next[j] = raw4(x + (long long)(t + j) * a.x.tok);
         else
 #pragma unroll
-            for (int i = 0; i < 8; i++) past[k][i] = 0.f;
+            for (int j = 0; j < 4; j++)
+                if (t + j < end) next[j] = raw4(x + (long long)(t + j) * a.x.tok);
+    };
+    auto row = [&](int t, int j, const Raw4<IO>& v) {
+        ring[j] = v.get();
+        Four p = bias;
+#pragma unroll
+        for (int k = 0; k < W; k++) p = fma(taps[k], ring[(j + 5 - W + k) & 3], p);
+        put(y + (long long)(t + j) * a.y.tok, SILU ? mul(p, sigmoid4(p)) : p);
+    };
+    ask(t0);
+    load_past<IO, W>(x, a.x.tok, a.s0, b, D, c, t0, ring);
+    int t = t0;
+    for (; t + 4 <= end; t += 4) {
+        const Raw4<IO> now[4] = {next[0], next[1], next[2], next[3]};
+        ask(t + 4);
+#pragma unroll
+        for (int j = 0; j < 4; j++) row(t, j, now[j]);
     }
-    for (int t = (int)t0; t < end; t += kAhead) {
-        Raw8<IO> raw[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAhead; j++)
-            if (t + j < end) raw[j] = raw8(x + (long long)(t + j) * a.x.tok);
+    for (int j = 0; j < 3; j++)
+        if (t + j < end) row(t, j, next[j]);
+    if (!a.sT || end != r.n) return;
+    // the last W - 1 rows: in the ring by their number modulo 4
 #pragma unroll
-        for (int j = 0; j < kAhead; j++)
-            if (t + j < end) {
-                float v[8], o[8];
-                values(raw[j], v);
-                step8<W>(taps, bias, past, v, a.s.silu, o);
-                store8(y + (long long)(t + j) * a.y.tok, o);
-            }
+    for (int k = 0; k < W - 1; k++) {
+        const int at = (end - (W - 1) + k) & 3;
+        const Four v = at == 0 ? ring[0] : at == 1 ? ring[1] : at == 2 ? ring[2] : ring[3];
+        put((IO*)a.sT + ((long long)b * (W - 1) + k) * D + c, v);
     }
-    if (a.sT && end == r.n)
-#pragma unroll
-        for (int k = 0; k < W - 1; k++) store8((IO*)a.sT + ((long long)b * (W - 1) + k) * D + c, past[k]);
 }
 
 // New tokens: a thread has 8 channels of a sequence.
@@ -149,97 +159,113 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs 
 }
 
 // Gradients.  dpre = dy silu'(pre), dx[r] = sum_k w[k] dpre[r + W - 1 - k], dw[k] = sum_t dpre[t] x[t - W + 1 + k].
-// A thread has 4 channels and keeps their sums of dw and dbias over the strips that its block takes: strip by strip of all
-// sequences in turn, `2^l` pieces of channels by kThreads >> l strips at a time.
-template <typename IO, int W>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs a, int l)
+// A thread has 4 channels and keeps their sums of dw and dbias over the strips that it takes: strip by strip of all sequences
+// in turn, `2^l` pieces of channels by kBackThreads >> l strips at a time.
+template <typename IO, int W, bool SILU>
+__global__ void __launch_bounds__(kBackThreads, 4) conv_bwd_kernel(const ConvArgs a, int l)
 {
-    __shared__ float4 share[kThreads];
-    const int D = a.s.D, tx = threadIdx.x & ((1 << l) - 1), ty = threadIdx.x >> l, strips = kThreads >> l;
+    __shared__ float4 share[kBackThreads];
+    const int D = a.s.D, tx = threadIdx.x & ((1 << l) - 1), ty = threadIdx.x >> l, strips = kBackThreads >> l;
     const int c = 4 * ((blockIdx.x << l) + tx);
-    const int each = (a.s.T + kBackStrip - 1) / kBackStrip;      // strips of a sequence, one at least
-    const long long items = (long long)a.s.B * (each > 0 ? each : 1);
-    float taps[W][4], bias[4] = {}, dw[W][4] = {}, db[4] = {};
+    const int each = a.s.T > 0 ? (a.s.T + kBackStrip - 1) / kBackStrip : 1;      // strips of a sequence
+    const long long items = (long long)a.s.B * each;
+    Four taps[W], bias = all(0.f), dw[W], db = all(0.f);
+#pragma unroll
+    for (int k = 0; k < W; k++) taps[k] = dw[k] = all(0.f);
     if (c < D) {
-        load_taps<W, 4>(a.w + (long long)c * W, taps);
-        if (a.bias) load4(a.bias + c, bias);
+        load_taps<W>(a.w + (long long)c * W, taps);
+        if (a.bias) bias = raw4(a.bias + c).get();
     }
     for (long long item = (long long)blockIdx.y * strips + ty; item < items && c < D; item += (long long)gridDim.y * strips) {
-        const int b = (int)(item / (each > 0 ? each : 1)), t0 = (int)(item - (long long)b * (each > 0 ? each : 1)) * kBackStrip;
+        const int b = (int)(item / each), t0 = (int)(item - (long long)b * each) * kBackStrip;
         const Rows r = rows_of(a.cu, b, a.s.T, a.s.rows);
         if (t0 >= r.n && t0 > 0) continue;
-        const int end = min(r.n, t0 + kBackStrip);
+        const int end = min(r.n, t0 + kBackStrip), from = t0 == 0 && a.ds0 ? -(W - 1) : t0;      // rows whose gradients it writes
         const IO* x = (const IO*)a.x.p + (long long)r.first * a.x.tok + c;
         const IO* dy = (const IO*)a.dy.p + (long long)r.first * a.dy.tok + c;
         IO* dx = (IO*)a.dx.p + (long long)r.first * a.dx.tok + c;
-        float past[W - 1][4], d[W][4] = {};      // earlier rows of x; dpre of this row (last) and those before it
+        Four ring[4], d[4];                          // rows of x and of dpre, by their number modulo 4
+        Raw4<IO> nx[4], ny[4];
+        const int seen = min(r.n, end + W - 1);      // rows that it reads end here
+        auto ask = [&](int t) {
+            if (t + 4 <= seen)
 #pragma unroll
-        for (int k = 0; k < W - 1; k++) {
-            const int t = t0 - (W - 1) + k;
-            if (t >= 0) load4(x + (long long)t * a.x.tok, past[k]);
-            else if (a.s0) load4((const IO*)a.s0 + ((long long)b * (W - 1) + t + W - 1) * D + c, past[k]);
+                for (int j = 0; j < 4; j++) {
+                    nx[j] = raw4(x + (long long)(t + j) * a.x.tok);
+                    ny[j] = raw4(dy + (long long)(t + j) * a.dy.tok);
+                }
             else
 #pragma unroll
-                for (int i = 0; i < 4; i++) past[k][i] = 0.f;
-        }
-        for (int t = t0; t < end + W - 1; t++) {
-#pragma unroll
-            for (int k = 0; k + 1 < W; k++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) d[k][i] = d[k + 1][i];
-#pragma unroll
-            for (int i = 0; i < 4; i++) d[W - 1][i] = 0.f;
-            if (t < r.n) {
-                float v[4], g[4];
-                load4(x + (long long)t * a.x.tok, v);
-                load4(dy + (long long)t * a.dy.tok, g);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    float p = bias[i];
-#pragma unroll
-                    for (int k = 0; k < W - 1; k++) p = fmaf(taps[k][i], past[k][i], p);
-                    p = fmaf(taps[W - 1][i], v[i], p);
-                    if (a.s.silu) {
-                        const float s = sigmoid(p);
-                        g[i] *= s * fmaf(p, 1.f - s, 1.f);
+                for (int j = 0; j < 4; j++)
+                    if (t + j < seen) {
+                        nx[j] = raw4(x + (long long)(t + j) * a.x.tok);
+                        ny[j] = raw4(dy + (long long)(t + j) * a.dy.tok);
                     }
-                    d[W - 1][i] = g[i];
-                    if (t < end) {
-                        db[i] += g[i];
+        };
+        auto pre = [&](int j, const Raw4<IO>& vx, const Raw4<IO>& vy) {      // d[j] of a row of the sequence
+            ring[j] = vx.get();
+            d[j] = vy.get();
+            if (!SILU) return;
+            Four p = bias;
 #pragma unroll
-                        for (int k = 0; k < W - 1; k++) dw[k][i] = fmaf(g[i], past[k][i], dw[k][i]);
-                        dw[W - 1][i] = fmaf(g[i], v[i], dw[W - 1][i]);
-                    }
+            for (int k = 0; k < W; k++) p = fma(taps[k], ring[(j + 5 - W + k) & 3], p);
+            const Four s = sigmoid4(p);
+            d[j] = mul(d[j], mul(s, fma(p, fma(s, all(-1.f), all(1.f)), all(1.f))));
+        };
+        auto own = [&](int j) {                      // a row of the strip's own goes into the sums
+            db = add(db, d[j]);
 #pragma unroll
-                    for (int k = 0; k + 1 < W - 1; k++) past[k][i] = past[k + 1][i];
-                    past[W - 2][i] = v[i];
+            for (int k = 0; k < W; k++) dw[k] = fma(d[j], ring[(j + 5 - W + k) & 3], dw[k]);
+        };
+        auto gradient = [&](int j) {                 // of row t + j - (W - 1): all rows that see it are done
+            Four o = mul(taps[0], d[j]);
+#pragma unroll
+            for (int k = 1; k < W; k++) o = fma(taps[k], d[(j + 4 - k) & 3], o);
+            return o;
+        };
+        auto edge = [&](int t) {                     // rows t .. t + 3 at an end of the strip, whatever holds of them
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if (t + j >= end + W - 1) break;
+                d[j] = all(0.f);
+                if (t + j < r.n) {
+                    pre(j, nx[j], ny[j]);
+                    if (t + j < end) own(j);
                 }
+                const int row = t + j - (W - 1), kept = row - (r.n - (W - 1));      // kept: its place in the new state
+                if (row < from) continue;
+                Four o = gradient(j);
+                if (a.dsT && kept >= 0) o = add(o, raw4((const IO*)a.dsT + ((long long)b * (W - 1) + kept) * D + c).get());
+                if (row >= 0) put(dx + (long long)row * a.dx.tok, o);
+                else put((IO*)a.ds0 + ((long long)b * (W - 1) + row + W - 1) * D + c, o);
             }
-            const int row = t - (W - 1);             // all rows that see it are done
-            if (row < t0 && !(t0 == 0 && a.ds0)) continue;
-            float o[4] = {};
+            ask(t + 4);
+        };
+        ask(t0);
+        load_past<IO, W>(x, a.x.tok, a.s0, b, D, c, t0, ring);
 #pragma unroll
-            for (int k = 0; k < W; k++)
+        for (int k = 0; k < 4; k++) d[k] = all(0.f);
+        edge(t0);
+        int t = t0 + 4;
+        for (; t + 4 <= end; t += 4) {               // rows within the strip, which end before the sequence does
+            const Raw4<IO> cx[4] = {nx[0], nx[1], nx[2], nx[3]}, cy[4] = {ny[0], ny[1], ny[2], ny[3]};
+            ask(t + 4);
 #pragma unroll
-                for (int i = 0; i < 4; i++) o[i] = fmaf(taps[k][i], d[W - 1 - k][i], o[i]);
-            const int kept = row - (r.n - (W - 1));  // its place in the new state
-            if (a.dsT && kept >= 0) {
-                float e[4];
-                load4((const IO*)a.dsT + ((long long)b * (W - 1) + kept) * D + c, e);
-#pragma unroll
-                for (int i = 0; i < 4; i++) o[i] += e[i];
+            for (int j = 0; j < 4; j++) {
+                pre(j, cx[j], cy[j]);
+                own(j);
+                put(dx + (long long)(t + j - (W - 1)) * a.dx.tok, gradient(j));
             }
-            if (row >= 0) store4(dx + (long long)row * a.dx.tok, o);
-            else store4((IO*)a.ds0 + ((long long)b * (W - 1) + row + W - 1) * D + c, o);
         }
+        for (; t < end + W - 1; t += 4) edge(t);
     }
     // the strips' sums in their order
     float* out = a.partial + (long long)blockIdx.y * D * (W + 1);
 #pragma unroll
     for (int k = 0; k <= W; k++) {
-        const float(&s)[4] = k < W ? dw[k < W ? k : 0] : db;
+        const Four s = k < W ? dw[k < W ? k : 0] : db;
         __syncthreads();
-        share[threadIdx.x] = make_float4(s[0], s[1], s[2], s[3]);
+        share[threadIdx.x] = make_float4(s.a.x, s.a.y, s.b.x, s.b.y);
         __syncthreads();
         if (ty == 0 && c < D) {
             float4 x = share[tx];
@@ -270,8 +296,10 @@ int back_pieces(const gdn_conv_t& s)
 template <typename IO, int W>
 cudaError_t launch_fwd_w(const ConvArgs& a, cudaStream_t st)
 {
-    const long long strips = (a.s.T + kStrip - 1) / kStrip, units = (strips > 0 ? strips : 1) * (a.s.D >> 3);
-    conv_kernel<IO, W><<<dim3((unsigned)((units + kThreads - 1) / kThreads), a.s.B), kThreads, 0, st>>>(a);
+    const long long strips = (a.s.T + kStrip - 1) / kStrip, units = (strips > 0 ? strips : 1) * (a.s.D >> 2);
+    const dim3 grid((unsigned)((units + kThreads - 1) / kThreads), a.s.B);
+    if (a.s.silu) conv_kernel<IO, W, true><<<grid, kThreads, 0, st>>>(a);
+    else conv_kernel<IO, W, false><<<grid, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename IO, int W>
@@ -285,7 +313,9 @@ template <typename IO, int W>
 cudaError_t launch_bwd_w(const ConvArgs& a, cudaStream_t st)
 {
     const int l = back_pieces(a.s), wide = ((a.s.D >> 2) + (1 << l) - 1) >> l;
-    conv_bwd_kernel<IO, W><<<dim3(wide, conv_bwd_blocks(a.s)), kThreads, 0, st>>>(a, l);
+    const dim3 grid(wide, conv_bwd_blocks(a.s));
+    if (a.s.silu) conv_bwd_kernel<IO, W, true><<<grid, kBackThreads, 0, st>>>(a, l);
+    else conv_bwd_kernel<IO, W, false><<<grid, kBackThreads, 0, st>>>(a, l);
     return cudaGetLastError();
 }
 
@@ -299,12 +329,12 @@ cudaError_t launch_bwd_w(const ConvArgs& a, cudaStream_t st)
 
 }  // namespace
 
-// blocks that share the strips of a block's channels: as many as run at once
+// blocks that share the strips of a block's channels, each with its row of shares of dw and dbias
 int conv_bwd_blocks(const gdn_conv_t& s)
 {
-    const int l = back_pieces(s), wide = ((s.D >> 2) + (1 << l) - 1) >> l, strips = kThreads >> l;
-    const long long each = (s.T + kBackStrip - 1) / kBackStrip, items = (long long)s.B * (each > 0 ? each : 1);
-    const long long need = (items + strips - 1) / strips, most = 152 * 4 / wide;
+    const int l = back_pieces(s), wide = ((s.D >> 2) + (1 << l) - 1) >> l, strips = kBackThreads >> l;
+    const long long each = s.T > 0 ? (s.T + kBackStrip - 1) / kBackStrip : 1, items = (long long)s.B * each;
+    const long long need = (items + strips - 1) / strips, most = 152 * 32 / wide;
     return need < most ? (int)need : most < 1 ? 1 : (int)most;
 }
 

@@ -21,7 +21,8 @@ __device__ __forceinline__ float max_nan(float a, float b)     // the larger one
     return y;
 }
 
-// What the 2^l threads of a row hold, joined in a fixed order; red: one place a warp and kind of value.
+// What the 2^l threads of a row hold, joined in a fixed order; red: a place for each warp and kind of value, in turn one of
+// two, so that a barrier is enough.
 template <int K, bool MAX>
 __device__ __forceinline__ void row_join(float (&x)[K], int l, float (*red)[kMostThreads / 32])
 {
@@ -34,7 +35,6 @@ __device__ __forceinline__ void row_join(float (&x)[K], int l, float (*red)[kMos
         }
     if (l == 5) return;
     const int w = threadIdx.x >> 5, first = w >> (l - 5) << (l - 5);
-    __syncthreads();
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
         for (int k = 0; k < K; k++) red[k][w] = x[k];
@@ -64,9 +64,9 @@ __device__ __forceinline__ void store8_e4m3(void* p, const float (&x)[8])
 
 // 2^l threads a row, V pieces of 8 values each
 template <typename IO, typename RES, int V, bool E4M3>
-__global__ void __launch_bounds__(kMostThreads) norm_kernel(const NormArgs a, int l)
+__global__ void __launch_bounds__(V > 2 ? kMostThreads : kThreads) norm_kernel(const NormArgs a, int l)
 {
-    __shared__ float red[1][kMostThreads / 32];
+    __shared__ float red[2][kMostThreads / 32];
     const int per = blockDim.x >> l, t = threadIdx.x & ((1 << l) - 1), D = a.s.D;
     const long long n = (long long)blockIdx.x * per + (threadIdx.x >> l);
     const bool row = n < a.s.N;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const NormArgs a, in
     if (!E4M3) return;
     if (a.s.group == 0) {
         float m[1] = {top};
-        row_join<1, true>(m, l, red);
+        row_join<1, true>(m, l, red + 1);
         top = m[0];
         if (row && t == 0) a.scale[n] = max_nan(top, kScaleFloor) * (1.f / kE4m3Top);
     }
@@ -145,47 +145,76 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const NormArgs a, in
     }
 }
 
-// d = inv (gw - s inv^2 mean(gw s)) + ds with gw = dy w; dw's share of the block's rows stays in registers until the end.
+// One row's inputs as they lie in memory.
 template <typename IO, typename RES, int V>
-__global__ void __launch_bounds__(kMostThreads) norm_bwd_kernel(const NormArgs a, int l)
-{
-    __shared__ float red[2][kMostThreads / 32];
-    extern __shared__ float dws[];      // [rows a block][D], where a block takes several rows
-    const int per = blockDim.x >> l, sub = threadIdx.x >> l, t = threadIdx.x & ((1 << l) - 1), D = a.s.D;
-    float dw[V][8] = {};
-    for (long long n0 = (long long)blockIdx.x * per; n0 < a.s.N; n0 += (long long)gridDim.x * per) {
-        const long long n = n0 + sub;
-        const bool row = n < a.s.N;
-        float s[V][8], g[V][8], sums[2] = {0.f, 0.f};
+struct BackRow {
+    Raw8<RES> s[V], ds[V];
+    Raw8<IO> dy[V];
+    __device__ __forceinline__ void load(const NormArgs& a, long long n, int t, int l)
+    {
 #pragma unroll
         for (int i = 0; i < V; i++) {
             const int c = 8 * (t + (i << l));
+            s[i] = ds[i] = Raw8<RES>{};
+            dy[i] = Raw8<IO>{};
+            if (n >= a.s.N || c >= a.s.D) continue;
+            s[i] = raw8((const RES*)a.res + n * a.res_tok + c);
+            dy[i] = raw8((const IO*)a.dy + n * a.dy_tok + c);
+            if (a.dsum) ds[i] = raw8((const RES*)a.dsum + n * a.dsum_tok + c);
+        }
+    }
+};
+
+// d = inv (gw - s inv^2 mean(gw s)) + ds with gw = dy w; dw's share of the block's rows stays in registers until the end.
+// AHEAD: the next row is asked for before this one is worked on (rows of up to 4096 values, whose registers allow it).
+template <typename IO, typename RES, int V, bool AHEAD>
+__global__ void __launch_bounds__(V > 2 ? kMostThreads : kThreads, V > 2 ? 1 : 2) norm_bwd_kernel(const NormArgs a, int l)
+{
+    __shared__ float red[2][2][kMostThreads / 32];
+    extern __shared__ float dws[];      // [rows a block][D], where a block takes several rows
+    const int per = blockDim.x >> l, sub = threadIdx.x >> l, t = threadIdx.x & ((1 << l) - 1), D = a.s.D;
+    const long long stride = (long long)gridDim.x * per;
+    float dw[V][8] = {}, w[AHEAD ? V : 1][8] = {};
+    if (AHEAD)
 #pragma unroll
-            for (int k = 0; k < 8; k++) s[i][k] = g[i][k] = 0.f;
-            if (!row || c >= D) continue;
-            float w[8];
-            load8((const RES*)a.res + n * a.res_tok + c, s[i]);
-            load8((const IO*)a.dy + n * a.dy_tok + c, g[i]);
-            load8(a.w + c, w);
+        for (int i = 0; i < V; i++)
+            if (8 * (t + (i << l)) < D) load8(a.w + 8 * (t + (i << l)), w[AHEAD ? i : 0]);
+    BackRow<IO, RES, V> next;
+    int turn = 0;
+    if (AHEAD) next.load(a, (long long)blockIdx.x * per + sub, t, l);
+    for (long long n0 = (long long)blockIdx.x * per; n0 < a.s.N; n0 += stride, turn ^= 1) {
+        const long long n = n0 + sub;
+        if (!AHEAD) next.load(a, n, t, l);
+        const BackRow<IO, RES, V> row = next;
+        if (AHEAD) next.load(a, n + stride, t, l);
+        float sums[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            float s[8], g[8];
+            values(row.s[i], s);
+            values(row.dy[i], g);
+            if (!AHEAD && 8 * (t + (i << l)) < D) load8(a.w + 8 * (t + (i << l)), w[0]);
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                sums[0] = fmaf(s[i][k], s[i][k], sums[0]);
-                sums[1] = fmaf(g[i][k] * w[k], s[i][k], sums[1]);
+                sums[0] = fmaf(s[k], s[k], sums[0]);
+                sums[1] = fmaf(g[k] * w[AHEAD ? i : 0][k], s[k], sums[1]);
             }
         }
-        row_join<2, false>(sums, l, red);
+        row_join<2, false>(sums, l, red[turn]);
         const float inv = rsqrtf(sums[0] / D + a.s.eps), back = inv * inv * (sums[1] / D);
 #pragma unroll
         for (int i = 0; i < V; i++) {
             const int c = 8 * (t + (i << l));
-            if (!row || c >= D) continue;
-            float w[8], d[8] = {};
-            if (a.dsum) load8((const RES*)a.dsum + n * a.dsum_tok + c, d);
-            load8(a.w + c, w);
+            if (n >= a.s.N || c >= D) continue;
+            float s[8], g[8], d[8];
+            values(row.s[i], s);
+            values(row.dy[i], g);
+            values(row.ds[i], d);
+            if (!AHEAD) load8(a.w + c, w[0]);
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                dw[i][k] = fmaf(g[i][k] * s[i][k], inv, dw[i][k]);
-                d[k] += inv * (g[i][k] * w[k] - s[i][k] * back);
+                dw[i][k] = fmaf(g[k] * s[k], inv, dw[i][k]);
+                d[k] += inv * (g[k] * w[AHEAD ? i : 0][k] - s[k] * back);
             }
             if (a.dx) store8((IO*)a.dx + n * a.dx_tok + c, d);
             if (a.dres) store8((RES*)a.dres + n * a.dres_tok + c, d);
@@ -219,7 +248,7 @@ struct Split {
 Split split(int D)
 {
     Split s;
-    s.V = D <= 256 ? 1 : D <= 2048 ? 2 : 4;
+    s.V = D <= 256 ? 1 : D <= 4096 ? 2 : 4;
     s.l = 5;
     while ((8 * s.V) << s.l < D) s.l++;
     s.block = (1 << s.l) > kThreads ? 1 << s.l : kThreads;
@@ -251,28 +280,28 @@ cudaError_t launch_bwd_typed(const NormArgs& a, cudaStream_t st)
     const int per = p.block >> p.l;
     const size_t smem = per > 1 ? (size_t)per * a.s.D * sizeof(float) : 0;
     const unsigned grid = norm_bwd_blocks(a.s);
-    if (p.V == 1) norm_bwd_kernel<IO, RES, 1><<<grid, p.block, smem, st>>>(a, p.l);
-    else if (p.V == 2) norm_bwd_kernel<IO, RES, 2><<<grid, p.block, smem, st>>>(a, p.l);
-    else norm_bwd_kernel<IO, RES, 4><<<grid, p.block, smem, st>>>(a, p.l);
+    if (p.V == 1) norm_bwd_kernel<IO, RES, 1, true><<<grid, p.block, smem, st>>>(a, p.l);
+    else if (p.V == 2) norm_bwd_kernel<IO, RES, 2, true><<<grid, p.block, smem, st>>>(a, p.l);
+    else norm_bwd_kernel<IO, RES, 4, false><<<grid, p.block, smem, st>>>(a, p.l);
     return cudaGetLastError();
 }
 
-// 32 columns a block; the rows are dealt to its 8 warps in turn, whose sums are then added in their order
-__global__ void __launch_bounds__(256) column_sums_kernel(const ColumnSums s)
+// 32 columns a block; the rows are dealt to its 32 warps in turn, whose sums are then added in their order
+__global__ void __launch_bounds__(1024) column_sums_kernel(const ColumnSums s)
 {
     cudaGridDependencySynchronize();      // launched as a dependent of the kernel that writes the shares
-    __shared__ float part[8][33];
+    __shared__ float part[32][33];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long c = (long long)blockIdx.x * 32 + lane;
     float x = 0.f;
     if (c < s.cols)
-#pragma unroll 4
-        for (int r = w; r < s.rows; r += 8) x += s.partial[r * s.cols + c];
+#pragma unroll 8
+        for (int r = w; r < s.rows; r += 32) x += s.partial[r * s.cols + c];
     part[w][lane] = x;
     __syncthreads();
     if (w || c >= s.cols) return;
 #pragma unroll
-    for (int i = 1; i < 8; i++) x += part[i][lane];
+    for (int i = 1; i < 32; i++) x += part[i][lane];
     if (c < s.a) {
         if (s.out_a) s.out_a[c] = s.decay ? x * -expf(s.decay[c]) : x;
     } else if (c < s.a + s.b) {
@@ -289,7 +318,7 @@ int norm_bwd_blocks(const gdn_norm_t& s)
 {
     const Split p = split(s.D);
     const long long need = ((long long)s.N * (1 << p.l) + p.block - 1) / p.block;
-    const int most = 152 * 4 * kThreads / p.block;
+    const int most = 152 * 2 * kThreads / p.block;
     return need < 1 ? 1 : need < most ? (int)need : most;
 }
 
@@ -297,7 +326,7 @@ cudaError_t launch_column_sums(const ColumnSums& s, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((s.cols + 31) / 32));
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(1024);
     cfg.stream = st;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -199,5 +199,26 @@ __device__ __forceinline__ void carry(const ScanArgs& a, const Spot& p, int lane
     }
 }
 
+// v[0 .. n - 1], n a power of two of at most LS: each summed over the LS lanes of a channel (lane = group of states * 32 / LS +
+// channel), v[i] to the lanes whose group of states begins with the bits of i; each of the first log2 n exchanges halves what
+// a lane still holds
+template <int LS, int n>
+__device__ __forceinline__ float states_sum(float (&v)[n], int lane)
+{
+    int m = 16;
+#pragma unroll
+    for (int k = n / 2; k; k >>= 1, m >>= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < k; i++) {
+            const float keep = up ? v[i + k] : v[i], send = up ? v[i] : v[i + k];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+        }
+    }
+#pragma unroll
+    for (; m > (32 / LS) / 2; m >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
+    return v[0];
+}
+
 }  // namespace ssm
 }  // namespace gdn

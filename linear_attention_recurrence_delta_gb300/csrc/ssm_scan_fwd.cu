@@ -135,59 +135,88 @@ cudaError_t launch_typed(const ScanArgs& a, cudaStream_t st)
     return a.s.N <= 32 ? launch_lanes<IO, 4>(a, st) : launch_lanes<IO, 8>(a, st);
 }
 
-// New tokens: a lane has 4 states of a channel, and takes the sequences blockIdx.y, blockIdx.y + gridDim.y, ... in turn.
+// New tokens.  LS = 2, 4, 8 or 16 lanes, CL = 32 / LS apart, hold a channel's states, 4 each, and take E = 2 or 4 sequences at
+// a time, each of them owned by some of the lanes, which work out its step size and store its result.  The states' bytes
+// bound it where sequences are many: A is read once a warp, and the next sequences' states are on their way meanwhile.
 constexpr int kStepThreads = 128;
 template <typename IO, int LS>
-__global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const ScanStepArgs a)
+__global__ void __launch_bounds__(kStepThreads, 7) scan_step_kernel(const ScanStepArgs a)
 {
-    const int N = a.s.N, D = a.s.D, q = threadIdx.x % LS;
-    const int u = (blockIdx.x * kStepThreads + threadIdx.x) / LS, d = min(u, D - 1), g = d / (D / a.s.G), n = 4 * q;
+    constexpr int CL = 32 / LS, E = LS < 4 ? LS : 4, REP = LS / E;
+    const int N = a.s.N, D = a.s.D, T = a.s.T, lane = threadIdx.x & 31, ng = lane / CL, own = ng / REP, n = 4 * ng;
+    const int u = (blockIdx.x * (kStepThreads / 32) + (threadIdx.x >> 5)) * CL + lane % CL, d = min(u, D - 1), g = d / (D / a.s.G);
     const bool mine = u < D && n < N;
-    float A[4] = {}, bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.D_skip ? a.D_skip[d] : 0.f;
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.D_skip ? a.D_skip[d] : 0.f;
+    Four A = all(0.f);
     if (mine) {
-        { const float4 v = *reinterpret_cast<const float4*>(a.A_log + (long long)d * N + n); A[0] = v.x; A[1] = v.y; A[2] = v.z; A[3] = v.w; }
-#pragma unroll
-        for (int i = 0; i < 4; i++) A[i] = -expf(A[i]) * kLog2e;
+        A = raw4(a.A_log + (long long)d * N + n).get();
+        A = {f2(-expf(A.a.x) * kLog2e, -expf(A.a.y) * kLog2e), f2(-expf(A.b.x) * kLog2e, -expf(A.b.y) * kLog2e)};
     }
-    for (int b = blockIdx.y; b < a.s.B; b += gridDim.y) {
-        const int src = a.src ? a.src[b] : b, dst = a.dst ? a.dst[b] : src;
-        float h[4] = {};
-        if (mine && src >= 0 && src < a.s.slots) { const float4 v = *reinterpret_cast<const float4*>(a.state + ((long long)src * D + d) * N + n); h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w; }
-        for (int t = 0; t < a.s.T; t++) {
-            const long long row = (long long)b * a.s.T + t;
-            const float x = rec::to_f(((const IO*)a.x.p)[row * a.x.tok + d]);
-            float w = rec::to_f(((const IO*)a.dt.p)[row * a.dt.tok + d]) + bias, slope, y = 0.f;
-            if (a.s.softplus) w = softplus(w, slope);
-            if (mine) {
+    auto slot = [&](int b, bool to) {
+        if (b >= a.s.B) return -1;
+        const int s = to && a.dst ? a.dst[b] : a.src ? a.src[b] : b;
+        return s < a.s.slots ? s : -1;
+    };
+    Four next[E];
+    auto ask = [&](int b0) {
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float B = rec::to_f(((const IO*)a.Bm.p)[row * a.Bm.tok + g * a.Bm.head + n + i]);
-                    const float C = rec::to_f(((const IO*)a.Cm.p)[row * a.Cm.tok + g * a.Cm.head + n + i]);
-                    h[i] = fmaf(ex2_approx(w * A[i]), h[i], w * x * B);
-                    y = fmaf(h[i], C, y);
-                }
-            }
-            #pragma unroll
-            for (int m = LS / 2; m; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
-            if (q == 0 && u < D) {
-                y = fmaf(skip, x, y);
-                if (a.z.p) {
-                    const float z = rec::to_f(((const IO*)a.z.p)[row * a.z.tok + d]);
-                    y *= z * sigmoid(z);
-                }
-                ((IO*)a.y.p)[row * a.y.tok + d] = rec::from_f<IO>(y);
-            }
+        for (int e = 0; e < E; e++) {
+            const int s = slot(b0 + e, false);
+            next[e] = all(0.f);
+            if (mine && s >= 0) next[e] = raw4(a.state + ((long long)s * D + d) * N + n).get();
         }
-        if (mine && dst >= 0 && dst < a.s.slots) *reinterpret_cast<float4*>(a.state + ((long long)dst * D + d) * N + n) = make_float4(h[0], h[1], h[2], h[3]);
+    };
+    ask(blockIdx.y * E);
+    for (int b0 = blockIdx.y * E; b0 < a.s.B; b0 += gridDim.y * E) {
+        Four h[E];
+#pragma unroll
+        for (int e = 0; e < E; e++) h[e] = next[e];
+        if (b0 + (int)gridDim.y * E < a.s.B) ask(b0 + gridDim.y * E);
+        const bool live = b0 + own < a.s.B;
+        for (int t = 0; t < T; t++) {
+            const long long row = (long long)min(b0 + own, a.s.B - 1) * T + t;
+            const float x = rec::to_f(((const IO*)a.x.p)[row * a.x.tok + d]);
+            float w = rec::to_f(((const IO*)a.dt.p)[row * a.dt.tok + d]) + bias, slope, y[E];
+            const float z = a.z.p ? rec::to_f(((const IO*)a.z.p)[row * a.z.tok + d]) : 0.f;
+            Raw4<IO> B[E], C[E];
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                const long long r = (long long)min(b0 + e, a.s.B - 1) * T + t;
+                B[e] = C[e] = Raw4<IO>{};
+                if (!mine) continue;
+                B[e] = raw4((const IO*)a.Bm.p + r * a.Bm.tok + g * a.Bm.head + n);
+                C[e] = raw4((const IO*)a.Cm.p + r * a.Cm.tok + g * a.Cm.head + n);
+            }
+            if (a.s.softplus) w = softplus(w, slope);
+            const float ux = w * x;
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                const int from = lane % CL + CL * REP * e;
+                const float we = __shfl_sync(0xffffffffu, w, from), ue = __shfl_sync(0xffffffffu, ux, from);
+                const Four f = mul(all(we), A);
+                h[e] = fma({f2(ex2_approx(f.a.x), ex2_approx(f.a.y)), f2(ex2_approx(f.b.x), ex2_approx(f.b.y))}, h[e], mul(all(ue), B[e].get()));
+                const Four o = mul(h[e], C[e].get());
+                const float2 s = add2(o.a, o.b);
+                y[e] = s.x + s.y;
+            }
+            const float v = fmaf(skip, x, states_sum<LS, E>(y, lane));
+            if (live && u < D && ng % REP == 0) ((IO*)a.y.p)[row * a.y.tok + d] = rec::from_f<IO>(a.z.p ? v * z * sigmoid(z) : v);
+        }
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            const int s = slot(b0 + e, true);
+            if (mine && s >= 0) put(a.state + ((long long)s * D + d) * N + n, h[e]);
+        }
     }
 }
 
 template <typename IO, int LS>
 cudaError_t launch_step_lanes(const ScanStepArgs& a, cudaStream_t st)
 {
-    const long long lanes = (long long)a.s.D * LS;
-    const dim3 grid((unsigned)((lanes + kStepThreads - 1) / kStepThreads), a.s.B < 65535 ? a.s.B : 65535);
-    scan_step_kernel<IO, LS><<<grid, kStepThreads, 0, st>>>(a);
+    constexpr int CL = 32 / LS, E = LS < 4 ? LS : 4;
+    const int wide = (a.s.D + 4 * CL - 1) / (4 * CL), groups = (a.s.B + E - 1) / E;
+    const int fit = 152 * 40 / wide, turns = fit < 1 ? groups : (groups + fit - 1) / fit;      // CTAs that run at once
+    scan_step_kernel<IO, LS><<<dim3(wide, (groups + turns - 1) / turns), kStepThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename IO>
