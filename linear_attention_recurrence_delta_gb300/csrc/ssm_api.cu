@@ -105,7 +105,8 @@ void scan_layout(const ScanPlan& p, void* ws, ScanArgs* a)
 {
     unsigned char* w = (unsigned char*)ws;
     a->ctas = p.ctas;
-    a->warps = p.warps;
+    a->blocks = p.blocks;
+    a->saved_blocks = saved_blocks_of(a->s);
     a->segments = p.segments;
     a->seg_len = p.seg_len;
     a->seg_h = (float*)(w + p.h_off);
@@ -122,21 +123,25 @@ namespace ssm {
 ScanPlan scan_plan(const gdn_scan_t& s, int backward)
 {
     ScanPlan p;
-    const int each = s.D / s.G, cta = backward ? kBackWarps * back_channels(s.N) : 32;
-    p.warps = (each + 31) / 32;
+    const int each = s.D / s.G, ch = backward ? back_channels(s.N) : fwd_channels(s.N), cta = backward ? kBackWarps * ch : ch;
+    p.blocks = (each + ch - 1) / ch;
     p.ctas = (each + cta - 1) / cta;
-    const long long blocks = (long long)p.ctas * s.G * (backward ? kBackWarps : 1), T = s.T < s.rows ? s.T : s.rows;
-    const long long warps = (long long)p.warps * s.G * s.B;
-    long long seg = 152 * 8 / warps;
-    if (seg > T / 128) seg = T / 128;
-    if (seg > 32) seg = 32;
-    if (seg < 3) seg = 1;
-    p.seg_len = seg > 1 ? (int)(((T + seg - 1) / seg + 31) / 32 * 32) : (T > 0 ? (int)((T + 31) / 32 * 32) : 32);
+    const long long warps = (long long)p.blocks * s.G * s.B, T = s.T < s.rows ? s.T : s.rows;
+    // Segments: as many as keep the SMs in warps, counted by the sequences that run at once on average.  Forwards (up to 16 warps an
+    // SM) the first launch is two thirds of the second: 9 prompts up to 1500 tokens take 211 us whole, 154 in 32 segments a
+    // sequence, 8 x 2048 of 2048 channels 300 and 270, one of 16001 2180 and 226.  Backwards (8 warps an SM by their registers)
+    // only where few warps would run: 8 x 2048 tokens take 1009 us whole and 1170 in 3 segments, 2 x 333 of 208 channels
+    // 145 and 82.
+    long long seg = T > 0 ? (long long)(152.0 * (backward ? 8 : 32) * T / ((double)p.blocks * s.G * s.rows)) : 1;
+    if (seg > T / 32) seg = T / 32;
+    if (seg > 64) seg = 64;
+    if (seg < (backward ? 3 : 4)) seg = 1;
+    p.seg_len = seg > 1 ? (int)(((T + seg - 1) / seg + kSaveEvery - 1) / kSaveEvery * kSaveEvery) : (T > 0 ? (int)((T + 31) / 32 * 32) : 32);
     p.segments = T > 0 ? (int)((T + p.seg_len - 1) / p.seg_len) : 1;
-    const size_t places = p.segments > 1 ? (size_t)p.segments * s.B * blocks : 0;
+    const size_t places = p.segments > 1 ? (size_t)p.segments * warps : 0;
     p.h_off = 256;
-    p.d_off = p.h_off + round_up(places * 32 * state_values(s.N) * 4, 256);      // blocks of 32 channels at most
-    p.w_off = p.d_off + round_up(places * 32 * 4, 256);
+    p.d_off = p.h_off + round_up(places * ch * state_values(s.N) * 4, 256);
+    p.w_off = p.d_off + round_up(places * ch * 4, 256);
     p.bc_off = p.w_off + (backward ? round_up((size_t)p.segments * s.B * s.D * (s.N + 2) * 4, 256) : 0);
     p.total = p.bc_off + (backward ? round_up((size_t)p.ctas * s.rows * s.G * 2 * s.N * 4, 256) : 0);
     return p;

@@ -46,11 +46,12 @@ struct ScanArgs {
     const float *A_log, *D_skip, *dt_bias, *h0, *dhT;
     const int* cu;
     float *hT, *dh0, *dA_log, *dD_skip, *ddt_bias;
-    float* saved;             // states entering every kSaveEvery tokens, [rows / kSaveEvery + B + 1][blocks of 32 channels]
+    float* saved;             // states entering every kSaveEvery tokens, [rows / kSaveEvery + B + 1][blocks]
     float* wpart;             // backward: [B * segments][D (N + 2)] shares of dA_log, dD_skip, ddt_bias
     float* bcpart;            // backward: [CTAs of a group][rows][G][2 N] shares of dBm, dCm
-    float *seg_h, *seg_d;     // split in time: states from zero and sums of delta, [segments][B][blocks of 32 channels]
-    int ctas, warps;          // CTAs that a group's channels need, and blocks of 32 channels that it has
+    float *seg_h, *seg_d;     // split in time: states from zero and sums of delta, [segments][B][blocks]
+    int ctas, blocks;         // CTAs that a group's channels need, and warps' blocks of channels
+    int saved_blocks;         // the forward's blocks
     int segments, seg_len;    // segments a sequence is cut into, tokens of one (a multiple of the tile)
 };
 
@@ -67,20 +68,21 @@ int conv_bwd_blocks(const gdn_conv_t& s);
 
 constexpr int kSaveEvery = 8;     // tokens between the states that a training forward keeps
 
-// How a scan's call is laid out: CTAs and blocks of 32 channels of a group, segments of time, workspace.
+// How a scan's call is laid out: CTAs and warps' blocks of channels of a group, segments of time, workspace.
 struct ScanPlan {
-    int ctas, warps;
+    int ctas, blocks;
     int segments, seg_len;
     size_t h_off, d_off, w_off, bc_off, total;
 };
-constexpr int kBackWarps = 2;     // warps of a CTA of the backward scan
-inline int back_channels(int N) { return N <= 8 ? 32 : N <= 16 ? 16 : 8; }      // and channels of one of them
+constexpr int kBackWarps = 4;     // warps of a CTA of the backward scan
+inline int fwd_channels(int N) { return N <= 16 ? 32 : N <= 32 ? 16 : 8; }      // that a warp takes forwards
+inline int back_channels(int N) { return N <= 8 ? 32 : N <= 16 ? 16 : 8; }      // and backwards
 ScanPlan scan_plan(const gdn_scan_t& s, int backward);
 inline int state_values(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }      // places of a channel's states
+inline int saved_blocks_of(const gdn_scan_t& s) { return (s.D / s.G + fwd_channels(s.N) - 1) / fwd_channels(s.N); }
 inline size_t saved_bytes_of(const gdn_scan_t& s)
 {
-    const size_t places = ((size_t)(s.rows / kSaveEvery) + s.B + 1) * s.G * ((s.D / s.G + 31) / 32);
-    return places * 32 * state_values(s.N) * 4;
+    return ((size_t)(s.rows / kSaveEvery) + s.B + 1) * s.G * saved_blocks_of(s) * fwd_channels(s.N) * state_values(s.N) * 4;
 }
 
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);

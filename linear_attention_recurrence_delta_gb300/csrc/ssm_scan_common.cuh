@@ -1,9 +1,9 @@
 // ssm_scan_common.cuh -- what the forward and the backward scan share: how a warp is laid out, and how tokens are staged.
 //
-// A warp takes CH neighbouring channels of one group of one sequence (or a segment of it).  LS = 1, 2, 4 or 8 lanes, CL =
-// 32 / LS apart, hold the same RC channels (RC <= LS, CH = RC CL), each lane 8 states of every one (8 LS >= N; those past N
-// stay zero).  So a write or read vector is fetched from shared memory 8 values a lane for RC channels' use, which
-// matters: 16 bytes a lane from shared memory take as long as four instructions of every scheduler, broadcast or not.
+// A warp takes CH neighbouring channels of one group of one sequence (or a segment of it).  LS lanes, CL = 32 / LS apart, hold
+// the same RC channels (CH = RC CL), each lane S states of every one (S LS >= N; those past N stay zero).  So a write or
+// read vector is fetched from shared memory S values a lane for RC channels' use, which matters: 16 bytes a lane from
+// shared memory take as long as four instructions of every scheduler, broadcast or not.
 // What goes by channel alone (rows of x, step sizes, gates, results) has an owner: lane l owns channel l % CH at the tokens
 // whose number is l / CH modulo OT = 32 / CH.  Place r of a lane's arrays is the channel that differs from its own by r CL,
 // its own for r = 0.
@@ -16,12 +16,23 @@ namespace ssm {
 
 constexpr int kTile = kSaveEvery;      // tokens that are loaded together
 
-template <int LS_, int RC_>
+template <int S_, int LS_, int RC_>
 struct Lay {
-    static constexpr int LS = LS_, RC = RC_, NS = 8 * LS, CL = 32 / LS, CH = RC * CL, OT = 32 / CH;
+    static constexpr int S = S_, LS = LS_, RC = RC_, NS = S * LS, CL = 32 / LS, CH = RC * CL, OT = 32 / CH, OWN = kTile / OT;
     // the channel of place r, within the warp's
     static __device__ __forceinline__ int channel(int lane, int r) { return (lane % CH) ^ (CL * r); }
 };
+// by N up to 8, 16, 32 and 64.  Forwards few instructions a token count; backwards the channels that a lane adds up by itself
+using Fwd8 = Lay<8, 1, 1>;
+using Fwd16 = Lay<8, 2, 2>;
+using Fwd32 = Lay<8, 4, 2>;
+using Fwd64 = Lay<8, 8, 2>;
+using Back8 = Lay<4, 2, 2>;
+using Back16 = Lay<4, 4, 2>;
+using Back32 = Lay<4, 8, 2>;
+using Back64 = Lay<8, 8, 2>;
+template <class L>
+using States = float2[L::RC][L::S / 2];
 
 // where a warp works
 struct Spot {
@@ -32,16 +43,16 @@ struct Spot {
     int t0, t1;           // tokens of the segment
     __device__ __forceinline__ bool has(int channel) const { return channel < channels; }
 };
-// W warps a CTA; a.ctas CTAs take a group's channels
+// W warps a CTA, a.ctas CTAs and a.blocks blocks of CH channels a group
 template <class L, int W>
 __device__ __forceinline__ Spot spot(const ScanArgs& a)
 {
     Spot p;
-    p.block = blockIdx.x * W + (threadIdx.x >> 5);
     p.g = blockIdx.x / a.ctas;
     p.b = blockIdx.y;
     p.seg = blockIdx.z;
-    const int each = a.s.D / a.s.G, c0 = min(each, (p.block - p.g * a.ctas * W) * L::CH);
+    const int each = a.s.D / a.s.G, n = (blockIdx.x - p.g * a.ctas) * W + (threadIdx.x >> 5), c0 = min(each, n * L::CH);
+    p.block = p.g * a.blocks + n;
     p.d0 = p.g * each + c0;
     p.channels = min(L::CH, each - c0);
     p.r = rows_of(a.cu, p.b, a.s.T, a.s.rows);
@@ -51,19 +62,21 @@ __device__ __forceinline__ Spot spot(const ScanArgs& a)
 }
 
 __device__ __forceinline__ float2 ex2x2(float2 x) { return f2(ex2_approx(x.x), ex2_approx(x.y)); }
-__device__ __forceinline__ void get8(const float* p, float2 (&x)[4])
+template <int H>
+__device__ __forceinline__ void get(const float* p, float2 (&x)[H])
 {
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < H / 2; i++) {
         const float4 v = reinterpret_cast<const float4*>(p)[i];
         x[2 * i] = f2(v.x, v.y);
         x[2 * i + 1] = f2(v.z, v.w);
     }
 }
-__device__ __forceinline__ void put8(float* p, const float2 (&x)[4])
+template <int H>
+__device__ __forceinline__ void put(float* p, const float2 (&x)[H])
 {
 #pragma unroll
-    for (int i = 0; i < 2; i++) reinterpret_cast<float4*>(p)[i] = make_float4(x[2 * i].x, x[2 * i].y, x[2 * i + 1].x, x[2 * i + 1].y);
+    for (int i = 0; i < H / 2; i++) reinterpret_cast<float4*>(p)[i] = make_float4(x[2 * i].x, x[2 * i].y, x[2 * i + 1].x, x[2 * i + 1].y);
 }
 
 // Without a branch, which would keep the compiler from moving instructions of one token among another's.
@@ -77,20 +90,21 @@ __device__ __forceinline__ void store_if(bool ok, __nv_bfloat16* p, float x)
     asm volatile("{ .reg .pred q; setp.ne.b32 q, %2, 0; @q st.global.b16 [%0], %1; }" ::"l"(p), "h"(*reinterpret_cast<const unsigned short*>(&v)), "r"((int)ok) : "memory");
 }
 
-// A tile of a lane's own channel: zeros from the segment's end on and past the warp's channels.
-template <typename IO>
+// A tile of what a lane owns of a tensor: zeros from the segment's end on and past the warp's channels.
+template <class L, typename IO>
 struct Column {
-    IO v[kTile];
+    IO v[L::OWN];
     __device__ __forceinline__ void load(const gdn_mla_view_t& view, const Spot& p, int t0, int lane)
     {
-        const IO* src = (const IO*)view.p + (long long)(p.r.first + t0) * view.tok + p.d0 + lane;
-        const bool in = p.has(lane);
+        const int oc = lane % L::CH, ot = lane / L::CH;
+        const IO* src = (const IO*)view.p + (long long)(p.r.first + t0 + ot) * view.tok + p.d0 + oc;
+        const bool in = p.has(oc);
         if (t0 + kTile <= p.t1) {
 #pragma unroll
-            for (int j = 0; j < kTile; j++) v[j] = in ? src[j * view.tok] : rec::from_f<IO>(0.f);
+            for (int i = 0; i < L::OWN; i++) v[i] = in ? src[i * L::OT * view.tok] : rec::from_f<IO>(0.f);
         } else {
 #pragma unroll
-            for (int j = 0; j < kTile; j++) v[j] = in && t0 + j < p.t1 ? src[j * view.tok] : rec::from_f<IO>(0.f);
+            for (int i = 0; i < L::OWN; i++) v[i] = in && t0 + i * L::OT + ot < p.t1 ? src[i * L::OT * view.tok] : rec::from_f<IO>(0.f);
         }
     }
 };
@@ -98,7 +112,7 @@ struct Column {
 // A tile's write or read vectors, kTile tokens of NS values, in pieces of 8.
 template <class L, typename IO>
 struct Vectors {
-    static constexpr int PIECES = kTile * L::LS, V = (PIECES + 31) / 32;
+    static constexpr int PER = L::NS / 8, PIECES = kTile * PER, V = (PIECES + 31) / 32;
     Raw8<IO> raw[V];
     // asked for: zeros from the segment's end on and past N
     __device__ __forceinline__ void load(const gdn_mla_view_t& v, const Spot& p, int N, int t0, int lane)
@@ -106,7 +120,7 @@ struct Vectors {
         const IO* src = (const IO*)v.p + p.g * v.head;
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            const int u = 32 * i + lane, j = u / L::LS, c = 8 * (u % L::LS);
+            const int u = 32 * i + lane, j = u / PER, c = 8 * (u % PER);
             raw[i] = Raw8<IO>{};
             if (u < PIECES && t0 + j < p.t1 && c < N) raw[i] = raw8(src + (long long)(p.r.first + t0 + j) * v.tok + c);
         }
@@ -125,78 +139,135 @@ struct Vectors {
     }
 };
 
-// where a lane's states of place r lie in [B, D, N]
+// where a lane's states of place r lie in [B, D, N], and whether they exist
 template <class L>
 __device__ __forceinline__ long long state_at(const ScanArgs& a, const Spot& p, int lane, int r)
 {
-    return ((long long)p.b * a.s.D + p.d0 + L::channel(lane, r)) * a.s.N + 8 * (lane / L::CL);
+    return ((long long)p.b * a.s.D + p.d0 + L::channel(lane, r)) * a.s.N + L::S * (lane / L::CL);
+}
+template <class L>
+__device__ __forceinline__ bool has_state(const ScanArgs& a, const Spot& p, int lane, int r)
+{
+    return p.has(L::channel(lane, r)) && L::S * (lane / L::CL) < a.s.N;
 }
 
 // -exp(A_log) log2(e) of a lane's states; zeros past N and past the warp's channels
 template <class L>
-__device__ __forceinline__ void load_rates(const ScanArgs& a, const Spot& p, int lane, float2 (&A)[L::RC][4])
+__device__ __forceinline__ void load_rates(const ScanArgs& a, const Spot& p, int lane, States<L>& A)
 {
-    const int n = 8 * (lane / L::CL);
 #pragma unroll
     for (int r = 0; r < L::RC; r++) {
 #pragma unroll
-        for (int k = 0; k < 4; k++) A[r][k] = f2(0.f, 0.f);
-        const int c = L::channel(lane, r);
-        if (!p.has(c) || n >= a.s.N) continue;
-        get8(a.A_log + (long long)(p.d0 + c) * a.s.N + n, A[r]);
+        for (int k = 0; k < L::S / 2; k++) A[r][k] = f2(0.f, 0.f);
+        if (!has_state<L>(a, p, lane, r)) continue;
+        get(a.A_log + (long long)(p.d0 + L::channel(lane, r)) * a.s.N + L::S * (lane / L::CL), A[r]);
 #pragma unroll
-        for (int k = 0; k < 4; k++) A[r][k] = f2(-expf(A[r][k].x) * kLog2e, -expf(A[r][k].y) * kLog2e);
+        for (int k = 0; k < L::S / 2; k++) A[r][k] = f2(-expf(A[r][k].x) * kLog2e, -expf(A[r][k].y) * kLog2e);
     }
 }
 
-// States that the kernels keep for one another lie as the lanes have them: place `at` of [places][RC][2][32] float4.
+// States that the kernels keep for one another lie as the lanes have them: place `at` of [places][RC][S / 4][32] float4.
 template <class L>
-__device__ __forceinline__ void put_state(float* to, long long at, int lane, const float2 (&h)[L::RC][4])
+__device__ __forceinline__ long long state_offset(long long at, int lane)
 {
-    float4* q = reinterpret_cast<float4*>(to) + at * (L::RC * 64) + lane;
-#pragma unroll
-    for (int r = 0; r < L::RC; r++)
-#pragma unroll
-        for (int i = 0; i < 2; i++) q[(2 * r + i) * 32] = make_float4(h[r][2 * i].x, h[r][2 * i].y, h[r][2 * i + 1].x, h[r][2 * i + 1].y);
+    return at * (L::RC * L::S / 4 * 32) + lane;
 }
 template <class L>
-__device__ __forceinline__ void get_state(const float* from, long long at, int lane, float2 (&h)[L::RC][4])
+__device__ __forceinline__ void put_state(float4* q, const States<L>& h)
 {
-    const float4* q = reinterpret_cast<const float4*>(from) + at * (L::RC * 64) + lane;
 #pragma unroll
     for (int r = 0; r < L::RC; r++)
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const float4 v = q[(2 * r + i) * 32];
+        for (int i = 0; i < L::S / 4; i++)
+            q[(r * (L::S / 4) + i) * 32] = make_float4(h[r][2 * i].x, h[r][2 * i].y, h[r][2 * i + 1].x, h[r][2 * i + 1].y);
+}
+template <class L>
+__device__ __forceinline__ void get_state(const float4* q, States<L>& h)
+{
+#pragma unroll
+    for (int r = 0; r < L::RC; r++)
+#pragma unroll
+        for (int i = 0; i < L::S / 4; i++) {
+            const float4 v = q[(r * (L::S / 4) + i) * 32];
             h[r][2 * i] = f2(v.x, v.y);
             h[r][2 * i + 1] = f2(v.z, v.w);
         }
 }
 // the place of what a segment hands on
-template <int W>
 __device__ __forceinline__ long long segment_at(const ScanArgs& a, const Spot& p, int seg)
 {
-    return ((long long)seg * a.s.B + p.b) * (a.s.G * a.ctas * W) + p.block;
+    return ((long long)seg * a.s.B + p.b) * (a.s.G * a.blocks) + p.block;
 }
-// the place of the states that enter chunk t / kSaveEvery of a sequence, [blocks of 32 channels] as the forward's lanes have
-// them: neighbouring sequences' places never meet
+// where the states lie that enter chunk t / kSaveEvery of a sequence (neighbouring sequences' places never meet), and in
+// them the four states n .. n + 3 of channel c of the group, as the forward's lanes have them
+template <class F>
 __device__ __forceinline__ long long saved_at(const ScanArgs& a, const Spot& p, int t)
 {
-    return ((long long)(p.r.first / kSaveEvery) + p.b + t / kSaveEvery) * (a.s.G * a.warps);
+    const long long place = (long long)(p.r.first / kSaveEvery) + p.b + t / kSaveEvery;
+    return (place * a.s.G + p.g) * a.saved_blocks * (F::RC * F::S / 4 * 32);
 }
-// h (what enters segment s) becomes what leaves it: exp(A sum delta) h + (the segment's state from zero)
-template <class L, int W>
-__device__ __forceinline__ void carry(const ScanArgs& a, const Spot& p, int lane, int s, const float2 (&A)[L::RC][4], float2 (&h)[L::RC][4])
+template <class F>
+__device__ __forceinline__ int saved_place(int c, int n)
 {
-    float2 e[L::RC][4];
-    const long long at = segment_at<W>(a, p, s);
-    get_state<L>(a.seg_h, at, lane, e);
+    const int cc = c % F::CH, lane = n / F::S * F::CL + cc % F::CL, r = (lane % F::CH ^ cc) / F::CL;
+    return ((c / F::CH * F::RC + r) * (F::S / 4) + n % F::S / 4) * 32 + lane;
+}
+// h (what enters segment s0) becomes what leaves segment s0 + (n - 1) step: for each of them in turn exp(A sum delta) h + (the
+// segment's state from zero).  Four segments' values are asked for together.
+template <class L>
+__device__ __forceinline__ void carry(const ScanArgs& a, const Spot& p, int lane, int s0, int step, int n, const States<L>& A, States<L>& h)
+{
+    for (int i0 = 0; i0 < n; i0 += 4) {
+        States<L> e[4];
+        float w[4][L::RC];
 #pragma unroll
-    for (int r = 0; r < L::RC; r++) {
-        const float w = a.seg_d[at * L::CH + L::channel(lane, r)];
+        for (int i = 0; i < 4; i++) {
+            const long long at = segment_at(a, p, s0 + min(i0 + i, n - 1) * step);
+            get_state<L>(reinterpret_cast<const float4*>(a.seg_h) + state_offset<L>(at, lane), e[i]);
 #pragma unroll
-        for (int k = 0; k < 4; k++) h[r][k] = fma2(ex2x2(mul2(f2(w, w), A[r][k])), h[r][k], e[r][k]);
+            for (int r = 0; r < L::RC; r++) w[i][r] = a.seg_d[at * L::CH + L::channel(lane, r)];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (i0 + i < n)
+#pragma unroll
+                for (int r = 0; r < L::RC; r++)
+#pragma unroll
+                    for (int k = 0; k < L::S / 2; k++) h[r][k] = fma2(ex2x2(mul2(f2(w[i][r], w[i][r]), A[r][k])), h[r][k], e[i][r][k]);
     }
+}
+
+// v[t][r]: a lane's share of a sum over the states, for token t of OT and place r.  Every lane gets the whole sum for the
+// channel and the token that it owns.
+template <class L>
+__device__ __forceinline__ float to_owner(const float (&v)[L::OT][L::RC], int lane)
+{
+    static_assert(L::RC == 1 || L::RC == 2 || (L::RC == L::LS && L::OT == 1), "how places and tokens are dealt");
+    float w[L::OT];
+#pragma unroll
+    for (int t = 0; t < L::OT; t++) {
+        w[t] = v[t][0];
+#pragma unroll
+        for (int r = 1; r < L::RC; r++) w[t] += __shfl_xor_sync(0xffffffffu, v[t][r], L::CL * r);
+    }
+    int m = 16;
+#pragma unroll
+    for (int k = L::OT / 2; k; k >>= 1, m >>= 1)
+#pragma unroll
+        for (int i = 0; i < k; i++) {
+            const float keep = lane & m ? w[i + k] : w[i], send = lane & m ? w[i] : w[i + k];
+            w[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+        }
+    return w[0];
+}
+
+// what the owner of token j has, at place r
+template <class L>
+__device__ __forceinline__ float from_owner(const float (&own)[L::OWN], int j, int r, int lane)
+{
+    const float v = own[j / L::OT];
+    if (L::OT == 1) return r ? __shfl_xor_sync(0xffffffffu, v, L::CL * r) : v;
+    return __shfl_sync(0xffffffffu, v, (j % L::OT) * L::CH + L::channel(lane, r));
 }
 
 // v[0 .. n - 1], n a power of two of at most LS: each summed over the LS lanes of a channel (lane = group of states * 32 / LS +

@@ -14,32 +14,29 @@ namespace ssm {
 namespace {
 
 // FIRST: the first of the two launches
-template <typename IO, int LS, bool FIRST>
-__global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a)
+template <typename IO, class L, bool FIRST>
+__global__ void __launch_bounds__(32, 16) scan_kernel(const ScanArgs a)
 {
-    using L = Lay<LS, LS>;
+    constexpr int OT = L::OT, OWN = L::OWN, RC = L::RC, H = L::S / 2;
     __shared__ __align__(16) float sB[kTile][L::NS], sC[FIRST ? 1 : kTile][L::NS];
-    const int lane = threadIdx.x, ng = lane / L::CL;
+    const int lane = threadIdx.x, n = L::S * (lane / L::CL), oc = lane % L::CH, ot = lane / L::CH;
     const Spot p = spot<L, 1>(a);
-    if (FIRST && p.t0 >= p.t1) return;
-    float2 A[LS][4], h[LS][4];
+    if (FIRST && (p.t0 >= p.t1 || p.t1 == p.r.n)) return;      // what a sequence's last segment hands on nobody takes
+    if (!FIRST && p.seg > 0 && p.t0 >= p.t1) return;
+    States<L> A, h;
     float sum = 0.f;
     load_rates<L>(a, p, lane, A);
 #pragma unroll
-    for (int r = 0; r < LS; r++) {
+    for (int r = 0; r < RC; r++) {
 #pragma unroll
-        for (int k = 0; k < 4; k++) h[r][k] = f2(0.f, 0.f);
-        if (!FIRST && a.h0 && p.has(L::channel(lane, r)) && 8 * ng < a.s.N) get8(a.h0 + state_at<L>(a, p, lane, r), h[r]);
+        for (int k = 0; k < H; k++) h[r][k] = f2(0.f, 0.f);
+        if (!FIRST && a.h0 && has_state<L>(a, p, lane, r)) get(a.h0 + state_at<L>(a, p, lane, r), h[r]);
     }
-    if (!FIRST)
-        for (int s = 0; s < p.seg; s++) {
-            if ((long long)s * a.seg_len >= p.r.n) break;
-            carry<L, 1>(a, p, lane, s, A, h);
-        }
-    const bool in = p.has(lane), gated = a.z.p != nullptr;
-    const float bias = in && a.dt_bias ? a.dt_bias[p.d0 + lane] : 0.f;
-    const float skip = !FIRST && in && a.D_skip ? a.D_skip[p.d0 + lane] : 0.f;
-    Column<IO> rx, rdt, rz;
+    if (!FIRST) carry<L>(a, p, lane, 0, 1, p.seg, A, h);
+    const bool in = p.has(oc), gated = a.z.p != nullptr;
+    const float bias = in && a.dt_bias ? a.dt_bias[p.d0 + oc] : 0.f;
+    const float skip = !FIRST && in && a.D_skip ? a.D_skip[p.d0 + oc] : 0.f;
+    Column<L, IO> rx, rdt, rz;
     Vectors<L, IO> rB, rC;
     auto ask = [&](int t0) {
         rx.load(a.x, p, t0, lane);
@@ -52,87 +49,95 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanArgs a)
     };
     if (p.t0 < p.t1) ask(p.t0);
     for (int t0 = p.t0; t0 < p.t1; t0 += kTile) {
-        float x[kTile], w[kTile], z[kTile], y[kTile], slope;
+        float x[OWN], w[OWN], ux[OWN], z[OWN], y[OWN], slope;
 #pragma unroll
-        for (int j = 0; j < kTile; j++) {
-            x[j] = rec::to_f(rx.v[j]);
-            if (!FIRST) z[j] = rec::to_f(rz.v[j]);
-            w[j] = rec::to_f(rdt.v[j]) + bias;
+        for (int i = 0; i < OWN; i++) {
+            x[i] = rec::to_f(rx.v[i]);
+            if (!FIRST) z[i] = rec::to_f(rz.v[i]);
+            w[i] = rec::to_f(rdt.v[i]) + bias;
         }
         if (a.s.softplus)
 #pragma unroll
-            for (int j = 0; j < kTile; j++) w[j] = softplus(w[j], slope);
+            for (int i = 0; i < OWN; i++) w[i] = softplus(w[i], slope);
         if (t0 + kTile > p.t1)
 #pragma unroll
-            for (int j = 0; j < kTile; j++)
-                if (t0 + j >= p.t1) w[j] = 0.f;      // a step of size zero changes nothing
+            for (int i = 0; i < OWN; i++)
+                if (t0 + i * OT + ot >= p.t1) w[i] = 0.f;      // a step of size zero changes nothing
+#pragma unroll
+        for (int i = 0; i < OWN; i++) {
+            ux[i] = w[i] * x[i];
+            if (FIRST) sum += w[i];
+        }
         __syncwarp();      // the last tile's vectors have been read
         rB.store(&sB[0][0], lane);
         if (!FIRST) rC.store(&sC[0][0], lane);
         __syncwarp();
         if (t0 + kTile < p.t1) ask(t0 + kTile);
-        if (!FIRST && a.saved) put_state<L>(a.saved, saved_at(a, p, t0) + p.block, lane, h);
+        if (!FIRST && a.saved) put_state<L>(reinterpret_cast<float4*>(a.saved) + saved_at<L>(a, p, t0) + state_offset<L>(p.block - p.g * a.blocks, lane), h);
+        // exchanges between lanes before and after, so that nothing keeps one token's arithmetic from another's
+        float wr[kTile][RC], ur[kTile][RC], part[OWN][OT][RC];
+#pragma unroll
+        for (int j = 0; j < kTile; j++)
+#pragma unroll
+            for (int r = 0; r < RC; r++) {
+                wr[j][r] = from_owner<L>(w, j, r, lane);
+                ur[j][r] = from_owner<L>(ux, j, r, lane);
+            }
 #pragma unroll
         for (int j = 0; j < kTile; j++) {
-            float2 B[4], C[4];
-            float part[LS];
-            get8(&sB[j][8 * ng], B);
-            if (!FIRST) get8(&sC[j][8 * ng], C);
-            const float ux = w[j] * x[j];
+            float2 B[H], C[H];
+            get(&sB[j][n], B);
+            if (!FIRST) get(&sC[j][n], C);
 #pragma unroll
-            for (int r = 0; r < LS; r++) {
-                const float wr = r ? __shfl_xor_sync(0xffffffffu, w[j], L::CL * r) : w[j];
-                const float ur = r ? __shfl_xor_sync(0xffffffffu, ux, L::CL * r) : ux;
+            for (int r = 0; r < RC; r++) {
                 float2 o = f2(0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    h[r][k] = fma2(ex2x2(mul2(f2(wr, wr), A[r][k])), h[r][k], mul2(f2(ur, ur), B[k]));
+                for (int k = 0; k < H; k++) {
+                    h[r][k] = fma2(ex2x2(mul2(f2(wr[j][r], wr[j][r]), A[r][k])), h[r][k], mul2(f2(ur[j][r], ur[j][r]), B[k]));
                     if (!FIRST) o = k ? fma2(h[r][k], C[k], o) : mul2(h[r][k], C[k]);
                 }
-                part[r] = o.x + o.y;
+                part[j / OT][j % OT][r] = o.x + o.y;
             }
-            if (FIRST) {
-                sum += w[j];
-                continue;
-            }
-            y[j] = part[0];
-#pragma unroll
-            for (int r = 1; r < LS; r++) y[j] += __shfl_xor_sync(0xffffffffu, part[r], L::CL * r);
         }
+        if (!FIRST)
+#pragma unroll
+            for (int i = 0; i < OWN; i++) y[i] = to_owner<L>(part[i], lane);
         if (FIRST) continue;
 #pragma unroll
-        for (int j = 0; j < kTile; j++) y[j] = fmaf(skip, x[j], y[j]);
+        for (int i = 0; i < OWN; i++) y[i] = fmaf(skip, x[i], y[i]);
         if (gated)
 #pragma unroll
-            for (int j = 0; j < kTile; j++) y[j] *= z[j] * sigmoid(z[j]);
-        IO* out = (IO*)a.y.p + (long long)(p.r.first + t0) * a.y.tok + p.d0 + lane;
+            for (int i = 0; i < OWN; i++) y[i] *= z[i] * sigmoid(z[i]);
+        IO* out = (IO*)a.y.p + (long long)(p.r.first + t0 + ot) * a.y.tok + p.d0 + oc;
 #pragma unroll
-        for (int j = 0; j < kTile; j++) store_if(in && t0 + j < p.t1, out + j * a.y.tok, y[j]);
+        for (int i = 0; i < OWN; i++) store_if(in && t0 + i * OT + ot < p.t1, out + i * OT * a.y.tok, y[i]);
     }
     if (FIRST) {
-        put_state<L>(a.seg_h, segment_at<1>(a, p, p.seg), lane, h);
-        a.seg_d[segment_at<1>(a, p, p.seg) * 32 + lane] = sum;
+        put_state<L>(reinterpret_cast<float4*>(a.seg_h) + state_offset<L>(segment_at(a, p, p.seg), lane), h);
+#pragma unroll
+        for (int m = L::CH; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        a.seg_d[segment_at(a, p, p.seg) * L::CH + oc] = sum;
     } else if (a.hT && p.t1 == p.r.n && (p.t0 < p.t1 || p.seg == 0)) {
 #pragma unroll
-        for (int r = 0; r < LS; r++)
-            if (p.has(L::channel(lane, r)) && 8 * ng < a.s.N) put8(a.hT + state_at<L>(a, p, lane, r), h[r]);
+        for (int r = 0; r < RC; r++)
+            if (has_state<L>(a, p, lane, r)) put(a.hT + state_at<L>(a, p, lane, r), h[r]);
     }
 }
 
-template <typename IO, int LS>
+template <typename IO, class L>
 cudaError_t launch_lanes(const ScanArgs& a, cudaStream_t st)
 {
     const dim3 grid(a.s.G * a.ctas, a.s.B, a.segments);
-    if (a.segments > 1) scan_kernel<IO, LS, true><<<grid, 32, 0, st>>>(a);
-    scan_kernel<IO, LS, false><<<grid, 32, 0, st>>>(a);
+    if (a.segments > 1) scan_kernel<IO, L, true><<<grid, 32, 0, st>>>(a);
+    scan_kernel<IO, L, false><<<grid, 32, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename IO>
 cudaError_t launch_typed(const ScanArgs& a, cudaStream_t st)
 {
-    if (a.s.N <= 8) return launch_lanes<IO, 1>(a, st);
-    if (a.s.N <= 16) return launch_lanes<IO, 2>(a, st);
-    return a.s.N <= 32 ? launch_lanes<IO, 4>(a, st) : launch_lanes<IO, 8>(a, st);
+    if (a.s.N <= 8) return launch_lanes<IO, Fwd8>(a, st);
+    if (a.s.N <= 16) return launch_lanes<IO, Fwd16>(a, st);
+    return a.s.N <= 32 ? launch_lanes<IO, Fwd32>(a, st) : launch_lanes<IO, Fwd64>(a, st);
 }
 
 // New tokens.  LS = 2, 4, 8 or 16 lanes, CL = 32 / LS apart, hold a channel's states, 4 each, and take E = 2 or 4 sequences at
