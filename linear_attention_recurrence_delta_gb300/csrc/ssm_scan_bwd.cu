@@ -350,10 +350,11 @@ cudaError_t launch_lanes(const ScanArgs& a, cudaStream_t st)
 {
     constexpr size_t stages = kBackWarps * sizeof(BackStage<IO, L>), whole = stages + sizeof(BackParts<L>);
     const dim3 grid(a.s.G * a.ctas, a.s.B, a.segments);
-    if (whole > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, F, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)whole);
-        if (e != cudaSuccess) return e;
-    }
+    cudaError_t e = cudaSuccess;
+    if (whole > 48 * 1024) e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, F, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)whole);
+    if (e == cudaSuccess && stages > 48 * 1024 && a.segments > 1)
+        e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, F, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)stages);
+    if (e != cudaSuccess) return e;
     if (a.segments > 1) scan_bwd_kernel<IO, L, F, true><<<grid, 32 * kBackWarps, stages, st>>>(a);
     scan_bwd_kernel<IO, L, F, false><<<grid, 32 * kBackWarps, whole, st>>>(a);
     const long long units = (long long)a.s.T * (a.s.G * 2 * a.s.N / 8);
