@@ -73,7 +73,7 @@ __device__ __forceinline__ void load_past(const IO* x, long long tok, const void
 
 // Sequence blockIdx.y; threads run over (strip, piece of 4 channels), pieces fastest.
 template <typename IO, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a)
+__global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a)
 {
     const int D = a.s.D, pieces = D >> 2, b = blockIdx.y;
     const long long u = (long long)blockIdx.x * kThreads + threadIdx.x;
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a)
     load_taps<W>(a.w + (long long)c * W, taps);
     if (a.bias) bias = raw4(a.bias + c).get();
     Raw4<IO> next[4];
-    auto ask = [&](int t) {      // without a branch a row where all four are there
+    auto ask = [&](int t) {      // without a branch a row where all are there
         if (t + 4 <= end)
 #pragma unroll
             for (int j = 0; j < 4; j++) next[j] = raw4(x + (long long)(t + j) * a.x.tok);
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a)
                 if (t + j < end) next[j] = raw4(x + (long long)(t + j) * a.x.tok);
     };
     auto row = [&](int t, int j, const Raw4<IO>& v) {
-        ring[j] = v.get();
+        ring[j & 3] = v.get();
         Four p = bias;
 #pragma unroll
         for (int k = 0; k < W; k++) p = fma(taps[k], ring[(j + 5 - W + k) & 3], p);
@@ -108,7 +108,9 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a)
     load_past<IO, W>(x, a.x.tok, a.s0, b, D, c, t0, ring);
     int t = t0;
     for (; t + 4 <= end; t += 4) {
-        const Raw4<IO> now[4] = {next[0], next[1], next[2], next[3]};
+        Raw4<IO> now[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) now[j] = next[j];
         ask(t + 4);
 #pragma unroll
         for (int j = 0; j < 4; j++) row(t, j, now[j]);

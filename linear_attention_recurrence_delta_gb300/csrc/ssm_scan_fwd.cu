@@ -140,78 +140,86 @@ cudaError_t launch_typed(const ScanArgs& a, cudaStream_t st)
     return a.s.N <= 32 ? launch_lanes<IO, Fwd32>(a, st) : launch_lanes<IO, Fwd64>(a, st);
 }
 
-// New tokens.  LS = 2, 4, 8 or 16 lanes, CL = 32 / LS apart, hold a channel's states, 4 each, and take E = 2 or 4 sequences at
-// a time, each of them owned by some of the lanes, which work out its step size and store its result.  The states' bytes
-// bound it where sequences are many: A is read once a warp, and the next sequences' states are on their way meanwhile.
+// New tokens.  LS = 1, 2, 4 or 8 lanes, CL = 32 / LS apart, hold a channel's states, 8 each, and take E <= LS sequences at a
+// time, each of them owned by some of the lanes, which work out its step size and store its result.  The states' bytes bound
+// it where sequences are many, next to the instructions around them: so few lanes a channel, and A taken once for all the
+// sequences of a warp.  ONE: a single token each.
 constexpr int kStepThreads = 128;
-template <typename IO, int LS>
-__global__ void __launch_bounds__(kStepThreads, 7) scan_step_kernel(const ScanStepArgs a)
+template <typename IO, int LS, bool ONE>
+__global__ void __launch_bounds__(kStepThreads, LS <= 2 ? 7 : 4) scan_step_kernel(const ScanStepArgs a)
 {
     constexpr int CL = 32 / LS, E = LS < 4 ? LS : 4, REP = LS / E;
-    const int N = a.s.N, D = a.s.D, T = a.s.T, lane = threadIdx.x & 31, ng = lane / CL, own = ng / REP, n = 4 * ng;
+    const int N = a.s.N, D = a.s.D, T = ONE ? 1 : a.s.T, lane = threadIdx.x & 31, ng = lane / CL, own = ng / REP, n = 8 * ng;
     const int u = (blockIdx.x * (kStepThreads / 32) + (threadIdx.x >> 5)) * CL + lane % CL, d = min(u, D - 1), g = d / (D / a.s.G);
     const bool mine = u < D && n < N;
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.f, skip = a.D_skip ? a.D_skip[d] : 0.f;
-    Four A = all(0.f);
+    float2 A[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) A[k] = f2(0.f, 0.f);
     if (mine) {
-        A = raw4(a.A_log + (long long)d * N + n).get();
-        A = {f2(-expf(A.a.x) * kLog2e, -expf(A.a.y) * kLog2e), f2(-expf(A.b.x) * kLog2e, -expf(A.b.y) * kLog2e)};
+        get(a.A_log + (long long)d * N + n, A);
+#pragma unroll
+        for (int k = 0; k < 4; k++) A[k] = f2(-expf(A[k].x) * kLog2e, -expf(A[k].y) * kLog2e);
     }
-    auto slot = [&](int b, bool to) {
-        if (b >= a.s.B) return -1;
-        const int s = to && a.dst ? a.dst[b] : a.src ? a.src[b] : b;
-        return s < a.s.slots ? s : -1;
-    };
-    Four next[E];
-    auto ask = [&](int b0) {
+    // from one sequence's rows to the next one's
+    const long long dB = T * a.Bm.tok, dC = T * a.Cm.tok;
+    float* state = a.state + (long long)d * N + n;
+    const long long slot = (long long)D * N;
+    for (int b0 = blockIdx.y * E; b0 < a.s.B; b0 += gridDim.y * E) {
+        float2 h[E][4];
+        int to[E];      // slots that are written
 #pragma unroll
         for (int e = 0; e < E; e++) {
-            const int s = slot(b0 + e, false);
-            next[e] = all(0.f);
-            if (mine && s >= 0) next[e] = raw4(a.state + ((long long)s * D + d) * N + n).get();
-        }
-    };
-    ask(blockIdx.y * E);
-    for (int b0 = blockIdx.y * E; b0 < a.s.B; b0 += gridDim.y * E) {
-        Four h[E];
+            int s = -1;
+            if (b0 + e < a.s.B) s = a.src ? a.src[b0 + e] : b0 + e;
+            to[e] = s;
+            if (a.dst && b0 + e < a.s.B) to[e] = a.dst[b0 + e];
 #pragma unroll
-        for (int e = 0; e < E; e++) h[e] = next[e];
-        if (b0 + (int)gridDim.y * E < a.s.B) ask(b0 + gridDim.y * E);
+            for (int k = 0; k < 4; k++) h[e][k] = f2(0.f, 0.f);
+            if (mine && (unsigned)s < (unsigned)a.s.slots) get(state + s * slot, h[e]);
+        }
         const bool live = b0 + own < a.s.B;
+        const int left = a.s.B - b0;
+        const long long row = (long long)(live ? b0 + own : b0) * T;
+        const IO* pB = (const IO*)a.Bm.p + (long long)b0 * dB + g * a.Bm.head + n;
+        const IO* pC = (const IO*)a.Cm.p + (long long)b0 * dC + g * a.Cm.head + n;
+#pragma unroll 1
         for (int t = 0; t < T; t++) {
-            const long long row = (long long)min(b0 + own, a.s.B - 1) * T + t;
-            const float x = rec::to_f(((const IO*)a.x.p)[row * a.x.tok + d]);
-            float w = rec::to_f(((const IO*)a.dt.p)[row * a.dt.tok + d]) + bias, slope, y[E];
-            const float z = a.z.p ? rec::to_f(((const IO*)a.z.p)[row * a.z.tok + d]) : 0.f;
-            Raw4<IO> B[E], C[E];
+            const float x = rec::to_f(((const IO*)a.x.p)[(row + t) * a.x.tok + d]);
+            const float z = a.z.p ? rec::to_f(((const IO*)a.z.p)[(row + t) * a.z.tok + d]) : 0.f;
+            float w = rec::to_f(((const IO*)a.dt.p)[(row + t) * a.dt.tok + d]) + bias, slope, y[E];
+            Raw8<IO> B[E], C[E];
 #pragma unroll
             for (int e = 0; e < E; e++) {
-                const long long r = (long long)min(b0 + e, a.s.B - 1) * T + t;
-                B[e] = C[e] = Raw4<IO>{};
-                if (!mine) continue;
-                B[e] = raw4((const IO*)a.Bm.p + r * a.Bm.tok + g * a.Bm.head + n);
-                C[e] = raw4((const IO*)a.Cm.p + r * a.Cm.tok + g * a.Cm.head + n);
+                B[e] = C[e] = Raw8<IO>{};
+                if (mine && e < left) {
+                    B[e] = raw8(pB + e * dB + t * a.Bm.tok);
+                    C[e] = raw8(pC + e * dC + t * a.Cm.tok);
+                }
             }
             if (a.s.softplus) w = softplus(w, slope);
             const float ux = w * x;
 #pragma unroll
             for (int e = 0; e < E; e++) {
                 const int from = lane % CL + CL * REP * e;
-                const float we = __shfl_sync(0xffffffffu, w, from), ue = __shfl_sync(0xffffffffu, ux, from);
-                const Four f = mul(all(we), A);
-                h[e] = fma({f2(ex2_approx(f.a.x), ex2_approx(f.a.y)), f2(ex2_approx(f.b.x), ex2_approx(f.b.y))}, h[e], mul(all(ue), B[e].get()));
-                const Four o = mul(h[e], C[e].get());
-                const float2 s = add2(o.a, o.b);
-                y[e] = s.x + s.y;
+                const float we = LS == 1 ? w : __shfl_sync(0xffffffffu, w, from), ue = LS == 1 ? ux : __shfl_sync(0xffffffffu, ux, from);
+                float b[8], c[8];
+                values(B[e], b);
+                values(C[e], c);
+                float2 o = f2(0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    h[e][k] = fma2(ex2x2(mul2(f2(we, we), A[k])), h[e][k], mul2(f2(ue, ue), f2(b[2 * k], b[2 * k + 1])));
+                    o = fma2(h[e][k], f2(c[2 * k], c[2 * k + 1]), o);
+                }
+                y[e] = o.x + o.y;
             }
             const float v = fmaf(skip, x, states_sum<LS, E>(y, lane));
-            if (live && u < D && ng % REP == 0) ((IO*)a.y.p)[row * a.y.tok + d] = rec::from_f<IO>(a.z.p ? v * z * sigmoid(z) : v);
+            store_if(live && u < D && ng % REP == 0, (IO*)a.y.p + (row + t) * a.y.tok + d, a.z.p ? v * z * sigmoid(z) : v);
         }
 #pragma unroll
-        for (int e = 0; e < E; e++) {
-            const int s = slot(b0 + e, true);
-            if (mine && s >= 0) put(a.state + ((long long)s * D + d) * N + n, h[e]);
-        }
+        for (int e = 0; e < E; e++)
+            if (mine && (unsigned)to[e] < (unsigned)a.s.slots) put(state + to[e] * slot, h[e]);
     }
 }
 
@@ -220,16 +228,18 @@ cudaError_t launch_step_lanes(const ScanStepArgs& a, cudaStream_t st)
 {
     constexpr int CL = 32 / LS, E = LS < 4 ? LS : 4;
     const int wide = (a.s.D + 4 * CL - 1) / (4 * CL), groups = (a.s.B + E - 1) / E;
-    const int fit = 152 * 40 / wide, turns = fit < 1 ? groups : (groups + fit - 1) / fit;      // CTAs that run at once
-    scan_step_kernel<IO, LS><<<dim3(wide, (groups + turns - 1) / turns), kStepThreads, 0, st>>>(a);
+    const int fit = 152 * 40 / wide, turns = fit < 1 ? groups : (groups + fit - 1) / fit;
+    const dim3 grid(wide, (groups + turns - 1) / turns);
+    if (a.s.T == 1) scan_step_kernel<IO, LS, true><<<grid, kStepThreads, 0, st>>>(a);
+    else scan_step_kernel<IO, LS, false><<<grid, kStepThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename IO>
 cudaError_t launch_step_typed(const ScanStepArgs& a, cudaStream_t st)
 {
-    if (a.s.N <= 8) return launch_step_lanes<IO, 2>(a, st);
-    if (a.s.N <= 16) return launch_step_lanes<IO, 4>(a, st);
-    return a.s.N <= 32 ? launch_step_lanes<IO, 8>(a, st) : launch_step_lanes<IO, 16>(a, st);
+    if (a.s.N <= 8) return launch_step_lanes<IO, 1>(a, st);
+    if (a.s.N <= 16) return launch_step_lanes<IO, 2>(a, st);
+    return a.s.N <= 32 ? launch_step_lanes<IO, 4>(a, st) : launch_step_lanes<IO, 8>(a, st);
 }
 
 }  // namespace
