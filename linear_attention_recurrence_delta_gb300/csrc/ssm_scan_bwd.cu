@@ -29,6 +29,17 @@ __device__ __forceinline__ void add_column(float (&acc)[4], float2 v, uint32_t o
                  : "r"(h0), "r"(h1), "r"(l0), "r"(l1), "r"(ones));
 }
 
+// A long sum that carries what its last addition lost (Kahan's summation).
+struct Sum {
+    float v = 0.f, lost = 0.f;
+    __device__ __forceinline__ void add(float x)
+    {
+        const float y = __fsub_rn(x, lost), t = __fadd_rn(v, y);
+        lost = __fsub_rn(__fsub_rn(t, v), y);
+        v = t;
+    }
+};
+
 // What a warp keeps in shared memory.
 template <typename IO, class L>
 struct BackStage {
@@ -82,7 +93,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
             for (int i = 0; i < L::S / 4; i++) saved[r][i] = saved_place<F>(p.d0 - p.g * (D / a.s.G) + L::channel(lane, r), n + 4 * i);
     const bool in = p.has(oc), gated = a.z.p != nullptr;
     const float bias = in && a.dt_bias ? a.dt_bias[p.d0 + oc] : 0.f, skip = !FIRST && in && a.D_skip ? a.D_skip[p.d0 + oc] : 0.f;
-    float dskip = 0.f, dbias = 0.f;
+    Sum dskip, dbias;
 
     // asks for a tile: zeros from the segment's end on, past the warp's channels and past N
     auto ask = [&](int t0, int buf) {
@@ -186,12 +197,13 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
                     const float wr = from_owner<L>(w, j, r, lane), gr = from_owner<L>(g, j, r, lane);
 #pragma unroll
                     for (int k = 0; k < H; k++)
-                        back[r][k] = mul2(ex2x2(mul2(f2(wr, wr), A[r][k])), fma2(f2(gr, gr), C[k], back[r][k]));
+                        back[r][k] = mul2(factor(f2(wr, wr), A[r][k]), fma2(f2(gr, gr), C[k], back[r][k]));
                 }
             }
             continue;
         }
-        States<L> tA;
+        States<L> tA;                               // this tile's share of the sums over tokens
+        float tskip = 0.f, tbias = 0.f;
 #pragma unroll
         for (int r = 0; r < RC; r++)
 #pragma unroll
@@ -211,7 +223,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
                     const float wr = from_owner<L>(w, j, r, lane), ur = from_owner<L>(ux, j, r, lane);
 #pragma unroll
                     for (int k = 0; k < H; k++) {
-                        const float2 e = ex2x2(mul2(f2(wr, wr), A[r][k]));
+                        const float2 e = factor(f2(wr, wr), A[r][k]);
                         if (M == K) f[jj][r][k] = e;
                         h[jj < 0 ? 0 : jj + 1][r][k] = fma2(e, h[jj < 0 ? 0 : jj][r][k], mul2(f2(ur, ur), B[k]));
                     }
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
 #pragma unroll
                         for (int k = 0; k < H; k++) {
                             const float2 dh = fma2(g2, C[k], back[r][k]);
-                            back[r][k] = mul2(M == K ? f[M == K ? jj : 0][r][k] : ex2x2(mul2(w2, A[r][k])), dh);
+                            back[r][k] = mul2(M == K ? f[M == K ? jj : 0][r][k] : factor(w2, A[r][k]), dh);
                             const float2 q = mul2(back[r][k], h[jj][r][k]);
                             tA[r][k] = fma2(q, w2, tA[r][k]);
                             sdu = k ? fma2(dh, B[k], sdu) : mul2(dh, B[k]);
@@ -265,8 +277,8 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
                 store_if(ok && gated, (IO*)a.dz.p + row * a.dz.tok + p.d0 + oc, dz);
                 store_if(ok, (IO*)a.dx.p + row * a.dx.tok + p.d0 + oc, fmaf(sdu, w[i], g[i] * skip));
                 store_if(ok, (IO*)a.ddt.p + row * a.ddt.tok + p.d0 + oc, ddt);
-                dskip = fmaf(g[i], x, dskip);       // zeros past the end
-                dbias += ok ? ddt : 0.f;
+                tskip = fmaf(g[i], x, tskip);       // zeros past the end
+                tbias += ok ? ddt : 0.f;
             }
             // row r of a product is lanes 4 r .., columns 2 q and 2 q + 1 lane q's tokens (q and q + 4 of M)
             const int r = lane >> 2, q = lane & 3;
@@ -284,6 +296,8 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
         for (int r = 0; r < RC; r++)
 #pragma unroll
             for (int k = 0; k < H; k++) dA[r][k] = add2(dA[r][k], tA[r][k]);      // tile by tile: long sums keep their accuracy
+        dskip.add(tskip);
+        dbias.add(tbias);
         __syncthreads();
         float* out = a.bcpart + ((long long)(blockIdx.x - p.g * a.ctas) * a.s.rows * a.s.G + p.g) * 2 * N;
 #pragma unroll
@@ -313,12 +327,12 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
     }
 #pragma unroll
     for (int m = L::CH; m < 32; m <<= 1) {
-        dskip += __shfl_xor_sync(0xffffffffu, dskip, m);
-        dbias += __shfl_xor_sync(0xffffffffu, dbias, m);
+        dskip.v += __shfl_xor_sync(0xffffffffu, dskip.v, m);
+        dbias.v += __shfl_xor_sync(0xffffffffu, dbias.v, m);
     }
     if (ot == 0 && in) {
-        share[(long long)D * N + p.d0 + oc] = dskip;
-        share[(long long)D * (N + 1) + p.d0 + oc] = dbias;
+        share[(long long)D * N + p.d0 + oc] = dskip.v;
+        share[(long long)D * (N + 1) + p.d0 + oc] = dbias.v;
     }
 }
 

@@ -62,6 +62,12 @@ __device__ __forceinline__ Spot spot(const ScanArgs& a)
 }
 
 __device__ __forceinline__ float2 ex2x2(float2 x) { return f2(ex2_approx(x.x), ex2_approx(x.y)); }
+// exp(delta A) of two states: 2^(w A2).  ex2.approx's results are 2.1e-8 low on average for exponents between -0.3 and -0.003
+// (measured; their other error, 3.7e-8, has no sign).  A state that forgets over a thousand tokens would add that up a thousand
+// times, so the exponent is raised by as much; 2^(that alone) is 1, and a step of size zero still changes nothing.
+constexpr float kLow = 3e-8f;
+__device__ __forceinline__ float2 factor(float2 w, float2 A2) { return ex2x2(fma2(w, A2, f2(kLow, kLow))); }
+
 template <int H>
 __device__ __forceinline__ void get(const float* p, float2 (&x)[H])
 {

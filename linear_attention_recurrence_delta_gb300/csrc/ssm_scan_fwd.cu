@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(32, 16) scan_kernel(const ScanArgs a)
                 float2 o = f2(0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < H; k++) {
-                    h[r][k] = fma2(ex2x2(mul2(f2(wr[j][r], wr[j][r]), A[r][k])), h[r][k], mul2(f2(ur[j][r], ur[j][r]), B[k]));
+                    h[r][k] = fma2(factor(f2(wr[j][r], wr[j][r]), A[r][k]), h[r][k], mul2(f2(ur[j][r], ur[j][r]), B[k]));
                     if (!FIRST) o = k ? fma2(h[r][k], C[k], o) : mul2(h[r][k], C[k]);
                 }
                 part[j / OT][j % OT][r] = o.x + o.y;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kStepThreads, LS <= 2 ? 7 : 4) scan_step_kerne
                 float2 o = f2(0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    h[e][k] = fma2(ex2x2(mul2(f2(we, we), A[k])), h[e][k], mul2(f2(ue, ue), f2(b[2 * k], b[2 * k + 1])));
+                    h[e][k] = fma2(factor(f2(we, we), A[k]), h[e][k], mul2(f2(ue, ue), f2(b[2 * k], b[2 * k + 1])));
                     o = fma2(h[e][k], f2(c[2 * k], c[2 * k + 1]), o);
                 }
                 y[e] = o.x + o.y;
