@@ -286,22 +286,23 @@ cudaError_t launch_bwd_typed(const NormArgs& a, cudaStream_t st)
     return cudaGetLastError();
 }
 
-// 32 columns a block; the rows are dealt to its 32 warps in turn, whose sums are then added in their order
-__global__ void __launch_bounds__(1024) column_sums_kernel(const ColumnSums s)
+// 32 columns a block; the rows are dealt to its R warps in turn, whose sums are then added in their order
+template <int R>
+__global__ void __launch_bounds__(32 * R) column_sums_kernel(const ColumnSums s)
 {
     cudaGridDependencySynchronize();      // launched as a dependent of the kernel that writes the shares
-    __shared__ float part[32][33];
+    __shared__ float part[R][33];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long c = (long long)blockIdx.x * 32 + lane;
     float x = 0.f;
     if (c < s.cols)
 #pragma unroll 8
-        for (int r = w; r < s.rows; r += 32) x += s.partial[r * s.cols + c];
+        for (int r = w; r < s.rows; r += R) x += s.partial[r * s.cols + c];
     part[w][lane] = x;
     __syncthreads();
     if (w || c >= s.cols) return;
 #pragma unroll
-    for (int i = 1; i < 32; i++) x += part[i][lane];
+    for (int i = 1; i < R; i++) x += part[i][lane];
     if (c < s.a) {
         if (s.out_a) s.out_a[c] = s.decay ? x * -expf(s.decay[c]) : x;
     } else if (c < s.a + s.b) {
@@ -326,14 +327,15 @@ cudaError_t launch_column_sums(const ColumnSums& s, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((s.cols + 31) / 32));
-    cfg.blockDim = dim3(1024);
+    const bool few = s.rows <= 64;        // shares of a scan's sequences: many columns instead
+    cfg.blockDim = dim3(few ? 128 : 1024);
     cfg.stream = st;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, column_sums_kernel, s);
+    return few ? cudaLaunchKernelEx(&cfg, column_sums_kernel<4>, s) : cudaLaunchKernelEx(&cfg, column_sums_kernel<32>, s);
 }
 
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st)
