@@ -40,7 +40,7 @@ extern "C" {
  * out = io: y is of the I/O type.  out = GDN_E4M3: y holds 8-bit values and scale one fp32 number for each `group` values
  * of a row (group = 0: for the whole row), y[n, i] ~ value * scale with scale = max(max |y| over the group, 1e-30) / 448
  * and value = y / scale rounded to nearest even.  A NaN in a row gives NaN for its values and scales.
- * Limits: N >= 0, 8 <= D <= 16384, group 0, 32, 64 or 128 and a divisor of D. */
+ * Limits: 0 <= N <= 2^30, 8 <= D <= 16384 a multiple of 8, group 0, 32, 64 or 128 and a divisor of D. */
 #define GDN_E4M3 2        /* value of gdn_norm_t.out beside gdn_dtype_t's */
 
 typedef struct {
@@ -72,7 +72,8 @@ gdn_status_t gdn_norm_bwd(const gdn_norm_t* shape, const void* sum, long long su
  *   pre[t, d] = bias[d] + sum_{k < W} w[d, k] x[t - (W - 1) + k, d],     y = silu ? pre / (1 + exp(-pre)) : pre
  *
  * within each sequence; the rows before its first are those of its state [W - 1, D] (NULL: zeros), and its new state is
- * the last W - 1 rows of state and sequence together.  Limits: 2 <= W <= 4, B, T >= 1 where rows > 0, B <= 65535. */
+ * the last W - 1 rows of state and sequence together.  Limits: 2 <= W <= 4, B >= 1,
+ * T >= 1 where rows > 0, B <= 65535, rows <= 2^30, D a multiple of 8 up to 2^24. */
 typedef struct {
     int B, T, D, W;       /* sequences, most rows of one, channels, taps       */
     int silu;
@@ -112,8 +113,8 @@ gdn_status_t gdn_conv_step(const gdn_conv_step_t* shape, const gdn_mla_view_t* x
  *   y[t, d]     = (sum_n h[t, d, n] Cm[t, g, n] + D[d] x[t, d]) * silu(z[t, d]),        g = d / (D / G)
  *
  * within each sequence, from its state h0 [D, N] (zeros without).  delta is meant to be >= 0 (without softplus a negative
- * one grows the state).  Limits: N a multiple of 8 up to 64, D a multiple of 8 G, B, T >= 1 where rows > 0, B <= 65535,
- * G <= 65535, B * D * N < 2^31. */
+ * one grows the state).  Limits: N a multiple of 8 up to 64, D a multiple of 8 G, B, G >= 1, T >= 1 where rows > 0,
+ * B, G <= 65535, rows <= 2^30, B * D * N and D (N + 2) < 2^31. */
 typedef struct {
     int B, T, D, N, G;    /* sequences, most rows of one, channels, states a channel, groups that share Bm and Cm */
     int softplus;

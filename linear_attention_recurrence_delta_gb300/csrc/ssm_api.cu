@@ -24,11 +24,13 @@ gdn_status_t rows_ok(const void* p, long long tok, int D, int type)
         if (r_ != GDN_OK) return r_;           \
     } while (0)
 
+constexpr int kMostRows = 1 << 30;      // so that a row's number and a tile more stay in 32 bits
+
 gdn_status_t norm_check(const gdn_norm_t* s)
 {
     if (!s) return GDN_ERR_NULL;
     if (!io_ok(s->io) || (s->res != GDN_F32 && s->res != s->io) || (s->out != s->io && s->out != GDN_E4M3)) return GDN_ERR_MODE;
-    if (s->N < 0 || s->D < 8 || s->D > 16384 || s->D % 8 || !(s->eps >= 0.f)) return GDN_ERR_SHAPE;
+    if (s->N < 0 || s->N > kMostRows || s->D < 8 || s->D > 16384 || s->D % 8 || !(s->eps >= 0.f)) return GDN_ERR_SHAPE;
     if (s->group != 0 && s->group != 32 && s->group != 64 && s->group != 128) return GDN_ERR_SHAPE;
     return s->group && (s->D % s->group || s->out != GDN_E4M3) ? GDN_ERR_SHAPE : GDN_OK;
 }
@@ -44,7 +46,7 @@ gdn_status_t conv_check(const gdn_conv_t* s)
 {
     if (!s) return GDN_ERR_NULL;
     if (!io_ok(s->io)) return GDN_ERR_MODE;
-    if (!conv_ok(s->B, s->D, s->W) || s->T < 0 || s->rows < 0 || (s->rows > 0 && s->T < 1)) return GDN_ERR_SHAPE;
+    if (!conv_ok(s->B, s->D, s->W) || s->T < 0 || s->rows < 0 || s->rows > kMostRows || (s->rows > 0 && s->T < 1)) return GDN_ERR_SHAPE;
     return GDN_OK;
 }
 
@@ -52,7 +54,7 @@ gdn_status_t scan_check(const gdn_scan_t* s)
 {
     if (!s) return GDN_ERR_NULL;
     if (!io_ok(s->io)) return GDN_ERR_MODE;
-    if (!scan_ok(s->B, s->D, s->N, s->G) || s->T < 0 || s->rows < 0 || (s->rows > 0 && s->T < 1)) return GDN_ERR_SHAPE;
+    if (!scan_ok(s->B, s->D, s->N, s->G) || s->T < 0 || s->rows < 0 || s->rows > kMostRows || (s->rows > 0 && s->T < 1)) return GDN_ERR_SHAPE;
     return GDN_OK;
 }
 

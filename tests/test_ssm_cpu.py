@@ -64,7 +64,7 @@ def norm_bwd(s, **kw):
 
 def test_norm_refusals():
     refused(norm_fwd(None), NULL)
-    for bad, want in ((dict(N=-1), SHAPE), (dict(D=0), SHAPE), (dict(D=12), SHAPE), (dict(D=16392), SHAPE), (dict(eps=-1.0), SHAPE),
+    for bad, want in ((dict(N=-1), SHAPE), (dict(N=(1 << 30) + 1), SHAPE), (dict(D=0), SHAPE), (dict(D=12), SHAPE), (dict(D=16392), SHAPE), (dict(eps=-1.0), SHAPE),
                       (dict(eps=math.nan), SHAPE), (dict(io=7), MODE), (dict(res=7), MODE), (dict(out=7), MODE), (dict(out="f32"), MODE),
                       (dict(io="f32", res="bf16"), MODE), (dict(out="e4m3", group=16), SHAPE), (dict(out="e4m3", D=264, group=128), SHAPE),
                       (dict(group=128), SHAPE), (dict(out="e4m3", group=-32), SHAPE)):
@@ -118,7 +118,7 @@ def conv(backward, s, **kw):
 def test_conv_refusals(backward):
     refused(conv(backward, None), NULL)
     for bad, want in ((dict(B=0), SHAPE), (dict(B=65536, rows=66), SHAPE), (dict(D=4), SHAPE), (dict(D=0), SHAPE), (dict(W=1), SHAPE),
-                      (dict(W=5), SHAPE), (dict(T=-1), SHAPE), (dict(T=0, rows=5), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=65), SHAPE),
+                      (dict(W=5), SHAPE), (dict(T=-1), SHAPE), (dict(T=0, rows=5), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=65), SHAPE), (dict(rows=(1 << 30) + 1), SHAPE), (dict(D=(1 << 24) + 8), SHAPE),
                       (dict(io=3), MODE)):
         refused(conv(backward, gdn.make_conv(**{**CONV, **bad})), want)
         if bad != dict(rows=65):                            # with offsets any number of rows will do
@@ -194,7 +194,7 @@ def test_scan_refusals(backward):
     refused(scan(backward, None), NULL)
     for bad, want in ((dict(B=0), SHAPE), (dict(B=65536, rows=66), SHAPE), (dict(N=0), SHAPE), (dict(N=12), SHAPE), (dict(N=72), SHAPE),
                       (dict(G=0), SHAPE), (dict(G=3), SHAPE), (dict(D=72), SHAPE), (dict(D=0), SHAPE), (dict(T=-1), SHAPE),
-                      (dict(T=0, rows=3), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=67), SHAPE), (dict(D=1 << 26), SHAPE),
+                      (dict(T=0, rows=3), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=67), SHAPE), (dict(rows=(1 << 30) + 1), SHAPE), (dict(D=1 << 26), SHAPE),
                       (dict(io=9), MODE)):
         refused(scan(backward, gdn.make_scan(**{**SCAN, **bad})), want)
         if bad != dict(rows=67):
