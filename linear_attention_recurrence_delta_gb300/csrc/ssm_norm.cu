@@ -1,7 +1,10 @@
 // ssm_norm.cu -- residual addition and RMS norm, in the I/O type or in 8 bits, with the gradients.
 //
 // y = s / sqrt(mean s^2 + eps) w of s = x + res.  Each value is read once and written once, so HBM bounds it: a row
-// stays in the registers of its threads, 8 values a piece, between the sum over it and the results.
+// stays in the registers of its threads, 8 values a piece, between the sum over it and the results.  32768 rows of 2048 bf16
+// values: 75 us forwards (537 MB, 81 % of DRAM's time), 93 us for the gradients (the next row asked for ahead; 187 without) and
+// 6 for the sum of dw's shares.  5371 rows of 4096 with a 32-bit residual, in 8 bits: 40 us (243 MB); two pieces a thread and
+// more threads a row, not four (46 us), because more warps then wait for memory.
 #include <cuda_fp8.h>
 
 #include "ssm_common.cuh"
