@@ -80,15 +80,32 @@ def make_scan_step(B, T, D, N, slots, G=1, io="bf16", softplus=True):
     return gdn_scan_step_t(int(B), int(T), int(D), int(N), int(G), int(bool(softplus)), _IO.get(io, io), int(slots))
 
 
-_F32 = _I32 = _DTYPE = _device = None      # torch's types; by gdn_dtype_t (and GDN_E4M3); the current device
+_F32 = _I32 = None      # torch's types, from here on known when the library is loaded
+_DTYPE = {}             # by gdn_dtype_t (and GDN_E4M3)
+_device = _raw_stream = None      # the current device, and its current stream without a Stream object around it
+
+
+class _Functions(dict):
+    """The library's functions by name: loads it when the first one is asked for."""
+
+    def __missing__(self, name):
+        self[name] = f = getattr(load(), name)
+        return f
+
+
+_FN = _Functions()
 
 
 def declare(lib):
     """Signatures of the library's functions (called once, when it is loaded)."""
-    global _F32, _I32, _DTYPE, _device
+    global _F32, _I32, _device, _raw_stream
     import torch
-    _F32, _I32, _device = torch.float32, torch.int32, torch._C._cuda_getDevice if torch.cuda.is_available() else lambda: -1
-    _DTYPE = {0: torch.float32, 1: torch.bfloat16, GDN_E4M3: torch.float8_e4m3fn}
+    _F32, _I32 = torch.float32, torch.int32
+    _DTYPE.update({0: torch.float32, 1: torch.bfloat16, GDN_E4M3: torch.float8_e4m3fn})
+    if torch.cuda.is_available():
+        _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    else:
+        _device, _raw_stream = lambda: -1, lambda dev: 0
     vp, ll, sz, vw, i = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_size_t, ctypes.POINTER(gdn_mla_view_t), ctypes.c_int
     n, c, cs, s, ss = (ctypes.POINTER(t) for t in (gdn_norm_t, gdn_conv_t, gdn_conv_step_t, gdn_scan_t, gdn_scan_step_t))
     for name, args, res in (
@@ -115,7 +132,7 @@ def _elsewhere(t):
     raise ValueError(f"a tensor on the current CUDA device ({_device()}) is wanted here, not on {t.device}")
 
 
-def _flat(t, dtype):
+def _flat(t, dtype, dev):
     """[rows, D] or [B, T, D] by reference."""
     if t is None:
         return None
@@ -123,7 +140,7 @@ def _flat(t, dtype):
         return _ref(t)
     if t.dtype is not dtype:
         _typed(t, dtype)
-    if t.get_device() != _device():
+    if t.get_device() != dev:
         _elsewhere(t)
     s = t.stride()
     if len(s) == 2 and s[1] == 1 and s[0] % 8 == 0 and s[0] > 0:
@@ -131,7 +148,7 @@ def _flat(t, dtype):
     return _ref(_view(t, heads=False))
 
 
-def _vectors(t, dtype):
+def _vectors(t, dtype, dev):
     """[rows, G, N] or [B, T, G, N] by reference."""
     if t is None:
         return None
@@ -139,7 +156,7 @@ def _vectors(t, dtype):
         return _ref(t)
     if t.dtype is not dtype:
         _typed(t, dtype)
-    if t.get_device() != _device():
+    if t.get_device() != dev:
         _elsewhere(t)
     s = t.stride()
     if len(s) == 3 and s[2] == 1 and s[0] % 8 == 0 and s[0] > 0:
@@ -147,7 +164,7 @@ def _vectors(t, dtype):
     return _ref(_view(t))
 
 
-def _rows(t, dtype):
+def _rows(t, dtype, dev):
     """[rows, D] as (address, row stride)."""
     if t is None:
         return None, 0
@@ -155,7 +172,7 @@ def _rows(t, dtype):
         return t.p, t.tok
     if t.dtype is not dtype:
         _typed(t, dtype)
-    if t.get_device() != _device():
+    if t.get_device() != dev:
         _elsewhere(t)
     s = t.stride()
     if len(s) == 2 and s[1] == 1 and s[0] % 8 == 0 and s[0] > 0:
@@ -164,31 +181,32 @@ def _rows(t, dtype):
     return v.p, v.tok
 
 
-def _dense(t, dtype):
+def _dense(t, dtype, dev):
     """The address of a contiguous tensor."""
     if t is None or type(t) is int:
         return t
     if t.dtype is not dtype:
         _typed(t, dtype)
-    if t.get_device() != _device():
+    if t.get_device() != dev:
         _elsewhere(t)
     if not t.is_contiguous():
         raise ValueError("weights, states, scales, offsets and slots are contiguous")
     return t.data_ptr()
 
 
-def _area(t, n):
+def _area(t, n, dev):
     """A workspace's address and bytes."""
-    if t is not None and type(t) is not int and t.get_device() != _device():
+    if t is not None and type(t) is not int and t.get_device() != dev:
         _elsewhere(t)
     return _ptr(t), _nbytes(t) if n is None and t is not None else (n or 0)
 
 
 def gdn_norm_fwd(shape, x, res, w, y, scale, sum_out, stream=None) -> int:
     """y (and scale, with an 8-bit y) of x + res, which goes to sum_out if given (it may be res itself)."""
-    f, d, r = load().gdn_norm_fwd, _DTYPE.get(shape.io), _DTYPE.get(shape.res)
-    return f(_ref(shape), *_rows(x, d), *_rows(res, r), _dense(w, _F32), *_rows(y, _DTYPE.get(shape.out)),
-             _dense(scale, _F32), *_rows(sum_out, r), _stream(stream))
+    f, d, r, dev = _FN["gdn_norm_fwd"], _DTYPE.get(shape.io), _DTYPE.get(shape.res), _device()
+    return f(_ref(shape), *_rows(x, d, dev), *_rows(res, r, dev), _dense(w, _F32, dev),
+             *_rows(y, _DTYPE.get(shape.out), dev), _dense(scale, _F32, dev), *_rows(sum_out, r, dev),
+             _raw_stream(dev) if stream is None else _stream(stream))
 
 
 def gdn_norm_workspace_bytes(shape) -> int:
@@ -197,16 +215,18 @@ def gdn_norm_workspace_bytes(shape) -> int:
 
 def gdn_norm_bwd(shape, s, w, dy, dsum, dx, dres, dw, ws, ws_bytes=None, stream=None) -> int:
     """From the forward's sum `s`: dx (io), dres (the residual's type) and dw [D] fp32; dsum is the sum's own gradient."""
-    f, d, r = load().gdn_norm_bwd, _DTYPE.get(shape.io), _DTYPE.get(shape.res)
-    return f(_ref(shape), *_rows(s, r), _dense(w, _F32), *_rows(dy, d), *_rows(dsum, r), *_rows(dx, d),
-             *_rows(dres, r), _dense(dw, _F32), *_area(ws, ws_bytes), _stream(stream))
+    f, d, r, dev = _FN["gdn_norm_bwd"], _DTYPE.get(shape.io), _DTYPE.get(shape.res), _device()
+    return f(_ref(shape), *_rows(s, r, dev), _dense(w, _F32, dev), *_rows(dy, d, dev), *_rows(dsum, r, dev),
+             *_rows(dx, d, dev), *_rows(dres, r, dev), _dense(dw, _F32, dev), *_area(ws, ws_bytes, dev),
+             _raw_stream(dev) if stream is None else _stream(stream))
 
 
 def gdn_conv_fwd(shape, x, w, bias, cu, s0, y, sT, stream=None) -> int:
     """y and, if given, the sequences' new states sT [B, W - 1, D]."""
-    f, d = load().gdn_conv_fwd, _DTYPE.get(shape.io)
-    return f(_ref(shape), _flat(x, d), _dense(w, _F32), _dense(bias, _F32), _dense(cu, _I32), _dense(s0, d),
-             _flat(y, d), _dense(sT, d), _stream(stream))
+    f, d, dev = _FN["gdn_conv_fwd"], _DTYPE.get(shape.io), _device()
+    return f(_ref(shape), _flat(x, d, dev), _dense(w, _F32, dev), _dense(bias, _F32, dev), _dense(cu, _I32, dev),
+             _dense(s0, d, dev), _flat(y, d, dev), _dense(sT, d, dev),
+             _raw_stream(dev) if stream is None else _stream(stream))
 
 
 def gdn_conv_workspace_bytes(shape) -> int:
@@ -215,17 +235,19 @@ def gdn_conv_workspace_bytes(shape) -> int:
 
 def gdn_conv_bwd(shape, x, w, bias, cu, s0, dy, dsT, dx, dw, dbias, ds0, ws, ws_bytes=None, stream=None) -> int:
     """The gradients of x, w [D, W], bias [D] and, if given, s0."""
-    f, d = load().gdn_conv_bwd, _DTYPE.get(shape.io)
-    return f(_ref(shape), _flat(x, d), _dense(w, _F32), _dense(bias, _F32), _dense(cu, _I32), _dense(s0, d),
-             _flat(dy, d), _dense(dsT, d), _flat(dx, d), _dense(dw, _F32), _dense(dbias, _F32), _dense(ds0, d),
-             *_area(ws, ws_bytes), _stream(stream))
+    f, d, dev = _FN["gdn_conv_bwd"], _DTYPE.get(shape.io), _device()
+    return f(_ref(shape), _flat(x, d, dev), _dense(w, _F32, dev), _dense(bias, _F32, dev), _dense(cu, _I32, dev),
+             _dense(s0, d, dev), _flat(dy, d, dev), _dense(dsT, d, dev), _flat(dx, d, dev), _dense(dw, _F32, dev),
+             _dense(dbias, _F32, dev), _dense(ds0, d, dev), *_area(ws, ws_bytes, dev),
+             _raw_stream(dev) if stream is None else _stream(stream))
 
 
 def gdn_conv_step(shape, x, w, bias, state, src, dst, y, stream=None) -> int:
     """y [B * T, D] of new tokens; state [slots, W - 1, D] is read at src [B] and written at dst [B] (None: src; None: b)."""
-    f, d = load().gdn_conv_step, _DTYPE.get(shape.io)
-    return f(_ref(shape), _flat(x, d), _dense(w, _F32), _dense(bias, _F32), _dense(state, d), _dense(src, _I32),
-             _dense(dst, _I32), _flat(y, d), _stream(stream))
+    f, d, dev = _FN["gdn_conv_step"], _DTYPE.get(shape.io), _device()
+    return f(_ref(shape), _flat(x, d, dev), _dense(w, _F32, dev), _dense(bias, _F32, dev), _dense(state, d, dev),
+             _dense(src, _I32, dev), _dense(dst, _I32, dev), _flat(y, d, dev),
+             _raw_stream(dev) if stream is None else _stream(stream))
 
 
 def gdn_scan_workspace_bytes(shape, backward) -> int:
@@ -240,26 +262,29 @@ def gdn_scan_saved_bytes(shape) -> int:
 def gdn_scan_fwd(shape, x, dt, z, Bm, Cm, A_log, D, dt_bias, cu, h0, y, hT, saved, ws, saved_bytes=None, ws_bytes=None,
                  stream=None) -> int:
     """y and, if given, the sequences' last states hT [B, D, N] and what gdn_scan_bwd needs (`saved`)."""
-    f, d = load().gdn_scan_fwd, _DTYPE.get(shape.io)
-    return f(_ref(shape), _flat(x, d), _flat(dt, d), _flat(z, d), _vectors(Bm, d), _vectors(Cm, d),
-             _dense(A_log, _F32), _dense(D, _F32), _dense(dt_bias, _F32), _dense(cu, _I32), _dense(h0, _F32),
-             _flat(y, d), _dense(hT, _F32), *_area(saved, saved_bytes), *_area(ws, ws_bytes), _stream(stream))
+    f, d, dev = _FN["gdn_scan_fwd"], _DTYPE.get(shape.io), _device()
+    return f(_ref(shape), _flat(x, d, dev), _flat(dt, d, dev), _flat(z, d, dev), _vectors(Bm, d, dev), _vectors(Cm, d, dev),
+             _dense(A_log, _F32, dev), _dense(D, _F32, dev), _dense(dt_bias, _F32, dev), _dense(cu, _I32, dev),
+             _dense(h0, _F32, dev), _flat(y, d, dev), _dense(hT, _F32, dev), *_area(saved, saved_bytes, dev),
+             *_area(ws, ws_bytes, dev), _raw_stream(dev) if stream is None else _stream(stream))
 
 
 def gdn_scan_bwd(shape, x, dt, z, Bm, Cm, A_log, D, dt_bias, cu, saved, dy, dhT, dx, ddt, dz, dBm, dCm, dA_log, dD, ddt_bias, dh0,
                  ws, saved_bytes=None, ws_bytes=None, stream=None) -> int:
     """The gradients of every input from dy, dhT and the forward's `saved`."""
-    f, d = load().gdn_scan_bwd, _DTYPE.get(shape.io)
-    return f(_ref(shape), _flat(x, d), _flat(dt, d), _flat(z, d), _vectors(Bm, d), _vectors(Cm, d),
-             _dense(A_log, _F32), _dense(D, _F32), _dense(dt_bias, _F32), _dense(cu, _I32),
-             *_area(saved, saved_bytes), _flat(dy, d), _dense(dhT, _F32), _flat(dx, d), _flat(ddt, d), _flat(dz, d),
-             _vectors(dBm, d), _vectors(dCm, d), _dense(dA_log, _F32), _dense(dD, _F32), _dense(ddt_bias, _F32),
-             _dense(dh0, _F32), *_area(ws, ws_bytes), _stream(stream))
+    f, d, dev = _FN["gdn_scan_bwd"], _DTYPE.get(shape.io), _device()
+    return f(_ref(shape), _flat(x, d, dev), _flat(dt, d, dev), _flat(z, d, dev), _vectors(Bm, d, dev), _vectors(Cm, d, dev),
+             _dense(A_log, _F32, dev), _dense(D, _F32, dev), _dense(dt_bias, _F32, dev), _dense(cu, _I32, dev),
+             *_area(saved, saved_bytes, dev), _flat(dy, d, dev), _dense(dhT, _F32, dev), _flat(dx, d, dev),
+             _flat(ddt, d, dev), _flat(dz, d, dev), _vectors(dBm, d, dev), _vectors(dCm, d, dev), _dense(dA_log, _F32, dev),
+             _dense(dD, _F32, dev), _dense(ddt_bias, _F32, dev), _dense(dh0, _F32, dev), *_area(ws, ws_bytes, dev),
+             _raw_stream(dev) if stream is None else _stream(stream))
 
 
 def gdn_scan_step(shape, x, dt, z, Bm, Cm, A_log, D, dt_bias, state, src, dst, y, stream=None) -> int:
     """y [B * T, D] of new tokens; state [slots, D, N] fp32 is read at src [B] and written at dst [B] (None: src; None: b)."""
-    f, d = load().gdn_scan_step, _DTYPE.get(shape.io)
-    return f(_ref(shape), _flat(x, d), _flat(dt, d), _flat(z, d), _vectors(Bm, d), _vectors(Cm, d),
-             _dense(A_log, _F32), _dense(D, _F32), _dense(dt_bias, _F32), _dense(state, _F32), _dense(src, _I32),
-             _dense(dst, _I32), _flat(y, d), _stream(stream))
+    f, d, dev = _FN["gdn_scan_step"], _DTYPE.get(shape.io), _device()
+    return f(_ref(shape), _flat(x, d, dev), _flat(dt, d, dev), _flat(z, d, dev), _vectors(Bm, d, dev), _vectors(Cm, d, dev),
+             _dense(A_log, _F32, dev), _dense(D, _F32, dev), _dense(dt_bias, _F32, dev), _dense(state, _F32, dev),
+             _dense(src, _I32, dev), _dense(dst, _I32, dev), _flat(y, d, dev),
+             _raw_stream(dev) if stream is None else _stream(stream))
