@@ -2,9 +2,9 @@
 //
 // pre[t] = bias + sum_k w[k] x[t - W + 1 + k], y = silu(pre).  A thread walks a strip of time for four neighbouring
 // channels with the last rows in registers, in rings of four whose turning the unrolled loop knows, so that a row is read
-// once (and W - 1 rows more a strip, from L2).  HBM bounds it, once four rows are asked for ahead, the arithmetic is packed
-// and no row within a strip has a branch: 8 x 4096 rows of 2048 channels, four taps, take 51 us forwards (268 MB; 71 with
-// eight channels a thread and a test a row) and 89 us back (403 MB; 252 with a row at a time), 5 for the sums of the shares.
+// once (and W - 1 rows more a strip, from L2).  HBM bounds it, once rows are asked for well ahead, the arithmetic is packed
+// and no row within a strip has a branch: 8 x 4096 rows of 2048 channels, four taps, take 50 us forwards (268 MB; 71 with
+// eight channels a thread and a test a row) and 86 us back (403 MB; 252 with a row at a time), 5 for the sums of the shares.
 #include "ssm_common.cuh"
 
 namespace gdn {
@@ -50,6 +50,37 @@ __device__ __forceinline__ void step8(const float (&taps)[W][8], const float (&b
     }
 }
 
+// Rows on their way to a thread: groups of four rows of its own four channels, by cp.async into a ring of its own in shared
+// memory, so that what is in flight takes no registers and no thread waits for another.  Three groups ahead with bf16 (138 us
+// for 8 x 4096 rows of 2048 channels both ways, 150 with one group ahead or with four rows in registers, 164 with seven groups
+// and fewer CTAs), one with f32, whose rows are twice the bytes.
+template <typename IO, int THREADS>
+struct Rows4 {
+    static constexpr int GROUPS = sizeof(IO) == 2 ? 4 : 2;
+    Raw4<IO> v[GROUPS][4][THREADS];
+    __device__ __forceinline__ static void copy(Raw4<IO>* to, const IO* from)
+    {
+        const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+        if (sizeof(IO) == 2) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(s), "l"(from) : "memory");
+        else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+    }
+    // rows t .. t + 3 of p, those before `end`
+    __device__ __forceinline__ void ask(const IO* p, long long tok, int t, int end)
+    {
+        Raw4<IO>* to = &v[(t >> 2) & (GROUPS - 1)][0][threadIdx.x];
+        if (t + 4 <= end)
+#pragma unroll
+            for (int j = 0; j < 4; j++) copy(to + j * THREADS, p + (t + j) * tok);
+        else
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                if (t + j < end) copy(to + j * THREADS, p + (t + j) * tok);
+    }
+    __device__ __forceinline__ Raw4<IO> get(int t, int j) const { return v[(t >> 2) & (GROUPS - 1)][j][threadIdx.x]; }
+    // the oldest group, if GROUPS - 1 have been asked for
+    __device__ __forceinline__ static void arrived() { asm volatile("cp.async.wait_group %0;" ::"n"(GROUPS - 2) : "memory"); }
+};
+
 template <int W>
 __device__ __forceinline__ void load_taps(const float* w, Four (&t)[W])
 {
@@ -89,37 +120,33 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a)
     Four taps[W], bias = all(0.f), ring[4];
     load_taps<W>(a.w + (long long)c * W, taps);
     if (a.bias) bias = raw4(a.bias + c).get();
-    Raw4<IO> next[4];
-    auto ask = [&](int t) {      // without a branch a row where all are there
-        if (t + 4 <= end)
-#pragma unroll
-            for (int j = 0; j < 4; j++) next[j] = raw4(x + (long long)(t + j) * a.x.tok);
-        else
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                if (t + j < end) next[j] = raw4(x + (long long)(t + j) * a.x.tok);
-    };
-    auto row = [&](int t, int j, const Raw4<IO>& v) {
-        ring[j & 3] = v.get();
+    using Ring = Rows4<IO, kThreads>;
+    __shared__ Ring rows;
+    auto row = [&](int t, int j) {
+        ring[j] = rows.get(t, j).get();
         Four p = bias;
 #pragma unroll
         for (int k = 0; k < W; k++) p = fma(taps[k], ring[(j + 5 - W + k) & 3], p);
         put(y + (long long)(t + j) * a.y.tok, SILU ? mul(p, sigmoid4(p)) : p);
     };
-    ask(t0);
+#pragma unroll
+    for (int g = 0; g < Ring::GROUPS - 1; g++) {
+        rows.ask(x, a.x.tok, t0 + 4 * g, end);
+        rec::cp_async_commit();
+    }
     load_past<IO, W>(x, a.x.tok, a.s0, b, D, c, t0, ring);
     int t = t0;
     for (; t + 4 <= end; t += 4) {
-        Raw4<IO> now[4];
+        Ring::arrived();
+        rows.ask(x, a.x.tok, t + 4 * (Ring::GROUPS - 1), end);
+        rec::cp_async_commit();
 #pragma unroll
-        for (int j = 0; j < 4; j++) now[j] = next[j];
-        ask(t + 4);
-#pragma unroll
-        for (int j = 0; j < 4; j++) row(t, j, now[j]);
+        for (int j = 0; j < 4; j++) row(t, j);
     }
+    rec::cp_async_wait_all();
 #pragma unroll
     for (int j = 0; j < 3; j++)
-        if (t + j < end) row(t, j, next[j]);
+        if (t + j < end) row(t, j);
     if (!a.sT || end != r.n) return;
     // the last W - 1 rows: in the ring by their number modulo 4
 #pragma unroll
@@ -170,6 +197,8 @@ template <typename IO, int W, bool SILU>
 __global__ void __launch_bounds__(kBackThreads, 4) conv_bwd_kernel(const ConvArgs a, int l)
 {
     __shared__ float4 share[kBackThreads];
+    using Ring = Rows4<IO, kBackThreads>;
+    __shared__ Ring rx, ry;
     const int D = a.s.D, tx = threadIdx.x & ((1 << l) - 1), ty = threadIdx.x >> l, strips = kBackThreads >> l;
     const int c = 4 * ((blockIdx.x << l) + tx);
     const int each = a.s.T > 0 ? (a.s.T + kBackStrip - 1) / kBackStrip : 1;      // strips of a sequence
@@ -190,26 +219,15 @@ __global__ void __launch_bounds__(kBackThreads, 4) conv_bwd_kernel(const ConvArg
         const IO* dy = (const IO*)a.dy.p + (long long)r.first * a.dy.tok + c;
         IO* dx = (IO*)a.dx.p + (long long)r.first * a.dx.tok + c;
         Four ring[4], d[4];                          // rows of x and of dpre, by their number modulo 4
-        Raw4<IO> nx[4], ny[4];
         const int seen = min(r.n, end + W - 1);      // rows that it reads end here
         auto ask = [&](int t) {
-            if (t + 4 <= seen)
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    nx[j] = raw4(x + (long long)(t + j) * a.x.tok);
-                    ny[j] = raw4(dy + (long long)(t + j) * a.dy.tok);
-                }
-            else
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    if (t + j < seen) {
-                        nx[j] = raw4(x + (long long)(t + j) * a.x.tok);
-                        ny[j] = raw4(dy + (long long)(t + j) * a.dy.tok);
-                    }
+            rx.ask(x, a.x.tok, t, seen);
+            ry.ask(dy, a.dy.tok, t, seen);
+            rec::cp_async_commit();
         };
-        auto pre = [&](int j, const Raw4<IO>& vx, const Raw4<IO>& vy) {      // d[j] of a row of the sequence
-            ring[j] = vx.get();
-            d[j] = vy.get();
+        auto pre = [&](int t, int j) {               // d[j] of a row of the sequence
+            ring[j] = rx.get(t, j).get();
+            d[j] = ry.get(t, j).get();
             if (!SILU) return;
             Four p = bias;
 #pragma unroll
@@ -229,12 +247,14 @@ __global__ void __launch_bounds__(kBackThreads, 4) conv_bwd_kernel(const ConvArg
             return o;
         };
         auto edge = [&](int t) {                     // rows t .. t + 3 at an end of the strip, whatever holds of them
+            Ring::arrived();
+            ask(t + 4 * (Ring::GROUPS - 1));
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 if (t + j >= end + W - 1) break;
                 d[j] = all(0.f);
                 if (t + j < r.n) {
-                    pre(j, nx[j], ny[j]);
+                    pre(t, j);
                     if (t + j < end) own(j);
                 }
                 const int row = t + j - (W - 1), kept = row - (r.n - (W - 1));      // kept: its place in the new state
@@ -244,20 +264,21 @@ __global__ void __launch_bounds__(kBackThreads, 4) conv_bwd_kernel(const ConvArg
                 if (row >= 0) put(dx + (long long)row * a.dx.tok, o);
                 else put((IO*)a.ds0 + ((long long)b * (W - 1) + row + W - 1) * D + c, o);
             }
-            ask(t + 4);
         };
-        ask(t0);
+        rec::cp_async_wait_all();                    // of the last strip
+#pragma unroll
+        for (int g = 0; g < Ring::GROUPS - 1; g++) ask(t0 + 4 * g);
         load_past<IO, W>(x, a.x.tok, a.s0, b, D, c, t0, ring);
 #pragma unroll
         for (int k = 0; k < 4; k++) d[k] = all(0.f);
         edge(t0);
         int t = t0 + 4;
         for (; t + 4 <= end; t += 4) {               // rows within the strip, which end before the sequence does
-            const Raw4<IO> cx[4] = {nx[0], nx[1], nx[2], nx[3]}, cy[4] = {ny[0], ny[1], ny[2], ny[3]};
-            ask(t + 4);
+            Ring::arrived();
+            ask(t + 4 * (Ring::GROUPS - 1));
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                pre(j, cx[j], cy[j]);
+                pre(t, j);
                 own(j);
                 put(dx + (long long)(t + j - (W - 1)) * a.dx.tok, gradient(j));
             }
