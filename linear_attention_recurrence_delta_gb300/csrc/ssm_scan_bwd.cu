@@ -99,36 +99,14 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
     const float bias = in && a.dt_bias ? a.dt_bias[p.d0 + oc] : 0.f, skip = !FIRST && in && a.D_skip ? a.D_skip[p.d0 + oc] : 0.f;
     Sum dskip, dbias;
 
-    // asks for a tile: zeros from the segment's end on, past the warp's channels and past N
+    // asks for a tile
     auto ask = [&](int t0, int buf) {
-        constexpr int PER = L::CH * sizeof(IO) / 16, UNIT = 16 / sizeof(IO);
-        auto rows = [&](const gdn_mla_view_t& v, IO (*to)[L::CH]) {
-#pragma unroll
-            for (int u0 = 0; u0 < K * PER; u0 += 32) {
-                const int u = u0 + lane, j = u / PER, c = u % PER * UNIT;
-                if (u < K * PER) {
-                    const bool ok = t0 + j < p.t1 && c < p.channels;
-                    cp_async16_zero(&to[j][c], (const IO*)v.p + (ok ? (long long)(p.r.first + t0 + j) * v.tok + p.d0 + c : 0), ok);
-                }
-            }
-        };
-        rows(a.dt, S.rows[buf][1]);
-        rows(a.dy, S.rows[buf][3]);
-        if (gated) rows(a.z, S.rows[buf][2]);
-        if (!FIRST) rows(a.x, S.rows[buf][0]);
-        auto vectors = [&](const gdn_mla_view_t& v, IO (*to)[NS]) {
-            constexpr int PERV = NS * sizeof(IO) / 16;
-#pragma unroll
-            for (int u0 = 0; u0 < K * PERV; u0 += 32) {
-                const int u = u0 + lane, j = u / PERV, m = u % PERV * UNIT;
-                if (u < K * PERV) {
-                    const bool ok = t0 + j < p.t1 && m < N;
-                    cp_async16_zero(&to[j][m], (const IO*)v.p + (ok ? (long long)(p.r.first + t0 + j) * v.tok + p.g * v.head + m : 0), ok);
-                }
-            }
-        };
-        if (!FIRST) vectors(a.Bm, S.vectors[buf][0]);
-        vectors(a.Cm, S.vectors[buf][1]);
+        ask_rows<L>(a.dt, p, t0, lane, S.rows[buf][1]);
+        ask_rows<L>(a.dy, p, t0, lane, S.rows[buf][3]);
+        if (gated) ask_rows<L>(a.z, p, t0, lane, S.rows[buf][2]);
+        if (!FIRST) ask_rows<L>(a.x, p, t0, lane, S.rows[buf][0]);
+        if (!FIRST) ask_vectors<L>(a.Bm, p, N, t0, lane, S.vectors[buf][0]);
+        ask_vectors<L>(a.Cm, p, N, t0, lane, S.vectors[buf][1]);
         if (!FIRST && p.channels > 0) {
             const float4* h = reinterpret_cast<const float4*>(a.saved) + saved_at<F>(a, p, t0);
 #pragma unroll
@@ -177,19 +155,8 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
             ux[i] = FIRST ? 0.f : w[i] * rec::to_f(S.rows[buf][0][i * OT + ot][oc]);
             if (FIRST) sum += w[i];
         }
-#pragma unroll
-        for (int u0 = 0; u0 < K * NS / 8; u0 += 32) {
-            const int u = u0 + lane;
-            if (u < K * NS / 8) {
-                float v[8];
-                load8(&S.vectors[buf][1][0][0] + 8 * u, v);
-                store8(&S.C[0][0] + 8 * u, v);
-                if (!FIRST) {
-                    load8(&S.vectors[buf][0][0][0] + 8 * u, v);
-                    store8(&S.B[0][0] + 8 * u, v);
-                }
-            }
-        }
+        widen<L>(S.vectors[buf][1], S.C, lane);
+        if (!FIRST) widen<L>(S.vectors[buf][0], S.B, lane);
         __syncwarp();
         if (FIRST) {
 #pragma unroll

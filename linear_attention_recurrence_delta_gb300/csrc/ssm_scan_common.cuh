@@ -96,54 +96,48 @@ __device__ __forceinline__ void store_if(bool ok, __nv_bfloat16* p, float x)
     asm volatile("{ .reg .pred q; setp.ne.b32 q, %2, 0; @q st.global.b16 [%0], %1; }" ::"l"(p), "h"(*reinterpret_cast<const unsigned short*>(&v)), "r"((int)ok) : "memory");
 }
 
-// A tile of what a lane owns of a tensor: zeros from the segment's end on and past the warp's channels.
+// A tile's rows of a tensor, or of the write or read vectors, asked for by cp.async: as they lie in memory, zeros from the
+// segment's end on, past the warp's channels and past N.
 template <class L, typename IO>
-struct Column {
-    IO v[L::OWN];
-    __device__ __forceinline__ void load(const gdn_mla_view_t& view, const Spot& p, int t0, int lane)
-    {
-        const int oc = lane % L::CH, ot = lane / L::CH;
-        const IO* src = (const IO*)view.p + (long long)(p.r.first + t0 + ot) * view.tok + p.d0 + oc;
-        const bool in = p.has(oc);
-        if (t0 + kTile <= p.t1) {
+__device__ __forceinline__ void ask_rows(const gdn_mla_view_t& v, const Spot& p, int t0, int lane, IO (*to)[L::CH])
+{
+    constexpr int PER = L::CH * sizeof(IO) / 16, UNIT = 16 / sizeof(IO);
 #pragma unroll
-            for (int i = 0; i < L::OWN; i++) v[i] = in ? src[i * L::OT * view.tok] : rec::from_f<IO>(0.f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < L::OWN; i++) v[i] = in && t0 + i * L::OT + ot < p.t1 ? src[i * L::OT * view.tok] : rec::from_f<IO>(0.f);
+    for (int u0 = 0; u0 < kTile * PER; u0 += 32) {
+        const int u = u0 + lane, j = u / PER, c = u % PER * UNIT;
+        if (u < kTile * PER) {
+            const bool ok = t0 + j < p.t1 && c < p.channels;
+            cp_async16_zero(&to[j][c], (const IO*)v.p + (ok ? (long long)(p.r.first + t0 + j) * v.tok + p.d0 + c : 0), ok);
         }
     }
-};
-
-// A tile's write or read vectors, kTile tokens of NS values, in pieces of 8.
+}
 template <class L, typename IO>
-struct Vectors {
-    static constexpr int PER = L::NS / 8, PIECES = kTile * PER, V = (PIECES + 31) / 32;
-    Raw8<IO> raw[V];
-    // asked for: zeros from the segment's end on and past N
-    __device__ __forceinline__ void load(const gdn_mla_view_t& v, const Spot& p, int N, int t0, int lane)
-    {
-        const IO* src = (const IO*)v.p + p.g * v.head;
+__device__ __forceinline__ void ask_vectors(const gdn_mla_view_t& v, const Spot& p, int N, int t0, int lane, IO (*to)[L::NS])
+{
+    constexpr int PER = L::NS * sizeof(IO) / 16, UNIT = 16 / sizeof(IO);
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-            const int u = 32 * i + lane, j = u / PER, c = 8 * (u % PER);
-            raw[i] = Raw8<IO>{};
-            if (u < PIECES && t0 + j < p.t1 && c < N) raw[i] = raw8(src + (long long)(p.r.first + t0 + j) * v.tok + c);
+    for (int u0 = 0; u0 < kTile * PER; u0 += 32) {
+        const int u = u0 + lane, j = u / PER, n = u % PER * UNIT;
+        if (u < kTile * PER) {
+            const bool ok = t0 + j < p.t1 && n < N;
+            cp_async16_zero(&to[j][n], (const IO*)v.p + (ok ? (long long)(p.r.first + t0 + j) * v.tok + p.g * v.head + n : 0), ok);
         }
     }
-    __device__ __forceinline__ void store(float* to, int lane) const
-    {
+}
+// the vectors as fp32
+template <class L, typename IO>
+__device__ __forceinline__ void widen(const IO (*from)[L::NS], float (*to)[L::NS], int lane)
+{
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-            const int u = 32 * i + lane;
-            if (u < PIECES) {
-                float x[8];
-                values(raw[i], x);
-                store8(to + 8 * u, x);
-            }
+    for (int u0 = 0; u0 < kTile * L::NS / 8; u0 += 32) {
+        const int u = u0 + lane;
+        if (u < kTile * L::NS / 8) {
+            float v[8];
+            load8(&from[0][0] + 8 * u, v);
+            store8(&to[0][0] + 8 * u, v);
         }
     }
-};
+}
 
 // where a lane's states of place r lie in [B, D, N], and whether they exist
 template <class L>

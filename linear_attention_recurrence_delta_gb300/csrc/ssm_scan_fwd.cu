@@ -22,6 +22,7 @@ __global__ void __launch_bounds__(32, 16) scan_kernel(const ScanArgs a)
 {
     constexpr int OT = L::OT, OWN = L::OWN, RC = L::RC, H = L::S / 2;
     __shared__ __align__(16) float sB[kTile][L::NS], sC[FIRST ? 1 : kTile][L::NS];
+    __shared__ __align__(16) IO rows[2][FIRST ? 2 : 3][kTile][L::CH], vectors[2][FIRST ? 1 : 2][kTile][L::NS];      // x, dt, z; B, C
     const int lane = threadIdx.x, n = L::S * (lane / L::CL), oc = lane % L::CH, ot = lane / L::CH;
     const Spot p = spot<L, 1>(a);
     if (FIRST && (p.t0 >= p.t1 || p.t1 == p.r.n)) return;      // what a sequence's last segment hands on nobody takes
@@ -39,25 +40,27 @@ __global__ void __launch_bounds__(32, 16) scan_kernel(const ScanArgs a)
     const bool in = p.has(oc), gated = a.z.p != nullptr;
     const float bias = in && a.dt_bias ? a.dt_bias[p.d0 + oc] : 0.f;
     const float skip = !FIRST && in && a.D_skip ? a.D_skip[p.d0 + oc] : 0.f;
-    Column<L, IO> rx, rdt, rz;
-    Vectors<L, IO> rB, rC;
-    auto ask = [&](int t0) {
-        rx.load(a.x, p, t0, lane);
-        rdt.load(a.dt, p, t0, lane);
-        rB.load(a.Bm, p, a.s.N, t0, lane);
+    auto ask = [&](int t0, int buf) {
+        ask_rows<L>(a.x, p, t0, lane, rows[buf][0]);
+        ask_rows<L>(a.dt, p, t0, lane, rows[buf][1]);
+        ask_vectors<L>(a.Bm, p, a.s.N, t0, lane, vectors[buf][0]);
         if (!FIRST) {
-            rC.load(a.Cm, p, a.s.N, t0, lane);
-            if (gated) rz.load(a.z, p, t0, lane);
+            if (gated) ask_rows<L>(a.z, p, t0, lane, rows[buf][FIRST ? 0 : 2]);
+            ask_vectors<L>(a.Cm, p, a.s.N, t0, lane, vectors[buf][FIRST ? 0 : 1]);
         }
+        rec::cp_async_commit();
     };
-    if (p.t0 < p.t1) ask(p.t0);
-    for (int t0 = p.t0; t0 < p.t1; t0 += kTile) {
-        float x[OWN], w[OWN], ux[OWN], z[OWN], y[OWN], slope;
+    if (p.t0 < p.t1) ask(p.t0, 0);
+    int buf = 0;
+    for (int t0 = p.t0; t0 < p.t1; t0 += kTile, buf ^= 1) {
+        rec::cp_async_wait_all();
+        __syncwarp();      // every lane's pieces are there, and the last tile's have been read
+        if (t0 + kTile < p.t1) ask(t0 + kTile, buf ^ 1);
+        float x[OWN], w[OWN], ux[OWN], y[OWN], slope;
 #pragma unroll
         for (int i = 0; i < OWN; i++) {
-            x[i] = rec::to_f(rx.v[i]);
-            if (!FIRST) z[i] = rec::to_f(rz.v[i]);
-            w[i] = rec::to_f(rdt.v[i]) + bias;
+            x[i] = rec::to_f(rows[buf][0][i * OT + ot][oc]);
+            w[i] = rec::to_f(rows[buf][1][i * OT + ot][oc]) + bias;
         }
         if (a.s.softplus)
 #pragma unroll
@@ -71,11 +74,9 @@ __global__ void __launch_bounds__(32, 16) scan_kernel(const ScanArgs a)
             ux[i] = w[i] * x[i];
             if (FIRST) sum += w[i];
         }
-        __syncwarp();      // the last tile's vectors have been read
-        rB.store(&sB[0][0], lane);
-        if (!FIRST) rC.store(&sC[0][0], lane);
+        widen<L>(vectors[buf][0], sB, lane);
+        if (!FIRST) widen<L>(vectors[buf][FIRST ? 0 : 1], sC, lane);
         __syncwarp();
-        if (t0 + kTile < p.t1) ask(t0 + kTile);
         if (!FIRST && a.saved) put_state<L>(reinterpret_cast<float4*>(a.saved) + saved_at<L>(a, p, t0) + state_offset<L>(p.block - p.g * a.blocks, lane), h);
         // exchanges between lanes before and after, so that nothing keeps one token's arithmetic from another's
         float wr[kTile][RC], ur[kTile][RC], part[OWN][OT][RC];
@@ -110,7 +111,10 @@ __global__ void __launch_bounds__(32, 16) scan_kernel(const ScanArgs a)
         for (int i = 0; i < OWN; i++) y[i] = fmaf(skip, x[i], y[i]);
         if (gated)
 #pragma unroll
-            for (int i = 0; i < OWN; i++) y[i] *= z[i] * sigmoid(z[i]);
+            for (int i = 0; i < OWN; i++) {
+                const float z = rec::to_f(rows[buf][FIRST ? 0 : 2][i * OT + ot][oc]);
+                y[i] *= z * sigmoid(z);
+            }
         IO* out = (IO*)a.y.p + (long long)(p.r.first + t0 + ot) * a.y.tok + p.d0 + oc;
 #pragma unroll
         for (int i = 0; i < OWN; i++) store_if(in && t0 + i * OT + ot < p.t1, out + i * OT * a.y.tok, y[i]);
