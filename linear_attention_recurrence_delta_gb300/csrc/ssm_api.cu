@@ -130,10 +130,10 @@ ScanPlan scan_plan(const gdn_scan_t& s, int backward)
     p.ctas = (each + cta - 1) / cta;
     const long long warps = (long long)p.blocks * s.G * s.B, T = s.T < s.rows ? s.T : s.rows;
     // Segments: as many as keep the SMs in warps, counted by the sequences that run at once on average.  Forwards (up to 16 warps an
-    // SM) the first launch is two thirds of the second: 9 prompts up to 1500 tokens take 211 us whole, 154 in 32 segments a
-    // sequence, 8 x 2048 of 2048 channels 300 and 270, one of 16001 2180 and 226.  Backwards (8 warps an SM by their registers)
-    // only where few warps would run: 8 x 2048 tokens take 1009 us whole and 1170 in 3 segments, 2 x 333 of 208 channels
-    // 145 and 82.
+    // SM) the first launch takes three fifths of the second: 9 prompts up to 1500 tokens take 213 us whole and 143 in 16
+    // segments, 8 x 2048 of 2048 channels 301 and 267 in 9, one of 16001 2207 and 215 in 64 (262 in 32).  Backwards (8 warps
+    // an SM by their registers) only where few warps would run: 8 x 2048 tokens take 1009 us whole and 1170 in 3 segments,
+    // 2 x 333 of 208 channels 145 and 82.
     long long seg = T > 0 ? (long long)(152.0 * (backward ? 8 : 32) * T / ((double)p.blocks * s.G * s.rows)) : 1;
     if (seg > T / 32) seg = T / 32;
     if (seg > 64) seg = 64;

@@ -3,12 +3,12 @@
 // h[t] = exp(delta[t] A) h[t-1] + delta[t] x[t] B[t], y[t] = (h[t] . C[t] + D x[t]) silu(z[t]).  Tiles of kTile tokens: what goes
 // by channel alone is worked out by the channel's owner, exchanged between lanes before the tile's recurrence, and the
 // outputs' shares after it, so that one token's arithmetic can run among another's; the next tile is asked for meanwhile.
-// Instructions bound it (about 135 a token and 32 channels of 16 states, 16 of them exponentials; the schedulers that have warps
+// Instructions bound it (about 131 a token and 32 channels of 16 states, 16 of them exponentials; the schedulers that have warps
 // issue 0.62 to 0.68 a cycle), not the special units (40 %) or DRAM (15 to 35 %).
 // Where sequences are few, segments of time run side by side: a first launch takes each segment's states from zero and
 // the sum of its step sizes; since a segment turns the state h it gets into exp(A sum delta) h + (its state from zero), each
 // segment of the second launch finds its own entering state from those of the segments before it.  8 x 2048 tokens of 2048
-// channels: 103 + 182 us split, 299 whole; 16001 tokens of 1536: 87 + 150 us; nine prompts up to 1500: 59 + 95 us, 211 whole.
+// channels: 100 + 168 us split, 301 whole; 16001 tokens of 1536: 215 us a call, 2207 whole; nine prompts up to 1500: 143 and 213.
 #include "ssm_scan_common.cuh"
 
 namespace gdn {
