@@ -21,8 +21,9 @@
  *
  * Sequences of the convolution and the scan: cu NULL: sequence b holds rows b * T .. of the tensors; else int32 [B + 1]
  * row offsets on the device, ascending, with sequences of at most T rows (longer ones are cut there, offsets outside
- * [0, rows] are taken as the nearer bound).  Rows of no sequence are neither read into a result nor written.  Values in
- * one sequence never reach another's rows or states, NaN and Inf included; the gradients of weights are sums over all.
+ * [0, rows] are taken as the nearer bound); T = rows will do where the longest is not known.  Rows of no sequence are
+ * neither read into a result nor written.  Values in one sequence never reach another's rows or states, NaN and Inf
+ * included; the gradients of weights are sums over all.
  */
 #ifndef GDN_SSM_H
 #define GDN_SSM_H
@@ -122,7 +123,8 @@ typedef struct {
     int rows;             /* rows of the tensors (B * T without cu)            */
 } gdn_scan_t;
 
-/* Workspace of gdn_scan_fwd (backward = 0) or gdn_scan_bwd (1); the bytes of `saved`.  0 if the shape is invalid. */
+/* Workspace of gdn_scan_fwd (backward = 0) or gdn_scan_bwd (1); the bytes of `saved`.  0 if the shape is invalid.  (Not
+ * ascending with the shape: fewer sequences may be split into more segments.) */
 size_t gdn_scan_workspace_bytes(const gdn_scan_t* shape, int backward);
 size_t gdn_scan_saved_bytes(const gdn_scan_t* shape);
 

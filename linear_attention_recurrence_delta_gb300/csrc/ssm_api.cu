@@ -111,6 +111,8 @@ void scan_layout(const ScanPlan& p, void* ws, ScanArgs* a)
     a->saved_blocks = saved_blocks_of(a->s);
     a->segments = p.segments;
     a->seg_len = p.seg_len;
+    a->shares = p.shares;
+    a->sparse = sparse(a->s.B, a->s.T, a->s.rows);
     a->seg_h = (float*)(w + p.h_off);
     a->seg_d = (float*)(w + p.d_off);
     a->wpart = (float*)(w + p.w_off);
@@ -128,7 +130,7 @@ ScanPlan scan_plan(const gdn_scan_t& s, int backward)
     const int each = s.D / s.G, ch = backward ? back_channels(s.N) : fwd_channels(s.N), cta = backward ? kBackWarps * ch : ch;
     p.blocks = (each + ch - 1) / ch;
     p.ctas = (each + cta - 1) / cta;
-    const long long warps = (long long)p.blocks * s.G * s.B, T = s.T < s.rows ? s.T : s.rows;
+    const long long T = s.T < s.rows ? s.T : s.rows;
     // Segments: as many as keep the SMs in warps, counted by the sequences that run at once on average.  Forwards (up to 16 warps an
     // SM) the first launch takes three fifths of the second: 9 prompts up to 1500 tokens take 213 us whole and 143 in 16
     // segments, 8 x 2048 of 2048 channels 301 and 267 in 9, one of 16001 2207 and 215 in 64 (262 in 32).  Backwards (8 warps
@@ -140,11 +142,12 @@ ScanPlan scan_plan(const gdn_scan_t& s, int backward)
     if (seg < (backward ? 3 : 4)) seg = 1;
     p.seg_len = seg > 1 ? (int)(((T + seg - 1) / seg + kSaveEvery - 1) / kSaveEvery * kSaveEvery) : (T > 0 ? (int)((T + 31) / 32 * 32) : 32);
     p.segments = T > 0 ? (int)((T + p.seg_len - 1) / p.seg_len) : 1;
-    const size_t places = p.segments > 1 ? (size_t)p.segments * warps : 0;
+    p.shares = sparse(s.B, s.T, s.rows) ? places(s.B, s.rows, p.seg_len) : p.segments * s.B;
+    const size_t kept = p.segments > 1 ? (size_t)places(s.B, s.rows, p.seg_len) * s.G * p.blocks : 0;
     p.h_off = 256;
-    p.d_off = p.h_off + round_up(places * ch * state_values(s.N) * 4, 256);
-    p.w_off = p.d_off + round_up(places * ch * 4, 256);
-    p.bc_off = p.w_off + (backward ? round_up((size_t)p.segments * s.B * s.D * (s.N + 2) * 4, 256) : 0);
+    p.d_off = p.h_off + round_up(kept * ch * state_values(s.N) * 4, 256);
+    p.w_off = p.d_off + round_up(kept * ch * 4, 256);
+    p.bc_off = p.w_off + (backward ? round_up((size_t)p.shares * s.D * (s.N + 2) * 4, 256) : 0);
     p.total = p.bc_off + (backward ? round_up((size_t)p.ctas * s.rows * s.G * 2 * s.N * 4, 256) : 0);
     return p;
 }

@@ -45,6 +45,30 @@ __device__ __forceinline__ float softplus(float v, float& slope)
     return fmaf(2.f * s, p, fmaxf(v, 0.f));
 }
 
+// the last of [0, n) whose key, which ascends, is at most k (0 if none is)
+template <typename Key>
+__device__ __forceinline__ int last_at_most(int n, int k, Key key)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (key(mid) <= k) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+__device__ __forceinline__ int offset_of(const int* cu, int b, int rows) { return min(max(cu[b], 0), rows); }
+// whose place k is: a sequence and its piece of L rows (which may lie past its end)
+struct Place {
+    int b, piece;
+};
+__device__ __forceinline__ Place place_of(const int* cu, int B, int rows, int L, int k)
+{
+    auto key = [&](int b) { return offset_of(cu, b, rows) / L + b; };
+    const int b = last_at_most(B, k, key), first = key(b);
+    return {b, k < first ? places(B, rows, L) : k - first};
+}
+
 // 16 bytes to shared memory, zeros unless ok
 __device__ __forceinline__ void cp_async16_zero(void* to, const void* from, bool ok)
 {

@@ -104,13 +104,19 @@ __device__ __forceinline__ void load_past(const IO* x, long long tok, const void
     }
 }
 
-// Sequence blockIdx.y; threads run over (strip, piece of 4 channels), pieces fastest.
-template <typename IO, int W, bool SILU>
+// Sequence blockIdx.y (SPARSE: whose place it is); threads run over (strip, piece of 4 channels), pieces fastest.
+template <typename IO, int W, bool SILU, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a)
 {
-    const int D = a.s.D, pieces = D >> 2, b = blockIdx.y;
+    const int D = a.s.D, pieces = D >> 2;
     const long long u = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int strip = (int)(u / pieces), c = (int)(u - (long long)strip * pieces) << 2;
+    int strip = (int)(u / pieces), b = blockIdx.y;
+    const int c = (int)(u - (long long)strip * pieces) << 2;
+    if (SPARSE) {
+        const Place p = place_of(a.cu, a.s.B, a.s.rows, kStrip, strip);
+        b = p.b;
+        strip = p.piece;
+    }
     const Rows r = rows_of(a.cu, b, a.s.T, a.s.rows);
     const long long first = (long long)strip * kStrip;
     if (first >= r.n && strip > 0) return;
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs 
 // A thread has 4 channels and keeps their sums of dw and dbias over the strips that it takes: strip by strip of all sequences
 // in turn, `2^l` pieces of channels by kBackThreads >> l strips at a time.
 // Four CTAs an SM: three leave loads unhidden (169 us for 149 both ways), five spill (208).
-template <typename IO, int W, bool SILU>
+template <typename IO, int W, bool SILU, bool SPARSE>
 __global__ void __launch_bounds__(kBackThreads, 4) conv_bwd_kernel(const ConvArgs a, int l)
 {
     __shared__ float4 share[kBackThreads];
@@ -202,7 +208,7 @@ __global__ void __launch_bounds__(kBackThreads, 4) conv_bwd_kernel(const ConvArg
     const int D = a.s.D, tx = threadIdx.x & ((1 << l) - 1), ty = threadIdx.x >> l, strips = kBackThreads >> l;
     const int c = 4 * ((blockIdx.x << l) + tx);
     const int each = a.s.T > 0 ? (a.s.T + kBackStrip - 1) / kBackStrip : 1;      // strips of a sequence
-    const long long items = (long long)a.s.B * each;
+    const long long items = SPARSE ? places(a.s.B, a.s.rows, kBackStrip) : (long long)a.s.B * each;
     Four taps[W], bias = all(0.f), dw[W], db = all(0.f);
 #pragma unroll
     for (int k = 0; k < W; k++) taps[k] = dw[k] = all(0.f);
@@ -211,9 +217,15 @@ __global__ void __launch_bounds__(kBackThreads, 4) conv_bwd_kernel(const ConvArg
         if (a.bias) bias = raw4(a.bias + c).get();
     }
     for (long long item = (long long)blockIdx.y * strips + ty; item < items && c < D; item += (long long)gridDim.y * strips) {
-        const int b = (int)(item / each), t0 = (int)(item - (long long)b * each) * kBackStrip;
+        int b = (int)(item / each), strip = (int)(item - (long long)b * each);
+        if (SPARSE) {
+            const Place p = place_of(a.cu, a.s.B, a.s.rows, kBackStrip, (int)item);
+            b = p.b;
+            strip = p.piece;
+        }
         const Rows r = rows_of(a.cu, b, a.s.T, a.s.rows);
-        if (t0 >= r.n && t0 > 0) continue;
+        if (strip > 0 && (long long)strip * kBackStrip >= r.n) continue;
+        const int t0 = strip * kBackStrip;
         const int end = min(r.n, t0 + kBackStrip), from = t0 == 0 && a.ds0 ? -(W - 1) : t0;      // rows whose gradients it writes
         const IO* x = (const IO*)a.x.p + (long long)r.first * a.x.tok + c;
         const IO* dy = (const IO*)a.dy.p + (long long)r.first * a.dy.tok + c;
@@ -322,10 +334,14 @@ int back_pieces(const gdn_conv_t& s)
 template <typename IO, int W>
 cudaError_t launch_fwd_w(const ConvArgs& a, cudaStream_t st)
 {
-    const long long strips = (a.s.T + kStrip - 1) / kStrip, units = (strips > 0 ? strips : 1) * (a.s.D >> 2);
-    const dim3 grid((unsigned)((units + kThreads - 1) / kThreads), a.s.B);
-    if (a.s.silu) conv_kernel<IO, W, true><<<grid, kThreads, 0, st>>>(a);
-    else conv_kernel<IO, W, false><<<grid, kThreads, 0, st>>>(a);
+    const bool sp = sparse(a.s.B, a.s.T, a.s.rows);
+    const long long strips = sp ? places(a.s.B, a.s.rows, kStrip) : (a.s.T + kStrip - 1) / kStrip;
+    const long long units = (strips > 0 ? strips : 1) * (a.s.D >> 2);
+    const dim3 grid((unsigned)((units + kThreads - 1) / kThreads), sp ? 1 : a.s.B);
+    if (sp && a.s.silu) conv_kernel<IO, W, true, true><<<grid, kThreads, 0, st>>>(a);
+    else if (sp) conv_kernel<IO, W, false, true><<<grid, kThreads, 0, st>>>(a);
+    else if (a.s.silu) conv_kernel<IO, W, true, false><<<grid, kThreads, 0, st>>>(a);
+    else conv_kernel<IO, W, false, false><<<grid, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename IO, int W>
@@ -340,8 +356,11 @@ cudaError_t launch_bwd_w(const ConvArgs& a, cudaStream_t st)
 {
     const int l = back_pieces(a.s), wide = ((a.s.D >> 2) + (1 << l) - 1) >> l;
     const dim3 grid(wide, conv_bwd_blocks(a.s));
-    if (a.s.silu) conv_bwd_kernel<IO, W, true><<<grid, kBackThreads, 0, st>>>(a, l);
-    else conv_bwd_kernel<IO, W, false><<<grid, kBackThreads, 0, st>>>(a, l);
+    const bool sp = sparse(a.s.B, a.s.T, a.s.rows);
+    if (sp && a.s.silu) conv_bwd_kernel<IO, W, true, true><<<grid, kBackThreads, 0, st>>>(a, l);
+    else if (sp) conv_bwd_kernel<IO, W, false, true><<<grid, kBackThreads, 0, st>>>(a, l);
+    else if (a.s.silu) conv_bwd_kernel<IO, W, true, false><<<grid, kBackThreads, 0, st>>>(a, l);
+    else conv_bwd_kernel<IO, W, false, false><<<grid, kBackThreads, 0, st>>>(a, l);
     return cudaGetLastError();
 }
 

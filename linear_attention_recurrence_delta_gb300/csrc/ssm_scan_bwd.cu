@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
     BackStage<IO, L>& S = stages[warp];
     const Spot p = spot<L, kBackWarps>(a);
     const int D = a.s.D, N = a.s.N;
+    if (p.share >= a.shares) return;
     if (FIRST && (p.channels == 0 || p.t0 >= p.t1 || p.t0 == 0)) return;
     States<L> A, back, dA;                          // back: the adjoint of the state that leaves the token
     float sum = 0.f;
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
         a.seg_d[segment_at(a, p, p.seg) * L::CH + oc] = sum;
         return;
     }
-    float* share = a.wpart + ((long long)p.seg * a.s.B + p.b) * D * (N + 2);
+    float* share = a.wpart + (long long)p.share * D * (N + 2);
 #pragma unroll
     for (int r = 0; r < RC; r++) {
         if (!has_state<L>(a, p, lane, r)) continue;
@@ -308,14 +309,17 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
 }
 
 // dB and dC of the sequences' rows: the shares of the group's blocks in their order
-template <typename IO>
+template <typename IO, bool SPARSE>
 __global__ void __launch_bounds__(256) scan_join_kernel(const ScanArgs a)
 {
     const int N = a.s.N, G = a.s.G, pieces = G * 2 * N / 8;
-    const Rows r = rows_of(a.cu, blockIdx.y, a.s.T, a.s.rows);
     const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int t = (int)(u / pieces), e = 8 * (int)(u - (long long)t * pieces), g = e / (2 * N), n = e - g * 2 * N;
-    if (t >= r.n) return;
+    int t = (int)(u / pieces), b = blockIdx.y;
+    const int e = 8 * (int)(u - (long long)t * pieces), g = e / (2 * N), n = e - g * 2 * N;
+    if (SPARSE) b = last_at_most(a.s.B, t, [&](int i) { return offset_of(a.cu, i, a.s.rows); });      // t: a row of any sequence
+    const Rows r = rows_of(a.cu, b, a.s.T, a.s.rows);
+    if (SPARSE) t -= r.first;
+    if (t < 0 || t >= r.n) return;
     const long long row = r.first + t, stride = (long long)a.s.rows * G * 2 * N;
     const float* in = a.bcpart + row * G * 2 * N + e;
     float s[8] = {};
@@ -334,7 +338,7 @@ template <typename IO, class L, class F>
 cudaError_t launch_lanes(const ScanArgs& a, cudaStream_t st)
 {
     constexpr size_t stages = kBackWarps * sizeof(BackStage<IO, L>), whole = stages + sizeof(BackParts<L>);
-    const dim3 grid(a.s.G * a.ctas, a.s.B, a.segments);
+    const dim3 grid = scan_grid(a);
     cudaError_t e = cudaSuccess;
     if (whole > 48 * 1024) e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, F, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)whole);
     if (e == cudaSuccess && stages > 48 * 1024 && a.segments > 1)
@@ -342,8 +346,10 @@ cudaError_t launch_lanes(const ScanArgs& a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     if (a.segments > 1) scan_bwd_kernel<IO, L, F, true><<<grid, 32 * kBackWarps, stages, st>>>(a);
     scan_bwd_kernel<IO, L, F, false><<<grid, 32 * kBackWarps, whole, st>>>(a);
-    const long long units = (long long)a.s.T * (a.s.G * 2 * a.s.N / 8);
-    if (units > 0) scan_join_kernel<IO><<<dim3((unsigned)((units + 255) / 256), a.s.B), 256, 0, st>>>(a);
+    const long long units = (long long)(a.sparse ? a.s.rows : a.s.T) * (a.s.G * 2 * a.s.N / 8);
+    const dim3 join((unsigned)((units + 255) / 256), a.sparse ? 1 : a.s.B);
+    if (units > 0 && a.sparse) scan_join_kernel<IO, true><<<join, 256, 0, st>>>(a);
+    else if (units > 0) scan_join_kernel<IO, false><<<join, 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename IO>
@@ -362,7 +368,7 @@ cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     ColumnSums c = {};
     c.partial = a.wpart;
-    c.rows = a.s.B * a.segments;
+    c.rows = a.shares;
     c.cols = (long long)a.s.D * (a.s.N + 2);
     c.a = (long long)a.s.D * a.s.N;
     c.b = a.s.D;

@@ -37,13 +37,19 @@ using States = float2[L::RC][L::S / 2];
 // where a warp works
 struct Spot {
     int g, b, seg;        // group, sequence, segment
+    int share;            // of the shares of sums over tokens (and may lie past them: nothing to do)
     int block;            // its number among all warps' blocks of channels
     int d0, channels;     // its first channel, how many it has (0: none)
     Rows r;               // the sequence's rows
     int t0, t1;           // tokens of the segment
     __device__ __forceinline__ bool has(int channel) const { return channel < channels; }
 };
-// W warps a CTA, a.ctas CTAs and a.blocks blocks of CH channels a group
+// W warps a CTA, a.ctas CTAs and a.blocks blocks of CH channels a group; the grid is segments of sequences, or their places
+inline dim3 scan_grid(const ScanArgs& a)
+{
+    const int n = places(a.s.B, a.s.rows, a.seg_len), z = (n + 65534) / 65535;
+    return a.sparse ? dim3(a.s.G * a.ctas, (n + z - 1) / z, z) : dim3(a.s.G * a.ctas, a.s.B, a.segments);
+}
 template <class L, int W>
 __device__ __forceinline__ Spot spot(const ScanArgs& a)
 {
@@ -51,6 +57,12 @@ __device__ __forceinline__ Spot spot(const ScanArgs& a)
     p.g = blockIdx.x / a.ctas;
     p.b = blockIdx.y;
     p.seg = blockIdx.z;
+    p.share = blockIdx.z * gridDim.y + blockIdx.y;
+    if (a.sparse) {
+        const Place at = place_of(a.cu, a.s.B, a.s.rows, a.seg_len, p.share);
+        p.b = at.b;
+        p.seg = at.piece;
+    }
     const int each = a.s.D / a.s.G, n = (blockIdx.x - p.g * a.ctas) * W + (threadIdx.x >> 5), c0 = min(each, n * L::CH);
     p.block = p.g * a.blocks + n;
     p.d0 = p.g * each + c0;
@@ -196,7 +208,7 @@ __device__ __forceinline__ void get_state(const float4* q, States<L>& h)
 // the place of what a segment hands on
 __device__ __forceinline__ long long segment_at(const ScanArgs& a, const Spot& p, int seg)
 {
-    return ((long long)seg * a.s.B + p.b) * (a.s.G * a.blocks) + p.block;
+    return (long long)(p.r.first / a.seg_len + p.b + seg) * (a.s.G * a.blocks) + p.block;
 }
 // where the states lie that enter chunk t / kSaveEvery of a sequence (neighbouring sequences' places never meet), and in
 // them the four states n .. n + 3 of channel c of the group, as the forward's lanes have them

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(32, 16) scan_kernel(const ScanArgs a)
 template <typename IO, class L>
 cudaError_t launch_lanes(const ScanArgs& a, cudaStream_t st)
 {
-    const dim3 grid(a.s.G * a.ctas, a.s.B, a.segments);
+    const dim3 grid = scan_grid(a);
     if (a.segments > 1) scan_kernel<IO, L, true><<<grid, 32, 0, st>>>(a);
     scan_kernel<IO, L, false><<<grid, 32, 0, st>>>(a);
     return cudaGetLastError();

@@ -249,12 +249,14 @@ def test_scan_step_refusals():
         refused(scan_step(s, **{k: FAKE + 1}), ALIGN)
 
 
-def test_workspaces_grow_with_their_shapes():
-    """No size of a shape takes less than a smaller one, so that a workspace for the largest batch serves all."""
+def test_workspaces_follow_the_rows():
+    """Every valid shape has a workspace; sequences that T allows and the rows do not hold take next to none of it."""
     for back in (0, 1):
         for D in (64, 512, 2048):
             sizes = [gdn.gdn_scan_workspace_bytes(gdn.make_scan(1, T, D, 16, rows=20000), back) for T in (1, 100, 20000)]
             assert all(n >= 256 for n in sizes)
+        one, many = (gdn.gdn_scan_workspace_bytes(gdn.make_scan(B, 16384, 2048, 16, rows=16384), back) for B in (1, 512))
+        assert many <= one + 2 * 512 * 2048 * 18 * 4
     assert gdn.gdn_scan_saved_bytes(gdn.make_scan(4, 1000, 64, 16)) >= (4000 // 16 + 4) * 64 * 16 * 4
 
 
