@@ -4,7 +4,7 @@
 // by channel alone is worked out by the channel's owner, exchanged between lanes before the tile's recurrence, and the
 // outputs' shares after it, so that one token's arithmetic can run among another's; the next tile is asked for meanwhile.
 // Instructions bound it (about 131 a token and 32 channels of 16 states, 16 of them exponentials; the schedulers that have warps
-// issue 0.62 to 0.68 a cycle), not the special units (40 %) or DRAM (15 to 35 %).
+// issue 0.65 to 0.70 a cycle, and a packed one of them takes two), not the special units (40 to 60 %) or DRAM (15 to 40 %).
 // Where sequences are few, segments of time run side by side: a first launch takes each segment's states from zero and
 // the sum of its step sizes; since a segment turns the state h it gets into exp(A sum delta) h + (its state from zero), each
 // segment of the second launch finds its own entering state from those of the segments before it.  8 x 2048 tokens of 2048
