@@ -123,8 +123,9 @@ typedef struct {
     int rows;             /* rows of the tensors (B * T without cu)            */
 } gdn_scan_t;
 
-/* Workspace of gdn_scan_fwd (backward = 0) or gdn_scan_bwd (1); the bytes of `saved`.  0 if the shape is invalid.  (Not
- * ascending with the shape: fewer sequences may be split into more segments.) */
+/* Workspace of gdn_scan_fwd (backward = 0) or gdn_scan_bwd (1); the bytes of `saved`.  0 if the shape is invalid.  The
+ * workspace of gdn_scan_bwd serves gdn_scan_fwd of the same shape too.  (Not ascending with the shape: fewer sequences may
+ * be split into more segments.) */
 size_t gdn_scan_workspace_bytes(const gdn_scan_t* shape, int backward);
 size_t gdn_scan_saved_bytes(const gdn_scan_t* shape);
 

@@ -1,4 +1,6 @@
 // ssm_api.cu -- the C ABI of the state-space operators: argument checks, workspace carve-up, dispatch.
+#include <algorithm>
+
 #include "ssm_internal.h"
 
 using namespace gdn;
@@ -149,6 +151,7 @@ ScanPlan scan_plan(const gdn_scan_t& s, int backward)
     p.w_off = p.d_off + round_up(kept * ch * 4, 256);
     p.bc_off = p.w_off + (backward ? round_up((size_t)p.shares * s.D * (s.N + 2) * 4, 256) : 0);
     p.total = p.bc_off + (backward ? round_up((size_t)p.ctas * s.rows * s.G * 2 * s.N * 4, 256) : 0);
+    if (backward) p.total = std::max(p.total, scan_plan(s, 0).total);      // one area serves a training step's both calls
     return p;
 }
 

@@ -257,6 +257,9 @@ def test_workspaces_follow_the_rows():
             assert all(n >= 256 for n in sizes)
         one, many = (gdn.gdn_scan_workspace_bytes(gdn.make_scan(B, 16384, 2048, 16, rows=16384), back) for B in (1, 512))
         assert many <= one + 2 * 512 * 2048 * 18 * 4
+    for B, T, D, N in ((8, 384, 2048, 8), (1, 384, 12992, 8), (3, 700, 40, 16), (12, 5000, 512, 64)):      # one area for both directions
+        fwd, bwd = (gdn.gdn_scan_workspace_bytes(gdn.make_scan(B, T, D, N), back) for back in (0, 1))
+        assert bwd >= fwd
     assert gdn.gdn_scan_saved_bytes(gdn.make_scan(4, 1000, 64, 16)) >= (4000 // 16 + 4) * 64 * 16 * 4
 
 
