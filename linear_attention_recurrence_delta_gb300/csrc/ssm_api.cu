@@ -134,11 +134,14 @@ ScanPlan scan_plan(const gdn_scan_t& s, int backward)
     p.ctas = (each + cta - 1) / cta;
     const long long T = s.T < s.rows ? s.T : s.rows;
     // Segments: as many as keep the SMs in warps, counted by the sequences that run at once on average.  Forwards (up to 16 warps an
-    // SM) the first launch takes three fifths of the second: 9 prompts up to 1500 tokens take 213 us whole and 143 in 16
-    // segments, 8 x 2048 of 2048 channels 301 and 267 in 9, one of 16001 2207 and 215 in 64 (262 in 32).  Backwards (8 warps
-    // an SM by their registers) only where few warps would run: 8 x 2048 tokens take 1009 us whole and 1170 in 3 segments,
-    // 2 x 333 of 208 channels 145 and 82.
-    long long seg = T > 0 ? (long long)(152.0 * (backward ? 8 : 32) * T / ((double)p.blocks * s.G * s.rows)) : 1;
+    // SM) the first launch takes three fifths of the second: 9 prompts up to 1500 tokens take 213 us whole and 135 in 16
+    // segments, which are two rounds of warps (one round, 8: 141; three, 24: 140), 8 x 2048 of 2048 channels 301 and 260 in 9
+    // (4, one round five sixths full: 300).  One round where equal sequences fill it: 16001 tokens of 1536 channels take 2207
+    // us whole, 205 in 50 and 217 in 64 or 101.  Backwards (8 warps an SM by their registers) only where few warps would
+    // run: 8 x 2048 tokens take 1009 us whole and 1170 in 3 segments, 2 x 333 of 208 channels 145 and 82.
+    const double each_round = T > 0 ? 152.0 * 16 * T / ((double)p.blocks * s.G * s.rows) : 1.0;      // segments in a round of 16 warps an SM
+    long long seg = (long long)(each_round * (backward ? 0.5 : 2.0));
+    if (!backward && (long long)s.B * T == s.rows && (long long)each_round >= 0.95 * each_round) seg = (long long)each_round;
     if (seg > T / 32) seg = T / 32;
     if (seg > 64) seg = 64;
     if (seg < (backward ? 3 : 4)) seg = 1;

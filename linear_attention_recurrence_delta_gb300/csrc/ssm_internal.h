@@ -105,6 +105,25 @@ cudaError_t launch_scan(const ScanArgs& a, cudaStream_t st);
 cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t st);
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t st);
 
+// Launches a kernel as the dependent of the one in front of it, which lets it start as soon as its own blocks have all begun
+// (or ended): it waits in cudaGridDependencySynchronize for what that one writes, and every block of it does so before it ends,
+// so that what follows in the stream finds both done.
+template <typename Args>
+cudaError_t launch_after(void (*kernel)(Args), dim3 grid, int threads, size_t smem, cudaStream_t st, const Args& args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 // Sums over the rows of partial [rows][cols], in a fixed order: the first `a` columns go to out_a, the next `b` to out_b,
 // the rest to out_c (NULL: dropped).
 struct ColumnSums {

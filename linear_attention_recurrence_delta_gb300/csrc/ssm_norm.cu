@@ -328,17 +328,9 @@ int norm_bwd_blocks(const gdn_norm_t& s)
 
 cudaError_t launch_column_sums(const ColumnSums& s, cudaStream_t st)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((s.cols + 31) / 32));
-    const bool few = s.rows <= 64;        // shares of a scan's sequences: many columns instead
-    cfg.blockDim = dim3(few ? 128 : 1024);
-    cfg.stream = st;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return few ? cudaLaunchKernelEx(&cfg, column_sums_kernel<4>, s) : cudaLaunchKernelEx(&cfg, column_sums_kernel<32>, s);
+    const dim3 grid((unsigned)((s.cols + 31) / 32));
+    // shares of a scan's few sequences: many columns instead
+    return s.rows <= 64 ? launch_after(column_sums_kernel<4>, grid, 128, 0, st, s) : launch_after(column_sums_kernel<32>, grid, 1024, 0, st, s);
 }
 
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st)

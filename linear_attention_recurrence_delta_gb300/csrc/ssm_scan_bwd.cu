@@ -75,7 +75,11 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
     BackStage<IO, L>& S = stages[warp];
     const Spot p = spot<L, kBackWarps>(a);
     const int D = a.s.D, N = a.s.N;
-    if (p.share >= a.shares) return;
+    cudaTriggerProgrammaticLaunchCompletion();
+    if (p.share >= a.shares) {
+        if (!FIRST) cudaGridDependencySynchronize();
+        return;
+    }
     if (FIRST && (p.channels == 0 || p.t0 >= p.t1 || p.t0 == 0)) return;
     States<L> A, back, dA;                          // back: the adjoint of the state that leaves the token
     float sum = 0.f;
@@ -86,9 +90,10 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
         for (int k = 0; k < H; k++) back[r][k] = dA[r][k] = f2(0.f, 0.f);
         if (!FIRST && a.dhT && has_state<L>(a, p, lane, r)) get(a.dhT + state_at<L>(a, p, lane, r), back[r]);
     }
-    if (!FIRST && p.channels > 0 && p.t0 < p.t1) {
-        const int last = (p.r.n - 1) / a.seg_len;       // the sequence's last segment
-        carry<L>(a, p, lane, last, -1, last - p.seg, A, back);
+    if (!FIRST && p.t1 < p.r.n) {                   // the last segments do not wait for the first launch
+        const int last = (p.r.n - 1) / a.seg_len;
+        cudaGridDependencySynchronize();
+        if (p.channels > 0) carry<L>(a, p, lane, last, -1, last - p.seg, A, back);
     }
     int saved[RC][L::S / 4];
     if (!FIRST)
@@ -306,12 +311,14 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
         share[(long long)D * N + p.d0 + oc] = dskip.v;
         share[(long long)D * (N + 1) + p.d0 + oc] = dbias.v;
     }
+    cudaGridDependencySynchronize();
 }
 
 // dB and dC of the sequences' rows: the shares of the group's blocks in their order
 template <typename IO, bool SPARSE>
 __global__ void __launch_bounds__(256) scan_join_kernel(const ScanArgs a)
 {
+    cudaGridDependencySynchronize();
     const int N = a.s.N, G = a.s.G, pieces = G * 2 * N / 8;
     const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
     int t = (int)(u / pieces), b = blockIdx.y;
@@ -345,12 +352,13 @@ cudaError_t launch_lanes(const ScanArgs& a, cudaStream_t st)
         e = cudaFuncSetAttribute(scan_bwd_kernel<IO, L, F, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)stages);
     if (e != cudaSuccess) return e;
     if (a.segments > 1) scan_bwd_kernel<IO, L, F, true><<<grid, 32 * kBackWarps, stages, st>>>(a);
-    scan_bwd_kernel<IO, L, F, false><<<grid, 32 * kBackWarps, whole, st>>>(a);
+    else scan_bwd_kernel<IO, L, F, false><<<grid, 32 * kBackWarps, whole, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (a.segments > 1 && (e = launch_after(scan_bwd_kernel<IO, L, F, false>, grid, 32 * kBackWarps, whole, st, a)) != cudaSuccess) return e;
     const long long units = (long long)(a.sparse ? a.s.rows : a.s.T) * (a.s.G * 2 * a.s.N / 8);
     const dim3 join((unsigned)((units + 255) / 256), a.sparse ? 1 : a.s.B);
-    if (units > 0 && a.sparse) scan_join_kernel<IO, true><<<join, 256, 0, st>>>(a);
-    else if (units > 0) scan_join_kernel<IO, false><<<join, 256, 0, st>>>(a);
-    return cudaGetLastError();
+    if (units == 0) return cudaSuccess;
+    return launch_after(a.sparse ? scan_join_kernel<IO, true> : scan_join_kernel<IO, false>, join, 256, 0, st, a);
 }
 template <typename IO>
 cudaError_t launch_typed(const ScanArgs& a, cudaStream_t st)

@@ -8,7 +8,9 @@
 // Where sequences are few, segments of time run side by side: a first launch takes each segment's states from zero and
 // the sum of its step sizes; since a segment turns the state h it gets into exp(A sum delta) h + (its state from zero), each
 // segment of the second launch finds its own entering state from those of the segments before it.  8 x 2048 tokens of 2048
-// channels: 100 + 168 us split, 301 whole; 16001 tokens of 1536: 215 us a call, 2207 whole; nine prompts up to 1500: 143 and 213.
+// channels: 100 + 169 us split, 301 whole; 16001 tokens of 1536: 205 us a call, 2207 whole; nine prompts up to 1500: 135 and 213.
+// The second launch begins while the first one ends: its warps get their rates, and those of first segments all their work, done
+// (prompts 145 us without).
 #include "ssm_scan_common.cuh"
 
 namespace gdn {
@@ -25,8 +27,12 @@ __global__ void __launch_bounds__(32, 16) scan_kernel(const ScanArgs a)
     __shared__ __align__(16) IO rows[2][FIRST ? 2 : 3][kTile][L::CH], vectors[2][FIRST ? 1 : 2][kTile][L::NS];      // x, dt, z; B, C
     const int lane = threadIdx.x, n = L::S * (lane / L::CL), oc = lane % L::CH, ot = lane / L::CH;
     const Spot p = spot<L, 1>(a);
+    if (FIRST) cudaTriggerProgrammaticLaunchCompletion();
     if (FIRST && (p.t0 >= p.t1 || p.t1 == p.r.n)) return;      // what a sequence's last segment hands on nobody takes
-    if (!FIRST && p.seg > 0 && p.t0 >= p.t1) return;
+    if (!FIRST && p.seg > 0 && p.t0 >= p.t1) {
+        cudaGridDependencySynchronize();
+        return;
+    }
     States<L> A, h;
     float sum = 0.f;
     load_rates<L>(a, p, lane, A);
@@ -36,7 +42,10 @@ __global__ void __launch_bounds__(32, 16) scan_kernel(const ScanArgs a)
         for (int k = 0; k < H; k++) h[r][k] = f2(0.f, 0.f);
         if (!FIRST && a.h0 && has_state<L>(a, p, lane, r)) get(a.h0 + state_at<L>(a, p, lane, r), h[r]);
     }
-    if (!FIRST) carry<L>(a, p, lane, 0, 1, p.seg, A, h);
+    if (!FIRST && p.seg > 0) {
+        cudaGridDependencySynchronize();      // the first segments do not wait for the first launch
+        carry<L>(a, p, lane, 0, 1, p.seg, A, h);
+    }
     const bool in = p.has(oc), gated = a.z.p != nullptr;
     const float bias = in && a.dt_bias ? a.dt_bias[p.d0 + oc] : 0.f;
     const float skip = !FIRST && in && a.D_skip ? a.D_skip[p.d0 + oc] : 0.f;
@@ -129,6 +138,7 @@ __global__ void __launch_bounds__(32, 16) scan_kernel(const ScanArgs a)
         for (int r = 0; r < RC; r++)
             if (has_state<L>(a, p, lane, r)) put(a.hT + state_at<L>(a, p, lane, r), h[r]);
     }
+    if (!FIRST) cudaGridDependencySynchronize();
 }
 
 template <typename IO, class L>
@@ -136,8 +146,9 @@ cudaError_t launch_lanes(const ScanArgs& a, cudaStream_t st)
 {
     const dim3 grid = scan_grid(a);
     if (a.segments > 1) scan_kernel<IO, L, true><<<grid, 32, 0, st>>>(a);
-    scan_kernel<IO, L, false><<<grid, 32, 0, st>>>(a);
-    return cudaGetLastError();
+    else scan_kernel<IO, L, false><<<grid, 32, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess && a.segments > 1 ? launch_after(scan_kernel<IO, L, false>, grid, 32, 0, st, a) : e;
 }
 template <typename IO>
 cudaError_t launch_typed(const ScanArgs& a, cudaStream_t st)
