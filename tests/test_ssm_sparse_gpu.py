@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import linear_attention_recurrence_delta_gb300 as gdn
-from tests.ssm_testlib import close, conv_all, gen, nan, normal, offsets, scan_inputs, tdtype
+from tests.ssm_testlib import ORDER, close, conv_all, cuda, gen, nan, normal, offsets, scan_inputs, tdtype
 from tests.test_ssm_scan_gpu import compare
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +66,31 @@ def test_the_longest_length_and_a_bound_agree():
             out.append((y, sT[:len(lens)]))
     for y, sT in out[1:]:
         assert torch.equal(y, out[0][0]) and torch.equal(sT, out[0][1])
+
+
+@pytest.mark.parametrize("lens,bound", [([700, 90, 260], False), ([900] + [3] * 30, True)])
+def test_calls_behind_one_another_share_a_workspace(lens, bound):
+    """Training steps of different inputs through one workspace and one `saved`, enqueued without a wait, give the bits of steps
+    alone: a split call's launches overlap with one another, and with nothing else."""
+    D, N, rows, B = 72, 16, sum(lens), len(lens)
+    cu, T = offsets(lens).cuda(), rows if bound else max(lens)
+    s = gdn.make_scan(B, T, D, N, 1, "bf16", rows=rows)
+    ws, saved = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in (gdn.gdn_scan_workspace_bytes(s, 1), gdn.gdn_scan_saved_bytes(s)))
+    sets = [cuda(scan_inputs(k, lens, D, N, 1, "bf16")) for k in range(3)]
+
+    def step(i):
+        args = [i[k] for k in ORDER]
+        out = {"y": nan((rows, D), torch.bfloat16), "hT": nan((B, D, N), torch.float32),
+               **{k: nan(i[k].shape, i[k].dtype) for k in ORDER + ("h0",)}}
+        gdn.check(gdn.gdn_scan_fwd(s, *args, cu, i["h0"], out["y"], out["hT"], saved, ws))
+        gdn.check(gdn.gdn_scan_bwd(s, *args, cu, saved, i["dy"], i["dhT"], *[out[k] for k in ORDER], out["h0"], ws))
+        return out
+
+    alone = []
+    for i in sets:
+        alone.append(step(i))
+        torch.cuda.synchronize()
+    for _ in range(10):
+        for got, want in zip([step(i) for i in sets], alone):
+            for k in want:
+                assert torch.isfinite(want[k]).all() and torch.equal(got[k], want[k]), k
