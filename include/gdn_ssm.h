@@ -138,7 +138,7 @@ gdn_status_t gdn_scan_fwd(const gdn_scan_t* shape, const gdn_mla_view_t* x, cons
                           const float* h0, const gdn_mla_view_t* y, float* hT, void* saved, size_t saved_bytes, void* ws,
                           size_t ws_bytes, gdn_stream_t stream);
 
-/* (A sum over channels in dBm or dCm of which a term is infinite is a NaN.)
+/* (A sum over channels in dBm or dCm of which a term is infinite is infinite or a NaN; other tokens' sums keep their values.)
  * Gradients from dy, dhT (NULL: zeros) and the forward's saved: dx, ddt, dz (NULL iff z is) views as their inputs, dBm,
  * dCm views; dA_log, dD_skip and ddt_bias (NULL iff theirs are) overwritten; dh0 (NULL: not written). */
 gdn_status_t gdn_scan_bwd(const gdn_scan_t* shape, const gdn_mla_view_t* x, const gdn_mla_view_t* dt,

@@ -5,7 +5,7 @@
 //   dB[t] = sum_d dh delta x,   dC[t] = sum_d g h,   dz = dy (sum_n h C + D x) silu'(z).
 // Tiles of kSaveEvery tokens are walked from the last to the first: the forward left the state that enters each, so a
 // tile's states are taken again into registers and then met by dh on its way back.
-// Sums over channels (dB, dC): a lane's two channels first, then lanes by matrix products with ones, then the CTA's warps, whose
+// Sums over channels (dB, dC): a lane's two channels first, then lanes by exchanges that halve them, then the CTA's warps, whose
 // sum it writes; a second launch joins the CTAs in their order.  Sums over tokens (dA_log, dD, d dt_bias) are joined likewise over
 // sequences and segments.  Instructions bound it (about 430 a token and 32 channels of 16 states, of which 110 are
 // packed multiplications and additions that the formulas need), at two warps a scheduler, which their registers allow:
@@ -19,19 +19,44 @@ namespace ssm {
 
 namespace {
 
-// Sums over lanes by matrix products with ones.  The 32 lanes' values v0, v1 are a 16 x 4 matrix whose rows 0 .. 7 are v0 of
-// lanes 4 r .. 4 r + 3 and whose rows 8 .. 15 are v1 of them; times a 4 x 8 matrix that is one in a column and zero elsewhere,
-// that column of acc gets the rows' sums added.  A product reads 11 bits of a value (tf32), so a value goes in as two,
-// its first 11 bits and those of the rest: 22 bits.
-__device__ __forceinline__ void add_column(float (&acc)[4], float2 v, uint32_t ones)
-{
-    const uint32_t h0 = __float_as_uint(v.x) & 0xffffe000u, h1 = __float_as_uint(v.y) & 0xffffe000u;
-    const float2 rest = fma2(f2(__uint_as_float(h0), __uint_as_float(h1)), f2(-1.f, -1.f), v);
-    const uint32_t l0 = __float_as_uint(rest.x) & 0xffffe000u, l1 = __float_as_uint(rest.y) & 0xffffe000u;
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %8}, {%0, %1, %2, %3};"
-                 : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
-                 : "r"(h0), "r"(h1), "r"(l0), "r"(l1), "r"(ones));
-}
+// A token's values v[0 .. 2 S - 1] (states of dB, then of dC), each summed over the CL lanes that hold the same states: each
+// exchange halves what a lane still holds, and LEFT whole sums stay, those from number (lane % CL) 2 S / CL on.  Plain fp32 additions of
+// one token's values alone: a NaN or an infinity reaches its own token's sums and no other's.  (Products with a matrix that is one
+// in the token's column and zero elsewhere, as tf32 in two parts, made NaN of every token's sums and kept 22 bits; a training pass
+// of 8 x 2048 tokens of 2048 channels took 979 us with them, 968 so.)
+template <class L>
+struct ChannelSums {
+    static constexpr int V = 2 * L::S, LEFT = V > L::CL ? V / L::CL : 1;
+    float x[LEFT];
+    __device__ __forceinline__ void take(float (&v)[V], int lane)
+    {
+        int m = L::CL / 2;
+#pragma unroll
+        for (int k = V / 2; k && m; k >>= 1, m >>= 1)
+#pragma unroll
+            for (int i = 0; i < k; i++) {
+                const bool up = lane & m;
+                const float keep = up ? v[i + k] : v[i], send = up ? v[i] : v[i + k];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+            }
+#pragma unroll
+        for (; m; m >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
+#pragma unroll
+        for (int i = 0; i < LEFT; i++) x[i] = v[i];
+    }
+    // where they go in a token's row of 2 NS sums, n being the lane's first state
+    static __device__ __forceinline__ int place(int lane, int n)
+    {
+        const int q = lane % L::CL * V / L::CL;
+        return (q < L::S ? 0 : L::NS - L::S) + n + q;
+    }
+    __device__ __forceinline__ void put(float* to) const
+    {
+        if (LEFT == 4) *reinterpret_cast<float4*>(to) = make_float4(x[0], x[LEFT / 4], x[LEFT / 2], x[LEFT - 1]);
+        else if (LEFT == 2) *reinterpret_cast<float2*>(to) = make_float2(x[0], x[LEFT - 1]);
+        else *to = x[0];
+    }
+};
 
 // A long sum that carries what its last addition lost (Kahan's summation).
 struct Sum {
@@ -52,12 +77,10 @@ struct BackStage {
     float4 h[2][L::RC * L::S / 4][32];              // the states that enter
     float B[kTile][L::NS], C[kTile][L::NS];
 };
-// And the CTA's shares of dB and dC: this tile's and the last one's.  A product's rows are lanes / 4: CS of them hold the same
-// states and are added later.  A token's row of shares is PART values, planes lie PLANE apart.
+// And the CTA's shares of dB and dC: this tile's and the last one's, a warp's row of 2 NS sums for each token.
 template <class L>
 struct BackParts {
-    static constexpr int CS = L::CL / 4, PART = 2 * L::NS + 1, PLANE = (kTile * PART + 31) / 32 * 32 + 16;
-    float v[2][kBackWarps][CS * PLANE];
+    float v[2][kBackWarps][kTile][2 * L::NS];
 };
 
 // F: how the forward's lanes had the states
@@ -65,7 +88,7 @@ template <typename IO, class L, class F, bool FIRST>
 __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArgs a)
 {
     using P = BackParts<L>;
-    constexpr int K = kTile, RC = L::RC, OT = L::OT, OWN = L::OWN, NS = L::NS, H = L::S / 2, CS = P::CS, PART = P::PART, PLANE = P::PLANE;
+    constexpr int K = kTile, RC = L::RC, OT = L::OT, OWN = L::OWN, NS = L::NS, H = L::S / 2;
     // the states of M tokens are kept in registers at a time, with their factors where that is the whole tile
     constexpr int M = RC * L::S <= 8 ? K : K / 2;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -206,7 +229,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
                     }
                 }
             }
-            float accB[H][4] = {}, accC[H][4] = {};
+            ChannelSums<L> sums[M];
 #pragma unroll
             for (int i0 = M - OT; i0 >= 0; i0 -= OT) {
                 float du[OT][RC], pa[OT][RC], yc[OT][RC];
@@ -237,12 +260,15 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
                         pa[t][r] = spa.x + spa.y;
                         yc[t][r] = syc.x + syc.y;
                     }
-                    const uint32_t ones = lane >> 2 == 2 * (jj & 3) + (jj >> 2) ? 0x3f800000u : 0u;
+                    float v[2 * L::S];
 #pragma unroll
                     for (int k = 0; k < H; k++) {
-                        add_column(accB[k], vB[k], ones);
-                        add_column(accC[k], vC[k], ones);
+                        v[2 * k] = vB[k].x;
+                        v[2 * k + 1] = vB[k].y;
+                        v[L::S + 2 * k] = vC[k].x;
+                        v[L::S + 2 * k + 1] = vC[k].y;
                     }
+                    sums[jj].take(v, lane);
                 }
                 const int j = i0 + ot + m0, i = (i0 + m0) / OT;
                 const float sdu = to_owner<L>(du, lane), spa = to_owner<L>(pa, lane), syc = to_owner<L>(yc, lane);
@@ -257,17 +283,9 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
                 tskip = fmaf(g[i], x, tskip);       // zeros past the end
                 tbias += ok ? ddt : 0.f;
             }
-            // row r of a product is lanes 4 r .., columns 2 q and 2 q + 1 lane q's tokens (q and q + 4 of M)
-            const int r = lane >> 2, q = lane & 3;
-            float* to = parts.v[buf][warp] + r % CS * PLANE + (m0 + q) * PART + L::S * (r / CS);
+            const int at = ChannelSums<L>::place(lane, n);
 #pragma unroll
-            for (int k = 0; k < H; k++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    if (M < K && (e & 1)) continue;
-                    to[4 * (e & 1) * PART + 2 * k + (e >> 1)] = accB[k][e];
-                    to[4 * (e & 1) * PART + NS + 2 * k + (e >> 1)] = accC[k][e];
-                }
+            for (int jj = 0; jj < M; jj++) sums[jj].put(&parts.v[buf][warp][m0 + jj][at]);
         }
 #pragma unroll
         for (int r = 0; r < RC; r++)
@@ -282,9 +300,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
             const int u = u0 + threadIdx.x, j = u / (2 * NS), e = u % (2 * NS), m = e % NS;
             float s = 0.f;
 #pragma unroll
-            for (int v = 0; v < kBackWarps; v++)
-#pragma unroll
-                for (int c = 0; c < CS; c++) s += parts.v[buf][v][c * PLANE + j * PART + e];
+            for (int v = 0; v < kBackWarps; v++) s += parts.v[buf][v][j][e];
             if (u < K * 2 * NS && t0 + j < p.t1 && m < N) out[(long long)(p.r.first + t0 + j) * a.s.G * 2 * N + (e < NS ? 0 : N) + m] = s;
         }
     }

@@ -1,0 +1,69 @@
+"""NaN, infinities and sums past fp32 in the scan: they reach what the definition makes of them, and nothing beside it."""
+import math
+
+import pytest
+import torch
+
+from tests.ssm_testlib import WORK, cuda, nan, offsets, scan_grads, scan_inputs, scan_run
+
+pytestmark = pytest.mark.gpu
+
+
+def same(got, ref, what, name):
+    """Finite exactly where the definition in 64 bits is, and there within the bounds of `close`."""
+    step = torch.finfo(got.dtype).eps / 2
+    got, ref = got.detach().double().cpu(), ref.detach().double()
+    ok = ref.isfinite()
+    assert torch.equal(got.isfinite(), ok), f"{name}: {(got.isfinite() != ok).sum().item()} of {ok.numel()} values differ in being finite"
+    if ok.any():
+        got, ref = got[ok], ref[ok]
+        assert (got - ref).abs().sub(step * ref.abs()).max() <= WORK[what] * ref.abs().max(), name
+
+
+def check(i, lens, io):
+    y, hT, grads = scan_grads(i, lens)
+    got = scan_run(cuda(i), lens, io, cu=offsets(lens).cuda(), train=True)
+    same(got["y"], y, "scan", "y")
+    same(got["hT"], hT, "scan", "hT")
+    for k, d in grads.items():
+        same(got["d" + k], d, "scan_bwd", "d" + k)
+
+
+POISON = [("x", math.nan), ("x", math.inf), ("dt", math.nan), ("z", math.nan), ("Bm", math.nan), ("Cm", math.nan), ("dy", math.nan),
+          ("dy", -math.inf)]
+
+
+@pytest.mark.parametrize("key,value", POISON)
+@pytest.mark.parametrize("io,D,N,G", [("f32", 24, 16, 1), ("bf16", 96, 16, 2), ("f32", 40, 8, 1), ("bf16", 24, 24, 1), ("f32", 16, 64, 1)])
+def test_one_token(io, D, N, G, key, value):
+    """One value at one token in the middle of a sequence: of dBm and dCm too only the tokens that depend on it."""
+    lens = [13, 40, 9]
+    i = scan_inputs(D + N, lens, D, N, G, io)
+    i[key].select(0, 13 + 21)[(0, 5) if i[key].ndim == 3 else 5] = value
+    check(i, lens, io)
+
+
+@pytest.mark.parametrize("key", ["x", "dy"])
+def test_one_token_of_split_calls(key):
+    """The same where segments of time run side by side."""
+    lens = [600, 433]
+    i = scan_inputs(2, lens, 16, 16, 1, "f32")
+    i[key][333, 5] = math.nan
+    check(i, lens, "f32")
+
+
+def test_products_past_fp32():
+    """A state times a gradient that passes fp32 at one token: an infinite row of dCm there, the others as they are."""
+    n, at = 30, 19
+    i = scan_inputs(6, [n], 24, 16, 1, "f32", gate=False)
+    i["x"][at, 3], i["dy"][at, 3] = 1e30, 1e20
+    _, _, grads = scan_grads(i, [n])
+    assert (grads["Cm"][at].abs().max() > 3.5e38) and grads["Cm"][at - 1].abs().max() < 1e8
+    got = scan_run(cuda(i), [n], "f32", cu=offsets([n]).cuda(), train=True)["dCm"].double().cpu()
+    for t in range(n):
+        ref = grads["Cm"][t]
+        if t == at:
+            big = ref.abs() > 3.5e38
+            assert got[t][big].isinf().all() and (got[t][big].sign() == ref[big].sign()).all()
+        else:
+            assert (got[t] - ref).abs().max() <= WORK["scan_bwd"] * ref.abs().max(), t
