@@ -58,13 +58,14 @@ struct ChannelSums {
     }
 };
 
-// A long sum that carries what its last addition lost (Kahan's summation).
+// A long sum that carries what its last addition lost (Kahan's summation); nothing is lost of an infinite one, whose difference
+// from itself would make it a NaN.
 struct Sum {
     float v = 0.f, lost = 0.f;
     __device__ __forceinline__ void add(float x)
     {
         const float y = __fsub_rn(x, lost), t = __fadd_rn(v, y);
-        lost = __fsub_rn(__fsub_rn(t, v), y);
+        lost = fabsf(t) < INFINITY ? __fsub_rn(__fsub_rn(t, v), y) : 0.f;
         v = t;
     }
 };

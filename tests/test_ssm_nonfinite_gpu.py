@@ -67,3 +67,19 @@ def test_products_past_fp32():
             assert got[t][big].isinf().all() and (got[t][big].sign() == ref[big].sign()).all()
         else:
             assert (got[t] - ref).abs().max() <= WORK["scan_bwd"] * ref.abs().max(), t
+
+
+@pytest.mark.parametrize("which", ["skip", "bias"])
+def test_sums_over_tokens_past_fp32(which):
+    """dD or d dt_bias past fp32 after some of its tokens is infinite, not a NaN.  Every term has one sign: rates of 2e-9 over 200
+    tokens change a state by less than 1e-6 of it, so d delta[t] = 8 (200 - t) g (C B) x to that."""
+    n, D, N = 200, 16, 8
+    i = scan_inputs(1, [n], D, N, 1, "f32", gate=False, softplus=False, h0=False)
+    i["x"], i["dt"], i["bias"], i["A_log"] = torch.ones(n, D), torch.full((n, D), 0.01), torch.zeros(D), torch.full((D, N), -20.0)
+    i["dhT"] = torch.zeros(1, D, N)
+    i["Bm"], i["Cm"] = torch.ones(n, 1, N), torch.full((n, 1, N), 1e-10 if which == "skip" else 1.0)
+    i["dy"] = torch.full((n, D), 3e37 if which == "skip" else 1e34)      # sums 6e39; 8 x 1e34 x 20100 = 1.6e39
+    got = scan_run(cuda(i), [n], "f32", softplus=False, cu=offsets([n]).cuda(), train=True)
+    assert got["d" + which].isposinf().all()
+    for k in ("x", "dt", "Bm", "skip" if which == "bias" else "bias"):
+        assert got["d" + k].isfinite().all(), k
