@@ -114,8 +114,8 @@ gdn_status_t gdn_conv_step(const gdn_conv_step_t* shape, const gdn_mla_view_t* x
  *   y[t, d]     = (sum_n h[t, d, n] Cm[t, g, n] + D[d] x[t, d]) * silu(z[t, d]),        g = d / (D / G)
  *
  * within each sequence, from its state h0 [D, N] (zeros without).  delta is meant to be >= 0 (without softplus a negative
- * one grows the state).  Limits: N a multiple of 8 up to 64, D a multiple of 8 G, B, G >= 1, T >= 1 where rows > 0,
- * B, G <= 65535, rows <= 2^30, B * D * N and D (N + 2) < 2^31. */
+ * one grows the state); an exp(A_log) past fp32 counts as its largest value.  Limits: N a multiple of 8 up to 64, D a
+ * multiple of 8 G, B, G >= 1, T >= 1 where rows > 0, B, G <= 65535, rows <= 2^30, B * D * N and D (N + 2) < 2^31. */
 typedef struct {
     int B, T, D, N, G;    /* sequences, most rows of one, channels, states a channel, groups that share Bm and Cm */
     int softplus;

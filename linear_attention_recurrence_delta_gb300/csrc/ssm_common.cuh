@@ -27,6 +27,13 @@ __device__ __forceinline__ float rcp(float x)     // 1 / x to about an ulp; 0 fo
     return y;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b)     // the larger one, NaN if either is
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2_approx(-kLog2e * x)); }
 
 // log(1 + exp(v)) and its derivative.  With e = exp(-|v|) in (0, 1] it is max(v, 0) + log(1 + e), and

@@ -131,7 +131,7 @@ struct ColumnSums {
     int rows;
     long long cols, a, b;
     float *out_a, *out_b, *out_c;
-    const float* decay;       // A_log: out_a's sums are multiplied by -exp of it (NULL: as they are)
+    const float* decay;       // A_log: out_a's sums are multiplied by -exp of it, at most fp32's largest value (NULL: as they are)
 };
 cudaError_t launch_column_sums(const ColumnSums& c, cudaStream_t st);
 

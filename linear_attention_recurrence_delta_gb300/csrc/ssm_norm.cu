@@ -6,6 +6,7 @@
 // 6 for the sum of dw's shares.  5371 rows of 4096 with a 32-bit residual, in 8 bits: 40 us (243 MB); two pieces a thread and
 // more threads a row, not four (46 us), because more warps then wait for memory.
 #include <cuda_fp8.h>
+#include <float.h>
 
 #include "ssm_common.cuh"
 
@@ -16,13 +17,6 @@ namespace {
 
 constexpr int kThreads = 256, kMostThreads = 512;      // of a block: as a rule, and for the widest rows
 constexpr float kE4m3Top = 448.f, kScaleFloor = 1e-30f;
-
-__device__ __forceinline__ float max_nan(float a, float b)     // the larger one, NaN if either is
-{
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
 
 // What the 2^l threads of a row hold, joined in a fixed order; red: a place for each warp and kind of value, in turn one of
 // two, so that a barrier is enough.
@@ -307,7 +301,7 @@ __global__ void __launch_bounds__(32 * R) column_sums_kernel(const ColumnSums s)
 #pragma unroll
     for (int i = 1; i < R; i++) x += part[i][lane];
     if (c < s.a) {
-        if (s.out_a) s.out_a[c] = s.decay ? x * -expf(s.decay[c]) : x;
+        if (s.out_a) s.out_a[c] = s.decay ? x * max_nan(-expf(s.decay[c]), -FLT_MAX) : x;
     } else if (c < s.a + s.b) {
         if (s.out_b) s.out_b[c - s.a] = x;
     } else if (s.out_c) {

@@ -9,6 +9,8 @@
 // its own for r = 0.
 #pragma once
 
+#include <float.h>
+
 #include "ssm_common.cuh"
 
 namespace gdn {
@@ -163,7 +165,15 @@ __device__ __forceinline__ bool has_state(const ScanArgs& a, const Spot& p, int 
     return p.has(L::channel(lane, r)) && L::S * (lane / L::CL) < a.s.N;
 }
 
-// -exp(A_log) log2(e) of a lane's states; zeros past N and past the warp's channels
+// -exp(A_log) log2(e) of two states.  Rates past fp32 count as its largest value: times any step size of use that forgets all the same,
+// and times zero (a step past a sequence's end, or a state's product with a factor of zero) it is zero, as in exact arithmetic,
+// where infinity times zero would make a NaN.  A NaN stays one.
+__device__ __forceinline__ float2 rates(float2 A_log)
+{
+    return f2(max_nan(-expf(A_log.x) * kLog2e, -FLT_MAX), max_nan(-expf(A_log.y) * kLog2e, -FLT_MAX));
+}
+
+// the rates of a lane's states; zeros past N and past the warp's channels
 template <class L>
 __device__ __forceinline__ void load_rates(const ScanArgs& a, const Spot& p, int lane, States<L>& A)
 {
@@ -174,7 +184,7 @@ __device__ __forceinline__ void load_rates(const ScanArgs& a, const Spot& p, int
         if (!has_state<L>(a, p, lane, r)) continue;
         get(a.A_log + (long long)(p.d0 + L::channel(lane, r)) * a.s.N + L::S * (lane / L::CL), A[r]);
 #pragma unroll
-        for (int k = 0; k < L::S / 2; k++) A[r][k] = f2(-expf(A[r][k].x) * kLog2e, -expf(A[r][k].y) * kLog2e);
+        for (int k = 0; k < L::S / 2; k++) A[r][k] = rates(A[r][k]);
     }
 }
 

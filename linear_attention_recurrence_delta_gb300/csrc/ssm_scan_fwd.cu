@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kStepThreads, LS <= 2 ? 7 : 4) scan_step_kerne
     if (mine) {
         get(a.A_log + (long long)d * N + n, A);
 #pragma unroll
-        for (int k = 0; k < 4; k++) A[k] = f2(-expf(A[k].x) * kLog2e, -expf(A[k].y) * kLog2e);
+        for (int k = 0; k < 4; k++) A[k] = rates(A[k]);
     }
     // from one sequence's rows to the next one's
     const long long dB = T * a.Bm.tok, dC = T * a.Cm.tok;

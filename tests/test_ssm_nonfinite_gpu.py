@@ -83,3 +83,28 @@ def test_sums_over_tokens_past_fp32(which):
     assert got["d" + which].isposinf().all()
     for k in ("x", "dt", "Bm", "skip" if which == "bias" else "bias"):
         assert got["d" + k].isfinite().all(), k
+
+
+@pytest.mark.parametrize("io,N", [("f32", 16), ("bf16", 8), ("f32", 40), ("bf16", 64)])
+@pytest.mark.parametrize("lens", [[13, 1, 40], [333]])
+def test_rates_past_fp32(io, N, lens):
+    """exp(A_log) past fp32 forgets at once, as in 64 bits, whatever a length leaves of the last tile: no NaN."""
+    i = scan_inputs(N, lens, 24, N, 1, io)
+    i["A_log"][::2] = 95.0
+    i["A_log"][1, ::3] = 88.9
+    check(i, lens, io)
+
+
+def test_rates_past_fp32_of_new_tokens():
+    import linear_attention_recurrence_delta_gb300 as gdn
+    from tests.ssm_testlib import ORDER, scan_all
+    B, T, D, N = 3, 2, 24, 16
+    i = scan_inputs(4, [T] * B, D, N, 1, "f32", softplus=False)
+    i["A_log"][::2] = 95.0
+    i["dt"][0], i["bias"] = 0.0, torch.zeros(D)      # a step of size zero changes nothing, whatever the rate
+    dev, y = cuda(i), nan((B * T, D), torch.float32)
+    state = dev["h0"].clone()
+    gdn.check(gdn.gdn_scan_step(gdn.make_scan_step(B, T, D, N, B, 1, "f32", softplus=False), *[dev[k] for k in ORDER], state, None, None, y))
+    ref, h = scan_all({k: t.double() for k, t in i.items()}, [T] * B, softplus=False)
+    same(y, ref, "scan", "y")
+    same(state, h, "scan", "state")
