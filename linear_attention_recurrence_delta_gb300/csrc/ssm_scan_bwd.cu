@@ -58,16 +58,17 @@ struct ChannelSums {
     }
 };
 
-// A long sum that carries what its last addition lost (Kahan's summation); nothing is lost of an infinite one, whose difference
-// from itself would make it a NaN.
+// A long sum and, beside it, the sum of what its additions lost (compensated summation), which joins it at the end: unless the
+// sum is infinite by then, whose difference from itself would make it a NaN.
 struct Sum {
     float v = 0.f, lost = 0.f;
     __device__ __forceinline__ void add(float x)
     {
-        const float y = __fsub_rn(x, lost), t = __fadd_rn(v, y);
-        lost = fabsf(t) < INFINITY ? __fsub_rn(__fsub_rn(t, v), y) : 0.f;
+        const float t = __fadd_rn(v, x);
+        lost = __fadd_rn(lost, __fsub_rn(x, __fsub_rn(t, v)));
         v = t;
     }
+    __device__ __forceinline__ float value() const { return fabsf(v) < INFINITY ? v + lost : v; }
 };
 
 // What a warp keeps in shared memory.
@@ -319,14 +320,15 @@ __global__ void __launch_bounds__(32 * kBackWarps) scan_bwd_kernel(const ScanArg
         if (a.dh0 && p.seg == 0) put(a.dh0 + state_at<L>(a, p, lane, r), back[r]);
         put(share + (long long)(p.d0 + L::channel(lane, r)) * N + n, dA[r]);
     }
+    float wskip = dskip.value(), wbias = dbias.value();
 #pragma unroll
     for (int m = L::CH; m < 32; m <<= 1) {
-        dskip.v += __shfl_xor_sync(0xffffffffu, dskip.v, m);
-        dbias.v += __shfl_xor_sync(0xffffffffu, dbias.v, m);
+        wskip += __shfl_xor_sync(0xffffffffu, wskip, m);
+        wbias += __shfl_xor_sync(0xffffffffu, wbias, m);
     }
     if (ot == 0 && in) {
-        share[(long long)D * N + p.d0 + oc] = dskip.v;
-        share[(long long)D * (N + 1) + p.d0 + oc] = dbias.v;
+        share[(long long)D * N + p.d0 + oc] = wskip;
+        share[(long long)D * (N + 1) + p.d0 + oc] = wbias;
     }
     cudaGridDependencySynchronize();
 }
