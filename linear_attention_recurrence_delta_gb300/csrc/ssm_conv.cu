@@ -378,7 +378,8 @@ cudaError_t launch_bwd_w(const ConvArgs& a, cudaStream_t st)
 int conv_bwd_blocks(const gdn_conv_t& s)
 {
     const int l = back_pieces(s), wide = ((s.D >> 2) + (1 << l) - 1) >> l, strips = kBackThreads >> l;
-    const long long each = s.T > 0 ? (s.T + kBackStrip - 1) / kBackStrip : 1, items = (long long)s.B * each;
+    const int T = s.T < s.rows ? s.T : s.rows;      // as the launch has it: a T past the rows is no bound
+    const long long each = T > 0 ? (T + kBackStrip - 1) / kBackStrip : 1, items = (long long)s.B * each;
     const long long need = (items + strips - 1) / strips, most = 152 * 32 / wide;
     return need < most ? (int)need : most < 1 ? 1 : (int)most;
 }
