@@ -168,7 +168,7 @@ template <typename IO, typename RES, int V, bool AHEAD>
 __global__ void __launch_bounds__(V > 2 ? kMostThreads : kThreads, V > 2 ? 1 : 2) norm_bwd_kernel(const NormArgs a, int l)
 {
     __shared__ float red[2][2][kMostThreads / 32];
-    extern __shared__ float dws[];      // [rows a block][D], where a block takes several rows
+    extern __shared__ __align__(16) float dws[];      // [rows a block][D], where a block takes several rows
     const int per = blockDim.x >> l, sub = threadIdx.x >> l, t = threadIdx.x & ((1 << l) - 1), D = a.s.D;
     const long long stride = (long long)gridDim.x * per;
     float dw[V][8] = {}, w[AHEAD ? V : 1][8] = {};
