@@ -40,7 +40,8 @@ extern "C" {
  *
  * out = io: y is of the I/O type.  out = GDN_E4M3: y holds 8-bit values and scale one fp32 number for each `group` values
  * of a row (group = 0: for the whole row), y[n, i] ~ value * scale with scale = max(max |y| over the group, 1e-30) / 448
- * and value = y / scale rounded to nearest even.  A NaN in a row gives NaN for its values and scales.
+ * and value = y / scale rounded to nearest even.  A NaN in a row gives NaN for its values and scales;
+ * a finite row whose sum of squares passes fp32 (values of 1e19 and more) gives zeros.
  * Limits: 0 <= N <= 2^30, 8 <= D <= 16384 a multiple of 8, group 0, 32, 64 or 128 and a divisor of D. */
 #define GDN_E4M3 2        /* value of gdn_norm_t.out beside gdn_dtype_t's */
 
@@ -125,7 +126,8 @@ typedef struct {
 
 /* Workspace of gdn_scan_fwd (backward = 0) or gdn_scan_bwd (1); the bytes of `saved`.  0 if the shape is invalid.  The
  * workspace of gdn_scan_bwd serves gdn_scan_fwd of the same shape too.  (Not ascending with the shape: fewer sequences may
- * be split into more segments.) */
+ * be split into more segments.)  The gradients' one holds shares of dA_log, dD and ddt_bias, D (N + 2) fp32 for each sequence
+ * however short it is: 65535 sequences of 2 rows of 1024 channels with 16 states ask for 5.1 GB, 4096 of 16 rows for 0.44 GB. */
 size_t gdn_scan_workspace_bytes(const gdn_scan_t* shape, int backward);
 size_t gdn_scan_saved_bytes(const gdn_scan_t* shape);
 

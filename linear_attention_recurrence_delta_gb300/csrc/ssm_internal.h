@@ -72,10 +72,16 @@ constexpr int kSaveEvery = 8;     // tokens between the states that a training f
 
 // Work over packed sequences is dealt as B x T rows, most of which is nobody's where one sequence is far longer than the
 // average or T is only a bound.  There it is dealt by places instead: piece i of L rows of sequence b has place cu[b] / L + b + i,
-// which no other sequence's piece has, `places` in all, and who works at a place looks up whose it is.  16384 rows of 2048 channels
-// as 512 sequences with T = 16384: convolution 36 us for 495, its gradients 75 for 379, scan 231 for 2256, its gradients 840 for
-// 1546; as 8 sequences 31 for 37, 58 for 82, 302 for 265 (sequences in turn, not their segments), 841 for 687: so not below four
-// times the rows, where little is nobody's.
+// which no other sequence's piece has, `places` in all, and who works at a place looks up whose it is.  16384 rows of 2048 channels with
+// T = 16384, us by places and as B x T rows (16 states; the sequences equal, but for the last two batches):
+//   sequences             2          5          8         16         32        128        512     9 uneven   30 uneven
+//   convolution                         31    37                                       36   495
+//   its gradients                       58    82                                       75   379
+//   scan           291  289   301  283   298  271   304  295   277  380   210  946   246 3333   306  322   313  406
+//   its gradients  886  867   939 1055   801  702   748  757   677  704   681  881   815 1651   919  886   829  831
+// So by places from over four times the rows on, where most of B x T is nobody's.  Up to 16 sequences either way of the scan is
+// faster by up to 14 %, as sequences and segments happen to fall to the SMs, and no ratio parts them; by places its workspace does not
+// grow with what T allows.
 inline bool sparse(int B, int T, int rows) { return (long long)B * (T < rows ? T : rows) > 4LL * rows; }
 __host__ __device__ inline int places(int B, int rows, int L) { return rows / L + B; }
 

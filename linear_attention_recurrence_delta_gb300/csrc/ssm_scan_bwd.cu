@@ -7,10 +7,10 @@
 // tile's states are taken again into registers and then met by dh on its way back.
 // Sums over channels (dB, dC): a lane's two channels first, then lanes by exchanges that halve them, then the CTA's warps, whose
 // sum it writes; a second launch joins the CTAs in their order.  Sums over tokens (dA_log, dD, d dt_bias) are joined likewise over
-// sequences and segments.  Instructions bound it (about 430 a token and 32 channels of 16 states, of which 110 are
-// packed multiplications and additions that the formulas need), at two warps a scheduler, which their registers allow:
-// 700 us for 8 x 2048 tokens of 2048 channels, 19 for the join.  With eight states a lane the sums over channels have twice the
-// values (840 us); eight states of two channels a lane do not fit the registers (1311).
+// sequences and segments.  Instructions bound it (425 a token and 32 channels of 16 states, of which 110 are
+// packed multiplications and additions that the formulas need and about 60 the sums over channels), at two warps a scheduler, which
+// their registers allow: 696 us for 8 x 2048 tokens of 2048 channels, 20 for the join.  With eight states a lane the sums over channels have
+// twice the values (840 us); eight states of two channels a lane do not fit the registers (1311).
 // Segments of time: as forwards, with the adjoint's recurrence in place of the state's.
 #include "ssm_scan_common.cuh"
 
@@ -22,11 +22,12 @@ namespace {
 // A token's values v[0 .. 2 S - 1] (states of dB, then of dC), each summed over the CL lanes that hold the same states: each
 // exchange halves what a lane still holds, and LEFT whole sums stay, those from number (lane % CL) 2 S / CL on.  Plain fp32 additions of
 // one token's values alone: a NaN or an infinity reaches its own token's sums and no other's.  (Products with a matrix that is one
-// in the token's column and zero elsewhere, as tf32 in two parts, made NaN of every token's sums and kept 22 bits; a training pass
-// of 8 x 2048 tokens of 2048 channels took 979 us with them, 968 so.)
+// in the token's column and zero elsewhere, as tf32 in two parts, made NaN of every token's sums and kept 22 bits; the gradients of
+// 8 x 2048 tokens of 2048 channels took 737 us a call with them and 736 so, with 8 states 591 and 529, with 32 1435 and 1360.)
 template <class L>
 struct ChannelSums {
     static constexpr int V = 2 * L::S, LEFT = V > L::CL ? V / L::CL : 1;
+    static_assert(LEFT == 1 || LEFT == 2 || LEFT == 4, "stored together");
     float x[LEFT];
     __device__ __forceinline__ void take(float (&v)[V], int lane)
     {
