@@ -136,10 +136,10 @@ ScanPlan scan_plan(const gdn_scan_t& s, int backward)
     // Segments: as many as keep the SMs in warps, counted by the sequences that run at once on average.  Forwards (up to 16 warps an
     // SM) the first launch takes three fifths of the second: 9 prompts up to 1500 tokens take 213 us whole and 135 in 16
     // segments, which are two rounds of warps (one round, 8: 141; three, 24: 140), 8 x 2048 of 2048 channels 301 and 260 in 9
-    // (4, one round five sixths full: 300).  One round where equal sequences fill it and it is of 15 segments or more: 16001 tokens
-    // of 1536 channels take 2207 us whole, 220 (a call by itself, as the next ones) in 50 segments and 233 in 64, 8 x 2048 of 608 channels 100 in 16 and 105 in 32,
-    // 2 x 4096 of 2560 channels 192 in 15 and 194 in 30; of fewer it leaves too much to one segment (4096 of 6208 channels 230 us in 12
-    // and 225 in 25, of 9376 331 in 8 and 318 in 16, 4 x 2048 of 4864 329 in 4 and 300 in 8).  Backwards (8 warps an SM by their
+    // (4, one round five sixths full: 300).  One round where equal sequences fill it and it is of 15 segments or more (us of a call by
+    // itself: 16001 tokens of 1536 channels 220 in 50 segments and 233 in 64, 2207 whole; 8 x 2048 of 608 channels 100 in 16 and
+    // 105 in 32; 2 x 4096 of 2560 channels 192 in 15 and 194 in 30); of fewer it is slower (4096 tokens of 6208 channels 230 in 12 and 225
+    // in 25, of 9376 331 in 8 and 318 in 16; 4 x 2048 of 4864 329 in 4 and 300 in 8).  Backwards (8 warps an SM by their
     // registers) only where few warps would run: 8 x 2048 tokens take 1009 us whole and 1170 in 3 segments, 2 x 333 of 208 channels
     // 145 and 82.
     const double each_round = T > 0 ? 152.0 * 16 * T / ((double)p.blocks * s.G * s.rows) : 1.0;      // segments in a round of 16 warps an SM
